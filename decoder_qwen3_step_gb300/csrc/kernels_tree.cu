@@ -1,0 +1,297 @@
+// kernels_tree.cu - draft trees over the paged KV cache: rotary tables, the
+// rotated append, the commit of an accepted path, and the merge of split
+// attention.  (Attention itself: kernels_tree_f32.cu, kernels_tree_f16.cu.)
+#include <limits.h>
+
+#include "tree_common.cuh"
+
+namespace dec {
+
+namespace {
+
+// ---- rotary table ---------------------------------------------------------------
+// (cos, sin)(p * freq_j) * mult.  The angle and its functions are formed in
+// 64 bits and rounded once: at position 40,959 a 32-bit angle would be off by
+// up to 2e-3.  Runs once per table.
+__global__ void k_rope_table(const __grid_constant__ RopeTableArgs a) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= a.positions * a.pairs) return;
+  double sn, cs;
+  sincos((double)(i / a.pairs) * a.freq[i % a.pairs], &sn, &cs);
+  reinterpret_cast<float2*>(a.table)[i] = make_float2((float)(cs * a.mult), (float)(sn * a.mult));
+}
+
+// ---- append ----------------------------------------------------------------------
+// y = x / sqrt(mean x^2 + eps) * gain (queries and keys, when a gain is given);
+// then for each pair (a, b) of the first rot channels
+//   a' = a cos - b sin,  b' = b cos + a sin;
+// queries go to q_out, keys and values to slot ctx + i of node i's sequence.
+// One pass over the data, so HBM bounds it: a head row is D/4 lanes with four
+// consecutive channels each (16-byte loads of fp32, 8 of 16-bit types); the
+// pair's other channel is in the same lane (interleaved) or rot/8 lanes away
+// (halves), one shuffle.  A lane keeps U rows in flight.
+template <int D, int U>
+__global__ void __launch_bounds__(256) k_tree_append(const __grid_constant__ TreeAppendArgs a) {
+  pdl_wait_prev();
+  pdl_launch_next();
+  constexpr int kLanes = D / 4, kSlots = 256 / kLanes;
+  const int H = a.q ? a.d.H : 0, Hkv = a.k ? a.d.Hkv : 0, heads = H + 2 * Hkv;
+  const int lane = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
+  const int64_t total = (int64_t)a.m.N * heads, row0 = ((int64_t)blockIdx.x * U) * kSlots + slot;
+  if (!tree_shape_ok(a.m)) return;
+  float4 x[U];
+  int node[U], head[U], pos[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t row = row0 + (int64_t)u * kSlots;
+    node[u] = row < total ? (int)((uint32_t)row / (uint32_t)heads) : -1;
+    head[u] = (int)(row - (int64_t)node[u] * heads);
+    pos[u] = -1;
+    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (node[u] < 0) continue;
+    pos[u] = __ldg(a.m.pos + node[u]);
+    if (a.rope && pos[u] >= a.rope_positions) {  // a replay whose plan outgrew the table of its capture
+      if (lane == 0) atomicOr(a.m.err, kErrBounds);
+      pos[u] = a.rope_positions - 1;
+    }
+    const int h = head[u];
+    if (h < H) x[u] = tree_load4(a.q, a.in_type, node[u] * a.ldq + h * D + lane * 4);
+    else if (h < H + Hkv) x[u] = tree_load4(a.k, a.in_type, node[u] * a.ldk + (h - H) * D + lane * 4);
+    else x[u] = tree_load4(a.v, a.in_type, node[u] * a.ldv + (h - H - Hkv) * D + lane * 4);
+  }
+  const int half = a.rot >> 1, el = lane * 4;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const bool is_q = head[u] < H, is_v = head[u] >= H + Hkv;
+    const float* gain = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
+    // every lane of the warp takes part in the shuffles; rows differ only in what they keep
+    float ss = x[u].x * x[u].x + x[u].y * x[u].y + x[u].z * x[u].z + x[u].w * x[u].w;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (gain) {
+      const float rn = 1.0f / sqrtf(ss / (float)D + a.d.eps);
+      const float4 g = *reinterpret_cast<const float4*>(gain + el);
+      x[u].x *= rn * g.x;
+      x[u].y *= rn * g.y;
+      x[u].z *= rn * g.z;
+      x[u].w *= rn * g.w;
+    }
+    if (a.rope) {
+      const bool turn = el < a.rot && !is_v && pos[u] >= 0;
+      const float2* t = reinterpret_cast<const float2*>(a.rope) + (size_t)max(pos[u], 0) * half;
+      if (a.interleaved) {
+        if (turn) {
+          const float4 cs = *reinterpret_cast<const float4*>(t + lane * 2);
+          const float4 y = x[u];
+          x[u] = make_float4(y.x * cs.x - y.y * cs.y, y.y * cs.x + y.x * cs.y, y.z * cs.z - y.w * cs.w,
+                             y.w * cs.z + y.z * cs.w);
+        }
+      } else {
+        const bool first = el < half;
+        const int other = el < a.rot ? (first ? lane + (half >> 2) : lane - (half >> 2)) : lane;
+        float4 p;
+        p.x = __shfl_sync(0xffffffffu, x[u].x, other, kLanes);
+        p.y = __shfl_sync(0xffffffffu, x[u].y, other, kLanes);
+        p.z = __shfl_sync(0xffffffffu, x[u].z, other, kLanes);
+        p.w = __shfl_sync(0xffffffffu, x[u].w, other, kLanes);
+        if (turn) {
+          const float4* c = reinterpret_cast<const float4*>(t + (first ? el : el - half));
+          const float4 c0 = c[0], c1 = c[1];
+          const float sg = first ? -1.f : 1.f;
+          x[u].x = x[u].x * c0.x + sg * p.x * c0.y;
+          x[u].y = x[u].y * c0.z + sg * p.y * c0.w;
+          x[u].z = x[u].z * c1.x + sg * p.z * c1.y;
+          x[u].w = x[u].w * c1.z + sg * p.w * c1.w;
+        }
+      }
+    }
+    if (node[u] < 0) continue;
+    if (is_q) {
+      // a padding node's query is zero: attention on it reads defined numbers
+      tree_store4(a.q_out, a.q_type, node[u] * a.ldo + head[u] * D + el, pos[u] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : x[u]);
+    } else if (pos[u] >= 0) {
+      const int dst = __ldg(a.m.dst + node[u]);
+      const int64_t off = kv_offset(a.layer, dst >> 4, is_v, head[u] - H - (is_v ? Hkv : 0), dst & 15, a.d.n_blocks,
+                                    a.d.Hkv, 16, D);
+      tree_store4(a.kv, a.kv_f16 ? kTreeF16 : kTreeF32, off + el, x[u]);
+    }
+  }
+}
+
+template <int D>
+cudaError_t append_d(const TreeAppendArgs& a, cudaStream_t s) {
+  constexpr int kSlots = 256 / (D / 4);
+  const int64_t rows = (int64_t)a.m.N * ((a.q ? a.d.H : 0) + (a.k ? 2 * a.d.Hkv : 0));
+  // one row per lane while that leaves SMs idle, then four for the loads in flight
+  if (rows <= 4 * 152 * kSlots) return launch_pdl(k_tree_append<D, 1>, (int)((rows + kSlots - 1) / kSlots), 256, 0, s, a);
+  return launch_pdl(k_tree_append<D, 4>, (int)((rows + 4 * kSlots - 1) / (4 * kSlots)), 256, 0, s, a);
+}
+
+// ---- commit ----------------------------------------------------------------------
+// The walk: from the root (taken as certain, or as prior chose) down to the
+// child whose token is the one the model chose at its parent, the lowest such
+// node, until there is none.  Then the K/V rows of the i-th node of the path
+// move from slot ctx + path[i] to ctx + i in every layer.  path[i] >= i and
+// path increases, so a row is never written before it has been read when the
+// rows move in order; each thread owns 16 bytes of the row of one (layer,
+// K or V, head) and moves them for the whole path, eight loads in flight, so
+// no two threads ever touch the same bytes.  Every block repeats the walk (a
+// few hundred loads) instead of waiting for another.
+constexpr int kCommitThreads = 256;
+
+__global__ void __launch_bounds__(kCommitThreads) k_tree_commit(const __grid_constant__ TreeCommitArgs a, int cols,
+                                                                int blocks_per_seq) {
+  pdl_wait_prev();
+  pdl_launch_next();
+  __shared__ int child[kTreeMaxNodes + 1], path[kTreeMaxNodes], n_path;
+  if (!tree_shape_ok(a.m)) return;
+  const int s = blockIdx.x / blocks_per_seq, part = blockIdx.x % blocks_per_seq;
+  const int b = __ldg(a.m.seq_start + s), T = __ldg(a.m.seq_start + s + 1) - b;
+  for (int i = threadIdx.x; i <= T; i += kCommitThreads) child[i] = INT_MAX;
+  __syncthreads();
+  for (int i = threadIdx.x; i < T; i += kCommitThreads) {
+    const int p = __ldg(a.m.parents + b + i);
+    if (p < -1) continue;  // padding
+    const bool ok = p >= 0 ? a.draft[b + i] == a.target[b + p] : !a.prior || a.draft[b + i] == a.prior[s];
+    if (ok) atomicMin(&child[p + 1], i);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int n = 0;
+    for (int at = child[0]; at != INT_MAX; at = child[at + 1]) path[n++] = at;
+    n_path = n;
+  }
+  __syncthreads();
+  const int n = n_path;
+  if (part == 0) {
+    for (int i = threadIdx.x; i < T; i += kCommitThreads) a.path[b + i] = i < n ? path[i] : -1;
+    if (threadIdx.x == 0) {
+      a.accepted[s] = n;
+      a.next[s] = n ? a.target[b + path[n - 1]] : a.prior ? a.prior[s] : -1;
+    }
+  }
+  const int row_chunks = a.d.D * a.kv_bytes / 16;  // 16-byte pieces of a head row
+  const int col = part * kCommitThreads + threadIdx.x;
+  if (col >= cols) return;
+  const int c = col % row_chunks, h = col / row_chunks % a.d.Hkv, lv = col / row_chunks / a.d.Hkv;
+  const int64_t slab = (int64_t)a.d.Hkv * 16 * row_chunks;  // pieces of one (layer, block, K or V)
+  int4* base = reinterpret_cast<int4*>(a.kv) + ((int64_t)(lv >> 1) * a.d.n_blocks * 2 + (lv & 1)) * slab +
+               (int64_t)h * 16 * row_chunks + c;
+  auto at = [&](int node) {
+    const int d = __ldg(a.m.dst + b + node);
+    return base + (int64_t)(d >> 4) * 2 * slab + (d & 15) * row_chunks;
+  };
+  int i0 = 0;
+  while (i0 < n && path[i0] == i0) ++i0;  // already in place
+  for (; i0 < n; i0 += 8) {
+    int4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i0 + u < n) v[u] = *at(path[i0 + u]);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i0 + u < n) *at(i0 + u) = v[u];
+  }
+}
+
+// ---- merge of split attention --------------------------------------------------------
+// A unit whose keys several CTAs shared: with each CTA's running maximum m_c
+// (base-2 logarithms), sum l_c and unnormalised output O_c,
+//   out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M),  M = max_c m_c,
+// the contributions added in CTA order.  One warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ TreeAttendArgs a) {
+  pdl_wait_prev();
+  pdl_launch_next();
+  if (!tree_shape_ok(a.m, true)) return;
+  constexpr int kPer = D / 32;
+  const int R = a.m.row_tile, G = a.d.H / a.d.Hkv, lane = threadIdx.x & 31, groups = R / 4;
+  const int n = __ldg(a.m.hdr + kHdrMerges);
+  for (int w = blockIdx.x; w < n * groups; w += gridDim.x) {
+    const TreeMerge e = a.m.merges[w / groups];
+    const int r = (w % groups) * 4 + (threadIdx.x >> 5);
+    const int node0 = __ldg(a.m.seq_start + e.seq);
+    const int row = e.row_tile * R + r;
+    if (row >= (__ldg(a.m.seq_start + e.seq + 1) - node0) * G) continue;
+    const int node = node0 + row / G;
+    auto rec = [&](int c) -> const float* { return tree_record(a, c, c == e.c0); };
+    float M = -INFINITY;
+    for (int c = e.c0 + lane; c <= e.c1; c += 32) M = fmaxf(M, __ldcg(rec(c) + R * D + r));
+    M = warp_max(M);
+    if (M == -INFINITY) M = 0.f;  // no contribution saw a finite score
+    float L = 0.f, o[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+    for (int c0 = e.c0; c0 <= e.c1; c0 += 32) {
+      float f = 0.f;
+      if (c0 + lane <= e.c1) {
+        const float* p = rec(c0 + lane) + R * D;
+        f = ex2(__ldcg(p + r) - M);
+        L = fmaf(__ldcg(p + R + r), f, L);
+      }
+      const int m = min(32, e.c1 - c0 + 1);
+#pragma unroll 4
+      for (int i = 0; i < m; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float* p = rec(c0 + i) + r * D + lane * kPer;
+        if constexpr (kPer == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
+          o[0] = fmaf(v.x, fi, o[0]);
+          o[1] = fmaf(v.y, fi, o[1]);
+          o[2] = fmaf(v.z, fi, o[2]);
+          o[3] = fmaf(v.w, fi, o[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) o[j] = fmaf(__ldcg(p + j), fi, o[j]);
+        }
+      }
+    }
+    L = warp_sum(L);
+    const bool pad = __ldg(a.m.pos + node) < 0;
+    const float inv = pad || L == 0.f ? 0.f : 1.0f / L;
+    const int64_t off = node * a.ldo + (int64_t)(e.head * G + row % G) * D + lane * kPer;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) o[j] = inv == 0.f ? 0.f : o[j] * inv;
+    if constexpr (kPer == 4) {
+      tree_store4(a.out, a.out_type, off, make_float4(o[0], o[1], o[2], o[3]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) tree_store(a.out, a.out_type, off + j, o[j]);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t s) {
+  k_rope_table<<<(a.positions * a.pairs + 255) / 256, 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tree_append(const TreeAppendArgs& a, cudaStream_t s) {
+  switch (a.d.D) {
+    case 32: return append_d<32>(a, s);
+    case 64: return append_d<64>(a, s);
+    case 128: return append_d<128>(a, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s) {
+  const int cols = a.d.n_layers * 2 * a.d.Hkv * (a.d.D * a.kv_bytes / 16);
+  const int per = (cols + kCommitThreads - 1) / kCommitThreads;
+  return launch_pdl(k_tree_commit, a.m.S * per, kCommitThreads, 0, s, a, cols, per);
+}
+
+cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, cudaStream_t s) {
+  // a replayed call may meet a plan with more merges than at its capture: the blocks loop
+  const int grid = max(n_merges, 1) * (a.m.row_tile / 4);
+  switch (a.d.D) {
+    case 32: return launch_pdl(k_tree_merge<32>, grid, 128, 0, s, a);
+    case 64: return launch_pdl(k_tree_merge<64>, grid, 128, 0, s, a);
+    case 128: return launch_pdl(k_tree_merge<128>, grid, 128, 0, s, a);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace dec

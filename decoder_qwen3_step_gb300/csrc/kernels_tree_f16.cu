@@ -1,0 +1,439 @@
+// kernels_tree_f16.cu - tree attention over an f16 cache (the serving modes)
+// on the warp-level f16 tensor cores.
+//
+// o_i = sum_j p_ij v_j / sum_j p_ij, p_ij = 2^(s_ij - m_i), s_ij = q_i . k_j *
+// log2(e) / sqrt(D) over the cached tokens, node i's ancestors and itself.
+//
+// A CTA takes a contiguous range of key tiles.  A producer warp streams each
+// tile (64 keys: 4 pool blocks, K and V, one 5-D TMA box per block) into a
+// ring; warp w of four folds block w of every tile for all R rows, so the
+// warps meet only at a unit's end: S = Q K^T by m16n8k16, the softmax in
+// fp32, O += P V with the accumulator in registers.  The running maximum is
+// raised (and O rescaled) only when a row's scores exceed it by 2^8, which
+// leaves the result exact: numerator and denominator use the same maximum.
+//
+// Rounded to f16: the queries, each row scaled by a power of two to [1, 2)
+// first so that no magnitude overflows (2^-12 relative per channel, as the
+// cached keys have it already), and the weights P (2^-12 relative each; they
+// are at most 2^8 and the row's largest at least 1).  Statistics and
+// accumulators are fp32.
+#include "attn_fold.cuh"
+#include "tc_common.cuh"
+#include "tree_common.cuh"
+
+namespace dec {
+
+namespace {
+
+template <int D, int R>
+struct F16Smem {
+  static constexpr int kSlab = 16 * D * 2;                     // K (or V) of one block
+  static constexpr int kStage = 4 * 2 * kSlab;
+  static constexpr int kStages = D == 128 ? 3 : D == 64 ? 6 : 8;
+  static constexpr int kQPitch = D * 2 + 16;                   // bytes; rows fall into different banks
+  static constexpr int kQ = kStages * kStage;                  // the queries, at a unit's end the warps' outputs
+  static constexpr int kRed = 4 * R * 16 * 4;
+  static constexpr int kML = kQ + (R * kQPitch > kRed ? R * kQPitch : kRed);  // float [4][R] maxima, [4][R] sums
+  static constexpr int kFac = kML + 2 * 4 * R * 4;             // float [R]: the rows' score factors
+  static constexpr int kBar = kFac + R * 4;
+  static constexpr int kBytes = kBar + 2 * kStages * 8 + 16;
+  static_assert(kML % 16 == 0 && kBar % 8 == 0, "alignment");
+};
+
+// Byte offset of (row r, channels d .. d+7) in a block's K or V slab.
+template <int D>
+__device__ __forceinline__ int slab_at(int r, int d) {
+  if constexpr (D >= 64) return (d >> 6) * 2048 + r * 128 + ((((d >> 3) & 7) ^ (r & 7)) << 4);
+  else return r * 64 + (((d >> 3) ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %2, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+constexpr int kF16Threads = 160;
+
+template <int D, int R>
+__global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid_constant__ CUtensorMap tm,
+                                                                    const __grid_constant__ TreeAttendArgs a) {
+  using SM = F16Smem<D, R>;
+  constexpr int MT = R / 16, kS = SM::kStages;
+  extern __shared__ __align__(1024) uint8_t dsm[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(dsm + SM::kBar);
+  uint64_t* empty = full + kS;
+  int* flags = reinterpret_cast<int*>(empty + kS);  // [0] abort, [1] a node's value of this unit is not finite
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 4);
+    }
+    flags[0] = flags[1] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  pdl_wait_prev();
+  pdl_launch_next();
+  if (!tree_shape_ok(a.m, true)) return;
+  volatile int* abort_flag = flags;
+  const int G = a.d.H / a.d.Hkv;
+  const TreeCut cut = a.m.cuts[blockIdx.x];
+  TreeUnit u{cut.seq, cut.head, cut.row_tile, 0, 0, 0, 0, 0};
+  if (cut.count > 0) tree_unit_load(a.m, G, R, u);
+  int tile = cut.tile, k = 0;
+
+  if (warp == 4) {
+    // ---- producer: lanes 0..3 copy one block each; table entries come 8 tiles at a time ----
+    for (int left = cut.count; left > 0;) {
+      const int t0 = tile, t1 = min(u.tiles, tile + left), blocks = (u.ctx + u.nodes + 15) >> 4;
+      const int32_t* table = a.m.tables + __ldg(a.m.tab_start + u.seq);
+      auto entries = [&](int t) {
+        const int b = t * 4 + lane;
+        int blk = b < blocks && b < t1 * 4 ? __ldg(table + b) : 0;
+#ifdef DEC_DEBUG
+        if ((unsigned)blk >= (unsigned)a.d.n_blocks) {
+          atomicOr(a.m.err, kErrBounds);
+          blk = 0;
+        }
+#endif
+        return blk;
+      };
+      int cur = 0, nxt = entries(t0);
+      for (int t = t0; t < t1; ++t, ++k) {
+        if (((t - t0) & 7) == 0) {
+          cur = nxt;
+          nxt = entries(t + 8);
+        }
+        const int blk = __shfl_sync(0xffffffffu, cur, (((t - t0) & 7) << 2) + (lane & 3));
+        const int slot = k % kS;
+        bool ok = true;
+        if (lane == 0 && k >= kS) ok = mbar_wait(&empty[slot], ((k / kS) - 1) & 1, abort_flag, a.m.err);
+        if (!__shfl_sync(0xffffffffu, (int)ok, 0)) goto produced;
+        if (lane == 0) mbar_expect_tx(&full[slot], min(4, blocks - t * 4) * 2 * SM::kSlab);
+        __syncwarp();
+        if (lane < 4 && t * 4 + lane < blocks)
+          tma_load_5d(dsm + slot * SM::kStage + lane * 2 * SM::kSlab, &tm, u.head * 16, a.layer * a.d.n_blocks + blk,
+                      &full[slot]);
+        __syncwarp();
+      }
+      left -= t1 - t0;
+      tile = 0;
+      if (left > 0) tree_unit_next(a.m, G, R, a.d.Hkv, u);
+    }
+  produced:;
+  } else {
+    // ---- consumers: warp w folds block w of every tile ----
+    uint8_t* Qs = dsm + SM::kQ;
+    float* red = reinterpret_cast<float*>(dsm + SM::kQ);
+    float* ml = reinterpret_cast<float*>(dsm + SM::kML);
+    float* fac = reinterpret_cast<float*>(dsm + SM::kFac);
+    auto group_bar = []() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    const int key = (lane & 7) + ((lane >> 4) << 3), doff = ((lane >> 3) & 1) * 8;
+    const int vkey = (lane & 7) + ((lane >> 3) & 1) * 8, vd = (lane >> 4) * 8;
+    bool alive = true;
+    for (int left = cut.count; left > 0;) {
+      const int t0 = tile, t1 = min(u.tiles, tile + left), end = u.ctx + u.nodes;
+      const int rows = min(R, u.nodes * G - u.row_tile * R);
+      // the queries: warp w takes rows w, w + 4, ...; each scaled by a power of two into f16's range
+      for (int r = warp; r < R; r += 4) {
+        const int row = u.row_tile * R + r;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        const int64_t off = (u.node0 + row / G) * a.ldq + (int64_t)(u.head * G + row % G) * D;
+        if (r < rows && lane * 4 < D) {
+          const float4 x = tree_load4(a.q, a.q_type, off + lane * 4);
+          v[0] = x.x;
+          v[1] = x.y;
+          v[2] = x.z;
+          v[3] = x.w;
+        }
+        const float mx = warp_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+        // 2^-e with 2^e <= mx < 2^(e+1); rows of zeros, infinities or subnormals stay as they are
+        const int e = (int)(__float_as_uint(mx) >> 23);
+        const bool scaled = e > 0 && e < 255;
+        const float f = scaled ? __uint_as_float((uint32_t)max(254 - e, 1) << 23) : 1.f;
+        if (lane * 4 < D) {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(Qs + r * SM::kQPitch + lane * 8);
+          dst[0] = af_pack_half(v[0] * f, v[1] * f);
+          dst[1] = af_pack_half(v[2] * f, v[3] * f);
+        }
+        if (lane == 0) fac[r] = a.scale_log2 * (scaled ? 1.f / f : 1.f);
+      }
+      group_bar();
+      const uint32_t qb = smem_u32(Qs) + (lane & 15) * SM::kQPitch + (lane >> 4) * 16;
+      float c[2 * MT], m[2 * MT], l[2 * MT], o[MT][D / 8][4];
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i) {
+        c[i] = fac[(i >> 1) * 16 + (i & 1) * 8 + (lane >> 2)];
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+
+      for (int t = t0; t < t1; ++t, ++k) {
+        const int slot = k % kS, key0 = t * kTreeKeys + warp * 16, nkeys = min(16, end - key0);
+        alive = __all_sync(0xffffffffu, alive && mbar_wait(&full[slot], (k / kS) & 1, abort_flag, a.m.err));
+        if (alive && nkeys > 0) {
+          uint8_t* Kb = dsm + slot * SM::kStage + warp * 2 * SM::kSlab;
+          uint8_t* Vb = Kb + SM::kSlab;
+          const uint32_t kb = smem_u32(Kb), vb = smem_u32(Vb);
+          float s[MT][2][4];
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) s[i][n][0] = s[i][n][1] = s[i][n][2] = s[i][n][3] = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t B[4];
+            af_ldsm4(kb + slab_at<D>(key, kk * 16 + doff), B);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              uint32_t A[4];
+              af_ldsm4(qb + i * 16 * SM::kQPitch + kk * 32, A);
+              af_mma_f16(s[i][0], A, B[0], B[1]);
+              af_mma_f16(s[i][1], A, B[2], B[3]);
+            }
+          }
+          const bool drafted = key0 + nkeys > u.ctx;  // some key of the block is a node
+          float mx[2 * MT];
+#pragma unroll
+          for (int i = 0; i < 2 * MT; ++i) {
+            float(&x)[2][4] = s[i >> 1];
+            const int e = (i & 1) * 2;
+            mx[i] = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              x[n][e] *= c[i];
+              x[n][e + 1] *= c[i];
+            }
+            if (drafted) {
+              const int row = u.row_tile * R + (i >> 1) * 16 + (i & 1) * 8 + (lane >> 2);
+              const int node = u.node0 + min(row / G, u.nodes - 1);
+#pragma unroll
+              for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const int j = key0 + n * 8 + 2 * (lane & 3) + z - u.ctx;
+                  if (j >= 0 && (j >= u.nodes || !tree_sees(a.m, node, j))) x[n][e + z] = -INFINITY;
+                }
+            }
+            mx[i] = fmaxf(fmaxf(x[0][e], x[0][e + 1]), fmaxf(x[1][e], x[1][e + 1]));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+          }
+          bool raise = false;
+#pragma unroll
+          for (int i = 0; i < 2 * MT; ++i) raise |= mx[i] > m[i] + 8.f;
+          if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+              const float mn = fmaxf(m[i], mx[i]);
+              const float f = mn == m[i] ? 1.f : ex2(m[i] - mn);
+              m[i] = mn;
+              l[i] *= f;
+#pragma unroll
+              for (int j = 0; j < D / 8; ++j) {
+                o[i >> 1][j][(i & 1) * 2] *= f;
+                o[i >> 1][j][(i & 1) * 2 + 1] *= f;
+              }
+            }
+          }
+          uint32_t P[MT][4];
+#pragma unroll
+          for (int i = 0; i < 2 * MT; ++i) {
+            float(&x)[2][4] = s[i >> 1];
+            const int e = (i & 1) * 2;
+            const float mu = m[i] == -INFINITY ? 0.f : m[i];  // nothing seen so far: every weight is 0
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float p0 = ex2(x[n][e] - mu), p1 = ex2(x[n][e + 1] - mu);
+              l[i] += p0 + p1;
+              P[i >> 1][2 * n + (i & 1)] = af_pack_half(p0, p1);
+            }
+          }
+          if (drafted) {
+            // value rows past the end hold anything: zero them; a node's value that is not finite must not meet
+            // another branch's zero weights: zero it too, its descendants get it back at the unit's end
+            bool odd = false;
+            for (int i = lane; i < 16 * (D / 8); i += 32) {
+              const int r = i / (D / 8);
+              uint4* p = reinterpret_cast<uint4*>(Vb + slab_at<D>(r, (i % (D / 8)) * 8));
+              uint4 x = *p;
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+              bool change = false;
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                if (r >= nkeys) {
+                  change |= w[z] != 0u;
+                  w[z] = 0u;
+                } else if (key0 + r >= u.ctx) {
+                  const uint32_t mk = ((w[z] & 0x7C00u) == 0x7C00u ? 0xFFFFu : 0u) |
+                                      ((w[z] & 0x7C000000u) == 0x7C000000u ? 0xFFFF0000u : 0u);
+                  if (mk) {
+                    w[z] &= ~mk;
+                    change = odd = true;
+                  }
+                }
+              }
+              if (change) *p = x;
+            }
+            if (__any_sync(0xffffffffu, odd) && lane == 0) flags[1] = 1;
+            // the slot is refilled by the async proxy later: order these stores before it
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t B[4];
+            af_ldsm4t(vb + slab_at<D>(vkey, j * 16 + vd), B);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              af_mma_f16(o[i][2 * j], P[i], B[0], B[1]);
+              af_mma_f16(o[i][2 * j + 1], P[i], B[2], B[3]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
+      }
+      // ---- the unit's end: the four warps' states in warp order ----
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        if ((lane & 3) == 0) {
+          const int r = (i >> 1) * 16 + (i & 1) * 8 + (lane >> 2);
+          ml[warp * R + r] = m[i];
+          ml[(4 + warp) * R + r] = l[i];
+        }
+      }
+      group_bar();
+      const bool odd = flags[1] != 0;
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i) {  // this warp's factor to the common maximum
+        const int r = (i >> 1) * 16 + (i & 1) * 8 + (lane >> 2);
+        const float M = fmaxf(fmaxf(ml[r], ml[R + r]), fmaxf(ml[2 * R + r], ml[3 * R + r]));
+        const float f = M == -INFINITY ? 0.f : ex2(m[i] - M);
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          o[i >> 1][j][(i & 1) * 2] *= f;
+          o[i >> 1][j][(i & 1) * 2 + 1] *= f;
+        }
+      }
+      const bool whole = t0 == 0 && t1 == u.tiles;
+      float* rec = tree_record(a, blockIdx.x, t0 == 0);
+      const int j0 = max(t0 * kTreeKeys - u.ctx, 0), j1 = min(t1 * kTreeKeys - u.ctx, u.nodes);
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {  // 16 channels at a time
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+              *reinterpret_cast<float2*>(red + (warp * R + i * 16 + z * 8 + (lane >> 2)) * 16 + n * 8 + 2 * (lane & 3)) =
+                  make_float2(o[i][2 * j + n][2 * z], o[i][2 * j + n][2 * z + 1]);
+        group_bar();
+        for (int i = threadIdx.x; i < rows * 4; i += 128) {
+          const int r = i >> 2, x = (i & 3) * 4, row = u.row_tile * R + r, node = u.node0 + row / G;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float4 y = *reinterpret_cast<const float4*>(red + (w * R + r) * 16 + x);
+            v.x += y.x;
+            v.y += y.y;
+            v.z += y.z;
+            v.w += y.w;
+          }
+          if (odd) {  // rare: the values that were taken out, for the rows that see them
+            const int32_t* table = a.m.tables + __ldg(a.m.tab_start + u.seq);
+            for (int n = j0; n < j1; ++n) {
+              if (!tree_sees(a.m, node, n)) continue;
+              const int p = u.ctx + n;
+              const float4 y = tree_load4(a.kv, kTreeF16, kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D) + j * 16 + x);
+              if (!isfinite(y.x)) v.x += y.x;
+              if (!isfinite(y.y)) v.y += y.y;
+              if (!isfinite(y.z)) v.z += y.z;
+              if (!isfinite(y.w)) v.w += y.w;
+            }
+          }
+          if (whole) {
+            const float M = fmaxf(fmaxf(ml[r], ml[R + r]), fmaxf(ml[2 * R + r], ml[3 * R + r]));
+            float L = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) L += M == -INFINITY ? 0.f : ml[(4 + w) * R + r] * ex2(ml[w * R + r] - M);
+            const bool zero = L == 0.f || __ldg(a.m.pos + node) < 0;
+            const float inv = 1.0f / L;
+            v = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            tree_store4(a.out, a.out_type, node * a.ldo + (int64_t)(u.head * G + row % G) * D + j * 16 + x, v);
+          } else {
+            *reinterpret_cast<float4*>(rec + r * D + j * 16 + x) = v;
+          }
+        }
+        group_bar();
+      }
+      if (!whole)
+        for (int r = threadIdx.x; r < rows; r += 128) {
+          const float M = fmaxf(fmaxf(ml[r], ml[R + r]), fmaxf(ml[2 * R + r], ml[3 * R + r]));
+          float L = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) L += M == -INFINITY ? 0.f : ml[(4 + w) * R + r] * ex2(ml[w * R + r] - M);
+          rec[R * D + r] = M;
+          rec[R * D + R + r] = L;
+        }
+      if (threadIdx.x == 0) flags[1] = 0;
+      group_bar();  // the statistics and the flag are free again
+      left -= t1 - t0;
+      tile = 0;
+      if (left > 0) tree_unit_next(a.m, G, R, a.d.Hkv, u);
+    }
+  }
+  __syncthreads();
+  // after an abort, let the copies still in flight land before the CTA exits
+  if (warp == 4 && lane == 0 && *abort_flag) {
+    const uint64_t w0 = global_ns();
+    for (int i = k > kS ? k - kS : 0; i < k; ++i)
+      while (!mbar_try(&full[i % kS], (i / kS) & 1) && global_ns() - w0 < kWaitLimitNs) {
+      }
+  }
+}
+
+template <int D, int R>
+cudaError_t one(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
+  static SmemOptIn opt;
+  constexpr int smem = F16Smem<D, R>::kBytes;
+  static_assert(smem <= 115712, "two CTAs per SM");
+  cudaError_t e = opt.ensure(k_tree_attend_f16<D, R>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_tree_attend_f16<D, R>, ctas, kF16Threads, smem, s, *tm, a);
+}
+
+template <int D>
+cudaError_t pick(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
+  return a.m.row_tile == 16 ? one<D, 16>(a, tm, ctas, s) : one<D, 32>(a, tm, ctas, s);
+}
+
+}  // namespace
+
+TreeVariant tree_variant(bool kv_f16, int D, int max_rows) {
+  (void)kv_f16;
+  (void)D;
+  return {max_rows <= 16 ? 16 : 32, 2};
+}
+
+cudaError_t launch_tree_attend_f16(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
+  switch (a.d.D) {
+    case 32: return pick<32>(a, tm, ctas, s);
+    case 64: return pick<64>(a, tm, ctas, s);
+    case 128: return pick<128>(a, tm, ctas, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace dec

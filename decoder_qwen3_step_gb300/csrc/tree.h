@@ -1,0 +1,128 @@
+// tree.h - draft trees over the paged KV cache: what the host plan (tree.cu)
+// uploads, and the launchers of the tree kernels (internal to libdec).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "optin.h"
+
+namespace dec {
+
+constexpr int kTreeMaxNodes = 256;  // nodes per sequence (a row of the ancestor mask is at most 8 words)
+constexpr int kTreeKeys = 64;       // keys per attention tile: 4 pool blocks
+constexpr uint32_t kErrShape = 16u; // a captured call met a plan of another shape (mirrors DEC_DEV_SHAPE)
+
+// Element types of the callers' tensors (mirror DEC_T_*).
+enum TreeType { kTreeF32 = 0, kTreeF16 = 1, kTreeBf16 = 2 };
+
+// Header words of the uploaded plan.
+enum TreeHdr { kHdrSeqs = 0, kHdrTokens, kHdrWords, kHdrRowTile, kHdrMerges, kHdrInts = 16 };
+
+// Attention work of one CTA: a contiguous range of key tiles in the order
+// (sequence, KV head, row tile, key tile); it starts at `tile` of this unit.
+struct TreeCut {
+  int32_t seq, head, row_tile, tile, count, pad0, pad1, pad2;
+};
+// A unit (sequence, KV head, row tile) that CTAs c0 .. c1 share.
+struct TreeMerge {
+  int32_t seq, head, row_tile, c0, c1, pad0, pad1, pad2;
+};
+
+// The plan on the device: one upload, arrays back to back.
+struct TreeMeta {
+  const int32_t* hdr;        // [kHdrInts]
+  const int32_t* seq_start;  // [S+1]
+  const int32_t* ctx;        // [S] cached tokens of each sequence
+  const int32_t* tab_start;  // [S] first entry of each sequence in tables
+  const int32_t* pos;        // [N] rotary position; -1: a padding node
+  const int32_t* dst;        // [N] pool block * 16 + slot
+  const int32_t* parents;    // [N] parent within the sequence, -1 root, -2 padding
+  const int32_t* seq;        // [N]
+  const uint32_t* anc;       // [N, words] bit j: the node sees node j (itself included)
+  const TreeCut* cuts;       // [CTAs]
+  const TreeMerge* merges;   // [hdr[kHdrMerges]]
+  const int32_t* tables;     // pool block ids, sequence after sequence
+  uint32_t* err;             // device error word
+  int S, N, words, row_tile; // the shape the launch was made for (checked against hdr)
+};
+
+struct TreePoolDims {
+  int H, Hkv, D, n_layers, n_blocks;
+  float eps;
+};
+
+struct TreeAppendArgs {
+  TreeMeta m;
+  TreePoolDims d;
+  const void *q, *k, *v;
+  int64_t ldq, ldk, ldv, ldo;
+  const float *q_norm, *k_norm;
+  const float* rope;  // [positions, rot/2, 2] (cos, sin); null: no rotation
+  int rot, interleaved, rope_positions;
+  void* q_out;
+  int in_type, q_type, kv_f16, layer;
+  void* kv;
+};
+cudaError_t launch_tree_append(const TreeAppendArgs& a, cudaStream_t s);
+
+struct TreeAttendArgs {
+  TreeMeta m;
+  TreePoolDims d;
+  const void* q;
+  int64_t ldq, ldo;
+  void* out;
+  int q_type, out_type, layer;
+  const void* kv;
+  float* part;  // [CTAs, 2, row_tile, D + 2] records
+  float scale_log2;  // log2(e) / sqrt(D)
+};
+// CTAs and rows per tile of the attention kernel for sequences of up to
+// max_rows (nodes x query heads per KV head) rows.
+struct TreeVariant {
+  int row_tile, ctas_per_sm;
+};
+TreeVariant tree_variant(bool kv_f16, int D, int max_rows);
+cudaError_t launch_tree_attend_f32(const TreeAttendArgs& a, int ctas, cudaStream_t s);
+cudaError_t launch_tree_attend_f16(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s);
+cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, cudaStream_t s);
+
+struct TreeCommitArgs {
+  TreeMeta m;
+  TreePoolDims d;
+  const int32_t *draft, *target, *prior;
+  int32_t *accepted, *path, *next;
+  void* kv;
+  int kv_bytes;
+};
+cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s);
+
+constexpr int kRopeMaxPairs = 64;
+struct RopeTableArgs {
+  float* table;
+  int positions, pairs;
+  double mult;
+  double freq[kRopeMaxPairs];
+};
+cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t s);
+
+// Launch with programmatic stream serialisation: the kernel may be scheduled
+// while its predecessor drains and waits for it before its first access.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*k)(P...), int grid, int block, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+}  // namespace dec

@@ -16,10 +16,14 @@ LIB_PATH = os.path.join(_HERE, "libdec_debug.so" if os.environ.get("DEC_DEBUG") 
 DEC_OK, DEC_EINVAL, DEC_ECAPACITY, DEC_EBLOCK, DEC_ERANGE, DEC_EVOCAB, DEC_ECUDA, DEC_EDEVICE = range(8)
 DEC_FP32, DEC_BF16_F16KV, DEC_INT4_F16KV = 0, 1, 2
 DEC_ROWS_ALL, DEC_ROWS_LAST = 0, 1
-DEC_DEV_BAD_ID, DEC_DEV_TIMEOUT, DEC_DEV_CAPACITY, DEC_DEV_BOUNDS = 1, 2, 4, 8
+DEC_DEV_BAD_ID, DEC_DEV_TIMEOUT, DEC_DEV_CAPACITY, DEC_DEV_BOUNDS, DEC_DEV_SHAPE = 1, 2, 4, 8, 16
 DEC_BUILD_DEBUG = 1
 DEC_PURPOSE_SAMPLE = 4
 DEC_SAMPLE_BAD_ID, DEC_SAMPLE_BAD_LOGIT, DEC_SAMPLE_NO_FINITE, DEC_SAMPLE_OVERFLOW = 1, 2, 4, 8
+DEC_T_F32, DEC_T_F16, DEC_T_BF16 = 0, 1, 2
+DEC_TREE_PAD, DEC_TREE_MAX_NODES = -2, 256
+DEC_ROPE_HALF, DEC_ROPE_INTERLEAVED = 0, 1
+DEC_ROPE_PLAIN, DEC_ROPE_LINEAR, DEC_ROPE_YARN, DEC_ROPE_BANDS = 0, 1, 2, 3
 
 ERROR_NAMES = {0: "DEC_OK", 1: "DEC_EINVAL", 2: "DEC_ECAPACITY", 3: "DEC_EBLOCK", 4: "DEC_ERANGE",
                5: "DEC_EVOCAB", 6: "DEC_ECUDA", 7: "DEC_EDEVICE"}
@@ -36,7 +40,9 @@ EXPORTS = (
     "dec_child_seed", "dec_rng_stream", "dec_rng_next_u32", "dec_rng_uniform", "dec_sampler_workspace_bytes",
     "dec_sampler_create", "dec_sampler_destroy", "dec_sampler_status", "dec_sample", "dec_debug_df_exp",
     "dec_quantize_int4", "dec_batch_check", "dec_attend_noalloc_status", "dec_debug_wait_timeout",
-    "dec_build_flags", "dec_debug_poison_table",
+    "dec_build_flags", "dec_debug_poison_table", "dec_rope_table_bytes", "dec_rope_table", "dec_tree_check",
+    "dec_tree_workspace_bytes", "dec_tree_create", "dec_tree_destroy", "dec_tree_set", "dec_tree_status",
+    "dec_tree_append", "dec_tree_attend", "dec_tree_commit",
 )
 KERNEL_CLASSES = ("embed", "qkv", "qkv_post", "attn", "attn_merge", "oproj", "gateup", "down", "lmhead", "argmax",
                   "step")
@@ -74,6 +80,23 @@ class dec_sampling(C.Structure):
 
 class dec_rng(C.Structure):
     _fields_ = [("state", C.c_uint64), ("inc", C.c_uint64)]
+
+
+class dec_tree_batch(C.Structure):
+    _fields_ = [("n_seqs", C.c_int32), ("n_tokens", C.c_int32), ("seq_start", _I32P), ("ctx", _I32P),
+                ("parents", _I32P), ("block_table", _I32P), ("max_blocks", C.c_int32)]
+
+
+class dec_rope(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("rot_dim", "layout", "scaling", "orig_positions")] + [
+        (n, C.c_double) for n in ("base", "factor", "low", "high", "attn_factor")]
+
+
+class dec_tree_qkv(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("ldq", C.c_int64), ("ldk", C.c_int64),
+                ("ldv", C.c_int64), ("in_type", C.c_int32), ("q_type", C.c_int32), ("q_norm", C.c_void_p),
+                ("k_norm", C.c_void_p), ("rope", C.POINTER(dec_rope)), ("rope_table", C.c_void_p),
+                ("rope_positions", C.c_int32), ("q_out", C.c_void_p), ("ldqo", C.c_int64)]
 
 
 _lib = None
@@ -144,6 +167,17 @@ def lib() -> C.CDLL:
             "dec_debug_wait_timeout": (I, [V, C.c_uint32, C.c_uint64]),
             "dec_build_flags": (C.c_uint32, []),
             "dec_debug_poison_table": (I, [V, C.c_int32, C.c_int32, C.c_int32]),
+            "dec_rope_table_bytes": (I, [C.POINTER(dec_rope), C.c_int32, C.POINTER(SZ)]),
+            "dec_rope_table": (I, [C.POINTER(dec_rope), C.c_int32, V, SZ, V]),
+            "dec_tree_check": (I, [V, C.POINTER(dec_tree_batch)]),
+            "dec_tree_workspace_bytes": (I, [V, C.c_int32, C.c_int32, C.c_int32, C.POINTER(SZ)]),
+            "dec_tree_create": (I, [V, C.c_int32, C.c_int32, C.c_int32, V, SZ, C.POINTER(V)]),
+            "dec_tree_destroy": (None, [V]),
+            "dec_tree_set": (I, [V, C.POINTER(dec_tree_batch), V]),
+            "dec_tree_status": (I, [V, V, C.POINTER(C.c_uint32)]),
+            "dec_tree_append": (I, [V, C.c_int32, C.POINTER(dec_tree_qkv), V]),
+            "dec_tree_attend": (I, [V, C.c_int32, V, C.c_int32, I64, V, C.c_int32, I64, V]),
+            "dec_tree_commit": (I, [V, V, V, V, V, V, V, V]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)

@@ -138,7 +138,10 @@ const char* dec_last_error(void);
 #define DEC_DEV_TIMEOUT  2u /* a bounded wait in a kernel gave up */
 #define DEC_DEV_CAPACITY 4u /* a kernel's fixed-size work list overflowed */
 #define DEC_DEV_BOUNDS   8u /* DEC_DEBUG builds only: a kernel met a block-table column or pool
-                               block id outside its range; it used block 0 instead */
+                               block id outside its range; it used block 0 instead (dec_tree_append,
+                               every build: a replayed call met a position past its rotary table) */
+#define DEC_DEV_SHAPE   16u /* a captured dec_tree_* call was replayed on a plan of another shape: it
+                               did nothing */
 
 /* ---- model ---------------------------------------------------------------- */
 /* Check a config; DEC_OK if the decoder can run it. */
@@ -488,6 +491,166 @@ int dec_sample(dec_sampler* s, const float* logits, int64_t ld, int32_t n_seqs, 
  * table-driven method, accurate to about 2^-46 relative down to e^-60, 0 below
  * e^-87) on n device doubles x <= 0, written as doubles (head + tail). */
 int dec_debug_df_exp(const double* x, double* y, int64_t n, void* stream);
+
+/* ---- draft trees --------------------------------------------------------------
+ * Verifying drafted tokens (speculative decoding; no counterpart on the
+ * pages): a step gives every sequence a tree of nodes behind its ctx cached
+ * tokens.  Node i of a sequence has a parent that is an earlier node of the
+ * same sequence (parents[i] < i), or -1: it follows the last cached token.
+ * It takes cache slot ctx + i and position ctx + depth(i), depth 0 for a node
+ * with parent -1.  A chain (parents[i] = i - 1) is a plain run of new tokens;
+ * one node per sequence is a decode step.  For each layer:
+ *
+ *   dec_tree_append  queries and keys normed and rotated, keys and values to
+ *                    the nodes' slots
+ *   dec_tree_attend  o_i = sum_j softmax_j(q_i . k_j / sqrt(D)) v_j over the
+ *                    cached tokens, node i's ancestors and node i; query head
+ *                    h reads KV head floor(h * Hkv / H)
+ *
+ * and after the LM head dec_tree_commit walks down each tree along the tokens
+ * the model chose and moves the accepted nodes' K/V to the slots a plain
+ * sequence would have them in.  The next step's ctx is ctx + accepted.
+ *
+ * The trees of a step are one plan, made once with dec_tree_set and used by
+ * every layer's calls.  A plan's calls share its workspace: order them on one
+ * stream (or by events); two plans are independent.  dec_tree_append,
+ * dec_tree_attend and dec_tree_commit can be captured into a CUDA graph; a
+ * replay uses the plan that is set then, as long as dec_tree_set (outside the
+ * graph, ordered before the replay) got the same seq_start as at the capture:
+ * pad with DEC_TREE_PAD nodes.  A replay on a plan with other counts of
+ * sequences or nodes, or another longest sequence, does nothing and sets
+ * DEC_DEV_SHAPE.  Calls run on the device that was current at
+ * dec_tree_create, whichever device is current then. */
+
+/* Element types. */
+#define DEC_T_F32  0
+#define DEC_T_F16  1
+#define DEC_T_BF16 2
+
+#define DEC_TREE_PAD (-2)       /* as a parent: a padding node.  It sees nothing and nothing sees it; its slot
+                                   is not written, its query and output rows are zeros, it is never accepted */
+#define DEC_TREE_MAX_NODES 256  /* nodes per sequence */
+
+typedef struct dec_tree dec_tree; /* opaque: the plan */
+
+/* HOST arrays, read during the call only. */
+typedef struct dec_tree_batch {
+    int32_t n_seqs;             /* S >= 1 */
+    int32_t n_tokens;           /* N = nodes of all sequences >= 1 */
+    const int32_t* seq_start;   /* [S+1] offsets of each sequence's nodes (equal offsets: no nodes) */
+    const int32_t* ctx;         /* [S] cached tokens of each sequence, >= 0 */
+    const int32_t* parents;     /* [N] parent within the sequence, -1, or DEC_TREE_PAD; NULL: chains */
+    const int32_t* block_table; /* [S * max_blocks] pool block ids, as in dec_batch, covering ctx + nodes slots */
+    int32_t max_blocks;
+} dec_tree_batch;
+
+/* The checks of dec_tree_set on host data only (no GPU needed): layout,
+ * parents, positions below max_positions, tables long enough and naming
+ * allocated blocks, and every block that holds a node's slot owned by its
+ * sequence alone (refcount 1, not in the prefix cache, written for no other
+ * sequence).  DEC_EINVAL, DEC_ERANGE, DEC_EBLOCK. */
+int dec_tree_check(const dec_pool* pool, const dec_tree_batch* b);
+
+/* Device workspace of a plan over `pool` for up to max_seqs sequences,
+ * max_tokens nodes and max_blocks blocks per sequence. */
+int dec_tree_workspace_bytes(const dec_pool* pool, int32_t max_seqs, int32_t max_tokens, int32_t max_blocks,
+                             size_t* bytes);
+/* workspace: caller-owned device memory, 256-byte aligned, not to be touched
+ * while the plan lives; pool must outlive the plan.  The plan owns only host
+ * memory (a small pinned staging ring). */
+int dec_tree_create(const dec_pool* pool, int32_t max_seqs, int32_t max_tokens, int32_t max_blocks, void* workspace,
+                    size_t bytes, dec_tree** out);
+void dec_tree_destroy(dec_tree* t);
+/* Check the batch and upload its plan (one copy, asynchronous on `stream`;
+ * refused while `stream` is being captured).  A refused batch leaves the
+ * previous plan in place.  The blocks must stay allocated while it is used. */
+int dec_tree_set(dec_tree* t, const dec_tree_batch* b, void* stream);
+/* Synchronise `stream`, then read and clear the plan's device error word
+ * (DEC_DEV_TIMEOUT, DEC_DEV_BOUNDS, DEC_DEV_SHAPE). */
+int dec_tree_status(dec_tree* t, void* stream, uint32_t* flags);
+
+/* Rotary positions.  Pair j of the first rot_dim channels of a head turns by
+ * the angle p * f_j at position p:
+ *   a' = (a cos - b sin) * attn_factor,  b' = (b cos + a sin) * attn_factor,
+ * (a, b) = channels (j, j + rot_dim/2) or (2j, 2j+1).  Frequencies, with
+ * f0_j = base^(-2j / rot_dim):
+ *   DEC_ROPE_PLAIN   f_j = f0_j
+ *   DEC_ROPE_LINEAR  f_j = f0_j / factor
+ *   DEC_ROPE_YARN    f_j = f0_j (1 - g_j) + f0_j / factor * g_j, g_j a ramp over the
+ *                    pair's index, 0 up to floor(i(high)) and 1 from ceil(i(low)),
+ *                    i(t) = rot_dim ln(orig_positions / (2 pi t)) / (2 ln base)
+ *                    the index that turns t times in orig_positions
+ *                    (both ends kept within 0 .. rot_dim - 1)
+ *   DEC_ROPE_BANDS   f_j = f0_j g_j + f0_j / factor (1 - g_j), g_j a ramp over the
+ *                    turns t_j = orig_positions f0_j / (2 pi): 0 at t_j <= low,
+ *                    1 at t_j >= high */
+#define DEC_ROPE_HALF        0
+#define DEC_ROPE_INTERLEAVED 1
+#define DEC_ROPE_PLAIN  0
+#define DEC_ROPE_LINEAR 1
+#define DEC_ROPE_YARN   2
+#define DEC_ROPE_BANDS  3
+typedef struct dec_rope {
+    int32_t rot_dim;        /* a multiple of 8, 8 .. head_dim; the other channels are not turned */
+    int32_t layout;         /* DEC_ROPE_HALF or DEC_ROPE_INTERLEAVED */
+    int32_t scaling;        /* DEC_ROPE_PLAIN, LINEAR, YARN or BANDS */
+    int32_t orig_positions; /* YARN, BANDS: the positions the base was trained for */
+    double base;            /* > 1 */
+    double factor;          /* LINEAR, YARN, BANDS: >= 1 */
+    double low, high;       /* YARN, BANDS: turns, 0 < low < high */
+    double attn_factor;     /* > 0; 1 changes nothing */
+} dec_rope;
+/* Bytes of the table: [n_positions][rot_dim/2][2] fp32 (cos, sin), attn_factor
+ * included; n_positions 1 .. 40,960. */
+int dec_rope_table_bytes(const dec_rope* r, int32_t n_positions, size_t* bytes);
+/* Fill a table (DEVICE, 16-byte aligned): angles, cosines and sines in 64
+ * bits, rounded once.  Asynchronous on `stream`. */
+int dec_rope_table(const dec_rope* r, int32_t n_positions, float* table, size_t bytes, void* stream);
+
+/* Row i of every tensor belongs to node i of the batch; heads of a row are
+ * back to back; row strides in elements, multiples of 4; pointers aligned to
+ * 4 elements. */
+typedef struct dec_tree_qkv {
+    const void* q;            /* DEVICE [N, n_heads, head_dim] before norm and rotation, or NULL */
+    const void* k;            /* DEVICE [N, n_kv_heads, head_dim], or NULL together with v */
+    const void* v;
+    int64_t ldq, ldk, ldv;    /* row strides: one packed q|k|v buffer works */
+    int32_t in_type;          /* DEC_T_* of q, k and v */
+    int32_t q_type;           /* DEC_T_* of q_out */
+    const float* q_norm;      /* DEVICE [head_dim] gain of the per-head RMSNorm (the pool's rms_eps); NULL: none */
+    const float* k_norm;
+    const dec_rope* rope;     /* HOST, read during the call; NULL: no rotation */
+    const float* rope_table;  /* DEVICE, from dec_rope_table with the same dec_rope */
+    int32_t rope_positions;   /* its n_positions: above the largest position of the trees (DEC_ERANGE) */
+    void* q_out;              /* DEVICE [N, n_heads, head_dim]; may be q itself if types and strides agree */
+    int64_t ldqo;
+} dec_tree_qkv;
+/* Norm, rotate, and write the keys and values of all nodes to their slots of
+ * `layer` (f16 caches: round to nearest even).  Computed in fp32. */
+int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* stream);
+/* Attention of all nodes.  q DEVICE [N, n_heads, head_dim] after norm and
+ * rotation, any DEC_T_*; out DEVICE [N, n_heads * head_dim]: any DEC_T_* for
+ * an fp32 cache, which is computed in fp32 throughout; DEC_T_F16 or
+ * DEC_T_BF16 for an f16 cache, where queries and weights are rounded to f16
+ * for the tensor cores and statistics and sums are fp32.  A node's result
+ * does not depend on what is cached in slots it does not see (infinities and
+ * NaN included); it may differ in its last bits with the rest of the batch,
+ * which decides how the keys are split over the GPU. */
+int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, int64_t ldq, void* out, int32_t out_type,
+                    int64_t ldo, void* stream);
+/* Accept drafted tokens.  DEVICE int32: draft [N] the nodes' tokens, target
+ * [N] the token the model chose after each node (argmax, or a sample of
+ * dec_sample: following samples keeps the model's distribution), prior [S]
+ * the token it chose after the last cached one, or NULL: the first node with
+ * parent -1 is certain (the token sampled last).  The walk goes from the root
+ * to the child whose token is the one chosen at its parent, the lowest such
+ * node, as long as there is one.  Outputs, DEVICE int32: accepted [S] how many
+ * nodes; path [N] their numbers within the sequence, then -1; next [S] the
+ * token chosen after the last of them (prior, or -1 without one, if none is
+ * accepted).  The K/V of the i-th accepted node move to slot ctx + i in every
+ * layer; the slots behind hold nothing of use. */
+int dec_tree_commit(dec_tree* t, const int32_t* draft, const int32_t* target, const int32_t* prior, int32_t* accepted,
+                    int32_t* path, int32_t* next, void* stream);
 
 /* Library version string. */
 const char* dec_version(void);
