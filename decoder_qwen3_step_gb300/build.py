@@ -23,7 +23,7 @@ BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libdec_debug.so")
 SOURCES = ["api.cu", "attend.cu", "prefix.cu", "kernels_core.cu", "kernels_attn.cu", "kernels_attn_tc.cu", "kernels_attn_dec_tc.cu", "kernels_tc.cu",
            "kernels_tc_skinny.cu", "kernels_mega.cu", "kernels_int4.cu", "sampler.cu", "tree.cu",
-           "kernels_tree.cu", "kernels_tree_f32.cu", "kernels_tree_f16.cu"]
+           "kernels_tree.cu", "kernels_tree_f32.cu", "kernels_tree_f16.cu", "kernels_tree_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

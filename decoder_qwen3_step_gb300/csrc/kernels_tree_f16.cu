@@ -25,6 +25,8 @@ namespace dec {
 
 namespace {
 
+constexpr int kTreeKeys = 64;  // keys per tile: 4 pool blocks
+
 template <int D, int R>
 struct F16Smem {
   static constexpr int kSlab = 16 * D * 2;                     // K (or V) of one block
@@ -138,30 +140,9 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
     for (int left = cut.count; left > 0;) {
       const int t0 = tile, t1 = min(u.tiles, tile + left), end = u.ctx + u.nodes;
       const int rows = min(R, u.nodes * G - u.row_tile * R);
-      // the queries: warp w takes rows w, w + 4, ...; each scaled by a power of two into f16's range
-      for (int r = warp; r < R; r += 4) {
-        const int row = u.row_tile * R + r;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        const int64_t off = (u.node0 + row / G) * a.ldq + (int64_t)(u.head * G + row % G) * D;
-        if (r < rows && lane * 4 < D) {
-          const float4 x = tree_load4(a.q, a.q_type, off + lane * 4);
-          v[0] = x.x;
-          v[1] = x.y;
-          v[2] = x.z;
-          v[3] = x.w;
-        }
-        const float mx = warp_max(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
-        // 2^-e with 2^e <= mx < 2^(e+1); rows of zeros, infinities or subnormals stay as they are
-        const int e = (int)(__float_as_uint(mx) >> 23);
-        const bool scaled = e > 0 && e < 255;
-        const float f = scaled ? __uint_as_float((uint32_t)max(254 - e, 1) << 23) : 1.f;
-        if (lane * 4 < D) {
-          uint32_t* dst = reinterpret_cast<uint32_t*>(Qs + r * SM::kQPitch + lane * 8);
-          dst[0] = af_pack_half(v[0] * f, v[1] * f);
-          dst[1] = af_pack_half(v[2] * f, v[3] * f);
-        }
-        if (lane == 0) fac[r] = a.scale_log2 * (scaled ? 1.f / f : 1.f);
-      }
+      tree_load_queries<D, R, 4>(a, u, G, warp, fac, [&](int r, int x, uint2 h) {
+        *reinterpret_cast<uint2*>(Qs + r * SM::kQPitch + x * 8) = h;
+      });
       group_bar();
       const uint32_t qb = smem_u32(Qs) + (lane & 15) * SM::kQPitch + (lane >> 4) * 16;
       float c[2 * MT], m[2 * MT], l[2 * MT], o[MT][D / 8][4];
@@ -420,12 +401,6 @@ cudaError_t pick(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaS
 }
 
 }  // namespace
-
-TreeVariant tree_variant(bool kv_f16, int D, int max_rows) {
-  (void)kv_f16;
-  (void)D;
-  return {max_rows <= 16 ? 16 : 32, 2};
-}
 
 cudaError_t launch_tree_attend_f16(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
   switch (a.d.D) {

@@ -17,6 +17,8 @@ namespace dec {
 
 namespace {
 
+constexpr int kTreeKeys = 64;  // keys per tile: 4 pool blocks
+
 template <int D, int R>
 struct F32Smem {
   static constexpr int kPitch = D + 4;  // the 16 keys a half-warp reads fall into different banks

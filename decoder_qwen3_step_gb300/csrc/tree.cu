@@ -44,18 +44,22 @@ struct TreeLayout {
   size_t meta_ints;
 };
 
-// Records of the attention kernels: two per CTA, of at most this many rows each.
-constexpr int kMaxRowTile = 32;
-constexpr int kMaxCtasPerSm = 2;
+// Which attention kernel takes a batch whose widest sequence has max_rows rows
+// (nodes x query heads per KV head).
+TreeVariant variant_for(bool f16, int D, int max_rows) {
+  if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, 2};
+  if (D >= 64 && max_rows > 32) return {kTreeTc, 128, 128, 2};
+  return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2};
+}
 
 TreeLayout tree_layout(const dec_config& c, int max_seqs, int max_tokens, int max_blocks, int sms) {
   TreeLayout L{};
-  const size_t S = max_seqs, N = max_tokens, P = (size_t)sms * kMaxCtasPerSm;
+  const size_t S = max_seqs, N = max_tokens, P = (size_t)sms * kTreeMaxCtasPerSm;
   // header, seq_start, ctx, tab_start, pos, dst, parents, seq, mask, cuts, merges, tables (each piece 16-byte aligned)
   L.meta_ints = kHdrInts + (3 * S + 1) + 4 * N + N * (kTreeMaxNodes / 32) + 2 * P * 8 + S * (size_t)max_blocks + 16 * 4;
   L.meta = 256;
   L.part = up256(L.meta + L.meta_ints * 4);
-  L.total = up256(L.part + P * 2 * kMaxRowTile * (size_t)(c.head_dim + 2) * 4);
+  L.total = up256(L.part + P * 2 * kTreeMaxRowTile * (size_t)(c.head_dim + 2) * 4);
   return L;
 }
 
@@ -91,19 +95,20 @@ struct dec_tree {
   cudaEvent_t stage_ev[kStages];
   int stage_next;
   bool f16;
-  CUtensorMap tm;
+  CUtensorMap tm, tm_panel;  // boxes of a whole block (K and V), and of one 64-channel panel of K or V
   // the plan that was set last
   bool set;
   TreeMeta meta;
-  int max_nodes, max_position, ctas, n_merges;
+  int kernel, max_nodes, max_position, ctas, n_merges;
 };
 
 namespace {
 
 // The pool's tensor map for the f16 attention: [64 channels][rows of a slab]
 // [halves of the head][K, V][layer and block]; one box is the K and V of one
-// KV head of one block, in 128-byte (64-byte for head_dim 32) swizzled rows.
-bool pool_map(CUtensorMap* out, const dec_pool* p) {
+// KV head of one block (panel: 64 channels of K or V), in 128-byte (64-byte
+// for head_dim 32) swizzled rows.
+bool pool_map(CUtensorMap* out, const dec_pool* p, bool panel) {
   typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -120,7 +125,7 @@ bool pool_map(CUtensorMap* out, const dec_pool* p) {
   const cuuint64_t D = c.head_dim, bd = D >= 64 ? 64 : D, slab = (cuuint64_t)c.n_kv_heads * 16 * D * 2;
   cuuint64_t dims[5] = {bd, (cuuint64_t)c.n_kv_heads * 16, D / bd, 2, (cuuint64_t)c.n_layers * p->n_blocks};
   cuuint64_t strides[4] = {D * 2, bd * 2, slab, 2 * slab};
-  cuuint32_t box[5] = {(cuuint32_t)bd, 16, (cuuint32_t)(D / bd), 2, 1};
+  cuuint32_t box[5] = {(cuuint32_t)bd, 16, panel ? 1 : (cuuint32_t)(D / bd), panel ? 1u : 2u, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return fn(out, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, p->slabs, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             bd == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -187,8 +192,8 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   int max_nodes = 0, max_position = 0;
   for (int s = 0; s < S; ++s) max_nodes = std::max(max_nodes, b->seq_start[s + 1] - b->seq_start[s]);
   const int W = std::max((max_nodes + 31) / 32, 1);
-  const TreeVariant var = tree_variant(t->f16, c.head_dim, max_nodes * G);
-  const int grid = t->sms * var.ctas_per_sm, R = var.row_tile;
+  const TreeVariant var = variant_for(t->f16, c.head_dim, max_nodes * G);
+  const int grid = t->sms * var.ctas_per_sm, R = var.row_tile, K = var.tile_keys;
   const size_t h_hdr = take(kHdrInts), h_start = take(S + 1), h_ctx = take(S), h_tab = take(S), h_pos = take(N),
                h_dst = take(N), h_par = take(N), h_seq = take(N), h_anc = take((size_t)N * W),
                h_cut = take((size_t)grid * 8), h_mrg = take((size_t)grid * 8), h_tables = o;
@@ -221,7 +226,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
       H[h_pos + a0 + i] = p < 0 ? ctx : H[h_pos + a0 + p] + 1;
       max_position = std::max(max_position, H[h_pos + a0 + i]);
     }
-    total += (int64_t)c.n_kv_heads * ((T * G + R - 1) / R) * ((ctx + T + kTreeKeys - 1) / kTreeKeys);
+    total += (int64_t)c.n_kv_heads * ((T * G + R - 1) / R) * ((ctx + T + K - 1) / K);
   }
   H[h_start + S] = N;
   // attention: every CTA takes an equal run of key tiles in the order (sequence, KV head, row tile, key tile)
@@ -234,7 +239,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   for (int s = 0; s < S; ++s) {
     const int T = b->seq_start[s + 1] - b->seq_start[s];
     if (T == 0) continue;
-    const int rts = (T * G + R - 1) / R, tiles = (b->ctx[s] + T + kTreeKeys - 1) / kTreeKeys;
+    const int rts = (T * G + R - 1) / R, tiles = (b->ctx[s] + T + K - 1) / K;
     for (int h = 0; h < c.n_kv_heads; ++h)
       for (int rt = 0; rt < rts; ++rt, done += tiles) {
         while (cta < P && begin(cta) < done + tiles) {
@@ -278,6 +283,8 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   m.N = N;
   m.words = W;
   m.row_tile = R;
+  m.tile_keys = K;
+  t->kernel = var.kernel;
   t->max_nodes = max_nodes;
   t->max_position = max_position;
   t->ctas = grid;
@@ -438,7 +445,7 @@ int dec_tree_create(const dec_pool* pool, int32_t max_seqs, int32_t max_tokens, 
   if (e == cudaSuccess) e = cudaMemset(t->ws, 0, 256);
   if (e != cudaSuccess) {
     rc = fail(DEC_ECUDA, "dec_tree_create: %s", cudaGetErrorString(e));
-  } else if (t->f16 && !pool_map(&t->tm, pool)) {
+  } else if (t->f16 && !(pool_map(&t->tm, pool, false) && pool_map(&t->tm_panel, pool, true))) {
     rc = fail(DEC_ECUDA, "tensor map of the KV pool failed");
   }
   if (rc) {
@@ -571,7 +578,9 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
   a.part = (float*)(t->ws + t->lay.part);
   a.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)c.head_dim));
   cudaStream_t st = (cudaStream_t)stream;
-  TREE_CUDA(t->f16 ? launch_tree_attend_f16(a, &t->tm, t->ctas, st) : launch_tree_attend_f32(a, t->ctas, st));
+  TREE_CUDA(t->kernel == kTreeTc    ? launch_tree_attend_tc(a, &t->tm_panel, t->ctas, st)
+            : t->kernel == kTreeMma ? launch_tree_attend_f16(a, &t->tm, t->ctas, st)
+                                    : launch_tree_attend_f32(a, t->ctas, st));
   TREE_CUDA(launch_tree_merge(a, t->n_merges, st));
   return DEC_OK;
 }

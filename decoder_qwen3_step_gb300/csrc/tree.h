@@ -12,7 +12,6 @@
 namespace dec {
 
 constexpr int kTreeMaxNodes = 256;  // nodes per sequence (a row of the ancestor mask is at most 8 words)
-constexpr int kTreeKeys = 64;       // keys per attention tile: 4 pool blocks
 constexpr uint32_t kErrShape = 16u; // a captured call met a plan of another shape (mirrors DEC_DEV_SHAPE)
 
 // Element types of the callers' tensors (mirror DEC_T_*).
@@ -47,6 +46,7 @@ struct TreeMeta {
   const int32_t* tables;     // pool block ids, sequence after sequence
   uint32_t* err;             // device error word
   int S, N, words, row_tile; // the shape the launch was made for (checked against hdr)
+  int tile_keys;             // keys per attention tile
 };
 
 struct TreePoolDims {
@@ -79,14 +79,16 @@ struct TreeAttendArgs {
   float* part;  // [CTAs, 2, row_tile, D + 2] records
   float scale_log2;  // log2(e) / sqrt(D)
 };
-// CTAs and rows per tile of the attention kernel for sequences of up to
-// max_rows (nodes x query heads per KV head) rows.
+// The attention kernel for sequences of up to max_rows (nodes x query heads
+// per KV head) rows, and its tiles.
+enum TreeKernel { kTreeFfma = 0, kTreeMma, kTreeTc };
 struct TreeVariant {
-  int row_tile, ctas_per_sm;
+  int kernel, row_tile, tile_keys, ctas_per_sm;
 };
-TreeVariant tree_variant(bool kv_f16, int D, int max_rows);
+constexpr int kTreeMaxRowTile = 128, kTreeMaxCtasPerSm = 2;
 cudaError_t launch_tree_attend_f32(const TreeAttendArgs& a, int ctas, cudaStream_t s);
 cudaError_t launch_tree_attend_f16(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s);
+cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s);
 cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, cudaStream_t s);
 
 struct TreeCommitArgs {

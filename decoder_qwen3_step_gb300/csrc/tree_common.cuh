@@ -28,7 +28,7 @@ __device__ __forceinline__ void tree_unit_load(const TreeMeta& m, int G, int R, 
   u.node0 = __ldg(m.seq_start + u.seq);
   u.nodes = __ldg(m.seq_start + u.seq + 1) - u.node0;
   u.ctx = __ldg(m.ctx + u.seq);
-  u.tiles = (u.ctx + u.nodes + kTreeKeys - 1) / kTreeKeys;
+  u.tiles = (u.ctx + u.nodes + m.tile_keys - 1) / m.tile_keys;
   u.n_row_tiles = (u.nodes * G + R - 1) / R;
 }
 // The unit after u (sequences without nodes have none).
@@ -96,6 +96,41 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Load the queries of a unit's row tile as f16 into shared memory: warp w of
+// W takes rows w, w + W, ..., eight in flight (a row's load takes about a
+// microsecond from HBM; one at a time, 128 rows cost more than a dozen key
+// tiles).  Each row is scaled by a power of two so that its largest magnitude
+// lies in [1, 2): f16 then rounds every channel by at most 2^-12 of that,
+// whatever the queries' range; fac[r] takes the row's score factor.  put(r,
+// lane, halves 4 lane .. 4 lane + 3).  Rows past the last are zeros.
+template <int D, int R, int W, typename F>
+__device__ __forceinline__ void tree_load_queries(const TreeAttendArgs& a, const TreeUnit& u, int G, int w, float* fac, F&& put) {
+  constexpr int kU = R / W < 8 ? R / W : 8;
+  const int lane = threadIdx.x & 31, rows = min(R, u.nodes * G - u.row_tile * R);
+  for (int r0 = w; r0 < R; r0 += W * kU) {
+    float4 v[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int r = r0 + i * W, row = u.row_tile * R + r;
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows && lane * 4 < D)
+        v[i] = tree_load4(a.q, a.q_type, (u.node0 + row / G) * a.ldq + (int64_t)(u.head * G + row % G) * D + lane * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int r = r0 + i * W;
+      const float mx = warp_max(fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
+      // the factor 2^-e, 2^e <= mx < 2^(e+1); rows of zeros, subnormals or infinities stay as they are
+      const int e = (int)(__float_as_uint(mx) >> 23);
+      const bool scaled = e > 0 && e < 255;
+      const float f = scaled ? __uint_as_float((uint32_t)max(254 - e, 1) << 23) : 1.f;
+      const __half2 lo = __floats2half2_rn(v[i].x * f, v[i].y * f), hi = __floats2half2_rn(v[i].z * f, v[i].w * f);
+      if (lane * 4 < D) put(r, lane, make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)));
+      if (lane == 0) fac[r] = a.scale_log2 * (scaled ? 1.f / f : 1.f);
+    }
+  }
 }
 
 }  // namespace dec
