@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
   pdl_launch_next();
   if (!tree_shape_ok(a.m, true)) return;
   constexpr int kPer = D / 32;
-  const int R = a.m.row_tile, G = a.d.H / a.d.Hkv, lane = threadIdx.x & 31, groups = R / 4;
+  const int R = a.m.row_tile, gs = a.d.gs, G = 1 << gs, lane = threadIdx.x & 31, groups = R / 4;
   const int n = __ldg(a.m.hdr + kHdrMerges);
   for (int w = blockIdx.x; w < n * groups; w += gridDim.x) {
     const TreeMerge e = a.m.merges[w / groups];
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
     const int node0 = __ldg(a.m.seq_start + e.seq);
     const int row = e.row_tile * R + r;
     if (row >= (__ldg(a.m.seq_start + e.seq + 1) - node0) * G) continue;
-    const int node = node0 + row / G;
+    const int node = node0 + (row >> gs);
     auto rec = [&](int c) -> const float* { return tree_record(a, c, c == e.c0); };
     float M = -INFINITY;
     for (int c = e.c0 + lane; c <= e.c1; c += 32) M = fmaxf(M, __ldcg(rec(c) + R * D + r));
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
     L = warp_sum(L);
     const bool pad = __ldg(a.m.pos + node) < 0;
     const float inv = pad || L == 0.f ? 0.f : 1.0f / L;
-    const int64_t off = node * a.ldo + (int64_t)(e.head * G + row % G) * D + lane * kPer;
+    const int64_t off = node * a.ldo + (int64_t)(e.head * G + (row & (G - 1))) * D + lane * kPer;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) o[j] = inv == 0.f ? 0.f : o[j] * inv;
     if constexpr (kPer == 4) {

@@ -82,10 +82,10 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
   pdl_launch_next();
   if (!tree_shape_ok(a.m, true)) return;
   volatile int* abort_flag = flags;
-  const int G = a.d.H / a.d.Hkv;
+  const int gs = a.d.gs, G = 1 << gs;
   const TreeCut cut = a.m.cuts[blockIdx.x];
   TreeUnit u{cut.seq, cut.head, cut.row_tile, 0, 0, 0, 0, 0};
-  if (cut.count > 0) tree_unit_load(a.m, G, R, u);
+  if (cut.count > 0) tree_unit_load(a.m, gs, R, u);
   int tile = cut.tile, k = 0;
 
   if (warp == 4) {
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
       }
       left -= t1 - t0;
       tile = 0;
-      if (left > 0) tree_unit_next(a.m, G, R, a.d.Hkv, u);
+      if (left > 0) tree_unit_next(a.m, gs, R, a.d.Hkv, u);
     }
   produced:;
   } else {
@@ -140,9 +140,11 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
     for (int left = cut.count; left > 0;) {
       const int t0 = tile, t1 = min(u.tiles, tile + left), end = u.ctx + u.nodes;
       const int rows = min(R, u.nodes * G - u.row_tile * R);
-      tree_load_queries<D, R, 4>(a, u, G, warp, fac, [&](int r, int x, uint2 h) {
-        *reinterpret_cast<uint2*>(Qs + r * SM::kQPitch + x * 8) = h;
-      });
+      if constexpr (R / 4 >= 32 / (D / 8)) {
+        tree_load_queries<D, R, 4>(a, u, warp, fac, [&](int r, int x, uint4 h) { *reinterpret_cast<uint4*>(Qs + r * SM::kQPitch + x * 16) = h; });
+      } else if (warp < 2) {  // D = 32, R = 16: a warp reads eight rows at a time
+        tree_load_queries<D, R, 2>(a, u, warp, fac, [&](int r, int x, uint4 h) { *reinterpret_cast<uint4*>(Qs + r * SM::kQPitch + x * 16) = h; });
+      }
       group_bar();
       const uint32_t qb = smem_u32(Qs) + (lane & 15) * SM::kQPitch + (lane >> 4) * 16;
       float c[2 * MT], m[2 * MT], l[2 * MT], o[MT][D / 8][4];
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
             }
             if (drafted) {
               const int row = u.row_tile * R + (i >> 1) * 16 + (i & 1) * 8 + (lane >> 2);
-              const int node = u.node0 + min(row / G, u.nodes - 1);
+              const int node = u.node0 + min((row >> gs), u.nodes - 1);
 #pragma unroll
               for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
                   make_float2(o[i][2 * j + n][2 * z], o[i][2 * j + n][2 * z + 1]);
         group_bar();
         for (int i = threadIdx.x; i < rows * 4; i += 128) {
-          const int r = i >> 2, x = (i & 3) * 4, row = u.row_tile * R + r, node = u.node0 + row / G;
+          const int r = i >> 2, x = (i & 3) * 4, row = u.row_tile * R + r, node = u.node0 + (row >> gs);
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
             const bool zero = L == 0.f || __ldg(a.m.pos + node) < 0;
             const float inv = 1.0f / L;
             v = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            tree_store4(a.out, a.out_type, node * a.ldo + (int64_t)(u.head * G + row % G) * D + j * 16 + x, v);
+            tree_store4(a.out, a.out_type, node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D + j * 16 + x, v);
           } else {
             *reinterpret_cast<float4*>(rec + r * D + j * 16 + x) = v;
           }
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
       group_bar();  // the statistics and the flag are free again
       left -= t1 - t0;
       tile = 0;
-      if (left > 0) tree_unit_next(a.m, G, R, a.d.Hkv, u);
+      if (left > 0) tree_unit_next(a.m, gs, R, a.d.Hkv, u);
     }
   }
   __syncthreads();

@@ -48,10 +48,10 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
   extern __shared__ __align__(16) float sm[];
   float *Qs = sm + SM::kQ, *Ks = sm + SM::kK, *Vs = sm + SM::kV, *Ps = sm + SM::kPr;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int G = a.d.H / a.d.Hkv;
+  const int gs = a.d.gs, G = 1 << gs;
   TreeCut cut = a.m.cuts[blockIdx.x];
   TreeUnit u{cut.seq, cut.head, cut.row_tile, 0, 0, 0, 0, 0};
-  if (cut.count > 0) tree_unit_load(a.m, G, R, u);
+  if (cut.count > 0) tree_unit_load(a.m, gs, R, u);
   int tile = cut.tile;
 
   for (int left = cut.count; left > 0;) {
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
       const int r = i / (D / 4), c = i % (D / 4), row = u.row_tile * R + r;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows)
-        v = tree_load4(a.q, a.q_type, (u.node0 + row / G) * a.ldq + (int64_t)(u.head * G + row % G) * D + c * 4);
+        v = tree_load4(a.q, a.q_type, (u.node0 + (row >> gs)) * a.ldq + (int64_t)(u.head * G + (row & (G - 1))) * D + c * 4);
       *reinterpret_cast<float4*>(Qs + r * SM::kPitch + c * 4) = v;
     }
     float m[kRows], l[kRows], o[kRows][kVec][kW];
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = ty + 16 * i;
-        const int node = u.node0 + min((u.row_tile * R + r) / G, u.nodes - 1);
+        const int node = u.node0 + min((u.row_tile * R + r) >> gs, u.nodes - 1);
         float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -204,10 +204,10 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
       for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
       const int r = ty + 16 * i, row = u.row_tile * R + r;
       if (r >= rows) continue;
-      const int node = u.node0 + row / G;
+      const int node = u.node0 + (row >> gs);
       const bool zero = __ldg(a.m.pos + node) < 0 || l[i] == 0.f;
       const float inv = 1.0f / l[i];
-      const int64_t off = node * a.ldo + (int64_t)(u.head * G + row % G) * D;
+      const int64_t off = node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D;
 #pragma unroll
       for (int c = 0; c < kVec; ++c)
 #pragma unroll
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
     }
     left -= t1 - t0;
     tile = 0;
-    if (left > 0) tree_unit_next(a.m, G, R, a.d.Hkv, u);
+    if (left > 0) tree_unit_next(a.m, gs, R, a.d.Hkv, u);
   }
 }
 

@@ -2,19 +2,25 @@
 // 5th-generation tensor cores (tcgen05, accumulators in TMEM).
 //
 // The same formula as kernels_tree_f16.cu with 128 rows (nodes x query heads
-// of one KV head) and 128 keys per step:
-//   warp 0      TMA producer: K and V tiles as 64-channel panels of 128 keys in
-//               128-byte swizzled rows (one box per block and panel)
-//   warp 1      issues S = Q K^T (both operands K-major in shared memory) and
-//               O += P V (P from TMEM, V as a channel-major operand: its
-//               panels are read transposed by the MMA itself)
-//   warps 2..5  softmax: thread = row = TMEM lane.  S is read from TMEM, the
-//               weights go back as f16 over the first half of the S columns,
-//               so a row's maximum and sum never leave their thread
-// S (128 columns) and O (D columns) fill half of TMEM: two CTAs per SM, and one
-// CTA's softmax runs under the other's MMAs.  O is rescaled in TMEM only when
-// a row's scores exceed its maximum by 2^8 (exact: numerator and denominator
-// share the maximum).  Roundings as in kernels_tree_f16.cu.
+// of one KV head) and 128 keys per step, one CTA per SM:
+//   warp 0        TMA producer: K and V tiles as 64-channel panels of 128 keys
+//                 in 128-byte swizzled rows (one box per block and panel), into
+//                 a ring of tile slots, K and V of a tile one after the other
+//   warp 1        issues S = Q K^T (both operands K-major in shared memory) and
+//                 O += P V (P from TMEM, V as a channel-major operand: its
+//                 panels are read transposed by the MMA itself); S of the next
+//                 tile is issued before P V of this one, so the tensor pipe
+//                 works while a softmax runs
+//   warps 2..9    two softmax groups that take the tiles in turn, each with its
+//                 own S, O, maxima and sums: thread = row = TMEM lane.  S is read
+//                 from TMEM, the weights go back as f16 over the first half of
+//                 its columns; a row's maximum and sum never leave their thread.
+//                 At a unit's end the two halves are joined, each group for half
+//                 of the channels
+//   warps 10, 11  the next unit's queries into the other of two buffers
+// O is rescaled in TMEM only when a row's scores exceed its maximum by 2^8
+// (exact: numerator and denominator share the maximum).  Warps whose rows are
+// all behind the last skip the softmax.  Roundings as in kernels_tree_f16.cu.
 #include "attn_fold.cuh"
 #include "tc_common.cuh"
 #include "tree_common.cuh"
@@ -24,19 +30,19 @@ namespace dec {
 namespace {
 
 constexpr int kTR = 128, kTK = 128;  // rows and keys of a step
-constexpr int kTcTreeThreads = 192;
-constexpr uint32_t kTmemCols = 256;  // S: columns 0..127, O: 128..128+D-1
+constexpr int kTcTreeThreads = 384;
+constexpr uint32_t kTmemCols = 512;  // S of the two groups: columns 0, 128; O: 256, 256 + D
 
 template <int D>
 struct TcSmem {
   static constexpr int kPanels = D / 64;
   static constexpr int kPanel = kTK * 128;            // bytes of 64 channels of 128 keys (or rows)
   static constexpr int kTile = kPanels * kPanel;
-  static constexpr int kStages = D == 128 ? 1 : 2;
-  static constexpr int kQ = 0, kK = kTile, kV = kK + kStages * kTile, kFac = kV + kStages * kTile;
-  static constexpr int kBar = kFac + kTR * 4;
-  // barriers: K full, K empty, V full, V empty [stages]; Q full, S full, P full, O full, MMA done
-  static constexpr int kBars = 4 * kStages + 5;
+  static constexpr int kSlots = D == 128 ? 5 : 10;    // of the ring; at least K, V, K are in use at once
+  static constexpr int kQ = 0, kRing = 2 * kTile, kFac = kRing + kSlots * kTile;  // fac: float [2][kTR]
+  static constexpr int kBar = kFac + 2 * kTR * 4;
+  // barriers: full, empty [slots]; Q full, Q empty, S full, P full [2]; O full, O empty, MMA done
+  static constexpr int kBars = 2 * kSlots + 8 + 3;
   static constexpr int kBytes = kBar + kBars * 8 + 32;
 };
 
@@ -81,27 +87,29 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* v) {
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 template <int D>
-__global__ void __launch_bounds__(kTcTreeThreads, 2) k_tree_attend_tc(const __grid_constant__ CUtensorMap tm,
+__global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __grid_constant__ CUtensorMap tm,
                                                                       const __grid_constant__ TreeAttendArgs a) {
   using SM = TcSmem<D>;
-  constexpr int kS = SM::kStages;
+  constexpr int kS = SM::kSlots;
   extern __shared__ __align__(1024) uint8_t dsm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(dsm + SM::kBar);
-  uint64_t *kfull = bars, *kempty = bars + kS, *vfull = bars + 2 * kS, *vempty = bars + 3 * kS;
-  uint64_t *qfull = bars + 4 * kS, *sfull = qfull + 1, *pfull = qfull + 2, *ofull = qfull + 3, *mma_done = qfull + 4;
-  int* flags = reinterpret_cast<int*>(bars + SM::kBars);  // [0] abort, [1] odd values, [2] TMEM base, [3] tiles copied
+  uint64_t *full = bars, *empty = bars + kS, *qfull = bars + 2 * kS, *qempty = qfull + 2, *sfull = qfull + 4,
+           *pfull = qfull + 6, *ofull = qfull + 8, *oempty = qfull + 9, *mma_done = qfull + 10;
+  int* flags = reinterpret_cast<int*>(bars + SM::kBars);  // [0] abort, [1] odd values, [2] TMEM base, [3] slots filled
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kS; ++i) {
-      mbar_init(&kfull[i], 1);
-      mbar_init(&kempty[i], 1);
-      mbar_init(&vfull[i], 1);
-      mbar_init(&vempty[i], 1);
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
     }
-    mbar_init(qfull, 128);
-    mbar_init(sfull, 1);
-    mbar_init(pfull, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&qfull[i], 64);
+      mbar_init(&qempty[i], 256);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 128);
+    }
     mbar_init(ofull, 1);
+    mbar_init(oempty, 256);
     mbar_init(mma_done, 1);
     flags[0] = flags[1] = flags[3] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -120,14 +128,15 @@ __global__ void __launch_bounds__(kTcTreeThreads, 2) k_tree_attend_tc(const __gr
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags + 2);
   volatile int* abort_flag = flags;
-  const int G = a.d.H / a.d.Hkv;
+  const int gs = a.d.gs, G = 1 << gs;
   const TreeCut cut = a.m.cuts[blockIdx.x];
   TreeUnit u{cut.seq, cut.head, cut.row_tile, 0, 0, 0, 0, 0};
-  if (cut.count > 0) tree_unit_load(a.m, G, kTR, u);
-  int tile = cut.tile, k = 0;  // k: tiles so far, over all units
+  if (cut.count > 0) tree_unit_load(a.m, gs, kTR, u);
+  int tile = cut.tile, n_unit = 0;
 
   if (warp == 0) {
     // ---- producer: lane = (panel, block) for K, then for V ----
+    int li = 0;  // loads so far: K of tile k is load 2k, V is 2k + 1
     for (int left = cut.count; left > 0;) {
       const int t0 = tile, t1 = min(u.tiles, tile + left), blocks = (u.ctx + u.nodes + 15) >> 4;
       const int32_t* table = a.m.tables + __ldg(a.m.tab_start + u.seq);
@@ -143,119 +152,164 @@ __global__ void __launch_bounds__(kTcTreeThreads, 2) k_tree_attend_tc(const __gr
         return blk;
       };
       int nxt = entry(t0);
-      for (int t = t0; t < t1; ++t, ++k) {
-        const int slot = k % kS, here = min(8, blocks - t * 8), blk = nxt;
+      for (int t = t0; t < t1; ++t) {
+        const int here = min(8, blocks - t * 8), blk = nxt;
         nxt = entry(t + 1);
         const uint32_t bytes = here * SM::kPanels * 2048;
         const int z = a.layer * a.d.n_blocks + blk, panel = lane >> 3;
 #pragma unroll
-        for (int is_v = 0; is_v < 2; ++is_v) {
-          uint64_t* full = is_v ? &vfull[slot] : &kfull[slot];
-          uint64_t* empty = is_v ? &vempty[slot] : &kempty[slot];
+        for (int is_v = 0; is_v < 2; ++is_v, ++li) {
+          const int slot = li % kS;
           bool ok = true;
-          if (lane == 0 && k >= kS) ok = mbar_wait(empty, ((k / kS) - 1) & 1, abort_flag, a.m.err);
+          if (lane == 0 && li >= kS) ok = mbar_wait(&empty[slot], ((li / kS) - 1) & 1, abort_flag, a.m.err);
           if (!__shfl_sync(0xffffffffu, (int)ok, 0)) goto produced;
           if (lane == 0) {
-            mbar_expect_tx(full, bytes);
-            flags[3] = 2 * k + 1 + is_v;
+            mbar_expect_tx(&full[slot], bytes);
+            flags[3] = li + 1;
           }
           __syncwarp();
           if (panel < SM::kPanels && (lane & 7) < here)
-            tma_box_5d(dsm + (is_v ? SM::kV : SM::kK) + slot * SM::kTile + panel * SM::kPanel + (lane & 7) * 2048, &tm,
-                       u.head * 16, panel, is_v, z, full);
+            tma_box_5d(dsm + SM::kRing + slot * SM::kTile + panel * SM::kPanel + (lane & 7) * 2048, &tm, u.head * 16,
+                       panel, is_v, z, &full[slot]);
           __syncwarp();
         }
       }
       left -= t1 - t0;
       tile = 0;
-      if (left > 0) tree_unit_next(a.m, G, kTR, a.d.Hkv, u);
+      if (left > 0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, u);
     }
   produced:;
   } else if (warp == 1) {
     // ---- MMA issuer ----
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_f16(kTR, kTK, false), id_o = idesc_f16(kTR, D, true);
-      const uint32_t qa = smem_u32(dsm + SM::kQ);
-      int n_unit = 0;
-      for (int left = cut.count; left > 0; ++n_unit) {
-        const int t0 = tile, t1 = min(u.tiles, tile + left);
-        if (!mbar_wait(qfull, n_unit & 1, abort_flag, a.m.err)) goto issued;
-        for (int t = t0; t < t1; ++t, ++k) {
-          const int slot = k % kS;
-          if (!mbar_wait(&kfull[slot], (k / kS) & 1, abort_flag, a.m.err)) goto issued;
-          tc_fence_after();
-          const uint32_t ka = smem_u32(dsm + SM::kK + slot * SM::kTile), va = smem_u32(dsm + SM::kV + slot * SM::kTile);
+      auto issue_s = [&](int k, bool first, int unit) -> bool {
+        const int li = 2 * k, slot = li % kS, b = k & 1;
+        if (first && !mbar_wait(&qfull[unit & 1], (unit >> 1) & 1, abort_flag, a.m.err)) return false;
+        if (!mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err)) return false;
+        tc_fence_after();
+        const uint32_t qa = smem_u32(dsm + SM::kQ + (unit & 1) * SM::kTile), ka = smem_u32(dsm + SM::kRing + slot * SM::kTile);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t off = (i >> 2) * SM::kPanel + (i & 3) * 32;
-            tc_mma(tmem, sw128_desc(qa + off), sw128_desc(ka + off), id_s, i != 0);
-          }
-          tc_commit(&kempty[slot]);
-          tc_commit(sfull);
-          if (!mbar_wait(&vfull[slot], (k / kS) & 1, abort_flag, a.m.err)) goto issued;
-          if (!mbar_wait(pfull, k & 1, abort_flag, a.m.err)) goto issued;
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t off = (i >> 2) * SM::kPanel + (i & 3) * 32;
+          tc_mma(tmem + b * 128, sw128_desc(qa + off), sw128_desc(ka + off), id_s, i != 0);
+        }
+        tc_commit(&empty[slot]);
+        tc_commit(&sfull[b]);
+        return true;
+      };
+      int k = 0;
+      bool ok = cut.count == 0 || issue_s(0, true, 0);
+      for (int left = cut.count; ok && left > 0; ++n_unit) {
+        const int t0 = tile, t1 = min(u.tiles, tile + left);
+        if (n_unit > 0 && !mbar_wait(oempty, (n_unit - 1) & 1, abort_flag, a.m.err)) break;
+        int fresh = 3;  // groups whose O this unit has not written yet
+        for (int t = t0; t < t1; ++t, ++k) {
+          const int li = 2 * k + 1, slot = li % kS, b = k & 1;
+          // the next tile's scores first: of this unit, or of the next one
+          if (k + 1 < cut.count && !(ok = issue_s(k + 1, t + 1 == t1, n_unit + (t + 1 == t1)))) break;
+          if (!(ok = mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err))) break;
+          if (!(ok = mbar_wait(&pfull[b], (k >> 1) & 1, abort_flag, a.m.err))) break;
           tc_fence_after();
+          const uint32_t va = smem_u32(dsm + SM::kRing + slot * SM::kTile);
 #pragma unroll
           for (int i = 0; i < kTK / 16; ++i)
-            tc_mma_ts(tmem + 128, tmem + i * 8, sw128_mn_desc(va + i * 2048, SM::kPanel), id_o, t != t0 || i != 0);
-          tc_commit(&vempty[slot]);
+            tc_mma_ts(tmem + 256 + b * D, tmem + b * 128 + i * 8, sw128_mn_desc(va + i * 2048, SM::kPanel), id_o,
+                      i != 0 || !((fresh >> b) & 1));
+          fresh &= ~(1 << b);
+          tc_commit(&empty[slot]);
         }
+        if (!ok) break;
         tc_commit(ofull);
         left -= t1 - t0;
         tile = 0;
-        if (left > 0) tree_unit_next(a.m, G, kTR, a.d.Hkv, u);
+        if (left > 0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, u);
       }
-    issued:
       tc_commit(mma_done);
     }
     __syncwarp();
-  } else {
-    // ---- softmax: thread = row ----
-    const int r = (warp & 3) * 32 + lane, st = threadIdx.x - 64;
-    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    float* fac = reinterpret_cast<float*>(dsm + SM::kFac);
-    auto group_bar = []() { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-    int n_unit = 0;
-    bool alive = true;
+  } else if (warp >= 10) {
+    // ---- queries: one unit ahead ----
     for (int left = cut.count; left > 0; ++n_unit) {
-      const int t0 = tile, t1 = min(u.tiles, tile + left), end = u.ctx + u.nodes;
-      const int rows = min(kTR, u.nodes * G - u.row_tile * kTR);
-      tree_load_queries<D, kTR, 4>(a, u, G, warp - 2, fac, [&](int q, int x, uint2 h) {
-        *reinterpret_cast<uint2*>(dsm + SM::kQ + (x >> 4) * SM::kPanel + q * 128 + ((((x & 15) >> 1) ^ (q & 7)) << 4) +
-                                  (x & 1) * 8) = h;
+      const int b = n_unit & 1;
+      if (!__all_sync(0xffffffffu, n_unit < 2 || mbar_wait(&qempty[b], ((n_unit >> 1) - 1) & 1, abort_flag, a.m.err))) break;
+      tree_load_queries<D, kTR, 2>(a, u, warp - 10, reinterpret_cast<float*>(dsm + SM::kFac) + b * kTR, [&](int q, int x, uint4 h) {
+        *reinterpret_cast<uint4*>(dsm + SM::kQ + b * SM::kTile + (x >> 3) * SM::kPanel + q * 128 + (((x & 7) ^ (q & 7)) << 4)) = h;
       });
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(qfull);
-      group_bar();
-      const float c = fac[r];
-      const int node = u.node0 + min((u.row_tile * kTR + r) / G, u.nodes - 1);
+      mbar_arrive(&qfull[b]);
+      left -= min(u.tiles, tile + left) - tile;
+      tile = 0;
+      if (left > 0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, u);
+    }
+  } else {
+    // ---- softmax: thread = row; group b takes the tiles k with k % 2 == b ----
+    const int b = (warp - 2) >> 2, wr = (warp & 3) * 32, r = wr + lane, st = (threadIdx.x - 64) & 127;
+    const uint32_t trow = tmem + ((uint32_t)wr << 16), ts = trow + b * 128, to = trow + 256 + b * D;
+    int k = 0;
+    bool alive = true;
+    for (int left = cut.count; left > 0; ++n_unit) {
+      const int t0 = tile, t1 = min(u.tiles, tile + left), end = u.ctx + u.nodes, k0 = k;
+      const int rows = min(kTR, u.nodes * G - u.row_tile * kTR);
+      const bool mine = wr < rows;  // some row of this warp is one
+      const int node = u.node0 + min((u.row_tile * kTR + r) >> gs, u.nodes - 1);
       const uint32_t* anc = a.m.anc + (size_t)node * a.m.words;
+      alive = __all_sync(0xffffffffu, alive && mbar_wait(&qfull[n_unit & 1], (n_unit >> 1) & 1, abort_flag, a.m.err));
+      const float c = reinterpret_cast<const float*>(dsm + SM::kFac)[(n_unit & 1) * kTR + r];
       float m = -INFINITY, l = 0.f;
+      bool first = true;
       for (int t = t0; t < t1; ++t, ++k) {
-        alive = __all_sync(0xffffffffu, alive && mbar_wait(sfull, k & 1, abort_flag, a.m.err));
-        if (alive) {
+        if ((k & 1) != b) continue;
+        const int key0 = t * kTK;
+        const bool drafted = key0 + kTK > u.ctx;
+        uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};  // keys of each 32 that this row sees
+        if (drafted) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int n = key0 + j * 32 - u.ctx;  // node number of the first; negative: cached tokens
+            const int w = n >> 5;
+            const uint32_t lo = n > -32 && w < a.m.words ? (w < 0 ? 0xffffffffu : __ldg(anc + w)) : 0u;
+            const uint32_t hi = n > -32 && w + 1 < a.m.words ? __ldg(anc + w + 1) : 0u;
+            if (n > -32) vis[j] = __funnelshift_r(lo, hi, n & 31);
+          }
+          // value rows past the end hold anything, a node's value that is not finite must not meet another branch's
+          // zero weights: zero them; its descendants get it back at the unit's end.  Eight threads per row
+          const int li = 2 * k + 1, slot = li % kS;
+          alive = __all_sync(0xffffffffu, alive && mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err));
+          for (int q = max(u.ctx - key0, 0) + (st >> 3); alive && q < kTK; q += 16) {
+#pragma unroll
+            for (int p = 0; p < SM::kPanels; ++p) {
+              uint4* at = reinterpret_cast<uint4*>(dsm + SM::kRing + slot * SM::kTile + p * SM::kPanel + q * 128 + (st & 7) * 16);
+              uint4 x = key0 + q < end ? *at : make_uint4(0u, 0u, 0u, 0u);
+              bool change = key0 + q >= end;
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const uint32_t mk = ((w[z] & 0x7C00u) == 0x7C00u ? 0xFFFFu : 0u) |
+                                    ((w[z] & 0x7C000000u) == 0x7C000000u ? 0xFFFF0000u : 0u);
+                if (mk) {
+                  w[z] &= ~mk;
+                  change = true;
+                  flags[1] = 1;
+                }
+              }
+              if (change) *at = x;
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        alive = __all_sync(0xffffffffu, alive && mbar_wait(&sfull[b], (k >> 1) & 1, abort_flag, a.m.err));
+        if (alive && mine) {
           tc_fence_after();
-          const int key0 = t * kTK;
-          const bool drafted = key0 + kTK > u.ctx;
-          // which of the 32 keys of column chunk j this row sees
-          auto sees = [&](int j) -> uint32_t {
-            const int b = key0 + j * 32 - u.ctx;  // node number of the chunk's first key; negative: cached tokens
-            if (b <= -32) return 0xffffffffu;
-            if (b < 0) return (__ldg(anc) << -b) | ((1u << -b) - 1u);
-            const int w = b >> 5;
-            const uint32_t lo = w < a.m.words ? __ldg(anc + w) : 0u, hi = w + 1 < a.m.words ? __ldg(anc + w + 1) : 0u;
-            return __funnelshift_r(lo, hi, b & 31);
-          };
           float mx = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t s[32];
-            tc_ld32(trow + j * 32, s);
+            tc_ld32(ts + j * 32, s);
             if (drafted) {
-              const uint32_t vis = sees(j);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if ((vis >> i) & 1u) mx = fmaxf(mx, __uint_as_float(s[i]));
+                if ((vis[j] >> i) & 1u) mx = fmaxf(mx, __uint_as_float(s[i]));
             } else {
 #pragma unroll
               for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
@@ -266,15 +320,15 @@ __global__ void __launch_bounds__(kTcTreeThreads, 2) k_tree_attend_tc(const __gr
             const float mn = fmaxf(m, mx), f = mn == m ? 1.f : ex2(m - mn);
             m = mn;
             l *= f;
-            if (t > t0) {  // the MMAs of the tiles before have run (S of this one was issued behind them)
+            if (!first) {  // this group's products so far have run: its S was issued behind them
 #pragma unroll
               for (int j = 0; j < D / 32; ++j) {
                 uint32_t o[32];
-                tc_ld32(trow + 128 + j * 32, o);
+                tc_ld32(to + j * 32, o);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tc_st16(trow + 128 + j * 32, o);
-                tc_st16(trow + 128 + j * 32 + 16, o + 16);
+                tc_st16(to + j * 32, o);
+                tc_st16(to + j * 32 + 16, o + 16);
               }
             }
           }
@@ -286,16 +340,15 @@ __global__ void __launch_bounds__(kTcTreeThreads, 2) k_tree_attend_tc(const __gr
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t s[32], p[16];
-            tc_ld32(trow + j * 32, s);
+            tc_ld32(ts + j * 32, s);
             if (plain) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(ex2(fmaf(__uint_as_float(s[i]), c, -mu)));
             } else {
-              const uint32_t vis = drafted ? sees(j) : 0xffffffffu;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float x = ex2(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), c), -mu));
-                s[i] = (vis >> i) & 1u ? __float_as_uint(x) : 0u;
+                s[i] = (vis[j] >> i) & 1u ? __float_as_uint(x) : 0u;
               }
             }
 #pragma unroll
@@ -306,98 +359,83 @@ __global__ void __launch_bounds__(kTcTreeThreads, 2) k_tree_attend_tc(const __gr
               const __half2 h = __floats2half2_rn(x, y);
               p[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            tc_st16(trow + j * 16, p);  // over columns that this thread has read
+            tc_st16(ts + j * 16, p);  // over columns that this thread has read
           }
           l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-          if (drafted) {
-            // thread = key: value rows past the end hold anything, a node's value that is not finite must not meet
-            // another branch's zero weights: zero them; its descendants get it back at the unit's end
-            const int slot = k % kS, key = key0 + st;
-            alive = __all_sync(0xffffffffu, mbar_wait(&vfull[slot], (k / kS) & 1, abort_flag, a.m.err));
-            if (key >= u.ctx) {
-              uint8_t* vrow = dsm + SM::kV + slot * SM::kTile + st * 128;
-#pragma unroll 4
-              for (int i = 0; i < D / 8; ++i) {
-                uint4* p = reinterpret_cast<uint4*>(vrow + (i >> 3) * SM::kPanel + (i & 7) * 16);
-                uint4 x = *p;
-                uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-                bool change = false;
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  if (key >= end) {
-                    change = true;
-                    w[z] = 0u;
-                  } else {
-                    const uint32_t mk = ((w[z] & 0x7C00u) == 0x7C00u ? 0xFFFFu : 0u) |
-                                        ((w[z] & 0x7C000000u) == 0x7C000000u ? 0xFFFF0000u : 0u);
-                    if (mk) {
-                      w[z] &= ~mk;
-                      change = true;
-                      flags[1] = 1;
-                    }
-                  }
-                }
-                if (change) *p = x;
-              }
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          }
           tc_wait_st();
           tc_fence_before();
         }
-        mbar_arrive(pfull);
+        first = false;
+        mbar_arrive(&pfull[b]);
       }
-      // ---- the unit's rows: final, or this CTA's record ----
+      // ---- the unit's end: the two groups joined, this group for channels b D/2 .. (b + 1) D/2 - 1 ----
       alive = __all_sync(0xffffffffu, alive && mbar_wait(ofull, n_unit & 1, abort_flag, a.m.err));
-      group_bar();
-      if (alive) {
+      float2* ml = reinterpret_cast<float2*>(dsm + SM::kQ + (n_unit & 1) * SM::kTile);  // the queries are done with
+      ml[b * kTR + r] = make_float2(m, l);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (alive && mine) {
         tc_fence_after();
+        const float2 s0 = ml[r], s1 = ml[kTR + r];
+        const bool has0 = t1 - t0 > 1 || (k0 & 1) == 0, has1 = t1 - t0 > 1 || (k0 & 1) == 1;
+        const float M = fmaxf(s0.x, s1.x), mu = M == -INFINITY ? 0.f : M;
+        const float f0 = has0 ? ex2(s0.x - mu) : 0.f, f1 = has1 ? ex2(s1.x - mu) : 0.f;
+        const float L = s0.y * f0 + s1.y * f1;
         const bool odd = *reinterpret_cast<volatile int*>(flags + 1) != 0, whole = t0 == 0 && t1 == u.tiles;
         float* rec = tree_record(a, blockIdx.x, t0 == 0);
         const int row = u.row_tile * kTR + r;
         const int j0 = max(t0 * kTK - u.ctx, 0), j1 = min(t1 * kTK - u.ctx, u.nodes);
-        const bool zero = l == 0.f || __ldg(a.m.pos + node) < 0;
-        const float inv = whole ? 1.0f / l : 1.0f;
-        const int64_t off = node * a.ldo + (int64_t)(u.head * G + row % G) * D;
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          uint32_t o[32];
-          tc_ld32(trow + 128 + j * 32, o);
+        const bool zero = L == 0.f || __ldg(a.m.pos + node) < 0;
+        const float inv = whole ? 1.0f / L : 1.0f, g0 = f0 * inv, g1 = f1 * inv;
+        const int64_t off = node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D;
+#pragma unroll 1
+        for (int ch = b * (D / 2); ch < (b + 1) * (D / 2); ch += 32) {
+          uint32_t x[32], y[32];
+          if (has0) tc_ld32(trow + 256 + ch, x);
+          if (has1) tc_ld32(trow + 256 + D + ch, y);
           if (r < rows) {
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              v[i] = has0 ? __uint_as_float(x[i]) * g0 : 0.f;
+              if (has1) v[i] = fmaf(__uint_as_float(y[i]), g1, v[i]);
+            }
             if (odd) {  // rare: the values that were taken out, for the rows that see them
               const int32_t* table = a.m.tables + __ldg(a.m.tab_start + u.seq);
               for (int n = j0; n < j1; ++n) {
                 if (!tree_sees(a.m, node, n)) continue;
                 const int p = u.ctx + n;
-                const int64_t at = kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D) + j * 32;
+                const __half* at = reinterpret_cast<const __half*>(a.kv) +
+                                   kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D) + ch;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                  const float y = __half2float(reinterpret_cast<const __half*>(a.kv)[at + i]);
-                  if (!isfinite(y)) o[i] = __float_as_uint(__uint_as_float(o[i]) + y);
+                  const float z = __half2float(at[i]);
+                  if (!isfinite(z)) v[i] += z;
                 }
               }
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              float4 v = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                                     __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-              if (whole) tree_store4(a.out, a.out_type, off + j * 32 + i, zero ? make_float4(0.f, 0.f, 0.f, 0.f) : v);
-              else *reinterpret_cast<float4*>(rec + r * D + j * 32 + i) = v;
+              const float4 z = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              if (whole) tree_store4(a.out, a.out_type, off + ch + i, zero ? make_float4(0.f, 0.f, 0.f, 0.f) : z);
+              else *reinterpret_cast<float4*>(rec + r * D + ch + i) = z;
             }
           }
+          __syncwarp();
         }
-        if (!whole && r < rows) {
-          rec[kTR * D + r] = m;
-          rec[kTR * D + kTR + r] = l;
+        if (!whole && r < rows && b == 0) {
+          rec[kTR * D + r] = M;
+          rec[kTR * D + kTR + r] = L;
         }
-        tc_fence_before();  // O has been read before the next unit's first P is announced
+        tc_fence_before();
       }
-      group_bar();
-      if (st == 0) flags[1] = 0;
-      group_bar();
+      mbar_arrive(oempty);           // O may be written again
+      mbar_arrive(&qempty[n_unit & 1]);
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // ml and the flag are free
+      if (threadIdx.x == 64) flags[1] = 0;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
       left -= t1 - t0;
       tile = 0;
-      if (left > 0) tree_unit_next(a.m, G, kTR, a.d.Hkv, u);
+      if (left > 0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, u);
     }
   }
 
@@ -408,11 +446,9 @@ __global__ void __launch_bounds__(kTcTreeThreads, 2) k_tree_attend_tc(const __gr
     while (!mbar_try(mma_done, 0) && global_ns() - w0 < kWaitLimitNs) {
     }
   if (threadIdx.x == 0 && *abort_flag)
-    for (int i = max(flags[3] - 2 * kS, 0); i < flags[3]; ++i) {
-      uint64_t* f = (i & 1) ? &vfull[(i >> 1) % kS] : &kfull[(i >> 1) % kS];
-      while (!mbar_try(f, ((i >> 1) / kS) & 1) && global_ns() - w0 < kWaitLimitNs) {
+    for (int i = max(flags[3] - kS, 0); i < flags[3]; ++i)
+      while (!mbar_try(&full[i % kS], (i / kS) & 1) && global_ns() - w0 < kWaitLimitNs) {
       }
-    }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -424,7 +460,7 @@ template <int D>
 cudaError_t one(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
   static SmemOptIn opt;
   constexpr int smem = TcSmem<D>::kBytes;
-  static_assert(smem <= 115712, "two CTAs per SM");
+  static_assert(smem <= 232448, "one CTA per SM");
   cudaError_t e = opt.ensure(k_tree_attend_tc<D>, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_tree_attend_tc<D>, ctas, kTcTreeThreads, smem, s, *tm, a);

@@ -48,7 +48,7 @@ struct TreeLayout {
 // (nodes x query heads per KV head).
 TreeVariant variant_for(bool f16, int D, int max_rows) {
   if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, 2};
-  if (D >= 64 && max_rows > 32) return {kTreeTc, 128, 128, 2};
+  if (D >= 64 && max_rows > 32) return {kTreeTc, 128, 128, 1};
   return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2};
 }
 
@@ -294,7 +294,8 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
 
 TreePoolDims pool_dims(const dec_tree* t) {
   const dec_config& c = t->cfg;
-  return {c.n_heads, c.n_kv_heads, c.head_dim, c.n_layers, t->pool->n_blocks, (float)c.rms_eps};
+  const int G = c.n_heads / c.n_kv_heads;
+  return {c.n_heads, c.n_kv_heads, c.head_dim, c.n_layers, t->pool->n_blocks, G == 4 ? 2 : G - 1, (float)c.rms_eps};
 }
 
 int check_rope(const dec_rope* r) {

@@ -51,6 +51,7 @@ struct TreeMeta {
 
 struct TreePoolDims {
   int H, Hkv, D, n_layers, n_blocks;
+  int gs;  // query heads per KV head: 1 << gs (a config has 1, 2 or 4)
   float eps;
 };
 

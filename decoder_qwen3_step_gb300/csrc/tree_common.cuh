@@ -16,23 +16,23 @@ __device__ __forceinline__ bool tree_shape_ok(const TreeMeta& m, bool rows = fal
   return ok;
 }
 
-// One unit of attention work: the rows row0 .. row0+rows-1 (row r: node r / G,
-// query head r % G of the group) of one sequence and KV head.
+// One unit of attention work: the rows row0 .. row0+rows-1 (row r: node r >> gs,
+// query head r & (2^gs - 1) of the group) of one sequence and KV head.
 struct TreeUnit {
   int seq, head, row_tile, n_row_tiles;
   int node0, ctx, nodes;  // the sequence's first node, cached tokens, nodes
   int tiles;              // key tiles of ctx + nodes keys
 };
 
-__device__ __forceinline__ void tree_unit_load(const TreeMeta& m, int G, int R, TreeUnit& u) {
+__device__ __forceinline__ void tree_unit_load(const TreeMeta& m, int gs, int R, TreeUnit& u) {
   u.node0 = __ldg(m.seq_start + u.seq);
   u.nodes = __ldg(m.seq_start + u.seq + 1) - u.node0;
   u.ctx = __ldg(m.ctx + u.seq);
   u.tiles = (u.ctx + u.nodes + m.tile_keys - 1) / m.tile_keys;
-  u.n_row_tiles = (u.nodes * G + R - 1) / R;
+  u.n_row_tiles = ((u.nodes << gs) + R - 1) / R;
 }
 // The unit after u (sequences without nodes have none).
-__device__ __forceinline__ void tree_unit_next(const TreeMeta& m, int G, int R, int Hkv, TreeUnit& u) {
+__device__ __forceinline__ void tree_unit_next(const TreeMeta& m, int gs, int R, int Hkv, TreeUnit& u) {
   if (++u.row_tile < u.n_row_tiles) return;
   u.row_tile = 0;
   if (++u.head < Hkv) return;
@@ -40,7 +40,7 @@ __device__ __forceinline__ void tree_unit_next(const TreeMeta& m, int G, int R, 
   do {
     ++u.seq;
   } while (u.seq < m.S && __ldg(m.seq_start + u.seq + 1) == __ldg(m.seq_start + u.seq));
-  if (u.seq < m.S) tree_unit_load(m, G, R, u);
+  if (u.seq < m.S) tree_unit_load(m, gs, R, u);
 }
 
 // Whether node `node` (numbered over the batch) sees node j of its sequence.
@@ -98,39 +98,93 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Load the queries of a unit's row tile as f16 into shared memory: warp w of
-// W takes rows w, w + W, ..., eight in flight (a row's load takes about a
-// microsecond from HBM; one at a time, 128 rows cost more than a dozen key
-// tiles).  Each row is scaled by a power of two so that its largest magnitude
-// lies in [1, 2): f16 then rounds every channel by at most 2^-12 of that,
-// whatever the queries' range; fac[r] takes the row's score factor.  put(r,
-// lane, halves 4 lane .. 4 lane + 3).  Rows past the last are zeros.
-template <int D, int R, int W, typename F>
-__device__ __forceinline__ void tree_load_queries(const TreeAttendArgs& a, const TreeUnit& u, int G, int w, float* fac, F&& put) {
-  constexpr int kU = R / W < 8 ? R / W : 8;
-  const int lane = threadIdx.x & 31, rows = min(R, u.nodes * G - u.row_tile * R);
-  for (int r0 = w; r0 < R; r0 += W * kU) {
-    float4 v[kU];
+// The two 16-bit elements of a word as fp32 (both conversions are exact).
+template <typename T>
+__device__ __forceinline__ float2 tree_pair(uint32_t w);
+template <>
+__device__ __forceinline__ float2 tree_pair<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 tree_pair<bf16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Load the queries of a unit's row tile as f16 into shared memory.  D/8 lanes
+// share a row (eight channels each), so a warp reads 32/(D/8) rows at a time
+// and has four such groups in flight; W warps split the rows.  The code has no
+// branch and no division per row: a first version with both, one row per warp
+// and step, took 0.7 us a row on instruction latency alone.
+// Each row is scaled by a power of two so that its largest magnitude lies in
+// [1, 2): f16 then rounds every channel by at most 2^-12 of that, whatever the
+// queries' range; fac[r] takes the row's score factor.  put(r, channel / 8,
+// eight halves).  Rows past the last are zeros.
+template <int D, int R, int W, typename T, typename F>
+__device__ __forceinline__ void tree_load_queries_of(const TreeAttendArgs& a, const TreeUnit& u, int w, float* fac, F&& put) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kSteps = R / (W * kRows), kU = kSteps < 4 ? kSteps : 4;
+  constexpr bool kWide = sizeof(T) == 4;
+  static_assert(kSteps >= 1 && kSteps % kU == 0, "rows split evenly");
+  const int lane = threadIdx.x & 31, x = lane % kLanes, gs = a.d.gs;
+  const int row0 = u.row_tile * R, rows = min(R, (u.nodes << gs) - row0);
+  const T* q = reinterpret_cast<const T*>(a.q) + (int64_t)u.node0 * a.ldq + (u.head << gs) * D + x * 8;
+#pragma unroll 1
+  for (int s = 0; s < kSteps; s += kU) {
+    uint4 raw[kU][kWide ? 2 : 1];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-      const int r = r0 + i * W, row = u.row_tile * R + r;
-      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < rows && lane * 4 < D)
-        v[i] = tree_load4(a.q, a.q_type, (u.node0 + row / G) * a.ldq + (int64_t)(u.head * G + row % G) * D + lane * 4);
+      const int row = row0 + min(((s + i) * W + w) * kRows + lane / kLanes, rows - 1);
+      const T* p = q + (int64_t)(row >> gs) * a.ldq + (row & ((1 << gs) - 1)) * D;
+      if constexpr (kWide) {
+        raw[i][0] = *reinterpret_cast<const uint4*>(p);
+        raw[i][1] = *reinterpret_cast<const uint4*>(p + 4);
+      } else {  // rows are aligned to four elements: 8 bytes
+        const uint2 a0 = *reinterpret_cast<const uint2*>(p), a1 = *reinterpret_cast<const uint2*>(p + 4);
+        raw[i][0] = make_uint4(a0.x, a0.y, a1.x, a1.y);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-      const int r = r0 + i * W;
-      const float mx = warp_max(fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
+      const int r = ((s + i) * W + w) * kRows + lane / kLanes;
+      float v[8];
+      if constexpr (kWide) {
+        const uint32_t b[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w, raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(b[e]);
+      } else {
+        const uint32_t b[4] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = tree_pair<T>(b[e]);
+          v[2 * e] = f.x;
+          v[2 * e + 1] = f.y;
+        }
+      }
+      float mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       // the factor 2^-e, 2^e <= mx < 2^(e+1); rows of zeros, subnormals or infinities stay as they are
       const int e = (int)(__float_as_uint(mx) >> 23);
       const bool scaled = e > 0 && e < 255;
-      const float f = scaled ? __uint_as_float((uint32_t)max(254 - e, 1) << 23) : 1.f;
-      const __half2 lo = __floats2half2_rn(v[i].x * f, v[i].y * f), hi = __floats2half2_rn(v[i].z * f, v[i].w * f);
-      if (lane * 4 < D) put(r, lane, make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi)));
-      if (lane == 0) fac[r] = a.scale_log2 * (scaled ? 1.f / f : 1.f);
+      const int fe = max(254 - e, 1);  // its exponent bits; the inverse has 254 - fe
+      const float f = r >= rows ? 0.f : scaled ? __uint_as_float((uint32_t)fe << 23) : 1.f;
+      uint32_t h[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const __half2 y = __floats2half2_rn(v[2 * z] * f, v[2 * z + 1] * f);
+        h[z] = r >= rows ? 0u : *reinterpret_cast<const uint32_t*>(&y);
+      }
+      put(r, x, make_uint4(h[0], h[1], h[2], h[3]));
+      if (x == 0) fac[r] = a.scale_log2 * (scaled ? __uint_as_float((uint32_t)max(254 - fe, 1) << 23) : 1.f);
     }
   }
+}
+template <int D, int R, int W, typename F>
+__device__ __forceinline__ void tree_load_queries(const TreeAttendArgs& a, const TreeUnit& u, int w, float* fac, F&& put) {
+  if (a.q_type == kTreeF32) tree_load_queries_of<D, R, W, float>(a, u, w, fac, put);
+  else if (a.q_type == kTreeF16) tree_load_queries_of<D, R, W, __half>(a, u, w, fac, put);
+  else tree_load_queries_of<D, R, W, bf16>(a, u, w, fac, put);
 }
 
 }  // namespace dec
