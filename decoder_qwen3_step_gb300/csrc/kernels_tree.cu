@@ -261,6 +261,56 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
   }
 }
 
+// The same for the 128-row tiles of wide trees, whose records are channel-major
+// ([D][128], then maxima and sums): thread = row, kMergeChannels channels per
+// block, so the reads are whole lines.
+template <int D, int kMergeChannels>
+__global__ void __launch_bounds__(128) k_tree_merge_wide(const __grid_constant__ TreeAttendArgs a) {
+  pdl_wait_prev();
+  pdl_launch_next();
+  if (!tree_shape_ok(a.m, true)) return;
+  constexpr int R = 128, kSlabs = D / kMergeChannels;
+  const int gs = a.d.gs, r = threadIdx.x;
+  const int n = __ldg(a.m.hdr + kHdrMerges);
+  for (int w = blockIdx.x; w < n * kSlabs; w += gridDim.x) {
+    const TreeMerge e = a.m.merges[w / kSlabs];
+    const int d0 = (w % kSlabs) * kMergeChannels, row = e.row_tile * R + r;
+    const int node0 = __ldg(a.m.seq_start + e.seq);
+    if (row >= (__ldg(a.m.seq_start + e.seq + 1) - node0) << gs) continue;
+    const int node = node0 + (row >> gs);
+    auto rec = [&](int c) -> const float* { return tree_record(a, c, c == e.c0); };
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int c = e.c0; c <= e.c1; ++c) M = fmaxf(M, __ldcg(rec(c) + R * D + r));
+    if (M == -INFINITY) M = 0.f;  // no contribution saw a finite score
+    float L = 0.f, o[kMergeChannels];
+#pragma unroll
+    for (int i = 0; i < kMergeChannels; ++i) o[i] = 0.f;
+#pragma unroll kMergeChannels == 4 ? 8 : 2
+    for (int c = e.c0; c <= e.c1; ++c) {
+      const float* p = rec(c);
+      const float f = ex2(__ldcg(p + R * D + r) - M);
+      L = fmaf(__ldcg(p + R * D + R + r), f, L);
+#pragma unroll
+      for (int i = 0; i < kMergeChannels; ++i) o[i] = fmaf(__ldcg(p + (d0 + i) * R + r), f, o[i]);
+    }
+    const bool zero = __ldg(a.m.pos + node) < 0 || L == 0.f;
+    const float inv = 1.0f / L;
+    const int64_t off = node * a.ldo + (int64_t)((e.head << gs) + (row & ((1 << gs) - 1))) * D + d0;
+#pragma unroll
+    for (int i = 0; i < kMergeChannels; i += 4)
+      tree_store4(a.out, a.out_type, off + i,
+                  zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv));
+  }
+}
+
+template <int D>
+cudaError_t merge_wide(const TreeAttendArgs& a, int n_merges, cudaStream_t s) {
+  // few units share their keys among many CTAs: four channels per block, or too few blocks read all those records
+  if (n_merges < 64) return launch_pdl(k_tree_merge_wide<D, 4>, n_merges * (D / 4), 128, 0, s, a);
+  return launch_pdl(k_tree_merge_wide<D, 16>, n_merges * (D / 16), 128, 0, s, a);
+}
+
 }  // namespace
 
 cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t s) {
@@ -285,6 +335,9 @@ cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s) {
 
 cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, cudaStream_t s) {
   // a replayed call may meet a plan with more merges than at its capture: the blocks loop
+  if (a.m.row_tile == 128) {
+    return a.d.D == 128 ? merge_wide<128>(a, max(n_merges, 1), s) : merge_wide<64>(a, max(n_merges, 1), s);
+  }
   const int grid = max(n_merges, 1) * (a.m.row_tile / 4);
   switch (a.d.D) {
     case 32: return launch_pdl(k_tree_merge<32>, grid, 128, 0, s, a);

@@ -84,8 +84,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
   volatile int* abort_flag = flags;
   const int gs = a.d.gs, G = 1 << gs;
   const TreeCut cut = a.m.cuts[blockIdx.x];
-  TreeUnit u{cut.seq, cut.head, cut.row_tile, 0, 0, 0, 0, 0};
-  if (cut.count > 0) tree_unit_load(a.m, gs, R, u);
+  TreeUnit u = tree_unit_first(a.m, gs, R, cut);
   int tile = cut.tile, k = 0;
 
   if (warp == 4) {
@@ -141,9 +140,9 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
       const int t0 = tile, t1 = min(u.tiles, tile + left), end = u.ctx + u.nodes;
       const int rows = min(R, u.nodes * G - u.row_tile * R);
       if constexpr (R / 4 >= 32 / (D / 8)) {
-        tree_load_queries<D, R, 4>(a, u, warp, fac, [&](int r, int x, uint4 h) { *reinterpret_cast<uint4*>(Qs + r * SM::kQPitch + x * 16) = h; });
+        tree_load_queries<D, R, 4, 4>(a, u, warp, fac, [&](int r, int x, uint4 h) { *reinterpret_cast<uint4*>(Qs + r * SM::kQPitch + x * 16) = h; });
       } else if (warp < 2) {  // D = 32, R = 16: a warp reads eight rows at a time
-        tree_load_queries<D, R, 2>(a, u, warp, fac, [&](int r, int x, uint4 h) { *reinterpret_cast<uint4*>(Qs + r * SM::kQPitch + x * 16) = h; });
+        tree_load_queries<D, R, 2, 4>(a, u, warp, fac, [&](int r, int x, uint4 h) { *reinterpret_cast<uint4*>(Qs + r * SM::kQPitch + x * 16) = h; });
       }
       group_bar();
       const uint32_t qb = smem_u32(Qs) + (lane & 15) * SM::kQPitch + (lane >> 4) * 16;

@@ -50,8 +50,7 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int gs = a.d.gs, G = 1 << gs;
   TreeCut cut = a.m.cuts[blockIdx.x];
-  TreeUnit u{cut.seq, cut.head, cut.row_tile, 0, 0, 0, 0, 0};
-  if (cut.count > 0) tree_unit_load(a.m, gs, R, u);
+  TreeUnit u = tree_unit_first(a.m, gs, R, cut);
   int tile = cut.tile;
 
   for (int left = cut.count; left > 0;) {

@@ -3,15 +3,15 @@
 //
 // The same formula as kernels_tree_f16.cu with 128 rows (nodes x query heads
 // of one KV head) and 128 keys per step, one CTA per SM:
-//   warp 0        TMA producer: K and V tiles as 64-channel panels of 128 keys
+//   warp 8        TMA producer: K and V tiles as 64-channel panels of 128 keys
 //                 in 128-byte swizzled rows (one box per block and panel), into
 //                 a ring of tile slots, K and V of a tile one after the other
-//   warp 1        issues S = Q K^T (both operands K-major in shared memory) and
+//   warp 9        issues S = Q K^T (both operands K-major in shared memory) and
 //                 O += P V (P from TMEM, V as a channel-major operand: its
 //                 panels are read transposed by the MMA itself); S of the next
 //                 tile is issued before P V of this one, so the tensor pipe
 //                 works while a softmax runs
-//   warps 2..9    two softmax groups that take the tiles in turn, each with its
+//   warps 0..7    two softmax groups that take the tiles in turn, each with its
 //                 own S, O, maxima and sums: thread = row = TMEM lane.  S is read
 //                 from TMEM, the weights go back as f16 over the first half of
 //                 its columns; a row's maximum and sum never leave their thread.
@@ -74,17 +74,56 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t panel
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-#define TREE_R32(v)                                                                                                 \
-  "r"((v)[0]), "r"((v)[1]), "r"((v)[2]), "r"((v)[3]), "r"((v)[4]), "r"((v)[5]), "r"((v)[6]), "r"((v)[7]),           \
-      "r"((v)[8]), "r"((v)[9]), "r"((v)[10]), "r"((v)[11]), "r"((v)[12]), "r"((v)[13]), "r"((v)[14]), "r"((v)[15])
+__device__ __forceinline__ void tc_ld64(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=r"(v[32]),
+        "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]),
+        "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]),
+        "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]), "=r"(v[56]),
+        "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16};" ::"r"(taddr),
-      TREE_R32(v)
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 operations per instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __grid_constant__ CUtensorMap tm,
@@ -103,7 +142,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&qfull[i], 64);
+      mbar_init(&qfull[i], 320);
       mbar_init(&qempty[i], 256);
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 128);
@@ -118,7 +157,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   pdl_wait_prev();
   pdl_launch_next();
   if (!tree_shape_ok(a.m, true)) return;
-  if (warp == 1) {
+  if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(flags + 2)), "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -130,11 +169,10 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   volatile int* abort_flag = flags;
   const int gs = a.d.gs, G = 1 << gs;
   const TreeCut cut = a.m.cuts[blockIdx.x];
-  TreeUnit u{cut.seq, cut.head, cut.row_tile, 0, 0, 0, 0, 0};
-  if (cut.count > 0) tree_unit_load(a.m, gs, kTR, u);
+  TreeUnit u = tree_unit_first(a.m, gs, kTR, cut);
   int tile = cut.tile, n_unit = 0;
 
-  if (warp == 0) {
+  if (warp == 8) {
     // ---- producer: lane = (panel, block) for K, then for V ----
     int li = 0;  // loads so far: K of tile k is load 2k, V is 2k + 1
     for (int left = cut.count; left > 0;) {
@@ -179,20 +217,23 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       if (left > 0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, u);
     }
   produced:;
-  } else if (warp == 1) {
+  } else if (warp == 9) {
     // ---- MMA issuer ----
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_f16(kTR, kTK, false), id_o = idesc_f16(kTR, D, true);
+      const uint64_t q_desc = sw128_desc(smem_u32(dsm + SM::kQ)), ring_desc = sw128_desc(smem_u32(dsm + SM::kRing));
+      const uint64_t v_desc = sw128_mn_desc(smem_u32(dsm + SM::kRing), SM::kPanel);
       auto issue_s = [&](int k, bool first, int unit) -> bool {
         const int li = 2 * k, slot = li % kS, b = k & 1;
         if (first && !mbar_wait(&qfull[unit & 1], (unit >> 1) & 1, abort_flag, a.m.err)) return false;
         if (!mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err)) return false;
         tc_fence_after();
-        const uint32_t qa = smem_u32(dsm + SM::kQ + (unit & 1) * SM::kTile), ka = smem_u32(dsm + SM::kRing + slot * SM::kTile);
+        // a step along K only moves the descriptors' start addresses (their low bits, in 16-byte units)
+        const uint64_t qd = q_desc + (unit & 1) * (SM::kTile >> 4), kd = ring_desc + slot * (SM::kTile >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = (i >> 2) * SM::kPanel + (i & 3) * 32;
-          tc_mma(tmem + b * 128, sw128_desc(qa + off), sw128_desc(ka + off), id_s, i != 0);
+          const uint32_t off = ((i >> 2) * SM::kPanel + (i & 3) * 32) >> 4;
+          tc_mma(tmem + b * 128, qd + off, kd + off, id_s, i != 0);
         }
         tc_commit(&empty[slot]);
         tc_commit(&sfull[b]);
@@ -202,6 +243,8 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       bool ok = cut.count == 0 || issue_s(0, true, 0);
       for (int left = cut.count; ok && left > 0; ++n_unit) {
         const int t0 = tile, t1 = min(u.tiles, tile + left);
+        TreeUnit nu = u;
+        if (left > t1 - t0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, nu);
         if (n_unit > 0 && !mbar_wait(oempty, (n_unit - 1) & 1, abort_flag, a.m.err)) break;
         int fresh = 3;  // groups whose O this unit has not written yet
         for (int t = t0; t < t1; ++t, ++k) {
@@ -211,10 +254,10 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           if (!(ok = mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err))) break;
           if (!(ok = mbar_wait(&pfull[b], (k >> 1) & 1, abort_flag, a.m.err))) break;
           tc_fence_after();
-          const uint32_t va = smem_u32(dsm + SM::kRing + slot * SM::kTile);
+          const uint64_t vd = v_desc + slot * (SM::kTile >> 4);
 #pragma unroll
           for (int i = 0; i < kTK / 16; ++i)
-            tc_mma_ts(tmem + 256 + b * D, tmem + b * 128 + i * 8, sw128_mn_desc(va + i * 2048, SM::kPanel), id_o,
+            tc_mma_ts(tmem + 256 + b * D, tmem + b * 128 + i * 8, vd + i * (2048 >> 4), id_o,
                       i != 0 || !((fresh >> b) & 1));
           fresh &= ~(1 << b);
           tc_commit(&empty[slot]);
@@ -223,17 +266,17 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
         tc_commit(ofull);
         left -= t1 - t0;
         tile = 0;
-        if (left > 0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, u);
+        u = nu;
       }
       tc_commit(mma_done);
     }
     __syncwarp();
   } else if (warp >= 10) {
-    // ---- queries: one unit ahead ----
+    // ---- queries: one unit ahead (the first unit's by the softmax warps, which have nothing else to do yet) ----
     for (int left = cut.count; left > 0; ++n_unit) {
       const int b = n_unit & 1;
       if (!__all_sync(0xffffffffu, n_unit < 2 || mbar_wait(&qempty[b], ((n_unit >> 1) - 1) & 1, abort_flag, a.m.err))) break;
-      tree_load_queries<D, kTR, 2>(a, u, warp - 10, reinterpret_cast<float*>(dsm + SM::kFac) + b * kTR, [&](int q, int x, uint4 h) {
+      if (n_unit > 0) tree_load_queries<D, kTR, 2, 4>(a, u, warp - 10, reinterpret_cast<float*>(dsm + SM::kFac) + b * kTR, [&](int q, int x, uint4 h) {
         *reinterpret_cast<uint4*>(dsm + SM::kQ + b * SM::kTile + (x >> 3) * SM::kPanel + q * 128 + (((x & 7) ^ (q & 7)) << 4)) = h;
       });
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -244,18 +287,28 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
     }
   } else {
     // ---- softmax: thread = row; group b takes the tiles k with k % 2 == b ----
-    const int b = (warp - 2) >> 2, wr = (warp & 3) * 32, r = wr + lane, st = (threadIdx.x - 64) & 127;
+    const int b = warp >> 2, wr = (warp & 3) * 32, r = wr + lane, st = threadIdx.x & 127;
     const uint32_t trow = tmem + ((uint32_t)wr << 16), ts = trow + b * 128, to = trow + 256 + b * D;
     int k = 0;
     bool alive = true;
+    if (cut.count > 0) {
+      tree_load_queries<D, kTR, 8, 8>(a, u, warp, reinterpret_cast<float*>(dsm + SM::kFac), [&](int q, int x, uint4 h) {
+        *reinterpret_cast<uint4*>(dsm + SM::kQ + (x >> 3) * SM::kPanel + q * 128 + (((x & 7) ^ (q & 7)) << 4)) = h;
+      });
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(&qfull[0]);
+    }
     for (int left = cut.count; left > 0; ++n_unit) {
       const int t0 = tile, t1 = min(u.tiles, tile + left), end = u.ctx + u.nodes, k0 = k;
       const int rows = min(kTR, u.nodes * G - u.row_tile * kTR);
       const bool mine = wr < rows;  // some row of this warp is one
       const int node = u.node0 + min((u.row_tile * kTR + r) >> gs, u.nodes - 1);
       const uint32_t* anc = a.m.anc + (size_t)node * a.m.words;
+      TreeUnit nu = u;  // its arrays are read now: at the unit's end nothing else would cover that
+      if (left > t1 - t0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, nu);
       alive = __all_sync(0xffffffffu, alive && mbar_wait(&qfull[n_unit & 1], (n_unit >> 1) & 1, abort_flag, a.m.err));
       const float c = reinterpret_cast<const float*>(dsm + SM::kFac)[(n_unit & 1) * kTR + r];
+      mbar_arrive(&qfull[(n_unit + 1) & 1]);  // the next unit's queries come from the other warps alone
       float m = -INFINITY, l = 0.f;
       bool first = true;
       for (int t = t0; t < t1; ++t, ++k) {
@@ -303,17 +356,20 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           tc_fence_after();
           float mx = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t s[32];
-            tc_ld32(ts + j * 32, s);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t s[64];
+            tc_ld64(ts + h * 64, s);
             if (drafted) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if ((vis[j] >> i) & 1u) mx = fmaxf(mx, __uint_as_float(s[i]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
+              for (int i = 0; i < 64; ++i)
+                if (!((vis[2 * h + (i >> 5)] >> (i & 31)) & 1u)) s[i] = 0xff800000u;  // -inf
             }
+            float y[4] = {mx, mx, mx, mx};
+#pragma unroll
+            for (int i = 0; i < 64; i += 8)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) y[z] = fmaxf(fmaxf(y[z], __uint_as_float(s[i + 2 * z])), __uint_as_float(s[i + 2 * z + 1]));
+            mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
           }
           mx *= c;
           if (__any_sync(0xffffffffu, mx > m + 8.f)) {
@@ -321,7 +377,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
             m = mn;
             l *= f;
             if (!first) {  // this group's products so far have run: its S was issued behind them
-#pragma unroll
+#pragma unroll 1
               for (int j = 0; j < D / 32; ++j) {
                 uint32_t o[32];
                 tc_ld32(to + j * 32, o);
@@ -333,35 +389,36 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
             }
           }
           const float mu = m == -INFINITY ? 0.f : m;
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
           // s c - m in one rounding while that is small against the weights' own (2^-12 at 2^12); far out the product is
           // rounded as the maximum was, or the largest score would miss it by its own last place
-          const bool plain = !drafted && !__any_sync(0xffffffffu, !(fabsf(mu) <= 4096.f));
+          const bool plain = !__any_sync(0xffffffffu, !(fabsf(mu) <= 4096.f));
+          const uint64_t c2 = plain ? pack2(c, c) : pack2(1.f, 1.f), m2 = plain ? pack2(-mu, -mu) : 0ull;
+          uint64_t l2[2] = {0ull, 0ull};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t s[32], p[16];
             tc_ld32(ts + j * 32, s);
-            if (plain) {
+            if (drafted) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(ex2(fmaf(__uint_as_float(s[i]), c, -mu)));
-            } else {
+              for (int i = 0; i < 32; ++i)
+                if (!((vis[j] >> i) & 1u)) s[i] = 0xff800000u;
+            }
+            if (!plain) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float x = ex2(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), c), -mu));
-                s[i] = (vis[j] >> i) & 1u ? __float_as_uint(x) : 0u;
-              }
+              for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), c), -mu));
             }
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float x = __uint_as_float(s[i]), y = __uint_as_float(s[i + 1]);
-              l4[i & 2] += x;
-              l4[(i & 2) + 1] += y;
-              const __half2 h = __floats2half2_rn(x, y);
-              p[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int i = 0; i < 16; ++i) {
+              const float2 z = unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, m2));
+              const float ex = ex2(z.x), ey = ex2(z.y);
+              l2[i & 1] = add2(l2[i & 1], pack2(ex, ey));
+              const __half2 hh = __floats2half2_rn(ex, ey);
+              p[i] = *reinterpret_cast<const uint32_t*>(&hh);
             }
-            tc_st16(ts + j * 16, p);  // over columns that this thread has read
+            tc_st16(ts + j * 16, p);  // over scores that this thread has read
           }
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          const float2 lx = unpack2(add2(l2[0], l2[1]));
+          l += lx.x + lx.y;
           tc_wait_st();
           tc_fence_before();
         }
@@ -399,28 +456,37 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
               v[i] = has0 ? __uint_as_float(x[i]) * g0 : 0.f;
               if (has1) v[i] = fmaf(__uint_as_float(y[i]), g1, v[i]);
             }
-            if (odd) {  // rare: the values that were taken out, for the rows that see them
-              const int32_t* table = a.m.tables + __ldg(a.m.tab_start + u.seq);
-              for (int n = j0; n < j1; ++n) {
-                if (!tree_sees(a.m, node, n)) continue;
-                const int p = u.ctx + n;
-                const __half* at = reinterpret_cast<const __half*>(a.kv) +
-                                   kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D) + ch;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float z = __half2float(at[i]);
-                  if (!isfinite(z)) v[i] += z;
-                }
-              }
-            }
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               const float4 z = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
               if (whole) tree_store4(a.out, a.out_type, off + ch + i, zero ? make_float4(0.f, 0.f, 0.f, 0.f) : z);
-              else *reinterpret_cast<float4*>(rec + r * D + ch + i) = z;
+              else {
+              // channel-major: the lanes of a warp write consecutive words
+              rec[(ch + i) * kTR + r] = z.x;
+              rec[(ch + i + 1) * kTR + r] = z.y;
+              rec[(ch + i + 2) * kTR + r] = z.z;
+              rec[(ch + i + 3) * kTR + r] = z.w;
+            }
             }
           }
           __syncwarp();
+        }
+        if (odd && r < rows) {  // rare: the values that were taken out, for the rows that see them
+          const int32_t* table = a.m.tables + __ldg(a.m.tab_start + u.seq);
+#pragma unroll 1
+          for (int n = j0; n < j1; ++n) {
+            if (!tree_sees(a.m, node, n)) continue;
+            const int p = u.ctx + n;
+            const __half* at = reinterpret_cast<const __half*>(a.kv) +
+                               kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D);
+#pragma unroll 1
+            for (int i = b * (D / 2); i < (b + 1) * (D / 2); ++i) {
+              const float z = __half2float(at[i]);
+              if (isfinite(z)) continue;
+              if (whole) tree_store(a.out, a.out_type, off + i, tree_load(a.out, a.out_type, off + i) + z);
+              else rec[i * kTR + r] += z;
+            }
+          }
         }
         if (!whole && r < rows && b == 0) {
           rec[kTR * D + r] = M;
@@ -431,26 +497,26 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       mbar_arrive(oempty);           // O may be written again
       mbar_arrive(&qempty[n_unit & 1]);
       asm volatile("bar.sync 1, 256;" ::: "memory");  // ml and the flag are free
-      if (threadIdx.x == 64) flags[1] = 0;
+      if (threadIdx.x == 0) flags[1] = 0;
       asm volatile("bar.sync 1, 256;" ::: "memory");
       left -= t1 - t0;
       tile = 0;
-      if (left > 0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, u);
+      u = nu;
     }
   }
 
   __syncthreads();
   // the last commit has arrived (every MMA and every commit before it has); after an abort also the copies in flight
   const uint64_t w0 = global_ns();
-  if (warp == 1)
+  if (warp == 9)
     while (!mbar_try(mma_done, 0) && global_ns() - w0 < kWaitLimitNs) {
     }
-  if (threadIdx.x == 0 && *abort_flag)
+  if (threadIdx.x == 256 && *abort_flag)
     for (int i = max(flags[3] - kS, 0); i < flags[3]; ++i)
       while (!mbar_try(&full[i % kS], (i / kS) & 1) && global_ns() - w0 < kWaitLimitNs) {
       }
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }

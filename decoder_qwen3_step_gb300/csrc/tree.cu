@@ -243,7 +243,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
     for (int h = 0; h < c.n_kv_heads; ++h)
       for (int rt = 0; rt < rts; ++rt, done += tiles) {
         while (cta < P && begin(cta) < done + tiles) {
-          cut[cta] = {s, h, rt, (int)(begin(cta) - done), (int)(begin(cta + 1) - begin(cta)), 0, 0, 0};
+          cut[cta] = {s, h, rt, (int)(begin(cta) - done), (int)(begin(cta + 1) - begin(cta)), b->seq_start[s], T, b->ctx[s]};
           ++cta;
         }
         // the CTAs with a tile of this unit: c0 holds its first, c1 its last

@@ -23,7 +23,8 @@ enum TreeHdr { kHdrSeqs = 0, kHdrTokens, kHdrWords, kHdrRowTile, kHdrMerges, kHd
 // Attention work of one CTA: a contiguous range of key tiles in the order
 // (sequence, KV head, row tile, key tile); it starts at `tile` of this unit.
 struct TreeCut {
-  int32_t seq, head, row_tile, tile, count, pad0, pad1, pad2;
+  int32_t seq, head, row_tile, tile, count;
+  int32_t node0, nodes, ctx;  // of the sequence, to start without reading them from the arrays
 };
 // A unit (sequence, KV head, row tile) that CTAs c0 .. c1 share.
 struct TreeMerge {

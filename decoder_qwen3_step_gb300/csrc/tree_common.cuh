@@ -24,12 +24,15 @@ struct TreeUnit {
   int tiles;              // key tiles of ctx + nodes keys
 };
 
-__device__ __forceinline__ void tree_unit_load(const TreeMeta& m, int gs, int R, TreeUnit& u) {
-  u.node0 = __ldg(m.seq_start + u.seq);
-  u.nodes = __ldg(m.seq_start + u.seq + 1) - u.node0;
-  u.ctx = __ldg(m.ctx + u.seq);
+__device__ __forceinline__ void tree_unit_sizes(const TreeMeta& m, int gs, int R, TreeUnit& u) {
   u.tiles = (u.ctx + u.nodes + m.tile_keys - 1) / m.tile_keys;
   u.n_row_tiles = ((u.nodes << gs) + R - 1) / R;
+}
+// The unit a CTA starts with.
+__device__ __forceinline__ TreeUnit tree_unit_first(const TreeMeta& m, int gs, int R, const TreeCut& c) {
+  TreeUnit u{c.seq, c.head, c.row_tile, 0, c.node0, c.ctx, c.nodes, 0};
+  tree_unit_sizes(m, gs, R, u);
+  return u;
 }
 // The unit after u (sequences without nodes have none).
 __device__ __forceinline__ void tree_unit_next(const TreeMeta& m, int gs, int R, int Hkv, TreeUnit& u) {
@@ -40,7 +43,11 @@ __device__ __forceinline__ void tree_unit_next(const TreeMeta& m, int gs, int R,
   do {
     ++u.seq;
   } while (u.seq < m.S && __ldg(m.seq_start + u.seq + 1) == __ldg(m.seq_start + u.seq));
-  if (u.seq < m.S) tree_unit_load(m, gs, R, u);
+  if (u.seq >= m.S) return;
+  u.node0 = __ldg(m.seq_start + u.seq);
+  u.nodes = __ldg(m.seq_start + u.seq + 1) - u.node0;
+  u.ctx = __ldg(m.ctx + u.seq);
+  tree_unit_sizes(m, gs, R, u);
 }
 
 // Whether node `node` (numbered over the batch) sees node j of its sequence.
@@ -112,16 +119,16 @@ __device__ __forceinline__ float2 tree_pair<bf16>(uint32_t w) {
 
 // Load the queries of a unit's row tile as f16 into shared memory.  D/8 lanes
 // share a row (eight channels each), so a warp reads 32/(D/8) rows at a time
-// and has four such groups in flight; W warps split the rows.  The code has no
+// and has up to kMaxU such groups in flight; W warps split the rows.  The code has no
 // branch and no division per row: a first version with both, one row per warp
 // and step, took 0.7 us a row on instruction latency alone.
 // Each row is scaled by a power of two so that its largest magnitude lies in
 // [1, 2): f16 then rounds every channel by at most 2^-12 of that, whatever the
 // queries' range; fac[r] takes the row's score factor.  put(r, channel / 8,
 // eight halves).  Rows past the last are zeros.
-template <int D, int R, int W, typename T, typename F>
+template <int D, int R, int W, int kMaxU, typename T, typename F>
 __device__ __forceinline__ void tree_load_queries_of(const TreeAttendArgs& a, const TreeUnit& u, int w, float* fac, F&& put) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kSteps = R / (W * kRows), kU = kSteps < 4 ? kSteps : 4;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kSteps = R / (W * kRows), kU = kSteps < kMaxU ? kSteps : kMaxU;
   constexpr bool kWide = sizeof(T) == 4;
   static_assert(kSteps >= 1 && kSteps % kU == 0, "rows split evenly");
   const int lane = threadIdx.x & 31, x = lane % kLanes, gs = a.d.gs;
@@ -180,11 +187,11 @@ __device__ __forceinline__ void tree_load_queries_of(const TreeAttendArgs& a, co
     }
   }
 }
-template <int D, int R, int W, typename F>
+template <int D, int R, int W, int kMaxU, typename F>
 __device__ __forceinline__ void tree_load_queries(const TreeAttendArgs& a, const TreeUnit& u, int w, float* fac, F&& put) {
-  if (a.q_type == kTreeF32) tree_load_queries_of<D, R, W, float>(a, u, w, fac, put);
-  else if (a.q_type == kTreeF16) tree_load_queries_of<D, R, W, __half>(a, u, w, fac, put);
-  else tree_load_queries_of<D, R, W, bf16>(a, u, w, fac, put);
+  if (a.q_type == kTreeF32) tree_load_queries_of<D, R, W, kMaxU, float>(a, u, w, fac, put);
+  else if (a.q_type == kTreeF16) tree_load_queries_of<D, R, W, kMaxU, __half>(a, u, w, fac, put);
+  else tree_load_queries_of<D, R, W, kMaxU, bf16>(a, u, w, fac, put);
 }
 
 }  // namespace dec
