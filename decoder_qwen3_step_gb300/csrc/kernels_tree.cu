@@ -210,26 +210,25 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
   for (int w = blockIdx.x; w < n * groups; w += gridDim.x) {
     const TreeMerge e = a.m.merges[w / groups];
     const int r = (w % groups) * 4 + (threadIdx.x >> 5);
-    const int node0 = __ldg(a.m.seq_start + e.seq);
-    const int row = e.row_tile * R + r;
-    if (row >= (__ldg(a.m.seq_start + e.seq + 1) - node0) * G) continue;
-    const int node = node0 + (row >> gs);
-    auto rec = [&](int c) -> const float* { return tree_record(a, c, c == e.c0); };
+    const int row = e.row_tile * R + r, n_rec = (e.c1 - e.c0) / e.stride + 1;
+    if (row >= e.nodes << gs) continue;
+    const int node = e.node0 + (row >> gs);
+    auto rec = [&](int c) -> const float* { return tree_record(a, e.c0 + c * e.stride, c == 0); };
     float M = -INFINITY;
-    for (int c = e.c0 + lane; c <= e.c1; c += 32) M = fmaxf(M, __ldcg(rec(c) + R * D + r));
+    for (int c = lane; c < n_rec; c += 32) M = fmaxf(M, __ldcg(rec(c) + R * D + r));
     M = warp_max(M);
     if (M == -INFINITY) M = 0.f;  // no contribution saw a finite score
     float L = 0.f, o[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-    for (int c0 = e.c0; c0 <= e.c1; c0 += 32) {
+    for (int c0 = 0; c0 < n_rec; c0 += 32) {
       float f = 0.f;
-      if (c0 + lane <= e.c1) {
+      if (c0 + lane < n_rec) {
         const float* p = rec(c0 + lane) + R * D;
         f = ex2(__ldcg(p + r) - M);
         L = fmaf(__ldcg(p + R + r), f, L);
       }
-      const int m = min(32, e.c1 - c0 + 1);
+      const int m = min(32, n_rec - c0);
 #pragma unroll 4
       for (int i = 0; i < m; ++i) {
         const float fi = __shfl_sync(0xffffffffu, f, i);
@@ -261,54 +260,61 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
   }
 }
 
-// The same for the 128-row tiles of wide trees, whose records are channel-major
-// ([D][128], then maxima and sums): thread = row, kMergeChannels channels per
-// block, so the reads are whole lines.
-template <int D, int kMergeChannels>
+// The same for the row tiles of wide trees (128 or 256 rows), whose records
+// are channel-major ([D/4][R] of four channels, then maxima and sums): thread =
+// row, kC channels per block, so the reads are whole lines.
+template <int D, int kC>
 __global__ void __launch_bounds__(128) k_tree_merge_wide(const __grid_constant__ TreeAttendArgs a) {
   pdl_wait_prev();
   pdl_launch_next();
   if (!tree_shape_ok(a.m, true)) return;
-  constexpr int R = 128, kSlabs = D / kMergeChannels;
-  const int gs = a.d.gs, r = threadIdx.x;
+  constexpr int kSlabs = D / kC;
+  const int gs = a.d.gs, R = a.m.row_tile, per = kSlabs * (R / 128);
   const int n = __ldg(a.m.hdr + kHdrMerges);
-  for (int w = blockIdx.x; w < n * kSlabs; w += gridDim.x) {
-    const TreeMerge e = a.m.merges[w / kSlabs];
-    const int d0 = (w % kSlabs) * kMergeChannels, row = e.row_tile * R + r;
-    const int node0 = __ldg(a.m.seq_start + e.seq);
-    if (row >= (__ldg(a.m.seq_start + e.seq + 1) - node0) << gs) continue;
-    const int node = node0 + (row >> gs);
-    auto rec = [&](int c) -> const float* { return tree_record(a, c, c == e.c0); };
+  for (int w = blockIdx.x; w < n * per; w += gridDim.x) {
+    const TreeMerge e = a.m.merges[w / per];
+    const int d0 = (w % kSlabs) * kC, r = (w % per) / kSlabs * 128 + threadIdx.x, row = e.row_tile * R + r;
+    if (row >= e.nodes << gs) continue;
+    const int node = e.node0 + (row >> gs), n_rec = (e.c1 - e.c0) / e.stride + 1;
+    auto rec = [&](int c) -> const float* { return tree_record(a, e.c0 + c * e.stride, c == 0); };
     float M = -INFINITY;
 #pragma unroll 8
-    for (int c = e.c0; c <= e.c1; ++c) M = fmaxf(M, __ldcg(rec(c) + R * D + r));
+    for (int c = 0; c < n_rec; ++c) M = fmaxf(M, __ldcg(rec(c) + R * D + r));
     if (M == -INFINITY) M = 0.f;  // no contribution saw a finite score
-    float L = 0.f, o[kMergeChannels];
+    float L = 0.f;
+    float4 o[kC / 4];
 #pragma unroll
-    for (int i = 0; i < kMergeChannels; ++i) o[i] = 0.f;
-#pragma unroll kMergeChannels == 4 ? 8 : 2
-    for (int c = e.c0; c <= e.c1; ++c) {
+    for (int i = 0; i < kC / 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll kC == 4 ? 8 : 2
+    for (int c = 0; c < n_rec; ++c) {
       const float* p = rec(c);
       const float f = ex2(__ldcg(p + R * D + r) - M);
       L = fmaf(__ldcg(p + R * D + R + r), f, L);
 #pragma unroll
-      for (int i = 0; i < kMergeChannels; ++i) o[i] = fmaf(__ldcg(p + (d0 + i) * R + r), f, o[i]);
+      for (int i = 0; i < kC / 4; ++i) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + (d0 / 4 + i) * R + r);
+        o[i].x = fmaf(v.x, f, o[i].x);
+        o[i].y = fmaf(v.y, f, o[i].y);
+        o[i].z = fmaf(v.z, f, o[i].z);
+        o[i].w = fmaf(v.w, f, o[i].w);
+      }
     }
     const bool zero = __ldg(a.m.pos + node) < 0 || L == 0.f;
     const float inv = 1.0f / L;
     const int64_t off = node * a.ldo + (int64_t)((e.head << gs) + (row & ((1 << gs) - 1))) * D + d0;
 #pragma unroll
-    for (int i = 0; i < kMergeChannels; i += 4)
-      tree_store4(a.out, a.out_type, off + i,
-                  zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv));
+    for (int i = 0; i < kC / 4; ++i)
+      tree_store4(a.out, a.out_type, off + 4 * i,
+                  zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv));
   }
 }
 
 template <int D>
 cudaError_t merge_wide(const TreeAttendArgs& a, int n_merges, cudaStream_t s) {
   // few units share their keys among many CTAs: four channels per block, or too few blocks read all those records
-  if (n_merges < 64) return launch_pdl(k_tree_merge_wide<D, 4>, n_merges * (D / 4), 128, 0, s, a);
-  return launch_pdl(k_tree_merge_wide<D, 16>, n_merges * (D / 16), 128, 0, s, a);
+  const int halves = a.m.row_tile / 128;
+  if (n_merges < 64) return launch_pdl(k_tree_merge_wide<D, 4>, n_merges * halves * (D / 4), 128, 0, s, a);
+  return launch_pdl(k_tree_merge_wide<D, 16>, n_merges * halves * (D / 16), 128, 0, s, a);
 }
 
 }  // namespace
@@ -335,7 +341,7 @@ cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s) {
 
 cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, cudaStream_t s) {
   // a replayed call may meet a plan with more merges than at its capture: the blocks loop
-  if (a.m.row_tile == 128) {
+  if (a.m.row_tile >= 128) {
     return a.d.D == 128 ? merge_wide<128>(a, max(n_merges, 1), s) : merge_wide<64>(a, max(n_merges, 1), s);
   }
   const int grid = max(n_merges, 1) * (a.m.row_tile / 4);

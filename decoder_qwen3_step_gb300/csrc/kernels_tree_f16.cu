@@ -84,14 +84,14 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
   volatile int* abort_flag = flags;
   const int gs = a.d.gs, G = 1 << gs;
   const TreeCut cut = a.m.cuts[blockIdx.x];
-  TreeUnit u = tree_unit_first(a.m, gs, R, cut);
+  TreeUnit u = tree_unit_first(a.m, cut);
   int tile = cut.tile, k = 0;
 
   if (warp == 4) {
     // ---- producer: lanes 0..3 copy one block each; table entries come 8 tiles at a time ----
     for (int left = cut.count; left > 0;) {
       const int t0 = tile, t1 = min(u.tiles, tile + left), blocks = (u.ctx + u.nodes + 15) >> 4;
-      const int32_t* table = a.m.tables + __ldg(a.m.tab_start + u.seq);
+      const int32_t* table = a.m.tables + u.tab;
       auto entries = [&](int t) {
         const int b = t * 4 + lane;
         int blk = b < blocks && b < t1 * 4 ? __ldg(table + b) : 0;
@@ -140,9 +140,9 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
       const int t0 = tile, t1 = min(u.tiles, tile + left), end = u.ctx + u.nodes;
       const int rows = min(R, u.nodes * G - u.row_tile * R);
       if constexpr (R / 4 >= 32 / (D / 8)) {
-        tree_load_queries<D, R, 4, 4>(a, u, warp, fac, [&](int r, int x, uint4 h) { *reinterpret_cast<uint4*>(Qs + r * SM::kQPitch + x * 16) = h; });
+        tree_load_queries<D, R, 4, 4>(a, u, u.row_tile * R, warp, fac, [&](int r, int x, uint4 h) { *reinterpret_cast<uint4*>(Qs + r * SM::kQPitch + x * 16) = h; });
       } else if (warp < 2) {  // D = 32, R = 16: a warp reads eight rows at a time
-        tree_load_queries<D, R, 2, 4>(a, u, warp, fac, [&](int r, int x, uint4 h) { *reinterpret_cast<uint4*>(Qs + r * SM::kQPitch + x * 16) = h; });
+        tree_load_queries<D, R, 2, 4>(a, u, u.row_tile * R, warp, fac, [&](int r, int x, uint4 h) { *reinterpret_cast<uint4*>(Qs + r * SM::kQPitch + x * 16) = h; });
       }
       group_bar();
       const uint32_t qb = smem_u32(Qs) + (lane & 15) * SM::kQPitch + (lane >> 4) * 16;
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
             v.w += y.w;
           }
           if (odd) {  // rare: the values that were taken out, for the rows that see them
-            const int32_t* table = a.m.tables + __ldg(a.m.tab_start + u.seq);
+            const int32_t* table = a.m.tables + u.tab;
             for (int n = j0; n < j1; ++n) {
               if (!tree_sees(a.m, node, n)) continue;
               const int p = u.ctx + n;

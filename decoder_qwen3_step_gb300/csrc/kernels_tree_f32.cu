@@ -50,12 +50,12 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int gs = a.d.gs, G = 1 << gs;
   TreeCut cut = a.m.cuts[blockIdx.x];
-  TreeUnit u = tree_unit_first(a.m, gs, R, cut);
+  TreeUnit u = tree_unit_first(a.m, cut);
   int tile = cut.tile;
 
   for (int left = cut.count; left > 0;) {
     const int t0 = tile, t1 = min(u.tiles, tile + left), end = u.ctx + u.nodes;
-    const int32_t* table = a.m.tables + __ldg(a.m.tab_start + u.seq);
+    const int32_t* table = a.m.tables + u.tab;
     auto load = [&](float* dst, int pitch, int t, int is_v) {
 #pragma unroll
       for (int i = tid; i < kTreeKeys * (D / 4); i += 256) {

@@ -1,23 +1,25 @@
 // kernels_tree_tc.cu - tree attention over an f16 cache for wide trees, on the
 // 5th-generation tensor cores (tcgen05, accumulators in TMEM).
 //
-// The same formula as kernels_tree_f16.cu with 128 rows (nodes x query heads
-// of one KV head) and 128 keys per step, one CTA per SM:
+// The same formula as kernels_tree_f16.cu with 128 keys and 128 or 256 rows
+// (nodes x query heads of one KV head) per step, one CTA per SM:
+//   warps 0..7    two softmax groups of 128 threads, each with its own S and O
+//                 in TMEM: thread = row = TMEM lane.  S is read from TMEM, the
+//                 weights go back as f16 over the first half of its columns; a
+//                 row's maximum and sum never leave their thread
 //   warp 8        TMA producer: K and V tiles as 64-channel panels of 128 keys
 //                 in 128-byte swizzled rows (one box per block and panel), into
 //                 a ring of tile slots, K and V of a tile one after the other
 //   warp 9        issues S = Q K^T (both operands K-major in shared memory) and
 //                 O += P V (P from TMEM, V as a channel-major operand: its
-//                 panels are read transposed by the MMA itself); S of the next
-//                 tile is issued before P V of this one, so the tensor pipe
-//                 works while a softmax runs
-//   warps 0..7    two softmax groups that take the tiles in turn, each with its
-//                 own S, O, maxima and sums: thread = row = TMEM lane.  S is read
-//                 from TMEM, the weights go back as f16 over the first half of
-//                 its columns; a row's maximum and sum never leave their thread.
-//                 At a unit's end the two halves are joined, each group for half
-//                 of the channels
-//   warps 10, 11  the next unit's queries into the other of two buffers
+//                 panels are read transposed by the MMA itself), always with a
+//                 group's next S queued while the other group's softmax runs
+//   warps 10, 11  narrow: the next unit's queries into the other of two buffers
+// Narrow (up to 128 rows): the groups take the key tiles of the same rows in
+// turn and join their halves at the unit's end, each for half of the channels.
+// Wide: group b takes rows 128 b .. 128 b + 127 of every tile, so a tile's bytes
+// serve 256 rows; with narrow units 8 x 256 nodes at contexts of 8000 read
+// every key four times and ran at HBM speed, 211 us against 64 for the products.
 // O is rescaled in TMEM only when a row's scores exceed its maximum by 2^8
 // (exact: numerator and denominator share the maximum).  Warps whose rows are
 // all behind the last skip the softmax.  Roundings as in kernels_tree_f16.cu.
@@ -39,10 +41,11 @@ struct TcSmem {
   static constexpr int kPanel = kTK * 128;            // bytes of 64 channels of 128 keys (or rows)
   static constexpr int kTile = kPanels * kPanel;
   static constexpr int kSlots = D == 128 ? 5 : 10;    // of the ring; at least K, V, K are in use at once
-  static constexpr int kQ = 0, kRing = 2 * kTile, kFac = kRing + kSlots * kTile;  // fac: float [2][kTR]
+  static constexpr int kQ = 0;                        // two tiles: the units' in turn (narrow), the groups' (wide)
+  static constexpr int kRing = 2 * kTile, kFac = kRing + kSlots * kTile;  // fac: float [2][kTR], as the queries
   static constexpr int kBar = kFac + 2 * kTR * 4;
-  // barriers: full, empty [slots]; Q full, Q empty, S full, P full [2]; O full, O empty, MMA done
-  static constexpr int kBars = 2 * kSlots + 8 + 3;
+  // barriers: full, empty [slots]; Q full, Q empty, S full, P full, O full, O empty [2]; MMA done
+  static constexpr int kBars = 2 * kSlots + 13;
   static constexpr int kBytes = kBar + kBars * 8 + 32;
 };
 
@@ -125,16 +128,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
   return r;
 }
 
-template <int D>
+template <int D, bool kWide>
 __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __grid_constant__ CUtensorMap tm,
                                                                       const __grid_constant__ TreeAttendArgs a) {
   using SM = TcSmem<D>;
-  constexpr int kS = SM::kSlots;
+  constexpr int kS = SM::kSlots, kR = kWide ? 2 * kTR : kTR;
   extern __shared__ __align__(1024) uint8_t dsm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(dsm + SM::kBar);
   uint64_t *full = bars, *empty = bars + kS, *qfull = bars + 2 * kS, *qempty = qfull + 2, *sfull = qfull + 4,
-           *pfull = qfull + 6, *ofull = qfull + 8, *oempty = qfull + 9, *mma_done = qfull + 10;
-  int* flags = reinterpret_cast<int*>(bars + SM::kBars);  // [0] abort, [1] odd values, [2] TMEM base, [3] slots filled
+           *pfull = qfull + 6, *ofull = qfull + 8, *oempty = qfull + 10, *mma_done = qfull + 12;
+  // [0] abort, [1] TMEM base, [2] slots filled, [4 + i] 1 + the unit (of parity i) that met a value that is not finite
+  int* flags = reinterpret_cast<int*>(bars + SM::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kS; ++i) {
@@ -142,15 +146,15 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&qfull[i], 320);
+      mbar_init(&qfull[i], kWide ? 128 : 320);
       mbar_init(&qempty[i], 256);
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 128);
+      mbar_init(&ofull[i], 1);
+      mbar_init(&oempty[i], kWide ? 128 : 256);
     }
-    mbar_init(ofull, 1);
-    mbar_init(oempty, 256);
     mbar_init(mma_done, 1);
-    flags[0] = flags[1] = flags[3] = 0;
+    for (int i = 0; i < 8; ++i) flags[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -158,26 +162,28 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   pdl_launch_next();
   if (!tree_shape_ok(a.m, true)) return;
   if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(flags + 2)), "r"(kTmemCols)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(flags + 1)), "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags + 2);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags + 1);
   volatile int* abort_flag = flags;
   const int gs = a.d.gs, G = 1 << gs;
   const TreeCut cut = a.m.cuts[blockIdx.x];
-  TreeUnit u = tree_unit_first(a.m, gs, kTR, cut);
+  TreeUnit u = tree_unit_first(a.m, cut);
   int tile = cut.tile, n_unit = 0;
+  // a wide unit with at most 128 rows leaves the second group out
+  auto both = [&](const TreeUnit& x) { return (x.nodes << gs) - x.row_tile * kR > kTR; };
 
   if (warp == 8) {
     // ---- producer: lane = (panel, block) for K, then for V ----
     int li = 0;  // loads so far: K of tile k is load 2k, V is 2k + 1
     for (int left = cut.count; left > 0;) {
       const int t0 = tile, t1 = min(u.tiles, tile + left), blocks = (u.ctx + u.nodes + 15) >> 4;
-      const int32_t* table = a.m.tables + __ldg(a.m.tab_start + u.seq);
+      const int32_t* table = a.m.tables + u.tab;
       auto entry = [&](int t) {
         const int b = t * 8 + (lane & 7);
         int blk = b < blocks && t < t1 ? __ldg(table + b) : 0;
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           if (!__shfl_sync(0xffffffffu, (int)ok, 0)) goto produced;
           if (lane == 0) {
             mbar_expect_tx(&full[slot], bytes);
-            flags[3] = li + 1;
+            flags[2] = li + 1;
           }
           __syncwarp();
           if (panel < SM::kPanels && (lane & 7) < here)
@@ -214,119 +220,178 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       }
       left -= t1 - t0;
       tile = 0;
-      if (left > 0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, u);
+      if (left > 0) tree_unit_next(a.m, gs, kR, a.d.Hkv, u);
     }
   produced:;
   } else if (warp == 9) {
     // ---- MMA issuer ----
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_f16(kTR, kTK, false), id_o = idesc_f16(kTR, D, true);
+      // a step along K only moves the descriptors' start addresses (their low bits, in 16-byte units)
       const uint64_t q_desc = sw128_desc(smem_u32(dsm + SM::kQ)), ring_desc = sw128_desc(smem_u32(dsm + SM::kRing));
       const uint64_t v_desc = sw128_mn_desc(smem_u32(dsm + SM::kRing), SM::kPanel);
-      auto issue_s = [&](int k, bool first, int unit) -> bool {
-        const int li = 2 * k, slot = li % kS, b = k & 1;
-        if (first && !mbar_wait(&qfull[unit & 1], (unit >> 1) & 1, abort_flag, a.m.err)) return false;
+      // scores of tile k into group b's S, from query tile q
+      auto scores = [&](int k, int b, int q, bool last) -> bool {
+        const int li = 2 * k, slot = li % kS;
         if (!mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err)) return false;
         tc_fence_after();
-        // a step along K only moves the descriptors' start addresses (their low bits, in 16-byte units)
-        const uint64_t qd = q_desc + (unit & 1) * (SM::kTile >> 4), kd = ring_desc + slot * (SM::kTile >> 4);
+        const uint64_t qd = q_desc + q * (SM::kTile >> 4), kd = ring_desc + slot * (SM::kTile >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint32_t off = ((i >> 2) * SM::kPanel + (i & 3) * 32) >> 4;
           tc_mma(tmem + b * 128, qd + off, kd + off, id_s, i != 0);
         }
-        tc_commit(&empty[slot]);
+        if (last) tc_commit(&empty[slot]);
         tc_commit(&sfull[b]);
         return true;
       };
-      int k = 0;
-      bool ok = cut.count == 0 || issue_s(0, true, 0);
-      for (int left = cut.count; ok && left > 0; ++n_unit) {
-        const int t0 = tile, t1 = min(u.tiles, tile + left);
-        TreeUnit nu = u;
-        if (left > t1 - t0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, nu);
-        if (n_unit > 0 && !mbar_wait(oempty, (n_unit - 1) & 1, abort_flag, a.m.err)) break;
-        int fresh = 3;  // groups whose O this unit has not written yet
-        for (int t = t0; t < t1; ++t, ++k) {
-          const int li = 2 * k + 1, slot = li % kS, b = k & 1;
-          // the next tile's scores first: of this unit, or of the next one
-          if (k + 1 < cut.count && !(ok = issue_s(k + 1, t + 1 == t1, n_unit + (t + 1 == t1)))) break;
-          if (!(ok = mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err))) break;
-          if (!(ok = mbar_wait(&pfull[b], (k >> 1) & 1, abort_flag, a.m.err))) break;
-          tc_fence_after();
-          const uint64_t vd = v_desc + slot * (SM::kTile >> 4);
+      auto values = [&](int k, int b, int n, bool fresh, bool last) -> bool {
+        const int li = 2 * k + 1, slot = li % kS;
+        if (!mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err)) return false;
+        if (!mbar_wait(&pfull[b], n & 1, abort_flag, a.m.err)) return false;
+        tc_fence_after();
+        const uint64_t vd = v_desc + slot * (SM::kTile >> 4);
 #pragma unroll
-          for (int i = 0; i < kTK / 16; ++i)
-            tc_mma_ts(tmem + 256 + b * D, tmem + b * 128 + i * 8, vd + i * (2048 >> 4), id_o,
-                      i != 0 || !((fresh >> b) & 1));
-          fresh &= ~(1 << b);
-          tc_commit(&empty[slot]);
+        for (int i = 0; i < kTK / 16; ++i)
+          tc_mma_ts(tmem + 256 + b * D, tmem + b * 128 + i * 8, vd + i * (2048 >> 4), id_o, i != 0 || !fresh);
+        if (last) tc_commit(&empty[slot]);
+        return true;
+      };
+      int k = 0;
+      if constexpr (!kWide) {
+        auto first_scores = [&](int x, int unit, bool first) -> bool {
+          if (first && !mbar_wait(&qfull[unit & 1], (unit >> 1) & 1, abort_flag, a.m.err)) return false;
+          return scores(x, x & 1, unit & 1, true);
+        };
+        bool ok = cut.count == 0 || first_scores(0, 0, true);
+        for (int left = cut.count; ok && left > 0; ++n_unit) {
+          const int t0 = tile, t1 = min(u.tiles, tile + left);
+          if (n_unit > 0 && !mbar_wait(&oempty[0], (n_unit - 1) & 1, abort_flag, a.m.err)) break;
+          int fresh = 3;  // groups whose O this unit has not written yet
+          for (int t = t0; ok && t < t1; ++t, ++k) {
+            const int b = k & 1;
+            // the next tile's scores first: of this unit, or of the next one
+            ok = (k + 1 >= cut.count || first_scores(k + 1, n_unit + (t + 1 == t1), t + 1 == t1)) &&
+                 values(k, b, k >> 1, (fresh >> b) & 1, true);
+            fresh &= ~(1 << b);
+          }
+          if (!ok) break;
+          tc_commit(&ofull[0]);
+          left -= t1 - t0;
+          tile = 0;
+          if (left > 0) tree_unit_next(a.m, gs, kR, a.d.Hkv, u);
         }
-        if (!ok) break;
-        tc_commit(ofull);
-        left -= t1 - t0;
-        tile = 0;
-        u = nu;
+      } else {
+        int n[2] = {0, 0}, units[2] = {0, 0};  // tiles and units of each group
+        auto first_scores = [&](int x, int b, const TreeUnit& v, bool first) -> bool {
+          if (b && !both(v)) return true;
+          if (first && !mbar_wait(&qfull[b], units[b] & 1, abort_flag, a.m.err)) return false;
+          return scores(x, b, b, b || !both(v));
+        };
+        bool ok = cut.count == 0 || (first_scores(0, 0, u, true) && first_scores(0, 1, u, true));
+        for (int left = cut.count; ok && left > 0;) {
+          const int t0 = tile, t1 = min(u.tiles, tile + left), groups = both(u) ? 2 : 1;
+          for (int b = 0; ok && b < groups; ++b)
+            if (units[b] > 0) ok = mbar_wait(&oempty[b], (units[b] - 1) & 1, abort_flag, a.m.err);
+          for (int t = t0; ok && t < t1; ++t, ++k) {
+            for (int b = 0; ok && b < groups; ++b) {
+              ok = values(k, b, n[b]++, t == t0, b == groups - 1);
+              if (t + 1 < t1) ok = ok && first_scores(k + 1, b, u, false);
+              else tc_commit(&ofull[b]);
+            }
+          }
+          if (!ok) break;
+          for (int b = 0; b < groups; ++b) ++units[b];
+          left -= t1 - t0;
+          tile = 0;
+          if (left > 0) {
+            tree_unit_next(a.m, gs, kR, a.d.Hkv, u);
+            ok = first_scores(k, 0, u, true) && first_scores(k, 1, u, true);
+          }
+        }
       }
       tc_commit(mma_done);
     }
     __syncwarp();
   } else if (warp >= 10) {
-    // ---- queries: one unit ahead (the first unit's by the softmax warps, which have nothing else to do yet) ----
-    for (int left = cut.count; left > 0; ++n_unit) {
+    // ---- queries one unit ahead (the first unit's by the softmax warps, which have nothing else to do yet) ----
+    for (int left = kWide ? 0 : cut.count; left > 0; ++n_unit) {
       const int b = n_unit & 1;
       if (!__all_sync(0xffffffffu, n_unit < 2 || mbar_wait(&qempty[b], ((n_unit >> 1) - 1) & 1, abort_flag, a.m.err))) break;
-      if (n_unit > 0) tree_load_queries<D, kTR, 2, 4>(a, u, warp - 10, reinterpret_cast<float*>(dsm + SM::kFac) + b * kTR, [&](int q, int x, uint4 h) {
-        *reinterpret_cast<uint4*>(dsm + SM::kQ + b * SM::kTile + (x >> 3) * SM::kPanel + q * 128 + (((x & 7) ^ (q & 7)) << 4)) = h;
-      });
+      if (n_unit > 0)
+        tree_load_queries<D, kTR, 2, 4>(a, u, u.row_tile * kTR, warp - 10, reinterpret_cast<float*>(dsm + SM::kFac) + b * kTR, [&](int q, int x, uint4 h) {
+          *reinterpret_cast<uint4*>(dsm + SM::kQ + b * SM::kTile + (x >> 3) * SM::kPanel + q * 128 + (((x & 7) ^ (q & 7)) << 4)) = h;
+        });
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&qfull[b]);
       left -= min(u.tiles, tile + left) - tile;
       tile = 0;
-      if (left > 0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, u);
+      if (left > 0) tree_unit_next(a.m, gs, kR, a.d.Hkv, u);
     }
   } else {
-    // ---- softmax: thread = row; group b takes the tiles k with k % 2 == b ----
+    // ---- softmax ----
     const int b = warp >> 2, wr = (warp & 3) * 32, r = wr + lane, st = threadIdx.x & 127;
+    const int row_in = (kWide ? b * kTR : 0) + r;  // row of the unit
     const uint32_t trow = tmem + ((uint32_t)wr << 16), ts = trow + b * 128, to = trow + 256 + b * D;
-    int k = 0;
-    bool alive = true;
-    if (cut.count > 0) {
-      tree_load_queries<D, kTR, 8, 8>(a, u, warp, reinterpret_cast<float*>(dsm + SM::kFac), [&](int q, int x, uint4 h) {
-        *reinterpret_cast<uint4*>(dsm + SM::kQ + (x >> 3) * SM::kPanel + q * 128 + (((x & 7) ^ (q & 7)) << 4)) = h;
+    float* fac = reinterpret_cast<float*>(dsm + SM::kFac);
+    auto group_bar = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(2 + b) : "memory"); };
+    // wide: this group's queries of unit x
+    auto load_group = [&](const TreeUnit& x) {
+      tree_load_queries<D, kTR, 4, 8>(a, x, x.row_tile * kR + b * kTR, warp & 3, fac + b * kTR, [&](int q, int c, uint4 h) {
+        *reinterpret_cast<uint4*>(dsm + SM::kQ + b * SM::kTile + (c >> 3) * SM::kPanel + q * 128 + (((c & 7) ^ (q & 7)) << 4)) = h;
       });
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&qfull[0]);
+      mbar_arrive(&qfull[b]);
+    };
+    int k = 0, n = 0, units = 0;  // tiles; of this group: tiles and units
+    bool alive = true;
+    if (cut.count > 0) {
+      if constexpr (kWide) {
+        if (b == 0 || both(u)) load_group(u);
+      } else {
+        tree_load_queries<D, kTR, 8, 8>(a, u, u.row_tile * kTR, warp, fac, [&](int q, int x, uint4 h) {
+          *reinterpret_cast<uint4*>(dsm + SM::kQ + (x >> 3) * SM::kPanel + q * 128 + (((x & 7) ^ (q & 7)) << 4)) = h;
+        });
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(&qfull[0]);
+      }
     }
     for (int left = cut.count; left > 0; ++n_unit) {
       const int t0 = tile, t1 = min(u.tiles, tile + left), end = u.ctx + u.nodes, k0 = k;
-      const int rows = min(kTR, u.nodes * G - u.row_tile * kTR);
-      const bool mine = wr < rows;  // some row of this warp is one
-      const int node = u.node0 + min((u.row_tile * kTR + r) >> gs, u.nodes - 1);
+      const int row = u.row_tile * kR + row_in, all_rows = u.nodes << gs;
+      const bool mine = row - lane < all_rows;  // some row of this warp is one
+      const bool in = !kWide || b == 0 || both(u);
+      const int node = u.node0 + min(row >> gs, u.nodes - 1);
       const uint32_t* anc = a.m.anc + (size_t)node * a.m.words;
-      TreeUnit nu = u;  // its arrays are read now: at the unit's end nothing else would cover that
-      if (left > t1 - t0) tree_unit_next(a.m, gs, kTR, a.d.Hkv, nu);
-      alive = __all_sync(0xffffffffu, alive && mbar_wait(&qfull[n_unit & 1], (n_unit >> 1) & 1, abort_flag, a.m.err));
-      const float c = reinterpret_cast<const float*>(dsm + SM::kFac)[(n_unit & 1) * kTR + r];
-      mbar_arrive(&qfull[(n_unit + 1) & 1]);  // the next unit's queries come from the other warps alone
-      float m = -INFINITY, l = 0.f;
+      float c = 0.f, m = -INFINITY, l = 0.f;
+      if (in) {
+        if constexpr (kWide) {
+          group_bar();  // the factors of the group's queries
+          c = fac[b * kTR + r];
+        } else {
+          alive = __all_sync(0xffffffffu, alive && mbar_wait(&qfull[n_unit & 1], (n_unit >> 1) & 1, abort_flag, a.m.err));
+          c = fac[(n_unit & 1) * kTR + r];
+          mbar_arrive(&qfull[(n_unit + 1) & 1]);  // the next unit's queries come from the other warps alone
+        }
+      }
       bool first = true;
       for (int t = t0; t < t1; ++t, ++k) {
-        if ((k & 1) != b) continue;
+        if (!in || (!kWide && (k & 1) != b)) continue;
         const int key0 = t * kTK;
         const bool drafted = key0 + kTK > u.ctx;
         uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};  // keys of each 32 that this row sees
         if (drafted) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int n = key0 + j * 32 - u.ctx;  // node number of the first; negative: cached tokens
-            const int w = n >> 5;
-            const uint32_t lo = n > -32 && w < a.m.words ? (w < 0 ? 0xffffffffu : __ldg(anc + w)) : 0u;
-            const uint32_t hi = n > -32 && w + 1 < a.m.words ? __ldg(anc + w + 1) : 0u;
-            if (n > -32) vis[j] = __funnelshift_r(lo, hi, n & 31);
+            const int x = key0 + j * 32 - u.ctx;  // node number of the first; negative: cached tokens
+            const int w = x >> 5;
+            const uint32_t lo = x > -32 && w < a.m.words ? (w < 0 ? 0xffffffffu : __ldg(anc + w)) : 0u;
+            const uint32_t hi = x > -32 && w + 1 < a.m.words ? __ldg(anc + w + 1) : 0u;
+            if (x > -32) vis[j] = __funnelshift_r(lo, hi, x & 31);
           }
           // value rows past the end hold anything, a node's value that is not finite must not meet another branch's
-          // zero weights: zero them; its descendants get it back at the unit's end.  Eight threads per row
+          // zero weights: zero them; its descendants get it back at the unit's end.  Eight threads per row.  (Wide: both
+          // groups do this for the tile, whichever comes first changes it)
           const int li = 2 * k + 1, slot = li % kS;
           alive = __all_sync(0xffffffffu, alive && mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err));
           for (int q = max(u.ctx - key0, 0) + (st >> 3); alive && q < kTK; q += 16) {
@@ -343,7 +408,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
                 if (mk) {
                   w[z] &= ~mk;
                   change = true;
-                  flags[1] = 1;
+                  flags[4 + (n_unit & 1)] = n_unit + 1;
                 }
               }
               if (change) *at = x;
@@ -351,7 +416,8 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        alive = __all_sync(0xffffffffu, alive && mbar_wait(&sfull[b], (k >> 1) & 1, abort_flag, a.m.err));
+        alive = __all_sync(0xffffffffu, alive && mbar_wait(&sfull[b], n & 1, abort_flag, a.m.err));
+        ++n;
         if (alive && mine) {
           tc_fence_after();
           float mx = -INFINITY;
@@ -425,80 +491,101 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
         first = false;
         mbar_arrive(&pfull[b]);
       }
-      // ---- the unit's end: the two groups joined, this group for channels b D/2 .. (b + 1) D/2 - 1 ----
-      alive = __all_sync(0xffffffffu, alive && mbar_wait(ofull, n_unit & 1, abort_flag, a.m.err));
-      float2* ml = reinterpret_cast<float2*>(dsm + SM::kQ + (n_unit & 1) * SM::kTile);  // the queries are done with
-      ml[b * kTR + r] = make_float2(m, l);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (alive && mine) {
-        tc_fence_after();
+      TreeUnit nu = u;
+      if (left > t1 - t0) tree_unit_next(a.m, gs, kR, a.d.Hkv, nu);
+      if constexpr (kWide) {
+        // this group's S of the unit's last tile is there, so its queries are done with: the next unit's, if it takes part
+        if (in) group_bar();  // every factor has been read
+        if (left > t1 - t0 && (b == 0 || both(nu))) load_group(nu);
+      }
+      // ---- the unit's end ----
+      float L = l, M = m, g0 = 1.f, g1 = 0.f;
+      bool has0 = true, has1 = false;
+      if (in) alive = __all_sync(0xffffffffu, alive && mbar_wait(&ofull[kWide ? b : 0], units & 1, abort_flag, a.m.err));
+      if constexpr (!kWide) {
+        // join the two groups, this one for channels b D/2 .. (b + 1) D/2 - 1
+        float2* ml = reinterpret_cast<float2*>(dsm + SM::kQ + (n_unit & 1) * SM::kTile);  // the queries are done with
+        ml[b * kTR + r] = make_float2(m, l);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
         const float2 s0 = ml[r], s1 = ml[kTR + r];
-        const bool has0 = t1 - t0 > 1 || (k0 & 1) == 0, has1 = t1 - t0 > 1 || (k0 & 1) == 1;
-        const float M = fmaxf(s0.x, s1.x), mu = M == -INFINITY ? 0.f : M;
-        const float f0 = has0 ? ex2(s0.x - mu) : 0.f, f1 = has1 ? ex2(s1.x - mu) : 0.f;
-        const float L = s0.y * f0 + s1.y * f1;
-        const bool odd = *reinterpret_cast<volatile int*>(flags + 1) != 0, whole = t0 == 0 && t1 == u.tiles;
+        has0 = t1 - t0 > 1 || (k0 & 1) == 0;
+        has1 = t1 - t0 > 1 || (k0 & 1) == 1;
+        M = fmaxf(s0.x, s1.x);
+        const float mu = M == -INFINITY ? 0.f : M;
+        g0 = has0 ? ex2(s0.x - mu) : 0.f;
+        g1 = has1 ? ex2(s1.x - mu) : 0.f;
+        L = s0.y * g0 + s1.y * g1;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        mbar_arrive(&qempty[n_unit & 1]);
+      }
+      if (in && alive && mine) {
+        tc_fence_after();
+        const bool odd = reinterpret_cast<volatile int*>(flags)[4 + (n_unit & 1)] == n_unit + 1;
+        const bool whole = t0 == 0 && t1 == u.tiles, valid = row < all_rows;
         float* rec = tree_record(a, blockIdx.x, t0 == 0);
-        const int row = u.row_tile * kTR + r;
         const int j0 = max(t0 * kTK - u.ctx, 0), j1 = min(t1 * kTK - u.ctx, u.nodes);
         const bool zero = L == 0.f || __ldg(a.m.pos + node) < 0;
-        const float inv = whole ? 1.0f / L : 1.0f, g0 = f0 * inv, g1 = f1 * inv;
-        const int64_t off = node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D;
+        if (whole) {
+          const float inv = 1.0f / L;
+          g0 *= inv;
+          g1 *= inv;
+        }
+        const int64_t off = node * a.ldo + (int64_t)((u.head << gs) + (row & (G - 1))) * D;
+        const int ch0 = kWide ? 0 : b * (D / 2), ch1 = kWide ? D : (b + 1) * (D / 2);
+        const uint32_t o0 = kWide ? to : trow + 256, o1 = trow + 256 + D;
 #pragma unroll 1
-        for (int ch = b * (D / 2); ch < (b + 1) * (D / 2); ch += 32) {
-          uint32_t x[32], y[32];
-          if (has0) tc_ld32(trow + 256 + ch, x);
-          if (has1) tc_ld32(trow + 256 + D + ch, y);
-          if (r < rows) {
-            float v[32];
+        for (int ch = ch0; ch < ch1; ch += 32) {
+          uint32_t x[32];
+          float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              v[i] = has0 ? __uint_as_float(x[i]) * g0 : 0.f;
-              if (has1) v[i] = fmaf(__uint_as_float(y[i]), g1, v[i]);
-            }
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          if (has0) {
+            tc_ld32(o0 + ch, x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x[i]) * g0;
+          }
+          if (!kWide && has1) {
+            tc_ld32(o1 + ch, x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), g1, v[i]);
+          }
+          if (valid) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               const float4 z = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
               if (whole) tree_store4(a.out, a.out_type, off + ch + i, zero ? make_float4(0.f, 0.f, 0.f, 0.f) : z);
-              else {
-              // channel-major: the lanes of a warp write consecutive words
-              rec[(ch + i) * kTR + r] = z.x;
-              rec[(ch + i + 1) * kTR + r] = z.y;
-              rec[(ch + i + 2) * kTR + r] = z.z;
-              rec[(ch + i + 3) * kTR + r] = z.w;
-            }
+              else reinterpret_cast<float4*>(rec)[((ch + i) / 4) * kR + row_in] = z;  // whole lines per warp
             }
           }
           __syncwarp();
         }
-        if (odd && r < rows) {  // rare: the values that were taken out, for the rows that see them
-          const int32_t* table = a.m.tables + __ldg(a.m.tab_start + u.seq);
+        if (odd && valid) {  // rare: the values that were taken out, for the rows that see them
+          const int32_t* table = a.m.tables + u.tab;
 #pragma unroll 1
-          for (int n = j0; n < j1; ++n) {
-            if (!tree_sees(a.m, node, n)) continue;
-            const int p = u.ctx + n;
+          for (int x = j0; x < j1; ++x) {
+            if (!tree_sees(a.m, node, x)) continue;
+            const int p = u.ctx + x;
             const __half* at = reinterpret_cast<const __half*>(a.kv) +
                                kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D);
 #pragma unroll 1
-            for (int i = b * (D / 2); i < (b + 1) * (D / 2); ++i) {
+            for (int i = ch0; i < ch1; ++i) {
               const float z = __half2float(at[i]);
               if (isfinite(z)) continue;
               if (whole) tree_store(a.out, a.out_type, off + i, tree_load(a.out, a.out_type, off + i) + z);
-              else rec[i * kTR + r] += z;
+              else rec[((i / 4) * kR + row_in) * 4 + (i & 3)] += z;
             }
           }
         }
-        if (!whole && r < rows && b == 0) {
-          rec[kTR * D + r] = M;
-          rec[kTR * D + kTR + r] = L;
+        if (!whole && valid && (kWide || b == 0)) {
+          rec[kR * D + row_in] = M;
+          rec[kR * D + kR + row_in] = L;
         }
         tc_fence_before();
       }
-      mbar_arrive(oempty);           // O may be written again
-      mbar_arrive(&qempty[n_unit & 1]);
-      asm volatile("bar.sync 1, 256;" ::: "memory");  // ml and the flag are free
-      if (threadIdx.x == 0) flags[1] = 0;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (in) {
+        mbar_arrive(&oempty[kWide ? b : 0]);  // O may be written again
+        ++units;
+      }
       left -= t1 - t0;
       tile = 0;
       u = nu;
@@ -512,7 +599,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
     while (!mbar_try(mma_done, 0) && global_ns() - w0 < kWaitLimitNs) {
     }
   if (threadIdx.x == 256 && *abort_flag)
-    for (int i = max(flags[3] - kS, 0); i < flags[3]; ++i)
+    for (int i = max(flags[2] - kS, 0); i < flags[2]; ++i)
       while (!mbar_try(&full[i % kS], (i / kS) & 1) && global_ns() - w0 < kWaitLimitNs) {
       }
   __syncthreads();
@@ -522,22 +609,22 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   }
 }
 
-template <int D>
+template <int D, bool kWide>
 cudaError_t one(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
   static SmemOptIn opt;
   constexpr int smem = TcSmem<D>::kBytes;
   static_assert(smem <= 232448, "one CTA per SM");
-  cudaError_t e = opt.ensure(k_tree_attend_tc<D>, smem);
+  cudaError_t e = opt.ensure(k_tree_attend_tc<D, kWide>, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_tree_attend_tc<D>, ctas, kTcTreeThreads, smem, s, *tm, a);
+  return launch_pdl(k_tree_attend_tc<D, kWide>, ctas, kTcTreeThreads, smem, s, *tm, a);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
+cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, bool wide, cudaStream_t s) {
   switch (a.d.D) {
-    case 64: return one<64>(a, tm, ctas, s);
-    case 128: return one<128>(a, tm, ctas, s);
+    case 64: return wide ? one<64, true>(a, tm, ctas, s) : one<64, false>(a, tm, ctas, s);
+    case 128: return wide ? one<128, true>(a, tm, ctas, s) : one<128, false>(a, tm, ctas, s);
     default: return cudaErrorInvalidValue;
   }
 }

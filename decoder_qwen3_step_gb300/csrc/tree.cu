@@ -47,19 +47,22 @@ struct TreeLayout {
 // Which attention kernel takes a batch whose widest sequence has max_rows rows
 // (nodes x query heads per KV head).
 TreeVariant variant_for(bool f16, int D, int max_rows) {
-  if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, 2};
-  if (D >= 64 && max_rows > 32) return {kTreeTc, 128, 128, 1};
-  return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2};
+  if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, 2, 2};
+  if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, 4};
+  if (D >= 64 && max_rows > 32) return {kTreeTc, 128, 128, 1, 4};
+  return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2};
 }
+// Records of the attention kernels: two per CTA; rows of all of them, per SM.
+constexpr int kRecordRows = 2 * 256;
 
 TreeLayout tree_layout(const dec_config& c, int max_seqs, int max_tokens, int max_blocks, int sms) {
   TreeLayout L{};
   const size_t S = max_seqs, N = max_tokens, P = (size_t)sms * kTreeMaxCtasPerSm;
-  // header, seq_start, ctx, tab_start, pos, dst, parents, seq, mask, cuts, merges, tables (each piece 16-byte aligned)
-  L.meta_ints = kHdrInts + (3 * S + 1) + 4 * N + N * (kTreeMaxNodes / 32) + 2 * P * 8 + S * (size_t)max_blocks + 16 * 4;
+  // header, seq_start, seqs, pos, dst, parents, mask, cuts, merges, tables (each piece 16-byte aligned)
+  L.meta_ints = kHdrInts + (S + 1) + 8 * S + 3 * N + N * (kTreeMaxNodes / 32) + P * 24 + S * (size_t)max_blocks + 16 * 4;
   L.meta = 256;
   L.part = up256(L.meta + L.meta_ints * 4);
-  L.total = up256(L.part + P * 2 * kTreeMaxRowTile * (size_t)(c.head_dim + 2) * 4);
+  L.total = up256(L.part + (size_t)sms * kRecordRows * (size_t)(c.head_dim + 2) * 4);
   return L;
 }
 
@@ -182,6 +185,110 @@ int check_trees(const dec_pool* pool, const dec_tree_batch* b) {
   return DEC_OK;
 }
 
+// Distribute the attention work over `grid` CTAs: cuts, and the units that CTAs
+// share.  Sequences fall into classes of equally many row tiles; a class gets
+// CTAs by its share of the work, in gangs of one CTA per row tile (up to
+// `max_gang`) that walk the same keys at the same time, so that a tile's
+// second reader finds it in L2.  The gangs of a class cut its (sequence, head)
+// list into equal runs, a unit's start and end counted as unit_cost tiles.
+int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVariant& var, int grid, int max_gang, TreeCut* cut,
+               TreeMerge* mrg) {
+  const int G = c.n_heads / c.n_kv_heads, R = var.row_tile, K = var.tile_keys, Hkv = c.n_kv_heads;
+  auto row_tiles = [&](const TreeSeq& s) { return (s.nodes * G + R - 1) / R; };
+  auto tiles = [&](const TreeSeq& s) { return (s.ctx + s.nodes + K - 1) / K; };
+  auto gang = [&](const TreeSeq& s) { return std::min(row_tiles(s), max_gang); };
+  std::stable_sort(seqs.begin(), seqs.end(), [&](const TreeSeq& x, const TreeSeq& y) { return gang(x) < gang(y); });
+  // work of each class, and its CTAs: whole gangs, one at least, the rest to whichever class is most behind
+  std::vector<double> work(max_gang + 1, 0.0);
+  std::vector<int> gangs(max_gang + 1, 0);
+  for (const TreeSeq& s : seqs) work[gang(s)] += (double)Hkv * row_tiles(s) * (tiles(s) + var.unit_cost);
+  int left = grid;
+  for (int g = 1; g <= max_gang; ++g)
+    if (work[g] > 0) {
+      gangs[g] = 1;
+      left -= g;
+    }
+  while (true) {
+    int most = 0;
+    for (int g = 1; g <= max_gang; ++g)
+      if (work[g] > 0 && g <= left && (!most || work[g] / (gangs[g] * g) > work[most] / (gangs[most] * most))) most = g;
+    if (!most) break;
+    ++gangs[most];
+    left -= most;
+  }
+  int n_mrg = 0, cta = 0;
+  for (size_t q0 = 0; q0 < seqs.size();) {
+    const int g = gang(seqs[q0]);
+    size_t q1 = q0;
+    while (q1 < seqs.size() && gang(seqs[q1]) == g) ++q1;
+    // the class as a line of units: of the row tiles i, i + g, .. of a (sequence, head) for gang member i.  Members run in
+    // step, so every member's line has the length of the first one's; a unit that a member lacks is no work to it
+    struct Unit {
+      int q, head, pass, tiles;
+    };
+    std::vector<Unit> units;
+    double cost = 0;
+    int64_t real = 0;
+    for (size_t q = q0; q < q1; ++q)
+      for (int h = 0; h < Hkv; ++h)
+        for (int pass = 0; pass * g < row_tiles(seqs[q]); ++pass) {
+          units.push_back({(int)q, h, pass, tiles(seqs[q])});
+          cost += tiles(seqs[q]) + var.unit_cost;
+          real += tiles(seqs[q]);
+        }
+    // cuts as (unit, tile); near a unit's border the cut moves there, where that costs less than another piece
+    const int n = gangs[g];
+    const double run = cost / n;
+    const int snap = (int)std::min(var.unit_cost / 2.0, run / 8);
+    std::vector<std::pair<int, int>> at;  // distinct, ascending
+    size_t x = 0;
+    double before = 0;
+    for (int i = 0; i < n; ++i) {
+      const double pos = cost * i / n;
+      while (x < units.size() && before + units[x].tiles + var.unit_cost <= pos) before += units[x++].tiles + var.unit_cost;
+      if (x == units.size()) break;
+      int t = std::min((int)(pos - before), units[x].tiles);
+      std::pair<int, int> here{(int)x, t};
+      if (t <= snap) here.second = 0;
+      else if (units[x].tiles - t <= snap) here = {(int)x + 1, 0};
+      if (here.first < (int)units.size() && (at.empty() || at.back() < here)) at.push_back(here);
+    }
+    const int used = (int)at.size();
+    at.push_back({(int)units.size(), 0});
+    for (int i = 0; i < used; ++i)
+      for (int member = 0; member < g; ++member) {
+        // this member's first unit in the run: its row tile may not exist in the first one
+        TreeCut& o = cut[cta + i * g + member];
+        o = {};
+        for (int y = at[i].first; y <= at[i + 1].first && y < (int)units.size(); ++y) {
+          const Unit& w = units[y];
+          const int t0 = y == at[i].first ? at[i].second : 0, t1 = y == at[i + 1].first ? at[i + 1].second : w.tiles;
+          const int rt = w.pass * g + member;
+          if (t1 <= t0 || rt >= row_tiles(seqs[w.q])) continue;
+          if (o.count == 0) o = {w.q, w.head, rt, t0, 0, g, 0, 0, seqs[w.q]};
+          o.count += t1 - t0;
+        }
+      }
+    // units with a cut inside
+    for (int i = 1; i < used; ++i) {
+      if (at[i].second == 0 || (i > 1 && at[i - 1].first == at[i].first && at[i - 1].second > 0)) continue;
+      const Unit& w = units[at[i].first];
+      int last = i;
+      while (last + 1 < used && at[last + 1].first == at[i].first) ++last;
+      for (int member = 0; member < g; ++member) {
+        const int rt = w.pass * g + member;
+        if (rt >= row_tiles(seqs[w.q])) continue;
+        mrg[n_mrg++] = {w.head, rt, cta + (i - 1) * g + member, cta + last * g + member, g, seqs[w.q].node0, seqs[w.q].nodes, 0};
+      }
+    }
+    cta += n * g;
+    for (int i = used * g; i < n * g; ++i) cut[cta - n * g + i] = {};
+    q0 = q1;
+  }
+  for (; cta < grid; ++cta) cut[cta] = {};
+  return n_mrg;
+}
+
 // Fill the pinned image of the plan and the kernels' view of its upload;
 // returns the ints used.
 size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
@@ -193,17 +300,16 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   for (int s = 0; s < S; ++s) max_nodes = std::max(max_nodes, b->seq_start[s + 1] - b->seq_start[s]);
   const int W = std::max((max_nodes + 31) / 32, 1);
   const TreeVariant var = variant_for(t->f16, c.head_dim, max_nodes * G);
-  const int grid = t->sms * var.ctas_per_sm, R = var.row_tile, K = var.tile_keys;
-  const size_t h_hdr = take(kHdrInts), h_start = take(S + 1), h_ctx = take(S), h_tab = take(S), h_pos = take(N),
-               h_dst = take(N), h_par = take(N), h_seq = take(N), h_anc = take((size_t)N * W),
-               h_cut = take((size_t)grid * 8), h_mrg = take((size_t)grid * 8), h_tables = o;
-  int64_t total = 0;
+  const int grid = t->sms * var.ctas_per_sm;
+  const size_t h_hdr = take(kHdrInts), h_start = take(S + 1), h_seqs = take((size_t)S * 8), h_pos = take(N), h_dst = take(N),
+               h_par = take(N), h_anc = take((size_t)N * W), h_cut = take((size_t)grid * 16), h_mrg = take((size_t)grid * 8),
+               h_tables = o;
+  std::vector<TreeSeq> seqs;
   for (int s = 0; s < S; ++s) {
     const int a0 = b->seq_start[s], T = b->seq_start[s + 1] - a0, ctx = b->ctx[s];
     H[h_start + s] = a0;
-    H[h_ctx + s] = ctx;
-    H[h_tab + s] = (int32_t)(o - h_tables);
     if (T == 0) continue;
+    seqs.push_back({a0, T, ctx, (int32_t)(o - h_tables), s, 0, 0, 0});
     const int32_t* row = b->block_table + (size_t)s * b->max_blocks;
     const int nb = (ctx + T + 15) / 16;
     std::copy(row, row + nb, H + o);
@@ -213,7 +319,6 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
       const int p = b->parents ? b->parents[a0 + i] : i - 1;
       uint32_t* w = anc + (size_t)i * W;
       H[h_par + a0 + i] = p;
-      H[h_seq + a0 + i] = s;
       H[h_dst + a0 + i] = row[(ctx + i) >> 4] * 16 + ((ctx + i) & 15);  // an accepted node may move to a padding node's slot
       if (p == DEC_TREE_PAD) {
         std::fill(w, w + W, 0u);
@@ -226,54 +331,26 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
       H[h_pos + a0 + i] = p < 0 ? ctx : H[h_pos + a0 + p] + 1;
       max_position = std::max(max_position, H[h_pos + a0 + i]);
     }
-    total += (int64_t)c.n_kv_heads * ((T * G + R - 1) / R) * ((ctx + T + K - 1) / K);
   }
   H[h_start + S] = N;
-  // attention: every CTA takes an equal run of key tiles in the order (sequence, KV head, row tile, key tile)
-  TreeCut* cut = reinterpret_cast<TreeCut*>(H + h_cut);
-  TreeMerge* mrg = reinterpret_cast<TreeMerge*>(H + h_mrg);
-  int n_mrg = 0, cta = 0;
-  int64_t done = 0;  // tiles before the current unit
-  const int P = (int)std::min<int64_t>(grid, total);  // no CTA among the first P goes without a tile
-  auto begin = [&](int i) { return total * i / P; };
-  for (int s = 0; s < S; ++s) {
-    const int T = b->seq_start[s + 1] - b->seq_start[s];
-    if (T == 0) continue;
-    const int rts = (T * G + R - 1) / R, tiles = (b->ctx[s] + T + K - 1) / K;
-    for (int h = 0; h < c.n_kv_heads; ++h)
-      for (int rt = 0; rt < rts; ++rt, done += tiles) {
-        while (cta < P && begin(cta) < done + tiles) {
-          cut[cta] = {s, h, rt, (int)(begin(cta) - done), (int)(begin(cta + 1) - begin(cta)), b->seq_start[s], T, b->ctx[s]};
-          ++cta;
-        }
-        // the CTAs with a tile of this unit: c0 holds its first, c1 its last
-        auto holder = [&](int64_t x) {  // the CTA whose run contains tile x
-          int i = (int)std::min<int64_t>(P - 1, x * P / total);
-          while (i + 1 < P && begin(i + 1) <= x) ++i;
-          while (begin(i) > x) --i;
-          return i;
-        };
-        const int c0 = holder(done), c1 = holder(done + tiles - 1);
-        if (c1 > c0) mrg[n_mrg++] = {s, h, rt, c0, c1, 0, 0, 0};
-      }
-  }
-  for (; cta < grid; ++cta) cut[cta] = {0, 0, 0, 0, 0, 0, 0, 0};
+  // only the wide kernel has the rows of a sequence walk the keys side by side; at most 1024 rows: gangs of four
+  const int n_mrg = distribute(c, seqs, var, grid, var.kernel == kTreeTcWide ? 4 : 1, reinterpret_cast<TreeCut*>(H + h_cut),
+                               reinterpret_cast<TreeMerge*>(H + h_mrg));
+  std::copy(seqs.begin(), seqs.end(), reinterpret_cast<TreeSeq*>(H + h_seqs));
   std::fill(H + h_hdr, H + h_hdr + kHdrInts, 0);
   H[h_hdr + kHdrSeqs] = S;
   H[h_hdr + kHdrTokens] = N;
   H[h_hdr + kHdrWords] = W;
-  H[h_hdr + kHdrRowTile] = R;
+  H[h_hdr + kHdrRowTile] = var.row_tile;
   H[h_hdr + kHdrMerges] = n_mrg;
   int32_t* d = reinterpret_cast<int32_t*>(t->ws + t->lay.meta);
   TreeMeta& m = t->meta;
   m.hdr = d + h_hdr;
   m.seq_start = d + h_start;
-  m.ctx = d + h_ctx;
-  m.tab_start = d + h_tab;
+  m.seqs = reinterpret_cast<const TreeSeq*>(d + h_seqs);
   m.pos = d + h_pos;
   m.dst = d + h_dst;
   m.parents = d + h_par;
-  m.seq = d + h_seq;
   m.anc = reinterpret_cast<const uint32_t*>(d + h_anc);
   m.cuts = reinterpret_cast<const TreeCut*>(d + h_cut);
   m.merges = reinterpret_cast<const TreeMerge*>(d + h_mrg);
@@ -282,8 +359,8 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   m.S = S;
   m.N = N;
   m.words = W;
-  m.row_tile = R;
-  m.tile_keys = K;
+  m.row_tile = var.row_tile;
+  m.tile_keys = var.tile_keys;
   t->kernel = var.kernel;
   t->max_nodes = max_nodes;
   t->max_position = max_position;
@@ -479,8 +556,13 @@ int dec_tree_set(dec_tree* t, const dec_tree_batch* b, void* stream) {
   const int slot = t->stage_next;
   TREE_CUDA(cudaEventSynchronize(t->stage_ev[slot]));  // the copy that last used this buffer has run
   t->stage_next = (slot + 1) % kStages;
-  const size_t ints = build_plan(t, b, t->stage[slot]);
   t->set = false;
+  size_t ints = 0;
+  try {
+    ints = build_plan(t, b, t->stage[slot]);
+  } catch (const std::bad_alloc&) {
+    return fail(DEC_ECAPACITY, "out of host memory");
+  }
   TREE_CUDA(cudaMemcpyAsync(t->ws + t->lay.meta, t->stage[slot], ints * 4, cudaMemcpyHostToDevice, st));
   TREE_CUDA(cudaEventRecord(t->stage_ev[slot], st));
   t->set = true;
@@ -579,9 +661,9 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
   a.part = (float*)(t->ws + t->lay.part);
   a.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)c.head_dim));
   cudaStream_t st = (cudaStream_t)stream;
-  TREE_CUDA(t->kernel == kTreeTc    ? launch_tree_attend_tc(a, &t->tm_panel, t->ctas, st)
+  TREE_CUDA(t->kernel == kTreeFfma  ? launch_tree_attend_f32(a, t->ctas, st)
             : t->kernel == kTreeMma ? launch_tree_attend_f16(a, &t->tm, t->ctas, st)
-                                    : launch_tree_attend_f32(a, t->ctas, st));
+                                    : launch_tree_attend_tc(a, &t->tm_panel, t->ctas, t->kernel == kTreeTcWide, st));
   TREE_CUDA(launch_tree_merge(a, t->n_merges, st));
   return DEC_OK;
 }

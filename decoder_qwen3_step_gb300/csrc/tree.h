@@ -20,27 +20,34 @@ enum TreeType { kTreeF32 = 0, kTreeF16 = 1, kTreeBf16 = 2 };
 // Header words of the uploaded plan.
 enum TreeHdr { kHdrSeqs = 0, kHdrTokens, kHdrWords, kHdrRowTile, kHdrMerges, kHdrInts = 16 };
 
-// Attention work of one CTA: a contiguous range of key tiles in the order
-// (sequence, KV head, row tile, key tile); it starts at `tile` of this unit.
-struct TreeCut {
-  int32_t seq, head, row_tile, tile, count;
-  int32_t node0, nodes, ctx;  // of the sequence, to start without reading them from the arrays
+// A sequence with nodes, as the attention kernels read it (two 16-byte loads).
+struct alignas(16) TreeSeq {
+  int32_t node0, nodes, ctx, tab;  // first node, nodes, cached tokens, first entry in tables
+  int32_t seq, pad0, pad1, pad2;
 };
-// A unit (sequence, KV head, row tile) that CTAs c0 .. c1 share.
-struct TreeMerge {
-  int32_t seq, head, row_tile, c0, c1, pad0, pad1, pad2;
+// Attention work of one CTA: `count` key tiles in the order (entry of seqs, KV
+// head, row tile, key tile), from `tile` of this unit on.  A row tile is
+// followed by row_tile + step of the same head while there is one, then by the
+// next head's row_tile % step.
+struct alignas(16) TreeCut {
+  int32_t q, head, row_tile, tile;
+  int32_t count, step, pad0, pad1;
+  TreeSeq s;  // seqs[q]: a CTA starts with a single read
+};
+// A unit (sequence, KV head, row tile) that CTAs c0, c0 + stride, .., c1 share.
+struct alignas(16) TreeMerge {
+  int32_t head, row_tile, c0, c1;
+  int32_t stride, node0, nodes, pad;
 };
 
 // The plan on the device: one upload, arrays back to back.
 struct TreeMeta {
   const int32_t* hdr;        // [kHdrInts]
   const int32_t* seq_start;  // [S+1]
-  const int32_t* ctx;        // [S] cached tokens of each sequence
-  const int32_t* tab_start;  // [S] first entry of each sequence in tables
+  const TreeSeq* seqs;       // the sequences with nodes, in the order of the attention work
   const int32_t* pos;        // [N] rotary position; -1: a padding node
   const int32_t* dst;        // [N] pool block * 16 + slot
   const int32_t* parents;    // [N] parent within the sequence, -1 root, -2 padding
-  const int32_t* seq;        // [N]
   const uint32_t* anc;       // [N, words] bit j: the node sees node j (itself included)
   const TreeCut* cuts;       // [CTAs]
   const TreeMerge* merges;   // [hdr[kHdrMerges]]
@@ -83,14 +90,15 @@ struct TreeAttendArgs {
 };
 // The attention kernel for sequences of up to max_rows (nodes x query heads
 // per KV head) rows, and its tiles.
-enum TreeKernel { kTreeFfma = 0, kTreeMma, kTreeTc };
+enum TreeKernel { kTreeFfma = 0, kTreeMma, kTreeTc, kTreeTcWide };
 struct TreeVariant {
   int kernel, row_tile, tile_keys, ctas_per_sm;
+  int unit_cost;  // what starting and finishing a unit costs a CTA, in key tiles
 };
-constexpr int kTreeMaxRowTile = 128, kTreeMaxCtasPerSm = 2;
+constexpr int kTreeMaxCtasPerSm = 2;
 cudaError_t launch_tree_attend_f32(const TreeAttendArgs& a, int ctas, cudaStream_t s);
 cudaError_t launch_tree_attend_f16(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s);
-cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s);
+cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, bool wide, cudaStream_t s);
 cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, cudaStream_t s);
 
 struct TreeCommitArgs {

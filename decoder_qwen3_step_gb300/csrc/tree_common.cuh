@@ -16,38 +16,35 @@ __device__ __forceinline__ bool tree_shape_ok(const TreeMeta& m, bool rows = fal
   return ok;
 }
 
-// One unit of attention work: the rows row0 .. row0+rows-1 (row r: node r >> gs,
-// query head r & (2^gs - 1) of the group) of one sequence and KV head.
+// One unit of attention work: the rows row_tile * R .. of one sequence and KV
+// head (row r: node r >> gs, query head r & (2^gs - 1) of the group).
 struct TreeUnit {
-  int seq, head, row_tile, n_row_tiles;
-  int node0, ctx, nodes;  // the sequence's first node, cached tokens, nodes
-  int tiles;              // key tiles of ctx + nodes keys
+  int q, head, row_tile, step;
+  int node0, nodes, ctx, tab;
+  int tiles;  // key tiles of ctx + nodes keys
 };
-
-__device__ __forceinline__ void tree_unit_sizes(const TreeMeta& m, int gs, int R, TreeUnit& u) {
+__device__ __forceinline__ void tree_unit_seq(const TreeMeta& m, const int4& s, TreeUnit& u) {
+  u.node0 = s.x;
+  u.nodes = s.y;
+  u.ctx = s.z;
+  u.tab = s.w;
   u.tiles = (u.ctx + u.nodes + m.tile_keys - 1) / m.tile_keys;
-  u.n_row_tiles = ((u.nodes << gs) + R - 1) / R;
 }
 // The unit a CTA starts with.
-__device__ __forceinline__ TreeUnit tree_unit_first(const TreeMeta& m, int gs, int R, const TreeCut& c) {
-  TreeUnit u{c.seq, c.head, c.row_tile, 0, c.node0, c.ctx, c.nodes, 0};
-  tree_unit_sizes(m, gs, R, u);
+__device__ __forceinline__ TreeUnit tree_unit_first(const TreeMeta& m, const TreeCut& c) {
+  TreeUnit u{c.q, c.head, c.row_tile, max(c.step, 1), 0, 0, 0, 0, 0};
+  tree_unit_seq(m, make_int4(c.s.node0, c.s.nodes, c.s.ctx, c.s.tab), u);
   return u;
 }
-// The unit after u (sequences without nodes have none).
+// The unit after u; there must be one.
 __device__ __forceinline__ void tree_unit_next(const TreeMeta& m, int gs, int R, int Hkv, TreeUnit& u) {
-  if (++u.row_tile < u.n_row_tiles) return;
-  u.row_tile = 0;
+  u.row_tile += u.step;
+  if (u.row_tile * R < u.nodes << gs) return;
+  u.row_tile %= u.step;
   if (++u.head < Hkv) return;
   u.head = 0;
-  do {
-    ++u.seq;
-  } while (u.seq < m.S && __ldg(m.seq_start + u.seq + 1) == __ldg(m.seq_start + u.seq));
-  if (u.seq >= m.S) return;
-  u.node0 = __ldg(m.seq_start + u.seq);
-  u.nodes = __ldg(m.seq_start + u.seq + 1) - u.node0;
-  u.ctx = __ldg(m.ctx + u.seq);
-  tree_unit_sizes(m, gs, R, u);
+  ++u.q;
+  tree_unit_seq(m, __ldg(reinterpret_cast<const int4*>(m.seqs + u.q)), u);
 }
 
 // Whether node `node` (numbered over the batch) sees node j of its sequence.
@@ -117,7 +114,8 @@ __device__ __forceinline__ float2 tree_pair<bf16>(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// Load the queries of a unit's row tile as f16 into shared memory.  D/8 lanes
+// Load R rows of a unit's queries, from row0 on (at least one of them is
+// there), as f16 into shared memory.  D/8 lanes
 // share a row (eight channels each), so a warp reads 32/(D/8) rows at a time
 // and has up to kMaxU such groups in flight; W warps split the rows.  The code has no
 // branch and no division per row: a first version with both, one row per warp
@@ -127,12 +125,12 @@ __device__ __forceinline__ float2 tree_pair<bf16>(uint32_t w) {
 // queries' range; fac[r] takes the row's score factor.  put(r, channel / 8,
 // eight halves).  Rows past the last are zeros.
 template <int D, int R, int W, int kMaxU, typename T, typename F>
-__device__ __forceinline__ void tree_load_queries_of(const TreeAttendArgs& a, const TreeUnit& u, int w, float* fac, F&& put) {
+__device__ __forceinline__ void tree_load_queries_of(const TreeAttendArgs& a, const TreeUnit& u, int row0, int w, float* fac, F&& put) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kSteps = R / (W * kRows), kU = kSteps < kMaxU ? kSteps : kMaxU;
   constexpr bool kWide = sizeof(T) == 4;
   static_assert(kSteps >= 1 && kSteps % kU == 0, "rows split evenly");
   const int lane = threadIdx.x & 31, x = lane % kLanes, gs = a.d.gs;
-  const int row0 = u.row_tile * R, rows = min(R, (u.nodes << gs) - row0);
+  const int rows = min(R, (u.nodes << gs) - row0);
   const T* q = reinterpret_cast<const T*>(a.q) + (int64_t)u.node0 * a.ldq + (u.head << gs) * D + x * 8;
 #pragma unroll 1
   for (int s = 0; s < kSteps; s += kU) {
@@ -188,10 +186,10 @@ __device__ __forceinline__ void tree_load_queries_of(const TreeAttendArgs& a, co
   }
 }
 template <int D, int R, int W, int kMaxU, typename F>
-__device__ __forceinline__ void tree_load_queries(const TreeAttendArgs& a, const TreeUnit& u, int w, float* fac, F&& put) {
-  if (a.q_type == kTreeF32) tree_load_queries_of<D, R, W, kMaxU, float>(a, u, w, fac, put);
-  else if (a.q_type == kTreeF16) tree_load_queries_of<D, R, W, kMaxU, __half>(a, u, w, fac, put);
-  else tree_load_queries_of<D, R, W, kMaxU, bf16>(a, u, w, fac, put);
+__device__ __forceinline__ void tree_load_queries(const TreeAttendArgs& a, const TreeUnit& u, int row0, int w, float* fac, F&& put) {
+  if (a.q_type == kTreeF32) tree_load_queries_of<D, R, W, kMaxU, float>(a, u, row0, w, fac, put);
+  else if (a.q_type == kTreeF16) tree_load_queries_of<D, R, W, kMaxU, __half>(a, u, row0, w, fac, put);
+  else tree_load_queries_of<D, R, W, kMaxU, bf16>(a, u, row0, w, fac, put);
 }
 
 }  // namespace dec
