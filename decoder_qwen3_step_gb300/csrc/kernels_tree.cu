@@ -197,21 +197,25 @@ __global__ void __launch_bounds__(kCommitThreads) k_tree_commit(const __grid_con
 // ---- merge of split attention --------------------------------------------------------
 // A unit whose keys several CTAs shared: with each CTA's running maximum m_c
 // (base-2 logarithms), sum l_c and unnormalised output O_c,
-//   out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M),  M = max_c m_c,
-// the contributions added in CTA order.  One warp per row.
-template <int D>
+//   out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M),  M = max_c m_c.
+// kWarps warps share a row, each adding every kWarps-th contribution in CTA
+// order, then the warps' sums in warp order.  With four, the 38 records of a
+// unit that 38 CTAs shared are two rounds of loads instead of ten.
+template <int D, int kWarps>
 __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ TreeAttendArgs a) {
   pdl_wait_prev();
   pdl_launch_next();
-  if (!tree_shape_ok(a.m, true)) return;
-  constexpr int kPer = D / 32;
-  const int R = a.m.row_tile, gs = a.d.gs, G = 1 << gs, lane = threadIdx.x & 31, groups = R / 4;
+  constexpr int kPer = D / 32, kRows = 4 / kWarps;
+  __shared__ float part[kWarps == 1 ? 1 : 4][D + 1];
+  const int R = a.m.row_tile, gs = a.d.gs, G = 1 << gs, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = R / kRows;
+  TreeMerge e = a.m.merges[blockIdx.x / groups];  // read beside the header, not behind it
   const int n = __ldg(a.m.hdr + kHdrMerges);
+  if (!tree_shape_ok(a.m, true)) return;
   for (int w = blockIdx.x; w < n * groups; w += gridDim.x) {
-    const TreeMerge e = a.m.merges[w / groups];
-    const int r = (w % groups) * 4 + (threadIdx.x >> 5);
+    if (w != blockIdx.x) e = a.m.merges[w / groups];
+    const int r = (w % groups) * kRows + warp / kWarps, c_first = warp % kWarps;
     const int row = e.row_tile * R + r, n_rec = (e.c1 - e.c0) / e.stride + 1;
-    if (row >= e.nodes << gs) continue;
+    if (row >= e.nodes << gs) continue;  // with four warps a row, the whole block
     const int node = e.node0 + (row >> gs);
     auto rec = [&](int c) -> const float* { return tree_record(a, e.c0 + c * e.stride, c == 0); };
     float M = -INFINITY;
@@ -221,36 +225,44 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
     float L = 0.f, o[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-    for (int c0 = 0; c0 < n_rec; c0 += 32) {
-      float f = 0.f;
-      if (c0 + lane < n_rec) {
-        const float* p = rec(c0 + lane) + R * D;
-        f = ex2(__ldcg(p + r) - M);
-        L = fmaf(__ldcg(p + R + r), f, L);
-      }
-      const int m = min(32, n_rec - c0);
-#pragma unroll 4
-      for (int i = 0; i < m; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float* p = rec(c0 + i) + r * D + lane * kPer;
-        if constexpr (kPer == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
-          o[0] = fmaf(v.x, fi, o[0]);
-          o[1] = fmaf(v.y, fi, o[1]);
-          o[2] = fmaf(v.z, fi, o[2]);
-          o[3] = fmaf(v.w, fi, o[3]);
-        } else {
+#pragma unroll 8
+    for (int c = c_first; c < n_rec; c += kWarps) {
+      const float* p = rec(c);
+      const float f = ex2(__ldcg(p + R * D + r) - M);
+      L = fmaf(__ldcg(p + R * D + R + r), f, L);
+      if constexpr (kPer == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p + r * D + lane * 4));
+        o[0] = fmaf(v.x, f, o[0]);
+        o[1] = fmaf(v.y, f, o[1]);
+        o[2] = fmaf(v.z, f, o[2]);
+        o[3] = fmaf(v.w, f, o[3]);
+      } else {
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) o[j] = fmaf(__ldcg(p + j), fi, o[j]);
-        }
+        for (int j = 0; j < kPer; ++j) o[j] = fmaf(__ldcg(p + r * D + lane * kPer + j), f, o[j]);
       }
     }
-    L = warp_sum(L);
-    const bool pad = __ldg(a.m.pos + node) < 0;
-    const float inv = pad || L == 0.f ? 0.f : 1.0f / L;
+    if constexpr (kWarps > 1) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) part[warp][lane * kPer + j] = o[j];
+      if (lane == 0) part[warp][D] = L;
+      __syncthreads();
+      L = 0.f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) o[j] = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        L += part[x][D];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) o[j] += part[x][lane * kPer + j];
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
+    const bool zero = __ldg(a.m.pos + node) < 0 || L == 0.f;
+    const float inv = 1.0f / L;
     const int64_t off = node * a.ldo + (int64_t)(e.head * G + (row & (G - 1))) * D + lane * kPer;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) o[j] = inv == 0.f ? 0.f : o[j] * inv;
+    for (int j = 0; j < kPer; ++j) o[j] = zero ? 0.f : o[j] * inv;
     if constexpr (kPer == 4) {
       tree_store4(a.out, a.out_type, off, make_float4(o[0], o[1], o[2], o[3]));
     } else {
@@ -258,6 +270,12 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
       for (int j = 0; j < kPer; ++j) tree_store(a.out, a.out_type, off + j, o[j]);
     }
   }
+}
+template <int D>
+cudaError_t merge_rows(const TreeAttendArgs& a, int n_merges, cudaStream_t s) {
+  // few units share their keys among many CTAs
+  if (n_merges < 64) return launch_pdl(k_tree_merge<D, 4>, n_merges * a.m.row_tile, 128, 0, s, a);
+  return launch_pdl(k_tree_merge<D, 1>, n_merges * (a.m.row_tile / 4), 128, 0, s, a);
 }
 
 // The same for the row tiles of wide trees (128 or 256 rows), whose records
@@ -267,12 +285,13 @@ template <int D, int kC>
 __global__ void __launch_bounds__(128) k_tree_merge_wide(const __grid_constant__ TreeAttendArgs a) {
   pdl_wait_prev();
   pdl_launch_next();
-  if (!tree_shape_ok(a.m, true)) return;
   constexpr int kSlabs = D / kC;
   const int gs = a.d.gs, R = a.m.row_tile, per = kSlabs * (R / 128);
+  TreeMerge e = a.m.merges[blockIdx.x / per];  // read beside the header, not behind it
   const int n = __ldg(a.m.hdr + kHdrMerges);
+  if (!tree_shape_ok(a.m, true)) return;
   for (int w = blockIdx.x; w < n * per; w += gridDim.x) {
-    const TreeMerge e = a.m.merges[w / per];
+    if (w != blockIdx.x) e = a.m.merges[w / per];
     const int d0 = (w % kSlabs) * kC, r = (w % per) / kSlabs * 128 + threadIdx.x, row = e.row_tile * R + r;
     if (row >= e.nodes << gs) continue;
     const int node = e.node0 + (row >> gs), n_rec = (e.c1 - e.c0) / e.stride + 1;
@@ -344,11 +363,10 @@ cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, cudaStream_
   if (a.m.row_tile >= 128) {
     return a.d.D == 128 ? merge_wide<128>(a, max(n_merges, 1), s) : merge_wide<64>(a, max(n_merges, 1), s);
   }
-  const int grid = max(n_merges, 1) * (a.m.row_tile / 4);
   switch (a.d.D) {
-    case 32: return launch_pdl(k_tree_merge<32>, grid, 128, 0, s, a);
-    case 64: return launch_pdl(k_tree_merge<64>, grid, 128, 0, s, a);
-    case 128: return launch_pdl(k_tree_merge<128>, grid, 128, 0, s, a);
+    case 32: return merge_rows<32>(a, max(n_merges, 1), s);
+    case 64: return merge_rows<64>(a, max(n_merges, 1), s);
+    case 128: return merge_rows<128>(a, max(n_merges, 1), s);
     default: return cudaErrorInvalidValue;
   }
 }

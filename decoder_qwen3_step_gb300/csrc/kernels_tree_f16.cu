@@ -80,10 +80,10 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
   __syncthreads();
   pdl_wait_prev();
   pdl_launch_next();
+  const TreeCut cut = a.m.cuts[blockIdx.x];  // read beside the header, not behind it
   if (!tree_shape_ok(a.m, true)) return;
   volatile int* abort_flag = flags;
   const int gs = a.d.gs, G = 1 << gs;
-  const TreeCut cut = a.m.cuts[blockIdx.x];
   TreeUnit u = tree_unit_first(a.m, cut);
   int tile = cut.tile, k = 0;
 

@@ -42,6 +42,7 @@ template <int D, int R>
 __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constant__ TreeAttendArgs a) {
   pdl_wait_prev();
   pdl_launch_next();
+  const TreeCut cut = a.m.cuts[blockIdx.x];  // read beside the header, not behind it
   if (!tree_shape_ok(a.m, true)) return;
   using SM = F32Smem<D, R>;
   constexpr int kRows = R / 16, kVec = D / 64 > 0 ? D / 64 : 1, kW = D >= 64 ? 4 : 2;  // channels: kVec groups of kW
@@ -49,7 +50,6 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
   float *Qs = sm + SM::kQ, *Ks = sm + SM::kK, *Vs = sm + SM::kV, *Ps = sm + SM::kPr;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int gs = a.d.gs, G = 1 << gs;
-  TreeCut cut = a.m.cuts[blockIdx.x];
   TreeUnit u = tree_unit_first(a.m, cut);
   int tile = cut.tile;
 

@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   __syncthreads();
   pdl_wait_prev();
   pdl_launch_next();
+  const TreeCut cut = a.m.cuts[blockIdx.x];  // read beside the header, not behind it
   if (!tree_shape_ok(a.m, true)) return;
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(flags + 1)), "r"(kTmemCols)
@@ -172,7 +173,6 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags + 1);
   volatile int* abort_flag = flags;
   const int gs = a.d.gs, G = 1 << gs;
-  const TreeCut cut = a.m.cuts[blockIdx.x];
   TreeUnit u = tree_unit_first(a.m, cut);
   int tile = cut.tile, n_unit = 0;
   // a wide unit with at most 128 rows leaves the second group out

@@ -49,7 +49,7 @@ struct TreeLayout {
 TreeVariant variant_for(bool f16, int D, int max_rows) {
   if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, 2, 2};
   if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, 4};
-  if (D >= 64 && max_rows > 32) return {kTreeTc, 128, 128, 1, 4};
+  if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, 4};
   return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2};
 }
 // Records of the attention kernels: two per CTA; rows of all of them, per SM.
@@ -228,17 +228,19 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
     };
     std::vector<Unit> units;
     double cost = 0;
-    int64_t real = 0;
+    int longest = 0;
     for (size_t q = q0; q < q1; ++q)
       for (int h = 0; h < Hkv; ++h)
         for (int pass = 0; pass * g < row_tiles(seqs[q]); ++pass) {
           units.push_back({(int)q, h, pass, tiles(seqs[q])});
           cost += tiles(seqs[q]) + var.unit_cost;
-          real += tiles(seqs[q]);
+          longest = std::max(longest, tiles(seqs[q]));
         }
     // cuts as (unit, tile); near a unit's border the cut moves there, where that costs less than another piece
     const int n = gangs[g];
     const double run = cost / n;
+    // short units that all have a gang of their own stay whole: joining parts costs more than a tile or two
+    const bool split = (int)units.size() > n || longest * var.tile_keys > 128;
     const int snap = (int)std::min(var.unit_cost / 2.0, run / 8);
     std::vector<std::pair<int, int>> at;  // distinct, ascending
     size_t x = 0;
@@ -249,7 +251,7 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
       if (x == units.size()) break;
       int t = std::min((int)(pos - before), units[x].tiles);
       std::pair<int, int> here{(int)x, t};
-      if (t <= snap) here.second = 0;
+      if (t <= snap || !split) here.second = 0;
       else if (units[x].tiles - t <= snap) here = {(int)x + 1, 0};
       if (here.first < (int)units.size() && (at.empty() || at.back() < here)) at.push_back(here);
     }
@@ -664,7 +666,10 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
   TREE_CUDA(t->kernel == kTreeFfma  ? launch_tree_attend_f32(a, t->ctas, st)
             : t->kernel == kTreeMma ? launch_tree_attend_f16(a, &t->tm, t->ctas, st)
                                     : launch_tree_attend_tc(a, &t->tm_panel, t->ctas, t->kernel == kTreeTcWide, st));
-  TREE_CUDA(launch_tree_merge(a, t->n_merges, st));
+  // nothing to join: no second launch, unless a replay may meet a plan that has something
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (t->n_merges == 0) TREE_CUDA(cudaStreamIsCapturing(st, &cap));
+  if (t->n_merges > 0 || cap != cudaStreamCaptureStatusNone) TREE_CUDA(launch_tree_merge(a, t->n_merges, st));
   return DEC_OK;
 }
 

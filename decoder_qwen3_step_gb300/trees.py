@@ -23,6 +23,7 @@ import torch
 from . import dec
 from .runtime import _i32, _ptr, make_config
 
+_empty, _raw_stream = torch.empty, torch._C._cuda_getCurrentRawStream
 _TYPES = {torch.float32: dec.DEC_T_F32, torch.float16: dec.DEC_T_F16, torch.bfloat16: dec.DEC_T_BF16}
 
 
@@ -80,6 +81,7 @@ class RopeTable:
         size = C.c_size_t()
         dec.check(L.dec_rope_table_bytes(C.byref(self.rope), n_positions, C.byref(size)), "dec_rope_table_bytes")
         self.table = torch.empty((n_positions, rot_dim // 2, 2), dtype=torch.float32, device=device)
+        self.pointer, self.address, self.index = C.pointer(self.rope), self.table.data_ptr(), self.table.get_device()
         with torch.cuda.device(self.table.device):
             dec.check(L.dec_rope_table(C.byref(self.rope), n_positions, C.c_void_p(self.table.data_ptr()), size.value,
                                        C.c_void_p(torch.cuda.current_stream().cuda_stream)), "dec_rope_table")
@@ -120,30 +122,31 @@ class DraftTrees:
                                              C.byref(h)), "dec_tree_create")
         self.handle = h
         self.n_tokens = self.n_seqs = 0
-        self._width = {"q": (self.cfg.n_heads, self.cfg.head_dim), "k": (self.cfg.n_kv_heads, self.cfg.head_dim),
-                       "v": (self.cfg.n_kv_heads, self.cfg.head_dim)}
+        self._heads, self._kv_heads, self._dim = self.cfg.n_heads, self.cfg.n_kv_heads, self.cfg.head_dim
+        # a step makes these calls for every layer: the lookups are done once
+        self._append, self._attend, self._commit = self.L.dec_tree_append, self.L.dec_tree_attend, self.L.dec_tree_commit
+        self._qkv = dec.dec_tree_qkv()
         self._out_type = torch.float32 if self.cfg.mode == dec.DEC_FP32 else torch.bfloat16
 
     def _stream(self, stream):
-        return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._index)
+        return stream.cuda_stream if stream is not None else _raw_stream(self._index)
 
     def _new(self, shape, dtype, stream):
         """An output that lives on the stream its kernel runs on."""
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return _empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return _empty(shape, dtype=dtype, device=self.device)
 
-    def _rows(self, x, name, what="q"):
+    def _rows(self, x, name, heads):
         """Row stride and type of a [nodes, heads, head_dim] (or [nodes, heads * head_dim]) tensor."""
-        heads, dim = self._width[what]
-        st, dt = x.stride(), _TYPES.get(x.dtype)
-        good = (x.shape == (self.n_tokens, heads, dim) and st[2] == 1 and (st[1] == dim or heads == 1)) or (
-            x.shape == (self.n_tokens, heads * dim) and st[1] == 1)
-        if dt is None or not good or x.get_device() != self._index:
+        st, shape, dim = x.stride(), x.shape, self._dim
+        good = (shape == (self.n_tokens, heads, dim) and st[2] == 1 and (st[1] == dim or heads == 1)) or (
+            shape == (self.n_tokens, heads * dim) and st[1] == 1)
+        if not good or x.dtype not in _TYPES or x.get_device() != self._index:
             raise ValueError(f"{name}: need a [{self.n_tokens}, {heads}, {dim}] tensor of f32, f16 or bf16 on cuda:{self._index}"
-                             f" with rows of back-to-back heads, got {x.dtype} {tuple(x.shape)} strides {st} on {x.device}")
-        return x.data_ptr(), (st[0] if self.n_tokens > 1 else heads * dim), dt
+                             f" with rows of back-to-back heads, got {x.dtype} {tuple(shape)} strides {st} on {x.device}")
+        return x.data_ptr(), (st[0] if self.n_tokens > 1 else heads * dim), _TYPES[x.dtype]
 
     def set(self, ctx, parents, tables, stream=None) -> None:
         """This step's trees: cached tokens, parents (an int n: a chain of n) and block table of every sequence."""
@@ -155,58 +158,84 @@ class DraftTrees:
                out=None, stream=None):
         """Norm (where gains are given), rotate, and write keys and values to
         the nodes' slots; returns the queries [nodes, heads, head_dim].  q, or k and v, may be None."""
-        x = dec.dec_tree_qkv()
-        kinds = set()
-        for name, t in (("q", q), ("k", k), ("v", v)):
-            if t is not None:
-                p, ld, kind = self._rows(t, name, name)
-                setattr(x, name, p)
-                setattr(x, "ld" + name, ld)
-                kinds.add(kind)
-        if len(kinds) > 1:
-            raise ValueError("q, k and v must have one type")
-        x.in_type = kinds.pop() if kinds else 0
-        for name, g in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if g is not None:
-                if g.dtype != torch.float32 or g.shape != (self.cfg.head_dim,) or not g.is_contiguous() or g.get_device() != self._index:
-                    raise ValueError(f"{name}: need [{self.cfg.head_dim}] f32 on cuda:{self._index}")
-                setattr(x, name, g.data_ptr())
-        if rope is not None:
-            if rope.table.get_device() != self._index:
-                raise ValueError(f"the rotary table is not on cuda:{self._index}")
-            x.rope, x.rope_table, x.rope_positions = C.pointer(rope.rope), rope.table.data_ptr(), rope.n_positions
+        x, kind = self._qkv, None  # the struct is read during the call only; every field below is set each time
         if q is not None:
+            x.q, x.ldq, kind = self._rows(q, "q", self._heads)
             if out is None:
-                out = self._new((self.n_tokens, *self._width["q"]), q_type, stream)
-            x.q_out, x.ldqo, x.q_type = self._rows(out, "out")
-        dec.check(self.L.dec_tree_append(self.handle, layer, x, self._stream(stream)), "dec_tree_append")
+                out = self._new((self.n_tokens, self._heads, self._dim), q_type, stream)
+                x.q_out, x.ldqo, x.q_type = out.data_ptr(), self._heads * self._dim, _TYPES[q_type]
+            else:
+                x.q_out, x.ldqo, x.q_type = self._rows(out, "out", self._heads)
+        else:
+            x.q = x.q_out = None
+        if k is not None:
+            x.k, x.ldk, kind_k = self._rows(k, "k", self._kv_heads)
+            if kind is not None and kind != kind_k:
+                raise ValueError("q, k and v must have one type")
+            kind = kind_k
+        else:
+            x.k = None
+        if v is not None:
+            x.v, x.ldv, kind_v = self._rows(v, "v", self._kv_heads)
+            if kind is not None and kind != kind_v:
+                raise ValueError("q, k and v must have one type")
+            kind = kind_v
+        else:
+            x.v = None
+        x.in_type = kind or 0
+        x.q_norm = self._gain(q_norm, "q_norm")
+        x.k_norm = self._gain(k_norm, "k_norm")
+        if rope is not None:
+            if rope.index != self._index:
+                raise ValueError(f"the rotary table is not on cuda:{self._index}")
+            x.rope, x.rope_table, x.rope_positions = rope.pointer, rope.address, rope.n_positions
+        else:
+            x.rope = None
+        code = self._append(self.handle, layer, x, self._stream(stream))
+        if code:
+            dec.check(code, "dec_tree_append")
         return out
+
+    def _gain(self, g, name):
+        if g is None:
+            return None
+        if g.dtype is not torch.float32 or g.shape != (self._dim,) or not g.is_contiguous() or g.get_device() != self._index:
+            raise ValueError(f"{name}: need [{self._dim}] f32 on cuda:{self._index}")
+        return g.data_ptr()
 
     def attend(self, layer: int, q, out=None, out_type=None, stream=None):
         """Attention of every node over what it sees: [nodes, heads * head_dim]
         (default type: f32 for an fp32 cache, else bf16)."""
-        p, ld, kind = self._rows(q, "q")
+        p, ld, kind = self._rows(q, "q", self._heads)
         if out is None:
-            out = self._new((self.n_tokens, self.cfg.n_heads * self.cfg.head_dim), out_type or self._out_type, stream)
-        po, ldo, kind_o = self._rows(out, "out")
-        dec.check(self.L.dec_tree_attend(self.handle, layer, p, kind, ld, po, kind_o, ldo, self._stream(stream)),
-                  "dec_tree_attend")
+            out_type = out_type or self._out_type
+            out = self._new((self.n_tokens, self._heads * self._dim), out_type, stream)
+            po, ldo, kind_o = out.data_ptr(), self._heads * self._dim, _TYPES[out_type]
+        else:
+            po, ldo, kind_o = self._rows(out, "out", self._heads)
+        code = self._attend(self.handle, layer, p, kind, ld, po, kind_o, ldo, self._stream(stream))
+        if code:
+            dec.check(code, "dec_tree_attend")
         return out
+
+    def _ids(self, t, name, n):
+        if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != self._index:
+            raise ValueError(f"{name}: need [{n}] int32 on cuda:{self._index}")
+        return t.data_ptr()
 
     def commit(self, draft, target, prior=None, out=None, stream=None):
         """Accept along the chosen tokens and compact the cache: device int32
         (accepted [sequences], path [nodes], next [sequences])."""
-        want = [("draft", draft, self.n_tokens), ("target", target, self.n_tokens), ("prior", prior, self.n_seqs)]
-        if out is None:
-            buf = self._new((self.n_tokens + 2 * self.n_seqs,), torch.int32, stream)
-            out = buf.split([self.n_seqs, self.n_tokens, self.n_seqs])
-        want += [("accepted", out[0], self.n_seqs), ("path", out[1], self.n_tokens), ("next", out[2], self.n_seqs)]
-        for name, t, n in want:
-            if t is not None and (t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != self._index):
-                raise ValueError(f"{name}: need [{n}] int32 on cuda:{self._index}")
-        dec.check(self.L.dec_tree_commit(self.handle, draft.data_ptr(), target.data_ptr(),
-                                         prior.data_ptr() if prior is not None else None, out[0].data_ptr(),
-                                         out[1].data_ptr(), out[2].data_ptr(), self._stream(stream)), "dec_tree_commit")
+        n, s = self.n_tokens, self.n_seqs
+        if out is None:  # three tensors: one buffer and its views cost twice as much host time
+            out = tuple(self._new(x, torch.int32, stream) for x in (s, n, s))
+            a, p, x = out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr()
+        else:
+            a, p, x = self._ids(out[0], "accepted", s), self._ids(out[1], "path", n), self._ids(out[2], "next", s)
+        code = self._commit(self.handle, self._ids(draft, "draft", n), self._ids(target, "target", n),
+                            None if prior is None else self._ids(prior, "prior", s), a, p, x, self._stream(stream))
+        if code:
+            dec.check(code, "dec_tree_commit")
         return out
 
     def status(self, stream=None) -> int:
