@@ -26,105 +26,94 @@ __global__ void k_rope_table(const __grid_constant__ RopeTableArgs a) {
 // then for each pair (a, b) of the first rot channels
 //   a' = a cos - b sin,  b' = b cos + a sin;
 // queries go to q_out, keys and values to slot ctx + i of node i's sequence.
-// One pass over the data, so HBM bounds it: a head row is D/4 lanes with four
-// consecutive channels each (16-byte loads of fp32, 8 of 16-bit types); the
-// pair's other channel is in the same lane (interleaved) or rot/8 lanes away
-// (halves), one shuffle.  A lane keeps U rows in flight.
+// One pass over the data, so HBM bounds it: D/4 lanes share a head row with four
+// consecutive channels each (16-byte loads of fp32, 8 of 16-bit types) and take U
+// heads of one node, all queries, all keys or all values, so that the node's
+// angles and the gain are read once for them.  The pair's other channel is in the
+// same lane (interleaved) or rot/8 lanes away (halves), one shuffle.
 template <int D, int U>
-__global__ void __launch_bounds__(256) k_tree_append(const __grid_constant__ TreeAppendArgs a) {
+__global__ void __launch_bounds__(256, U == 1 ? 4 : 5) k_tree_append(const __grid_constant__ TreeAppendArgs a) {
   pdl_wait_prev();
   pdl_launch_next();
   constexpr int kLanes = D / 4, kSlots = 256 / kLanes;
-  const int H = a.q ? a.d.H : 0, Hkv = a.k ? a.d.Hkv : 0, heads = H + 2 * Hkv;
-  const int lane = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
-  const int64_t total = (int64_t)a.m.N * heads, row0 = ((int64_t)blockIdx.x * U) * kSlots + slot;
   if (!tree_shape_ok(a.m)) return;
+  const int H = a.q ? a.d.H : 0, Hkv = a.k ? a.d.Hkv : 0, cq = (H + U - 1) / U, ck = (Hkv + U - 1) / U;
+  const int lane = threadIdx.x % kLanes, el = lane * 4, half = a.rot >> 1;
+  const uint32_t id = blockIdx.x * kSlots + threadIdx.x / kLanes, per = cq + 2 * ck;
+  const int node = min((int)(id / per), a.m.N - 1), c = id % per;
+  const bool live = id / per < (uint32_t)a.m.N;  // lanes behind the last node stay for the shuffles
+  const bool is_q = c < cq, is_v = c >= cq + ck;
+  const int h0 = (is_q ? c : is_v ? c - cq - ck : c - cq) * U, heads = is_q ? H : Hkv;
+  const void* src = is_q ? a.q : is_v ? a.v : a.k;
+  const int64_t from = node * (is_q ? a.ldq : is_v ? a.ldv : a.ldk) + h0 * D + el;
+  int pos = __ldg(a.m.pos + node);
+  const int dst = __ldg(a.m.dst + node);
   float4 x[U];
-  int node[U], head[U], pos[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t row = row0 + (int64_t)u * kSlots;
-    node[u] = row < total ? (int)((uint32_t)row / (uint32_t)heads) : -1;
-    head[u] = (int)(row - (int64_t)node[u] * heads);
-    pos[u] = -1;
-    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (node[u] < 0) continue;
-    pos[u] = __ldg(a.m.pos + node[u]);
-    if (a.rope && pos[u] >= a.rope_positions) {  // a replay whose plan outgrew the table of its capture
-      if (lane == 0) atomicOr(a.m.err, kErrBounds);
-      pos[u] = a.rope_positions - 1;
-    }
-    const int h = head[u];
-    if (h < H) x[u] = tree_load4(a.q, a.in_type, node[u] * a.ldq + h * D + lane * 4);
-    else if (h < H + Hkv) x[u] = tree_load4(a.k, a.in_type, node[u] * a.ldk + (h - H) * D + lane * 4);
-    else x[u] = tree_load4(a.v, a.in_type, node[u] * a.ldv + (h - H - Hkv) * D + lane * 4);
+  for (int u = 0; u < U; ++u) x[u] = tree_load4(src, a.in_type, from + min(u, heads - 1 - h0) * D);
+  const float* gain = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
+  const float4 g = gain ? *reinterpret_cast<const float4*>(gain + el) : make_float4(1.f, 1.f, 1.f, 1.f);
+  const bool pad = pos < 0;
+  if (a.rope && pos >= a.rope_positions) {  // a replay whose plan outgrew the table of its capture
+    if (lane == 0) atomicOr(a.m.err, kErrBounds);
+    pos = a.rope_positions - 1;
   }
-  const int half = a.rot >> 1, el = lane * 4;
+  const bool turn = a.rope && el < a.rot && !is_v && !pad;
+  const bool first = el < half;  // halves: this lane's channels are the pairs' first
+  float4 c0 = make_float4(1.f, 0.f, 1.f, 0.f), c1 = c0;  // (cos, sin) of the lane's pairs: four, or two when interleaved
+  if (turn) {
+    const float4* t = reinterpret_cast<const float4*>(a.rope + (size_t)pos * a.rot + (a.interleaved ? el : (first ? el : el - half) * 2));
+    c0 = t[0];
+    if (!a.interleaved) c1 = t[1];
+  }
+  const int other = turn ? (first ? lane + (half >> 2) : lane - (half >> 2)) : lane;
+  const float sg = first ? -1.f : 1.f;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const bool is_q = head[u] < H, is_v = head[u] >= H + Hkv;
-    const float* gain = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
-    // every lane of the warp takes part in the shuffles; rows differ only in what they keep
-    float ss = x[u].x * x[u].x + x[u].y * x[u].y + x[u].z * x[u].z + x[u].w * x[u].w;
+    float4 y = x[u];
+    if (a.q_norm || a.k_norm) {
+      float ss = y.x * y.x + y.y * y.y + y.z * y.z + y.w * y.w;
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (gain) {
-      const float rn = 1.0f / sqrtf(ss / (float)D + a.d.eps);
-      const float4 g = *reinterpret_cast<const float4*>(gain + el);
-      x[u].x *= rn * g.x;
-      x[u].y *= rn * g.y;
-      x[u].z *= rn * g.z;
-      x[u].w *= rn * g.w;
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float rn = gain ? 1.0f / sqrtf(ss / (float)D + a.d.eps) : 1.f;
+      y = make_float4(y.x * (rn * g.x), y.y * (rn * g.y), y.z * (rn * g.z), y.w * (rn * g.w));
     }
     if (a.rope) {
-      const bool turn = el < a.rot && !is_v && pos[u] >= 0;
-      const float2* t = reinterpret_cast<const float2*>(a.rope) + (size_t)max(pos[u], 0) * half;
       if (a.interleaved) {
-        if (turn) {
-          const float4 cs = *reinterpret_cast<const float4*>(t + lane * 2);
-          const float4 y = x[u];
-          x[u] = make_float4(y.x * cs.x - y.y * cs.y, y.y * cs.x + y.x * cs.y, y.z * cs.z - y.w * cs.w,
-                             y.w * cs.z + y.z * cs.w);
-        }
+        y = make_float4(y.x * c0.x - y.y * c0.y, y.y * c0.x + y.x * c0.y, y.z * c0.z - y.w * c0.w, y.w * c0.z + y.z * c0.w);
       } else {
-        const bool first = el < half;
-        const int other = el < a.rot ? (first ? lane + (half >> 2) : lane - (half >> 2)) : lane;
         float4 p;
-        p.x = __shfl_sync(0xffffffffu, x[u].x, other, kLanes);
-        p.y = __shfl_sync(0xffffffffu, x[u].y, other, kLanes);
-        p.z = __shfl_sync(0xffffffffu, x[u].z, other, kLanes);
-        p.w = __shfl_sync(0xffffffffu, x[u].w, other, kLanes);
-        if (turn) {
-          const float4* c = reinterpret_cast<const float4*>(t + (first ? el : el - half));
-          const float4 c0 = c[0], c1 = c[1];
-          const float sg = first ? -1.f : 1.f;
-          x[u].x = x[u].x * c0.x + sg * p.x * c0.y;
-          x[u].y = x[u].y * c0.z + sg * p.y * c0.w;
-          x[u].z = x[u].z * c1.x + sg * p.z * c1.y;
-          x[u].w = x[u].w * c1.z + sg * p.w * c1.w;
-        }
+        p.x = __shfl_sync(0xffffffffu, y.x, other, kLanes);
+        p.y = __shfl_sync(0xffffffffu, y.y, other, kLanes);
+        p.z = __shfl_sync(0xffffffffu, y.z, other, kLanes);
+        p.w = __shfl_sync(0xffffffffu, y.w, other, kLanes);
+        if (turn)
+          y = make_float4(y.x * c0.x + sg * p.x * c0.y, y.y * c0.z + sg * p.y * c0.w, y.z * c1.x + sg * p.z * c1.y,
+                          y.w * c1.z + sg * p.w * c1.w);
       }
     }
-    if (node[u] < 0) continue;
+    if (!live || h0 + u >= heads) continue;
     if (is_q) {
       // a padding node's query is zero: attention on it reads defined numbers
-      tree_store4(a.q_out, a.q_type, node[u] * a.ldo + head[u] * D + el, pos[u] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : x[u]);
-    } else if (pos[u] >= 0) {
-      const int dst = __ldg(a.m.dst + node[u]);
-      const int64_t off = kv_offset(a.layer, dst >> 4, is_v, head[u] - H - (is_v ? Hkv : 0), dst & 15, a.d.n_blocks,
-                                    a.d.Hkv, 16, D);
-      tree_store4(a.kv, a.kv_f16 ? kTreeF16 : kTreeF32, off + el, x[u]);
+      tree_store4(a.q_out, a.q_type, node * a.ldo + (h0 + u) * D + el, pad ? make_float4(0.f, 0.f, 0.f, 0.f) : y);
+    } else if (!pad) {
+      const int64_t off = kv_offset(a.layer, dst >> 4, is_v, h0 + u, dst & 15, a.d.n_blocks, a.d.Hkv, 16, D);
+      tree_store4(a.kv, a.kv_f16 ? kTreeF16 : kTreeF32, off + el, y);
     }
   }
 }
 
+template <int D, int U>
+cudaError_t append_u(const TreeAppendArgs& a, cudaStream_t s) {
+  constexpr int kSlots = 256 / (D / 4);
+  const int64_t units = (int64_t)a.m.N * ((a.q ? (a.d.H + U - 1) / U : 0) + (a.k ? 2 * ((a.d.Hkv + U - 1) / U) : 0));
+  return launch_pdl(k_tree_append<D, U>, (int)((units + kSlots - 1) / kSlots), 256, 0, s, a);
+}
 template <int D>
 cudaError_t append_d(const TreeAppendArgs& a, cudaStream_t s) {
-  constexpr int kSlots = 256 / (D / 4);
+  // a head per lane group while that leaves SMs idle
   const int64_t rows = (int64_t)a.m.N * ((a.q ? a.d.H : 0) + (a.k ? 2 * a.d.Hkv : 0));
-  // one row per lane while that leaves SMs idle, then four for the loads in flight
-  if (rows <= 4 * 152 * kSlots) return launch_pdl(k_tree_append<D, 1>, (int)((rows + kSlots - 1) / kSlots), 256, 0, s, a);
-  return launch_pdl(k_tree_append<D, 4>, (int)((rows + 4 * kSlots - 1) / (4 * kSlots)), 256, 0, s, a);
+  return rows <= 4 * 152 * (256 / (D / 4)) ? append_u<D, 1>(a, s) : append_u<D, 4>(a, s);
 }
 
 // ---- commit ----------------------------------------------------------------------
