@@ -31,8 +31,8 @@ __global__ void k_rope_table(const __grid_constant__ RopeTableArgs a) {
 // heads of one node, all queries, all keys or all values, so that the node's
 // angles and the gain are read once for them.  The pair's other channel is in the
 // same lane (interleaved) or rot/8 lanes away (halves), one shuffle.
-template <int D, int U>
-__global__ void __launch_bounds__(256, U == 1 ? 4 : 5) k_tree_append(const __grid_constant__ TreeAppendArgs a) {
+template <int D, int U, typename T>
+__global__ void __launch_bounds__(256, U == 4 && sizeof(T) == 4 ? 5 : 4) k_tree_append(const __grid_constant__ TreeAppendArgs a) {
   pdl_wait_prev();
   pdl_launch_next();
   constexpr int kLanes = D / 4, kSlots = 256 / kLanes;
@@ -44,13 +44,13 @@ __global__ void __launch_bounds__(256, U == 1 ? 4 : 5) k_tree_append(const __gri
   const bool live = id / per < (uint32_t)a.m.N;  // lanes behind the last node stay for the shuffles
   const bool is_q = c < cq, is_v = c >= cq + ck;
   const int h0 = (is_q ? c : is_v ? c - cq - ck : c - cq) * U, heads = is_q ? H : Hkv;
-  const void* src = is_q ? a.q : is_v ? a.v : a.k;
-  const int64_t from = node * (is_q ? a.ldq : is_v ? a.ldv : a.ldk) + h0 * D + el;
+  const T* src = reinterpret_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) +
+                  node * (is_q ? a.ldq : is_v ? a.ldv : a.ldk) + h0 * D + el;
   int pos = __ldg(a.m.pos + node);
   const int dst = __ldg(a.m.dst + node);
   float4 x[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) x[u] = tree_load4(src, a.in_type, from + min(u, heads - 1 - h0) * D);
+  for (int u = 0; u < U; ++u) x[u] = tree_load4(src + min(u, heads - 1 - h0) * D);
   const float* gain = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
   const float4 g = gain ? *reinterpret_cast<const float4*>(gain + el) : make_float4(1.f, 1.f, 1.f, 1.f);
   const bool pad = pos < 0;
@@ -107,7 +107,10 @@ template <int D, int U>
 cudaError_t append_u(const TreeAppendArgs& a, cudaStream_t s) {
   constexpr int kSlots = 256 / (D / 4);
   const int64_t units = (int64_t)a.m.N * ((a.q ? (a.d.H + U - 1) / U : 0) + (a.k ? 2 * ((a.d.Hkv + U - 1) / U) : 0));
-  return launch_pdl(k_tree_append<D, U>, (int)((units + kSlots - 1) / kSlots), 256, 0, s, a);
+  const int grid = (int)((units + kSlots - 1) / kSlots);
+  return a.in_type == kTreeF32   ? launch_pdl(k_tree_append<D, U, float>, grid, 256, 0, s, a)
+         : a.in_type == kTreeF16 ? launch_pdl(k_tree_append<D, U, __half>, grid, 256, 0, s, a)
+                                 : launch_pdl(k_tree_append<D, U, bf16>, grid, 256, 0, s, a);
 }
 template <int D>
 cudaError_t append_d(const TreeAppendArgs& a, cudaStream_t s) {

@@ -77,24 +77,25 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t panel
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-__device__ __forceinline__ void tc_ld64(uint32_t taddr, uint32_t* v) {
+// A load that runs on: its values are there after the next tc_wait32 on them.
+__device__ __forceinline__ void tc_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
         "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=r"(v[32]),
-        "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]),
-        "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]),
-        "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]), "=r"(v[56]),
-        "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
-      : "r"(taddr)
-      : "memory");
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tc_wait32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
+                 "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                 "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -363,6 +364,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       const bool in = !kWide || b == 0 || both(u);
       const int node = u.node0 + min(row >> gs, u.nodes - 1);
       const uint32_t* anc = a.m.anc + (size_t)node * a.m.words;
+      const bool pad = __ldg(a.m.pos + node) < 0;
       float c = 0.f, m = -INFINITY, l = 0.f;
       if (in) {
         if constexpr (kWide) {
@@ -420,22 +422,43 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
         ++n;
         if (alive && mine) {
           tc_fence_after();
-          float mx = -INFINITY;
+          if (drafted) {  // rare: hide in place what the rows do not see
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t see = j == 0 ? vis[0] : j == 1 ? vis[1] : j == 2 ? vis[2] : vis[3];
+              if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+              uint32_t s[32];
+              tc_ld32(ts + j * 32, s);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t s[64];
-            tc_ld64(ts + h * 64, s);
-            if (drafted) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i)
-                if (!((vis[2 * h + (i >> 5)] >> (i & 31)) & 1u)) s[i] = 0xff800000u;  // -inf
+              for (int i = 0; i < 32; ++i)
+                if (!((see >> i) & 1u)) s[i] = 0xff800000u;  // -inf
+              tc_st16(ts + j * 32, s);
+              tc_st16(ts + j * 32 + 16, s + 16);
             }
-            float y[4] = {mx, mx, mx, mx};
+            tc_wait_st();
+          }
+          // two passes over S, 32 columns at a time, the next ones on their way while these are worked on (the loops stay
+          // loops: unrolled, the tile's code ran out of the instruction cache at every turn)
+          uint32_t sa[32], sb[32];
+          float mx = -INFINITY;
+          auto largest = [&](const uint32_t (&x)[32]) {
+            float y[2] = {mx, mx};
 #pragma unroll
-            for (int i = 0; i < 64; i += 8)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) y[z] = fmaxf(fmaxf(y[z], __uint_as_float(s[i + 2 * z])), __uint_as_float(s[i + 2 * z + 1]));
-            mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+            for (int i = 0; i < 32; i += 4) {
+              y[0] = fmaxf(fmaxf(y[0], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+              y[1] = fmaxf(fmaxf(y[1], __uint_as_float(x[i + 2])), __uint_as_float(x[i + 3]));
+            }
+            mx = fmaxf(y[0], y[1]);
+          };
+          tc_ld32_async(ts, sa);
+#pragma unroll 1
+          for (int j = 0; j < 4; j += 2) {
+            tc_wait32(sa);
+            tc_ld32_async(ts + j * 32 + 32, sb);
+            largest(sa);
+            tc_wait32(sb);
+            tc_ld32_async(ts + ((j * 32 + 64) & 127), sa);  // at the end the first columns again, for the weights
+            largest(sb);
           }
           mx *= c;
           if (__any_sync(0xffffffffu, mx > m + 8.f)) {
@@ -443,6 +466,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
             m = mn;
             l *= f;
             if (!first) {  // this group's products so far have run: its S was issued behind them
+              tc_wait32(sa);
 #pragma unroll 1
               for (int j = 0; j < D / 32; ++j) {
                 uint32_t o[32];
@@ -455,33 +479,45 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
             }
           }
           const float mu = m == -INFINITY ? 0.f : m;
+          uint64_t c2 = pack2(c, c), m2 = pack2(-mu, -mu), l2[2] = {0ull, 0ull};
           // s c - m in one rounding while that is small against the weights' own (2^-12 at 2^12); far out the product is
           // rounded as the maximum was, or the largest score would miss it by its own last place
-          const bool plain = !__any_sync(0xffffffffu, !(fabsf(mu) <= 4096.f));
-          const uint64_t c2 = plain ? pack2(c, c) : pack2(1.f, 1.f), m2 = plain ? pack2(-mu, -mu) : 0ull;
-          uint64_t l2[2] = {0ull, 0ull};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t s[32], p[16];
-            tc_ld32(ts + j * 32, s);
-            if (drafted) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((vis[j] >> i) & 1u)) s[i] = 0xff800000u;
-            }
-            if (!plain) {
+          if (__any_sync(0xffffffffu, !(fabsf(mu) <= 4096.f))) {
+            tc_wait32(sa);
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+              uint32_t s[32];
+              tc_ld32(ts + j * 32, s);
 #pragma unroll
               for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), c), -mu));
+              tc_st16(ts + j * 32, s);
+              tc_st16(ts + j * 32 + 16, s + 16);
             }
+            tc_wait_st();
+            tc_ld32_async(ts, sa);
+            c2 = pack2(1.f, 1.f);
+            m2 = 0ull;
+          }
+          auto weights = [&](const uint32_t (&x)[32], int j) {
+            uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 z = unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, m2));
+              const float2 z = unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, m2));
               const float ex = ex2(z.x), ey = ex2(z.y);
               l2[i & 1] = add2(l2[i & 1], pack2(ex, ey));
               const __half2 hh = __floats2half2_rn(ex, ey);
               p[i] = *reinterpret_cast<const uint32_t*>(&hh);
             }
             tc_st16(ts + j * 16, p);  // over scores that this thread has read
+          };
+#pragma unroll 1
+          for (int j = 0; j < 4; j += 2) {
+            tc_wait32(sa);
+            tc_ld32_async(ts + j * 32 + 32, sb);
+            weights(sa, j);
+            tc_wait32(sb);
+            if (j == 0) tc_ld32_async(ts + 64, sa);
+            weights(sb, j + 1);
           }
           const float2 lx = unpack2(add2(l2[0], l2[1]));
           l += lx.x + lx.y;
@@ -524,7 +560,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
         const bool whole = t0 == 0 && t1 == u.tiles, valid = row < all_rows;
         float* rec = tree_record(a, blockIdx.x, t0 == 0);
         const int j0 = max(t0 * kTK - u.ctx, 0), j1 = min(t1 * kTK - u.ctx, u.nodes);
-        const bool zero = L == 0.f || __ldg(a.m.pos + node) < 0;
+        const bool zero = L == 0.f || pad;
         if (whole) {
           const float inv = 1.0f / L;
           g0 *= inv;
@@ -537,9 +573,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
         for (int ch = ch0; ch < ch1; ch += 32) {
           uint32_t x[32];
           float v[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          if (has0) {
+          if (kWide || has0) {
             tc_ld32(o0 + ch, x);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(x[i]) * g0;
@@ -547,15 +581,30 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           if (!kWide && has1) {
             tc_ld32(o1 + ch, x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), g1, v[i]);
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), g1, has0 ? v[i] : 0.f);
           }
-          if (valid) {
+          if (valid && !whole) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 z = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-              if (whole) tree_store4(a.out, a.out_type, off + ch + i, zero ? make_float4(0.f, 0.f, 0.f, 0.f) : z);
-              else reinterpret_cast<float4*>(rec)[((ch + i) / 4) * kR + row_in] = z;  // whole lines per warp
+            for (int i = 0; i < 32; i += 4)  // whole lines per warp
+              reinterpret_cast<float4*>(rec)[((ch + i) / 4) * kR + row_in] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          } else if (valid) {
+            uint32_t h[16];
+            if (a.out_type == kTreeBf16) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const __nv_bfloat162 z = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                h[i] = *reinterpret_cast<const uint32_t*>(&z);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const __half2 z = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                h[i] = *reinterpret_cast<const uint32_t*>(&z);
+              }
             }
+            uint2* to_out = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + off + ch);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) to_out[i / 2] = zero ? make_uint2(0u, 0u) : make_uint2(h[i], h[i + 1]);
           }
           __syncwarp();
         }

@@ -52,6 +52,18 @@ __device__ __forceinline__ bool tree_sees(const TreeMeta& m, int node, int j) {
   return (__ldg(m.anc + (size_t)node * m.words + (j >> 5)) >> (j & 31)) & 1u;
 }
 
+// The two 16-bit elements of a word as fp32 (both conversions are exact).
+template <typename T>
+__device__ __forceinline__ float2 tree_pair(uint32_t w);
+template <>
+__device__ __forceinline__ float2 tree_pair<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 tree_pair<bf16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
 __device__ __forceinline__ float tree_load(const void* p, int type, int64_t i) {
   if (type == kTreeF32) return reinterpret_cast<const float*>(p)[i];
   if (type == kTreeF16) return __half2float(reinterpret_cast<const __half*>(p)[i]);
@@ -73,6 +85,13 @@ __device__ __forceinline__ float4 tree_load4(const void* p, int type, int64_t i)
   }
   return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
                      __uint_as_float(u.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ float4 tree_load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+template <typename T>
+__device__ __forceinline__ float4 tree_load4(const T* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const float2 x = tree_pair<T>(u.x), y = tree_pair<T>(u.y);
+  return make_float4(x.x, x.y, y.x, y.y);
 }
 __device__ __forceinline__ void tree_store4(void* p, int type, int64_t i, float4 v) {
   if (type == kTreeF32) {
@@ -100,18 +119,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// The two 16-bit elements of a word as fp32 (both conversions are exact).
-template <typename T>
-__device__ __forceinline__ float2 tree_pair(uint32_t w);
-template <>
-__device__ __forceinline__ float2 tree_pair<__half>(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-template <>
-__device__ __forceinline__ float2 tree_pair<bf16>(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
 // Load R rows of a unit's queries, from row0 on (at least one of them is
