@@ -225,94 +225,114 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
     }
   produced:;
   } else if (warp == 9) {
-    // ---- MMA issuer ----
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_f16(kTR, kTK, false), id_o = idesc_f16(kTR, D, true);
-      // a step along K only moves the descriptors' start addresses (their low bits, in 16-byte units)
-      const uint64_t q_desc = sw128_desc(smem_u32(dsm + SM::kQ)), ring_desc = sw128_desc(smem_u32(dsm + SM::kRing));
-      const uint64_t v_desc = sw128_mn_desc(smem_u32(dsm + SM::kRing), SM::kPanel);
-      // scores of tile k into group b's S, from query tile q
-      auto scores = [&](int k, int b, int q, bool last) -> bool {
-        const int li = 2 * k, slot = li % kS;
-        if (!mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err)) return false;
-        tc_fence_after();
-        const uint64_t qd = q_desc + q * (SM::kTile >> 4), kd = ring_desc + slot * (SM::kTile >> 4);
+    // ---- MMA issuer: the whole warp walks the tiles, one elected lane issues.  Everything that the MMAs' operands and the
+    // loops go by is broadcast, so that the compiler keeps it in uniform registers, where the MMAs take their operands from ----
+    constexpr uint32_t id_s = idesc_f16(kTR, kTK, false), id_o = idesc_f16(kTR, D, true);
+    auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    auto wait = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, abort_flag, a.m.err)) != 0;
+    };
+    uint32_t leader;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
+    const uint32_t td = uni(tmem), smem0 = uni(smem_u32(dsm));
+    // a step along K only moves the descriptors' start addresses (their low bits, in 16-byte units)
+    const uint64_t q_desc = sw128_desc(smem0 + SM::kQ), ring_desc = sw128_desc(smem0 + SM::kRing);
+    const uint64_t v_desc = sw128_mn_desc(smem0 + SM::kRing, SM::kPanel);
+    // scores of tile k into group b's S, from query tile q
+    auto scores = [&](int k, int b, int q, bool last) -> bool {
+      const int li = 2 * k, slot = li % kS;
+      if (!wait(&full[slot], li / kS)) return false;
+      tc_fence_after();
+      const uint64_t qd = q_desc + q * (SM::kTile >> 4), kd = ring_desc + slot * (SM::kTile >> 4);
+      if (leader) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint32_t off = ((i >> 2) * SM::kPanel + (i & 3) * 32) >> 4;
-          tc_mma(tmem + b * 128, qd + off, kd + off, id_s, i != 0);
+          tc_mma(td + b * 128, qd + off, kd + off, id_s, i != 0);
         }
         if (last) tc_commit(&empty[slot]);
         tc_commit(&sfull[b]);
-        return true;
-      };
-      auto values = [&](int k, int b, int n, bool fresh, bool last) -> bool {
-        const int li = 2 * k + 1, slot = li % kS;
-        if (!mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err)) return false;
-        if (!mbar_wait(&pfull[b], n & 1, abort_flag, a.m.err)) return false;
-        tc_fence_after();
-        const uint64_t vd = v_desc + slot * (SM::kTile >> 4);
+      }
+      __syncwarp();
+      return true;
+    };
+    // weights (tile n of group b) times values of tile k
+    auto values = [&](int k, int b, int n, bool fresh, bool last) -> bool {
+      const int li = 2 * k + 1, slot = li % kS;
+      if (!wait(&full[slot], li / kS) || !wait(&pfull[b], n)) return false;
+      tc_fence_after();
+      const uint64_t vd = v_desc + slot * (SM::kTile >> 4);
+      if (leader) {
 #pragma unroll
         for (int i = 0; i < kTK / 16; ++i)
-          tc_mma_ts(tmem + 256 + b * D, tmem + b * 128 + i * 8, vd + i * (2048 >> 4), id_o, i != 0 || !fresh);
+          tc_mma_ts(td + 256 + b * D, td + b * 128 + i * 8, vd + i * (2048 >> 4), id_o, i != 0 || !fresh);
         if (last) tc_commit(&empty[slot]);
-        return true;
+      }
+      __syncwarp();
+      return true;
+    };
+    const int count = uni(cut.count);
+    int k = 0;
+    if constexpr (!kWide) {
+      auto first_scores = [&](int x, int unit, bool first) -> bool {
+        if (first && !wait(&qfull[unit & 1], unit >> 1)) return false;
+        return scores(x, x & 1, unit & 1, true);
       };
-      int k = 0;
-      if constexpr (!kWide) {
-        auto first_scores = [&](int x, int unit, bool first) -> bool {
-          if (first && !mbar_wait(&qfull[unit & 1], (unit >> 1) & 1, abort_flag, a.m.err)) return false;
-          return scores(x, x & 1, unit & 1, true);
-        };
-        bool ok = cut.count == 0 || first_scores(0, 0, true);
-        for (int left = cut.count; ok && left > 0; ++n_unit) {
-          const int t0 = tile, t1 = min(u.tiles, tile + left);
-          if (n_unit > 0 && !mbar_wait(&oempty[0], (n_unit - 1) & 1, abort_flag, a.m.err)) break;
-          int fresh = 3;  // groups whose O this unit has not written yet
-          for (int t = t0; ok && t < t1; ++t, ++k) {
-            const int b = k & 1;
-            // the next tile's scores first: of this unit, or of the next one
-            ok = (k + 1 >= cut.count || first_scores(k + 1, n_unit + (t + 1 == t1), t + 1 == t1)) &&
-                 values(k, b, k >> 1, (fresh >> b) & 1, true);
-            fresh &= ~(1 << b);
-          }
-          if (!ok) break;
-          tc_commit(&ofull[0]);
-          left -= t1 - t0;
-          tile = 0;
-          if (left > 0) tree_unit_next(a.m, gs, kR, a.d.Hkv, u);
+      bool ok = count == 0 || first_scores(0, 0, true);
+      for (int left = count; ok && left > 0; ++n_unit) {
+        const int tiles = uni(min(u.tiles - tile, left));
+        if (n_unit > 0 && !wait(&oempty[0], n_unit - 1)) break;
+        int fresh = 3;  // groups whose O this unit has not written yet
+        for (int t = 0; ok && t < tiles; ++t, ++k) {
+          const int b = k & 1;
+          // the next tile's scores first: of this unit, or of the next one
+          ok = (k + 1 >= count || first_scores(k + 1, n_unit + (t + 1 == tiles), t + 1 == tiles)) &&
+               values(k, b, k >> 1, (fresh >> b) & 1, true);
+          fresh &= ~(1 << b);
         }
-      } else {
-        int n[2] = {0, 0}, units[2] = {0, 0};  // tiles and units of each group
-        auto first_scores = [&](int x, int b, const TreeUnit& v, bool first) -> bool {
-          if (b && !both(v)) return true;
-          if (first && !mbar_wait(&qfull[b], units[b] & 1, abort_flag, a.m.err)) return false;
-          return scores(x, b, b, b || !both(v));
-        };
-        bool ok = cut.count == 0 || (first_scores(0, 0, u, true) && first_scores(0, 1, u, true));
-        for (int left = cut.count; ok && left > 0;) {
-          const int t0 = tile, t1 = min(u.tiles, tile + left), groups = both(u) ? 2 : 1;
-          for (int b = 0; ok && b < groups; ++b)
-            if (units[b] > 0) ok = mbar_wait(&oempty[b], (units[b] - 1) & 1, abort_flag, a.m.err);
-          for (int t = t0; ok && t < t1; ++t, ++k) {
-            for (int b = 0; ok && b < groups; ++b) {
-              ok = values(k, b, n[b]++, t == t0, b == groups - 1);
-              if (t + 1 < t1) ok = ok && first_scores(k + 1, b, u, false);
-              else tc_commit(&ofull[b]);
-            }
-          }
-          if (!ok) break;
-          for (int b = 0; b < groups; ++b) ++units[b];
-          left -= t1 - t0;
-          tile = 0;
-          if (left > 0) {
-            tree_unit_next(a.m, gs, kR, a.d.Hkv, u);
-            ok = first_scores(k, 0, u, true) && first_scores(k, 1, u, true);
-          }
+        if (!ok) break;
+        if (leader) tc_commit(&ofull[0]);
+        left -= tiles;
+        tile = 0;
+        if (left > 0) tree_unit_next(a.m, gs, kR, a.d.Hkv, u);
+      }
+    } else {
+      int n0 = 0, n1 = 0, units0 = 0, units1 = 0;  // tiles and units of each group
+      int groups = uni(both(u) ? 2 : 1);
+      bool ok = true;
+      // the scores of a unit's first tile
+      auto first_scores = [&](int x) -> bool {
+        if (!wait(&qfull[0], units0) || !scores(x, 0, 0, groups == 1)) return false;
+        return groups == 1 || (wait(&qfull[1], units1) && scores(x, 1, 1, true));
+      };
+      if (count > 0) ok = first_scores(0);
+      for (int left = count; ok && left > 0;) {
+        const int tiles = uni(min(u.tiles - tile, left));
+        if (units0 > 0) ok = wait(&oempty[0], units0 - 1);
+        if (groups == 2 && units1 > 0) ok = ok && wait(&oempty[1], units1 - 1);
+        for (int t = 0; ok && t < tiles; ++t, ++k) {
+          const bool more = t + 1 < tiles;
+          ok = values(k, 0, n0++, t == 0, groups == 1);
+          if (ok && more) ok = scores(k + 1, 0, 0, groups == 1);
+          if (ok && !more && leader) tc_commit(&ofull[0]);
+          if (groups == 1) continue;
+          ok = ok && values(k, 1, n1++, t == 0, true);
+          if (ok && more) ok = scores(k + 1, 1, 1, true);
+          if (ok && !more && leader) tc_commit(&ofull[1]);
+        }
+        if (!ok) break;
+        ++units0;
+        units1 += groups - 1;
+        left -= tiles;
+        tile = 0;
+        if (left > 0) {
+          tree_unit_next(a.m, gs, kR, a.d.Hkv, u);
+          groups = uni(both(u) ? 2 : 1);
+          ok = first_scores(k);
         }
       }
-      tc_commit(mma_done);
     }
+    if (leader) tc_commit(mma_done);
     __syncwarp();
   } else if (warp >= 10) {
     // ---- queries one unit ahead (the first unit's by the softmax warps, which have nothing else to do yet) ----
