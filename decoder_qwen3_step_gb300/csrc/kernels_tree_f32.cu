@@ -39,7 +39,7 @@ __device__ __forceinline__ void cp_wait() {
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constant__ TreeAttendArgs a) {
+__global__ void __launch_bounds__(256, D == 128 ? 2 : 3) k_tree_attend_f32(const __grid_constant__ TreeAttendArgs a) {
   pdl_wait_prev();
   pdl_launch_next();
   const TreeCut cut = a.m.cuts[blockIdx.x];  // read beside the header, not behind it
@@ -95,13 +95,14 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
 #pragma unroll
         for (int e = 0; e < kW; ++e) o[i][c][e] = 0.f;
     }
+    bool odd = false;  // a node's value of this unit is not finite
     for (int t = t0; t < t1; ++t) {
       cp_wait<1>();
       __syncthreads();  // K of this tile (and, first time, Q)
       float s[kRows][4];
 #pragma unroll
       for (int i = 0; i < kRows; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
       for (int d = 0; d < D; d += 4) {
         float4 q[kRows], k[4];
 #pragma unroll
@@ -154,7 +155,19 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
       }
       cp_wait<1>();
       __syncthreads();  // V of this tile and the weights
-#pragma unroll 2
+      if (drafted) {
+        // a node's value that is not finite must not meet another branch's zero weights: zero it; its descendants get it
+        // back at the unit's end
+        bool found = false;
+#pragma unroll 1
+        for (int x = max(u.ctx - t * kTreeKeys, 0) * D + tid; x < kTreeKeys * D; x += 256)
+          if (!isfinite(Vs[x])) {
+            Vs[x] = 0.f;
+            found = true;
+          }
+        odd |= __syncthreads_or(found);
+      }
+#pragma unroll 1
       for (int k0 = 0; k0 < kTreeKeys; k0 += 4) {
         float p[kRows][4];
 #pragma unroll
@@ -170,23 +183,22 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
 #pragma unroll
           for (int c = 0; c < kVec; ++c) {
             float v[kW];
-#pragma unroll
-            for (int e = 0; e < kW; e += 2) {
-              const float2 w = *reinterpret_cast<const float2*>(Vs + (k0 + k) * D + c * 64 + tx * kW + e);
-              v[e] = w.x;
-              v[e + 1] = w.y;
-            }
-            if (drafted) {  // a masked node's value may be anything: 0 * inf must not reach the sum
-#pragma unroll
-              for (int i = 0; i < kRows; ++i)
-#pragma unroll
-                for (int e = 0; e < kW; ++e) o[i][c][e] = fmaf(p[i][k], p[i][k] == 0.f ? 0.f : v[e], o[i][c][e]);
+            const float* at = Vs + (k0 + k) * D + c * 64 + tx * kW;
+            if constexpr (kW == 4) {
+              const float4 w = *reinterpret_cast<const float4*>(at);
+              v[0] = w.x;
+              v[1] = w.y;
+              v[2] = w.z;
+              v[3] = w.w;
             } else {
-#pragma unroll
-              for (int i = 0; i < kRows; ++i)
-#pragma unroll
-                for (int e = 0; e < kW; ++e) o[i][c][e] = fmaf(p[i][k], v[e], o[i][c][e]);
+              const float2 w = *reinterpret_cast<const float2*>(at);
+              v[0] = w.x;
+              v[1] = w.y;
             }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+#pragma unroll
+              for (int e = 0; e < kW; ++e) o[i][c][e] = fmaf(p[i][k], v[e], o[i][c][e]);
           }
       }
       __syncthreads();  // every thread is done with V and the weights
@@ -204,17 +216,43 @@ __global__ void __launch_bounds__(256, 2) k_tree_attend_f32(const __grid_constan
       const int r = ty + 16 * i, row = u.row_tile * R + r;
       if (r >= rows) continue;
       const int node = u.node0 + (row >> gs);
+      if (odd) {  // rare: the values that were taken out, for the rows that see them
+#pragma unroll 1
+        for (int n = max(t0 * kTreeKeys - u.ctx, 0); n < min(t1 * kTreeKeys - u.ctx, u.nodes); ++n) {
+          if (!tree_sees(a.m, node, n)) continue;
+          const int p = u.ctx + n;
+          const float* at = reinterpret_cast<const float*>(a.kv) +
+                            kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D);
+#pragma unroll
+          for (int c = 0; c < kVec; ++c)
+#pragma unroll
+            for (int e = 0; e < kW; ++e) {
+              const float v = at[c * 64 + tx * kW + e];
+              if (!isfinite(v)) o[i][c][e] += v;
+            }
+        }
+      }
       const bool zero = __ldg(a.m.pos + node) < 0 || l[i] == 0.f;
-      const float inv = 1.0f / l[i];
+      const float f = whole ? 1.0f / l[i] : 1.f;
       const int64_t off = node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D;
 #pragma unroll
-      for (int c = 0; c < kVec; ++c)
+      for (int c = 0; c < kVec; ++c) {
+        const int d = c * 64 + tx * kW;
+        float v[kW];
 #pragma unroll
-        for (int e = 0; e < kW; ++e) {
-          const int d = c * 64 + tx * kW + e;
-          if (whole) tree_store(a.out, a.out_type, off + d, zero ? 0.f : o[i][c][e] * inv);
-          else rec[r * D + d] = o[i][c][e];
+        for (int e = 0; e < kW; ++e) v[e] = whole && zero ? 0.f : o[i][c][e] * f;
+        if constexpr (kW == 4) {
+          const float4 w = make_float4(v[0], v[1], v[2], v[3]);
+          if (whole) tree_store4(a.out, a.out_type, off + d, w);
+          else *reinterpret_cast<float4*>(rec + r * D + d) = w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < kW; ++e) {
+            if (whole) tree_store(a.out, a.out_type, off + d + e, v[e]);
+            else rec[r * D + d + e] = v[e];
+          }
         }
+      }
       if (!whole && tx == 0) {
         rec[R * D + r] = m[i];
         rec[R * D + R + r] = l[i];

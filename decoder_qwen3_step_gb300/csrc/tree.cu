@@ -47,7 +47,7 @@ struct TreeLayout {
 // Which attention kernel takes a batch whose widest sequence has max_rows rows
 // (nodes x query heads per KV head).
 TreeVariant variant_for(bool f16, int D, int max_rows) {
-  if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, 2, 2};
+  if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2};
   if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, 4};
   if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, 4};
   return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2};

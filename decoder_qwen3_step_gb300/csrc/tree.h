@@ -95,7 +95,7 @@ struct TreeVariant {
   int kernel, row_tile, tile_keys, ctas_per_sm;
   int unit_cost;  // what starting and finishing a unit costs a CTA, in key tiles
 };
-constexpr int kTreeMaxCtasPerSm = 2;
+constexpr int kTreeMaxCtasPerSm = 3;
 cudaError_t launch_tree_attend_f32(const TreeAttendArgs& a, int ctas, cudaStream_t s);
 cudaError_t launch_tree_attend_f16(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s);
 cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, bool wide, cudaStream_t s);
