@@ -77,11 +77,14 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
     flags[0] = flags[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // the plan is older than the kernels before this one: read before they are waited for
+  const int here = tree_place();
+  const TreeCut cut = a.m.cuts[here];
+  const bool ok_shape = tree_shape_ok(a.m, true);
   __syncthreads();
   pdl_wait_prev();
   pdl_launch_next();
-  const TreeCut cut = a.m.cuts[blockIdx.x];  // read beside the header, not behind it
-  if (!tree_shape_ok(a.m, true)) return;
+  if (!ok_shape) return;
   volatile int* abort_flag = flags;
   const int gs = a.d.gs, G = 1 << gs;
   TreeUnit u = tree_unit_first(a.m, cut);
@@ -309,7 +312,10 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
         }
       }
       const bool whole = t0 == 0 && t1 == u.tiles;
-      float* rec = tree_record(a, blockIdx.x, t0 == 0);
+      float* rec = tree_record(a, here, t0 == 0);
+      const int follow = !whole && t0 == 0 ? cut.follow : 0;  // CTAs whose parts are joined here
+      // to join, this CTA's part goes to the ring, which is idle: the unit is its last
+      float* own = reinterpret_cast<float*>(dsm);
       const int j0 = max(t0 * kTreeKeys - u.ctx, 0), j1 = min(t1 * kTreeKeys - u.ctx, u.nodes);
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {  // 16 channels at a time
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
             v = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
             tree_store4(a.out, a.out_type, node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D + j * 16 + x, v);
           } else {
-            *reinterpret_cast<float4*>(rec + r * D + j * 16 + x) = v;
+            *reinterpret_cast<float4*>((follow ? own : rec) + r * D + j * 16 + x) = v;
           }
         }
         group_bar();
@@ -366,9 +372,63 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
           float L = 0.f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) L += M == -INFINITY ? 0.f : ml[(4 + w) * R + r] * ex2(ml[w * R + r] - M);
-          rec[R * D + r] = M;
-          rec[R * D + R + r] = L;
+          float* to = follow ? own : rec;
+          to[R * D + r] = M;
+          to[R * D + R + r] = L;
         }
+      if (follow) {
+        // every part's maxima and sums in one round trip, then the sums of the parts; a thread has the four channels 4 c ..
+        // of kRows rows and up to 16 loads in flight
+        float* mm = own + R * (D + 2);  // [follow + 1][R] maxima, own first, and as many sums behind them
+        float* ll = mm + (follow + 1) * R;
+        if (threadIdx.x < follow) tree_await(a.m, here + (threadIdx.x + 1) * cut.step);
+        group_bar();
+        for (int x = threadIdx.x; x < (follow + 1) * R; x += 128) {
+          const float* p = x < R ? own : tree_record(a, here + x / R * cut.step, false);
+          mm[x] = x < R ? p[R * D + x] : __ldcg(p + R * D + x % R);
+          ll[x] = x < R ? p[R * D + R + x] : __ldcg(p + R * D + R + x % R);
+        }
+        group_bar();
+        constexpr int kLanes = D / 4, kRows = R * kLanes / 128;
+        const int c = threadIdx.x % kLanes;
+        float M[kRows], L[kRows];
+        float4 v[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int r = threadIdx.x / kLanes + i * (128 / kLanes);
+          M[i] = -INFINITY;
+          for (int x = 0; x <= follow; ++x) M[i] = fmaxf(M[i], mm[x * R + r]);
+          if (M[i] == -INFINITY) M[i] = 0.f;
+          const float f = ex2(mm[r] - M[i]);
+          L[i] = ll[r] * f;
+          const float4 y = *reinterpret_cast<const float4*>(own + r * D + c * 4);
+          v[i] = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+        }
+#pragma unroll 4
+        for (int x = 1; x <= follow; ++x) {
+          const float* p = tree_record(a, here + x * cut.step, false);
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const int r = threadIdx.x / kLanes + i * (128 / kLanes);
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + min(r, rows - 1) * D + c * 4));
+            const float f = ex2(mm[x * R + r] - M[i]);
+            L[i] = fmaf(ll[x * R + r], f, L[i]);
+            v[i] = make_float4(fmaf(y.x, f, v[i].x), fmaf(y.y, f, v[i].y), fmaf(y.z, f, v[i].z), fmaf(y.w, f, v[i].w));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int r = threadIdx.x / kLanes + i * (128 / kLanes), row = u.row_tile * R + r, node = u.node0 + (row >> gs);
+          if (r >= rows) continue;
+          const bool zero = L[i] == 0.f || __ldg(a.m.pos + node) < 0;
+          const float inv = 1.0f / L[i];
+          tree_store4(a.out, a.out_type, node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D + c * 4,
+                      zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v[i].x * inv, v[i].y * inv, v[i].z * inv, v[i].w * inv));
+        }
+      } else if (!whole && t0 > 0) {
+        group_bar();
+        if (threadIdx.x == 0) tree_publish(a.m, here);
+      }
       if (threadIdx.x == 0) flags[1] = 0;
       group_bar();  // the statistics and the flag are free again
       left -= t1 - t0;
@@ -377,6 +437,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
     }
   }
   __syncthreads();
+  if (threadIdx.x < cut.follow) a.m.flags[here + (threadIdx.x + 1) * cut.step] = 0;
   // after an abort, let the copies still in flight land before the CTA exits
   if (warp == 4 && lane == 0 && *abort_flag) {
     const uint64_t w0 = global_ns();
@@ -396,18 +457,13 @@ cudaError_t one(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaSt
   return launch_pdl(k_tree_attend_f16<D, R>, ctas, kF16Threads, smem, s, *tm, a);
 }
 
-template <int D>
-cudaError_t pick(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
-  return a.m.row_tile == 16 ? one<D, 16>(a, tm, ctas, s) : one<D, 32>(a, tm, ctas, s);
-}
-
 }  // namespace
 
 cudaError_t launch_tree_attend_f16(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
   switch (a.d.D) {
-    case 32: return pick<32>(a, tm, ctas, s);
-    case 64: return pick<64>(a, tm, ctas, s);
-    case 128: return pick<128>(a, tm, ctas, s);
+    case 32: return a.m.row_tile == 16 ? one<32, 16>(a, tm, ctas, s) : one<32, 32>(a, tm, ctas, s);
+    case 64: return one<64, 16>(a, tm, ctas, s);
+    case 128: return one<128, 16>(a, tm, ctas, s);
     default: return cudaErrorInvalidValue;
   }
 }

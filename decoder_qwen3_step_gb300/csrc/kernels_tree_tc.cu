@@ -158,11 +158,14 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
     for (int i = 0; i < 8; ++i) flags[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // the plan is older than the kernels before this one: read before they are waited for
+  const int here = tree_place();
+  const TreeCut cut = a.m.cuts[here];
+  const bool ok_shape = tree_shape_ok(a.m, true);
   __syncthreads();
   pdl_wait_prev();
   pdl_launch_next();
-  const TreeCut cut = a.m.cuts[blockIdx.x];  // read beside the header, not behind it
-  if (!tree_shape_ok(a.m, true)) return;
+  if (!ok_shape) return;
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(flags + 1)), "r"(kTmemCols)
                  : "memory");
@@ -574,18 +577,38 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
         asm volatile("bar.sync 1, 256;" ::: "memory");
         mbar_arrive(&qempty[n_unit & 1]);
       }
+      const bool whole = t0 == 0 && t1 == u.tiles;
+      const int follow = !whole && t0 == 0 ? cut.follow : 0;  // CTAs whose parts are joined here
+      const bool final = whole || follow;
+      if (in && follow) {
+        if (st < follow) tree_await(a.m, here + (st + 1) * cut.step);
+        group_bar();
+      }
       if (in && alive && mine) {
         tc_fence_after();
         const bool odd = reinterpret_cast<volatile int*>(flags)[4 + (n_unit & 1)] == n_unit + 1;
-        const bool whole = t0 == 0 && t1 == u.tiles, valid = row < all_rows;
-        float* rec = tree_record(a, blockIdx.x, t0 == 0);
+        const bool valid = row < all_rows;
+        float* rec = tree_record(a, here, t0 == 0);
         const int j0 = max(t0 * kTK - u.ctx, 0), j1 = min(t1 * kTK - u.ctx, u.nodes);
-        const bool zero = L == 0.f || pad;
-        if (whole) {
-          const float inv = 1.0f / L;
-          g0 *= inv;
-          g1 *= inv;
+        // the parts that are joined: record y - 1's rows, their common maximum and sum
+        auto part = [&](int y) -> const float* { return tree_record(a, here + y * cut.step, false); };
+        float top = M;
+        for (int y = 1; y <= follow; ++y) top = fmaxf(top, __ldcg(part(y) + kR * D + row_in));
+        const float mu = top == -INFINITY ? 0.f : top;
+        if (follow) {
+          const float own = ex2(M - mu);
+          L *= own;
+          g0 *= own;
+          g1 *= own;
+          for (int y = 1; y <= follow; ++y) {
+            const float* p = part(y) + kR * D + row_in;
+            L = fmaf(__ldcg(p + kR), ex2(__ldcg(p) - mu), L);
+          }
         }
+        const bool zero = L == 0.f || pad;
+        const float inv = final ? 1.0f / L : 1.f;
+        g0 *= inv;
+        g1 *= inv;
         const int64_t off = node * a.ldo + (int64_t)((u.head << gs) + (row & (G - 1))) * D;
         const int ch0 = kWide ? 0 : b * (D / 2), ch1 = kWide ? D : (b + 1) * (D / 2);
         const uint32_t o0 = kWide ? to : trow + 256, o1 = trow + 256 + D;
@@ -603,7 +626,20 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(x[i]), g1, has0 ? v[i] : 0.f);
           }
-          if (valid && !whole) {
+#pragma unroll 1
+          for (int y = 1; y <= follow; ++y) {
+            const float f = ex2(__ldcg(part(y) + kR * D + row_in) - mu) * inv;
+            const float4* p = reinterpret_cast<const float4*>(part(y)) + (ch / 4) * kR + row_in;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 z = __ldcg(p + i * kR);
+              v[4 * i] = fmaf(z.x, f, v[4 * i]);
+              v[4 * i + 1] = fmaf(z.y, f, v[4 * i + 1]);
+              v[4 * i + 2] = fmaf(z.z, f, v[4 * i + 2]);
+              v[4 * i + 3] = fmaf(z.w, f, v[4 * i + 3]);
+            }
+          }
+          if (valid && !final) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)  // whole lines per warp
               reinterpret_cast<float4*>(rec)[((ch + i) / 4) * kR + row_in] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -640,12 +676,12 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
             for (int i = ch0; i < ch1; ++i) {
               const float z = __half2float(at[i]);
               if (isfinite(z)) continue;
-              if (whole) tree_store(a.out, a.out_type, off + i, tree_load(a.out, a.out_type, off + i) + z);
+              if (final) tree_store(a.out, a.out_type, off + i, tree_load(a.out, a.out_type, off + i) + z);
               else rec[((i / 4) * kR + row_in) * 4 + (i & 3)] += z;
             }
           }
         }
-        if (!whole && valid && (kWide || b == 0)) {
+        if (!final && valid && (kWide || b == 0)) {
           rec[kR * D + row_in] = M;
           rec[kR * D + kR + row_in] = L;
         }
@@ -654,6 +690,10 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       if (in) {
         mbar_arrive(&oempty[kWide ? b : 0]);  // O may be written again
         ++units;
+      }
+      if (!whole && t0 > 0) {  // a part for another CTA: both groups have written it (a group that sat out has nothing to)
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (threadIdx.x == 0) tree_publish(a.m, here);
       }
       left -= t1 - t0;
       tile = 0;
@@ -672,6 +712,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       while (!mbar_try(&full[i % kS], (i / kS) & 1) && global_ns() - w0 < kWaitLimitNs) {
       }
   __syncthreads();
+  if (threadIdx.x < cut.follow) a.m.flags[here + (threadIdx.x + 1) * cut.step] = 0;
   if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");

@@ -58,8 +58,8 @@ constexpr int kRecordRows = 2 * 256;
 TreeLayout tree_layout(const dec_config& c, int max_seqs, int max_tokens, int max_blocks, int sms) {
   TreeLayout L{};
   const size_t S = max_seqs, N = max_tokens, P = (size_t)sms * kTreeMaxCtasPerSm;
-  // header, seq_start, seqs, pos, dst, parents, mask, cuts, merges, tables (each piece 16-byte aligned)
-  L.meta_ints = kHdrInts + (S + 1) + 8 * S + 3 * N + N * (kTreeMaxNodes / 32) + P * 24 + S * (size_t)max_blocks + 16 * 4;
+  // header, flags, seq_start, seqs, pos, dst, parents, mask, cuts, merges, tables (each piece 16-byte aligned)
+  L.meta_ints = kHdrInts + P + (S + 1) + 8 * S + 3 * N + N * (kTreeMaxNodes / 32) + P * 24 + S * (size_t)max_blocks + 16 * 4;
   L.meta = 256;
   L.part = up256(L.meta + L.meta_ints * 4);
   L.total = up256(L.part + (size_t)sms * kRecordRows * (size_t)(c.head_dim + 2) * 4);
@@ -191,8 +191,10 @@ int check_trees(const dec_pool* pool, const dec_tree_batch* b) {
 // `max_gang`) that walk the same keys at the same time, so that a tile's
 // second reader finds it in L2.  The gangs of a class cut its (sequence, head)
 // list into equal runs, a unit's start and end counted as unit_cost tiles.
+// *join: few CTAs share a unit, and the one that starts it joins the others'
+// parts by itself (cuts' follow is set); else they are merges.
 int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVariant& var, int grid, int max_gang, TreeCut* cut,
-               TreeMerge* mrg) {
+               TreeMerge* mrg, bool* join) {
   const int G = c.n_heads / c.n_kv_heads, R = var.row_tile, K = var.tile_keys, Hkv = c.n_kv_heads;
   auto row_tiles = [&](const TreeSeq& s) { return (s.nodes * G + R - 1) / R; };
   auto tiles = [&](const TreeSeq& s) { return (s.ctx + s.nodes + K - 1) / K; };
@@ -283,12 +285,26 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
         mrg[n_mrg++] = {w.head, rt, cta + (i - 1) * g + member, cta + last * g + member, g, seqs[w.q].node0, seqs[w.q].nodes, 0};
       }
     }
-    cta += n * g;
-    for (int i = used * g; i < n * g; ++i) cut[cta - n * g + i] = {};
+    cta += used * g;
     q0 = q1;
   }
-  for (; cta < grid; ++cta) cut[cta] = {};
-  return n_mrg;
+  // the first blocks take the last places: none without work before one that has some
+  const int idle = grid - cta;
+  std::copy_backward(cut, cut + cta, cut + grid);
+  std::fill(cut, cut + idle, TreeCut{});
+  for (int i = 0; i < n_mrg; ++i) {
+    mrg[i].c0 += idle;
+    mrg[i].c1 += idle;
+  }
+  // Joining costs a fence, a flag's round trip and the reads behind it, some 5 us at the end of the call; a second kernel
+  // costs about 3 us where the records are few or small (1 sequence x 5 nodes over 500 keys: 9.3 us against 11.8), and
+  // more with the records of a full batch (32 x 64 nodes at 1024-2048: 61 us against 56; at most two parts to join there).
+  *join = true;
+  for (int i = 0; i < n_mrg; ++i)
+    if ((mrg[i].c1 - mrg[i].c0) / mrg[i].stride > 2) *join = false;
+  if (!*join) return n_mrg;
+  for (int i = 0; i < n_mrg; ++i) cut[mrg[i].c0].follow = (mrg[i].c1 - mrg[i].c0) / mrg[i].stride;
+  return 0;
 }
 
 // Fill the pinned image of the plan and the kernels' view of its upload;
@@ -303,7 +319,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   const int W = std::max((max_nodes + 31) / 32, 1);
   const TreeVariant var = variant_for(t->f16, c.head_dim, max_nodes * G);
   const int grid = t->sms * var.ctas_per_sm;
-  const size_t h_hdr = take(kHdrInts), h_start = take(S + 1), h_seqs = take((size_t)S * 8), h_pos = take(N), h_dst = take(N),
+  const size_t h_hdr = take(kHdrInts), h_flags = take((size_t)t->sms * kTreeMaxCtasPerSm), h_start = take(S + 1), h_seqs = take((size_t)S * 8), h_pos = take(N), h_dst = take(N),
                h_par = take(N), h_anc = take((size_t)N * W), h_cut = take((size_t)grid * 16), h_mrg = take((size_t)grid * 8),
                h_tables = o;
   std::vector<TreeSeq> seqs;
@@ -336,8 +352,10 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   }
   H[h_start + S] = N;
   // only the wide kernel has the rows of a sequence walk the keys side by side; at most 1024 rows: gangs of four
+  bool join = false;
   const int n_mrg = distribute(c, seqs, var, grid, var.kernel == kTreeTcWide ? 4 : 1, reinterpret_cast<TreeCut*>(H + h_cut),
-                               reinterpret_cast<TreeMerge*>(H + h_mrg));
+                               reinterpret_cast<TreeMerge*>(H + h_mrg), &join);
+  std::fill(H + h_flags, H + h_flags + t->sms * kTreeMaxCtasPerSm, 0);
   std::copy(seqs.begin(), seqs.end(), reinterpret_cast<TreeSeq*>(H + h_seqs));
   std::fill(H + h_hdr, H + h_hdr + kHdrInts, 0);
   H[h_hdr + kHdrSeqs] = S;
@@ -345,6 +363,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   H[h_hdr + kHdrWords] = W;
   H[h_hdr + kHdrRowTile] = var.row_tile;
   H[h_hdr + kHdrMerges] = n_mrg;
+  H[h_hdr + kHdrJoin] = join;
   int32_t* d = reinterpret_cast<int32_t*>(t->ws + t->lay.meta);
   TreeMeta& m = t->meta;
   m.hdr = d + h_hdr;
@@ -358,6 +377,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   m.merges = reinterpret_cast<const TreeMerge*>(d + h_mrg);
   m.tables = d + h_tables;
   m.err = reinterpret_cast<uint32_t*>(t->ws);
+  m.flags = reinterpret_cast<uint32_t*>(d + h_flags);
   m.S = S;
   m.N = N;
   m.words = W;

@@ -18,7 +18,7 @@ constexpr uint32_t kErrShape = 16u; // a captured call met a plan of another sha
 enum TreeType { kTreeF32 = 0, kTreeF16 = 1, kTreeBf16 = 2 };
 
 // Header words of the uploaded plan.
-enum TreeHdr { kHdrSeqs = 0, kHdrTokens, kHdrWords, kHdrRowTile, kHdrMerges, kHdrInts = 16 };
+enum TreeHdr { kHdrSeqs = 0, kHdrTokens, kHdrWords, kHdrRowTile, kHdrMerges, kHdrJoin, kHdrInts = 16 };
 
 // A sequence with nodes, as the attention kernels read it (two 16-byte loads).
 struct alignas(16) TreeSeq {
@@ -31,7 +31,9 @@ struct alignas(16) TreeSeq {
 // next head's row_tile % step.
 struct alignas(16) TreeCut {
   int32_t q, head, row_tile, tile;
-  int32_t count, step, pad0, pad1;
+  int32_t count, step;
+  int32_t follow;  // CTAs cta + step, cta + 2 step, .. that finish this one's last unit, for this one to join
+  int32_t pad;
   TreeSeq s;  // seqs[q]: a CTA starts with a single read
 };
 // A unit (sequence, KV head, row tile) that CTAs c0, c0 + stride, .., c1 share.
@@ -53,6 +55,7 @@ struct TreeMeta {
   const TreeMerge* merges;   // [hdr[kHdrMerges]]
   const int32_t* tables;     // pool block ids, sequence after sequence
   uint32_t* err;             // device error word
+  uint32_t* flags;           // a word per place: its part of a shared unit is there
   int S, N, words, row_tile; // the shape the launch was made for (checked against hdr)
   int tile_keys;             // keys per attention tile
 };

@@ -115,6 +115,38 @@ __device__ __forceinline__ float* tree_record(const TreeAttendArgs& a, int cta, 
   return a.part + ((size_t)cta * 2 + leaves) * a.m.row_tile * (a.d.D + 2);
 }
 
+// ---- joining shared units without a second launch -------------------------------
+// The CTA that starts a unit (and whose run ends in it) joins the parts of the
+// CTAs that finish it: each of those publishes its record, the first thing of
+// its run, with a flag, and the joining CTA waits for the flags at its own end
+// and clears them at its exit.  What a CTA waits for lies behind its place, and
+// the last place is the first block's, so it waits only for blocks that were
+// started before it (a place from an atomic ticket instead cost 3 us of a 9 us
+// call).
+__device__ __forceinline__ int tree_place() { return gridDim.x - 1 - blockIdx.x; }
+// After a barrier behind the record's stores; one thread.
+__device__ __forceinline__ void tree_publish(const TreeMeta& m, int place) {
+  __threadfence();
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(m.flags + place), "r"(1u) : "memory");
+}
+// Wait for the record of `place` (one thread; a barrier then spreads it).  Gives up after a second.
+__device__ __forceinline__ void tree_await(const TreeMeta& m, int place) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(m.flags + place) : "memory");
+    if (v) break;
+    uint64_t now;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+    if (!t0) t0 = now;
+    if (now - t0 > 1000000000ull) {
+      atomicOr(m.err, kErrTimeout);
+      break;
+    }
+  }
+  __threadfence();
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
