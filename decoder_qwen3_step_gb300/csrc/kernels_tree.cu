@@ -33,10 +33,11 @@ __global__ void k_rope_table(const __grid_constant__ RopeTableArgs a) {
 // same lane (interleaved) or rot/8 lanes away (halves), one shuffle.
 template <int D, int U, typename T>
 __global__ void __launch_bounds__(256, U == 4 && sizeof(T) == 4 ? 5 : 4) k_tree_append(const __grid_constant__ TreeAppendArgs a) {
+  constexpr int kLanes = D / 4, kSlots = 256 / kLanes;
+  const bool ok = tree_shape_ok(a.m);  // the plan is older than the kernels before this one
   pdl_wait_prev();
   pdl_launch_next();
-  constexpr int kLanes = D / 4, kSlots = 256 / kLanes;
-  if (!tree_shape_ok(a.m)) return;
+  if (!ok) return;
   const int H = a.q ? a.d.H : 0, Hkv = a.k ? a.d.Hkv : 0, cq = (H + U - 1) / U, ck = (Hkv + U - 1) / U;
   const int lane = threadIdx.x % kLanes, el = lane * 4, half = a.rot >> 1;
   const uint32_t id = blockIdx.x * kSlots + threadIdx.x / kLanes, per = cq + 2 * ck;
@@ -133,13 +134,14 @@ constexpr int kCommitThreads = 256;
 
 __global__ void __launch_bounds__(kCommitThreads) k_tree_commit(const __grid_constant__ TreeCommitArgs a, int cols,
                                                                 int blocks_per_seq) {
+  __shared__ int child[kTreeMaxNodes + 1], path[kTreeMaxNodes], n_path;
+  const int s = blockIdx.x / blocks_per_seq, part = blockIdx.x % blocks_per_seq;
+  const bool ok = tree_shape_ok(a.m);  // the plan is older than the kernels before this one
+  const int b = __ldg(a.m.seq_start + s), T = min(__ldg(a.m.seq_start + s + 1) - b, kTreeMaxNodes);
+  for (int i = threadIdx.x; i <= T; i += kCommitThreads) child[i] = INT_MAX;
   pdl_wait_prev();
   pdl_launch_next();
-  __shared__ int child[kTreeMaxNodes + 1], path[kTreeMaxNodes], n_path;
-  if (!tree_shape_ok(a.m)) return;
-  const int s = blockIdx.x / blocks_per_seq, part = blockIdx.x % blocks_per_seq;
-  const int b = __ldg(a.m.seq_start + s), T = __ldg(a.m.seq_start + s + 1) - b;
-  for (int i = threadIdx.x; i <= T; i += kCommitThreads) child[i] = INT_MAX;
+  if (!ok) return;
   __syncthreads();
   for (int i = threadIdx.x; i < T; i += kCommitThreads) {
     const int p = __ldg(a.m.parents + b + i);
@@ -195,14 +197,15 @@ __global__ void __launch_bounds__(kCommitThreads) k_tree_commit(const __grid_con
 // unit that 38 CTAs shared are two rounds of loads instead of ten.
 template <int D, int kWarps>
 __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ TreeAttendArgs a) {
-  pdl_wait_prev();
-  pdl_launch_next();
   constexpr int kPer = D / 32, kRows = 4 / kWarps;
   __shared__ float part[kWarps == 1 ? 1 : 4][D + 1];
   const int R = a.m.row_tile, gs = a.d.gs, G = 1 << gs, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = R / kRows;
-  TreeMerge e = a.m.merges[blockIdx.x / groups];  // read beside the header, not behind it
+  TreeMerge e = a.m.merges[blockIdx.x / groups];  // the plan is older than the kernels before this one
   const int n = __ldg(a.m.hdr + kHdrMerges);
-  if (!tree_shape_ok(a.m, true)) return;
+  const bool ok = tree_shape_ok(a.m, true);
+  pdl_wait_prev();
+  pdl_launch_next();
+  if (!ok) return;
   for (int w = blockIdx.x; w < n * groups; w += gridDim.x) {
     if (w != blockIdx.x) e = a.m.merges[w / groups];
     const int r = (w % groups) * kRows + warp / kWarps, c_first = warp % kWarps;
@@ -272,32 +275,41 @@ cudaError_t merge_rows(const TreeAttendArgs& a, int n_merges, cudaStream_t s) {
 
 // The same for the row tiles of wide trees (128 or 256 rows), whose records
 // are channel-major ([D/4][R] of four channels, then maxima and sums): thread =
-// row, kC channels per block, so the reads are whole lines.
-template <int D, int kC>
-__global__ void __launch_bounds__(128) k_tree_merge_wide(const __grid_constant__ TreeAttendArgs a) {
+// row, kC channels per block, so the reads are whole lines.  kG groups of 128
+// threads share the records of a row.
+template <int D, int kC, int kG>
+__global__ void __launch_bounds__(128 * kG) k_tree_merge_wide(const __grid_constant__ TreeAttendArgs a) {
+  constexpr int kSlabs = D / kC;
+  __shared__ float top[kG][128], sum[kG][128];
+  __shared__ float4 part[kG == 1 ? 1 : kG][kC / 4][128];
+  const int gs = a.d.gs, R = a.m.row_tile, per = kSlabs * (R / 128), grp = threadIdx.x >> 7, t = threadIdx.x & 127;
+  TreeMerge e = a.m.merges[blockIdx.x / per];  // the plan is older than the kernels before this one
+  const int n = __ldg(a.m.hdr + kHdrMerges);
+  const bool ok = tree_shape_ok(a.m, true);
   pdl_wait_prev();
   pdl_launch_next();
-  constexpr int kSlabs = D / kC;
-  const int gs = a.d.gs, R = a.m.row_tile, per = kSlabs * (R / 128);
-  TreeMerge e = a.m.merges[blockIdx.x / per];  // read beside the header, not behind it
-  const int n = __ldg(a.m.hdr + kHdrMerges);
-  if (!tree_shape_ok(a.m, true)) return;
+  if (!ok) return;
   for (int w = blockIdx.x; w < n * per; w += gridDim.x) {
     if (w != blockIdx.x) e = a.m.merges[w / per];
-    const int d0 = (w % kSlabs) * kC, r = (w % per) / kSlabs * 128 + threadIdx.x, row = e.row_tile * R + r;
-    if (row >= e.nodes << gs) continue;
-    const int node = e.node0 + (row >> gs), n_rec = (e.c1 - e.c0) / e.stride + 1;
+    const int d0 = (w % kSlabs) * kC, r = (w % per) / kSlabs * 128 + t, row = e.row_tile * R + r;
+    const int node = e.node0 + min(row >> gs, e.nodes - 1), n_rec = (e.c1 - e.c0) / e.stride + 1;
     auto rec = [&](int c) -> const float* { return tree_record(a, e.c0 + c * e.stride, c == 0); };
     float M = -INFINITY;
 #pragma unroll 8
-    for (int c = 0; c < n_rec; ++c) M = fmaxf(M, __ldcg(rec(c) + R * D + r));
+    for (int c = grp; c < n_rec; c += kG) M = fmaxf(M, __ldcg(rec(c) + R * D + r));
+    if constexpr (kG > 1) {
+      top[grp][t] = M;
+      __syncthreads();
+#pragma unroll
+      for (int g = 0; g < kG; ++g) M = fmaxf(M, top[g][t]);
+    }
     if (M == -INFINITY) M = 0.f;  // no contribution saw a finite score
     float L = 0.f;
     float4 o[kC / 4];
 #pragma unroll
     for (int i = 0; i < kC / 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll kC == 4 ? 8 : 2
-    for (int c = 0; c < n_rec; ++c) {
+    for (int c = grp; c < n_rec; c += kG) {
       const float* p = rec(c);
       const float f = ex2(__ldcg(p + R * D + r) - M);
       L = fmaf(__ldcg(p + R * D + R + r), f, L);
@@ -310,6 +322,25 @@ __global__ void __launch_bounds__(128) k_tree_merge_wide(const __grid_constant__
         o[i].w = fmaf(v.w, f, o[i].w);
       }
     }
+    if constexpr (kG > 1) {
+      sum[grp][t] = L;
+#pragma unroll
+      for (int i = 0; i < kC / 4; ++i) part[grp][i][t] = o[i];
+      __syncthreads();
+      if (grp == 0) {
+#pragma unroll
+        for (int g = 1; g < kG; ++g) {
+          L += sum[g][t];
+#pragma unroll
+          for (int i = 0; i < kC / 4; ++i) {
+            const float4 v = part[g][i][t];
+            o[i] = make_float4(o[i].x + v.x, o[i].y + v.y, o[i].z + v.z, o[i].w + v.w);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (grp > 0 || row >= e.nodes << gs) continue;
     const bool zero = __ldg(a.m.pos + node) < 0 || L == 0.f;
     const float inv = 1.0f / L;
     const int64_t off = node * a.ldo + (int64_t)((e.head << gs) + (row & ((1 << gs) - 1))) * D + d0;
@@ -322,10 +353,11 @@ __global__ void __launch_bounds__(128) k_tree_merge_wide(const __grid_constant__
 
 template <int D>
 cudaError_t merge_wide(const TreeAttendArgs& a, int n_merges, cudaStream_t s) {
-  // few units share their keys among many CTAs: four channels per block, or too few blocks read all those records
+  // few units share their keys among many CTAs: four channels and four record groups per block, or too few loads are in
+  // flight for all those records
   const int halves = a.m.row_tile / 128;
-  if (n_merges < 64) return launch_pdl(k_tree_merge_wide<D, 4>, n_merges * halves * (D / 4), 128, 0, s, a);
-  return launch_pdl(k_tree_merge_wide<D, 16>, n_merges * halves * (D / 16), 128, 0, s, a);
+  if (n_merges < 64) return launch_pdl(k_tree_merge_wide<D, 4, 4>, n_merges * halves * (D / 4), 512, 0, s, a);
+  return launch_pdl(k_tree_merge_wide<D, 16, 1>, n_merges * halves * (D / 16), 128, 0, s, a);
 }
 
 }  // namespace
