@@ -560,6 +560,8 @@ int dec_tree_set(dec_tree* t, const dec_tree_batch* b, void* stream) {
   if (!t) return fail(DEC_EINVAL, "NULL argument");
   int rc = dec_tree_check(t->pool, b);
   if (rc) return rc;
+  if ((int64_t)b->n_tokens * (t->cfg.n_heads + 2 * t->cfg.n_kv_heads) > INT32_MAX)
+    return fail(DEC_ERANGE, "%d nodes of %d heads are too many rows", b->n_tokens, t->cfg.n_heads);
   if (b->n_seqs > t->max_seqs || b->n_tokens > t->max_tokens)
     return fail(DEC_ERANGE, "%d sequences and %d nodes exceed the plan (%d / %d)", b->n_seqs, b->n_tokens, t->max_seqs,
                 t->max_tokens);
@@ -665,6 +667,7 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
   const dec_config& c = t->cfg;
   if ((rc = check_rows(q, ldq, c.n_heads, c.head_dim, q_type, "q"))) return rc;
   if ((rc = check_rows(out, ldo, c.n_heads, c.head_dim, out_type, "out"))) return rc;
+  if (q == out) return fail(DEC_EINVAL, "the output must not be the queries: other units still read them");
   if (t->f16 && out_type == DEC_T_F32)
     return fail(DEC_EINVAL, "an f16 cache gives f16 or bf16 outputs (its weights are rounded to f16)");
   DeviceGuard g(t->device);

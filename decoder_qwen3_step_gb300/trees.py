@@ -91,7 +91,7 @@ def tree_batch(ctx, parents, tables):
     """A dec_tree_batch from lists per sequence: cached tokens, parents of the
     nodes (an int n stands for a chain of n), pool blocks.  Returns the struct
     and the arrays that it points to."""
-    nodes = [list(range(-1, p - 1)) if isinstance(p, int) else list(p) for p in parents]
+    nodes = [np.arange(-1, int(p) - 1, dtype=np.int32) if np.ndim(p) == 0 else np.asarray(p, dtype=np.int32) for p in parents]
     if not len(ctx) == len(nodes) == len(tables):
         raise ValueError("one context, one tree and one table per sequence")
     start = _i32(np.concatenate([[0], np.cumsum([len(p) for p in nodes])]) if nodes else [0])
@@ -99,7 +99,7 @@ def tree_batch(ctx, parents, tables):
     tab = np.zeros((max(len(tables), 1), width), dtype=np.int32)
     for i, t in enumerate(tables):
         tab[i, :len(t)] = t
-    flat = _i32([p for tree in nodes for p in tree] or [0])
+    flat = np.concatenate(nodes + [np.zeros(1, dtype=np.int32)])  # never empty
     arrays = (start, _i32(ctx if len(ctx) else [0]), flat, tab)
     return dec.dec_tree_batch(len(nodes), int(start[-1]), *(_ptr(a) for a in arrays), width), arrays
 
@@ -161,11 +161,6 @@ class DraftTrees:
         x, kind = self._qkv, None  # the struct is read during the call only; every field below is set each time
         if q is not None:
             x.q, x.ldq, kind = self._rows(q, "q", self._heads)
-            if out is None:
-                out = self._new((self.n_tokens, self._heads, self._dim), q_type, stream)
-                x.q_out, x.ldqo, x.q_type = out.data_ptr(), self._heads * self._dim, _TYPES[q_type]
-            else:
-                x.q_out, x.ldqo, x.q_type = self._rows(out, "out", self._heads)
         else:
             x.q = x.q_out = None
         if k is not None:
@@ -191,6 +186,12 @@ class DraftTrees:
             x.rope, x.rope_table, x.rope_positions = rope.pointer, rope.address, rope.n_positions
         else:
             x.rope = None
+        # outputs last: an allocation close behind the call before waits for that call's doorbell
+        if out is not None:
+            x.q_out, x.ldqo, x.q_type = self._rows(out, "out", self._heads)
+        elif q is not None:
+            out = self._new((self.n_tokens, self._heads, self._dim), q_type, stream)
+            x.q_out, x.ldqo, x.q_type = out.data_ptr(), self._heads * self._dim, _TYPES[q_type]
         code = self._append(self.handle, layer, x, self._stream(stream))
         if code:
             dec.check(code, "dec_tree_append")
@@ -227,13 +228,13 @@ class DraftTrees:
         """Accept along the chosen tokens and compact the cache: device int32
         (accepted [sequences], path [nodes], next [sequences])."""
         n, s = self.n_tokens, self.n_seqs
+        ids = self._ids(draft, "draft", n), self._ids(target, "target", n), None if prior is None else self._ids(prior, "prior", s)
         if out is None:  # three tensors: one buffer and its views cost twice as much host time
             out = tuple(self._new(x, torch.int32, stream) for x in (s, n, s))
             a, p, x = out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr()
         else:
             a, p, x = self._ids(out[0], "accepted", s), self._ids(out[1], "path", n), self._ids(out[2], "next", s)
-        code = self._commit(self.handle, self._ids(draft, "draft", n), self._ids(target, "target", n),
-                            None if prior is None else self._ids(prior, "prior", s), a, p, x, self._stream(stream))
+        code = self._commit(self.handle, *ids, a, p, x, self._stream(stream))
         if code:
             dec.check(code, "dec_tree_commit")
         return out

@@ -632,8 +632,8 @@ int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* str
  * rotation, any DEC_T_*; out DEVICE [N, n_heads * head_dim]: any DEC_T_* for
  * an fp32 cache, which is computed in fp32 throughout; DEC_T_F16 or
  * DEC_T_BF16 for an f16 cache, where queries and weights are rounded to f16
- * for the tensor cores and statistics and sums are fp32.  A node's result
- * does not depend on what is cached in slots it does not see (infinities and
+ * for the tensor cores and statistics and sums are fp32.  out must not overlap
+ * q.  A node's result does not depend on what is cached in slots it does not see (infinities and
  * NaN included); it may differ in its last bits with the rest of the batch,
  * which decides how the keys are split over the GPU. */
 int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, int64_t ldq, void* out, int32_t out_type,
@@ -647,7 +647,7 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
  * node, as long as there is one.  Outputs, DEVICE int32: accepted [S] how many
  * nodes; path [N] their numbers within the sequence, then -1; next [S] the
  * token chosen after the last of them (prior, or -1 without one, if none is
- * accepted).  The K/V of the i-th accepted node move to slot ctx + i in every
+ * accepted).  Outputs and inputs must not overlap.  The K/V of the i-th accepted node move to slot ctx + i in every
  * layer; the slots behind hold nothing of use. */
 int dec_tree_commit(dec_tree* t, const int32_t* draft, const int32_t* target, const int32_t* prior, int32_t* accepted,
                     int32_t* path, int32_t* next, void* stream);

@@ -628,6 +628,35 @@ def test_two_plans_on_two_streams():
     b.close()
 
 
+@pytest.mark.parametrize("nodes", [6, 50])
+def test_full_batches_on_two_streams(nodes):
+    """Batches whose units are joined by the CTAs that start them, side by side on one GPU."""
+    a, b = (Setup("16:8x128", "f16", [900 + 7 * i for i in range(30)], [nodes] * 30, seed=k) for k in (1, 2))
+    qa, qb = a.rand(a.N, a.H, a.D), b.rand(b.N, b.H, b.D)
+    want = a.trees.attend(0, qa).clone(), b.trees.attend(0, qb).clone()
+    check(a, want[0], 0, qa, sorted(random.Random(1).sample(range(a.N), 20)))
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [(a.trees.attend(0, qa, stream=sa), b.trees.attend(0, qb, stream=sb)) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, want[0]) and torch.equal(y, want[1]) for x, y in got)
+    a.close()
+    b.close()
+
+
+@pytest.mark.parametrize("shape", ["16:8x128", "8:2x128", "8:4x64", "4:2x32"])
+def test_trees_of_every_width_in_one_batch(shape):
+    """Sequences of one to eight row tiles share the CTAs; some contexts are a few keys, some fill many tiles."""
+    counts = [256, 1, 70, 129, 33, 17, 200, 0, 65, 3]
+    ctx = [0, 2000, 500, 7, 130, 64, 1000, 9, 3, 300]
+    w = Setup(shape, "f16", ctx, [random_tree(n, n) if n else 0 for n in counts], seed=6)
+    q = w.rand(w.N, w.H, w.D)
+    out = w.trees.attend(1, q)
+    check(w, out, 1, q, sorted(random.Random(2).sample(range(w.N), 120)))
+    w.close()
+
+
 def test_the_same_inputs_give_the_same_bits():
     w = Setup("16:8x128", "f16", [1234, 77], [random_tree(64, 1), 3], seed=1)
     q = w.rand(w.N, w.H, w.D)
@@ -653,7 +682,7 @@ def test_refusals():
 
     assert attend() == dec.DEC_OK
     for bad in ({"layer": -1}, {"layer": 2}, {"q": None}, {"out": None}, {"qt": 3}, {"qt": -1}, {"ot": 5}, {"ot": 0}, {"ldq": ld - 4}, {"ldq": ld + 2},
-                {"ldo": 0}, {"ldo": ld + 1}, {"q": P + 4}, {"out": O + 4}):
+                {"ldo": 0}, {"ldo": ld + 1}, {"q": P + 4}, {"out": O + 4}, {"q": O, "qt": 2}):
         assert attend(**bad) == dec.DEC_EINVAL, bad
         assert L.dec_last_error()
     rope = RopeTable(64, 26)

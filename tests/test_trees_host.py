@@ -144,6 +144,6 @@ def test_batch_marshalling():
     b, (start, ctx, flat, tab) = trees.tree_batch([7, 0, 3], [3, [], [-1, 0, 0]], [[4, 5], [], [9]])
     assert (b.n_seqs, b.n_tokens, b.max_blocks) == (3, 6, 2)
     assert start.tolist() == [0, 3, 3, 6] and ctx.tolist() == [7, 0, 3]
-    assert flat.tolist() == [-1, 0, 1, -1, 0, 0] and tab.tolist() == [[4, 5], [0, 0], [9, 0]]
+    assert flat[:6].tolist() == [-1, 0, 1, -1, 0, 0] and tab.tolist() == [[4, 5], [0, 0], [9, 0]]
     with pytest.raises(ValueError):
         trees.tree_batch([1], [1, 1], [[0]])
