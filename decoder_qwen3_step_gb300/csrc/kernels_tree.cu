@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
     if (row >= e.nodes << gs) continue;  // with four warps a row, the whole block
     const int node = e.node0 + (row >> gs);
     auto rec = [&](int c) -> const float* { return tree_record(a, e.c0 + c * e.stride, c == 0); };
+    const bool pad = __ldg(a.m.pos + node) < 0;
     float M = -INFINITY;
     for (int c = lane; c < n_rec; c += 32) M = fmaxf(M, __ldcg(rec(c) + R * D + r));
     M = warp_max(M);
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
       __syncthreads();
       if (warp != 0) continue;
     }
-    const bool zero = __ldg(a.m.pos + node) < 0 || L == 0.f;
+    const bool zero = pad || L == 0.f;
     const float inv = 1.0f / L;
     const int64_t off = node * a.ldo + (int64_t)(e.head * G + (row & (G - 1))) * D + lane * kPer;
 #pragma unroll
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(128 * kG) k_tree_merge_wide(const __grid_const
     const int d0 = (w % kSlabs) * kC, r = (w % per) / kSlabs * 128 + t, row = e.row_tile * R + r;
     const int node = e.node0 + min(row >> gs, e.nodes - 1), n_rec = (e.c1 - e.c0) / e.stride + 1;
     auto rec = [&](int c) -> const float* { return tree_record(a, e.c0 + c * e.stride, c == 0); };
+    const bool pad = __ldg(a.m.pos + node) < 0;
     float M = -INFINITY;
 #pragma unroll 8
     for (int c = grp; c < n_rec; c += kG) M = fmaxf(M, __ldcg(rec(c) + R * D + r));
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(128 * kG) k_tree_merge_wide(const __grid_const
       __syncthreads();
     }
     if (grp > 0 || row >= e.nodes << gs) continue;
-    const bool zero = __ldg(a.m.pos + node) < 0 || L == 0.f;
+    const bool zero = pad || L == 0.f;
     const float inv = 1.0f / L;
     const int64_t off = node * a.ldo + (int64_t)((e.head << gs) + (row & ((1 << gs) - 1))) * D + d0;
 #pragma unroll

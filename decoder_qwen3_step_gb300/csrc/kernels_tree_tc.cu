@@ -284,13 +284,12 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       bool ok = count == 0 || first_scores(0, 0, true);
       for (int left = count; ok && left > 0; ++n_unit) {
         const int tiles = uni(min(u.tiles - tile, left));
-        if (n_unit > 0 && !wait(&oempty[0], n_unit - 1)) break;
         int fresh = 3;  // groups whose O this unit has not written yet
         for (int t = 0; ok && t < tiles; ++t, ++k) {
           const int b = k & 1;
-          // the next tile's scores first: of this unit, or of the next one
+          // the next tile's scores first: of this unit, or of the next one; O once the unit before has been read out of it
           ok = (k + 1 >= count || first_scores(k + 1, n_unit + (t + 1 == tiles), t + 1 == tiles)) &&
-               values(k, b, k >> 1, (fresh >> b) & 1, true);
+               (t > 0 || n_unit == 0 || wait(&oempty[0], n_unit - 1)) && values(k, b, k >> 1, (fresh >> b) & 1, true);
           fresh &= ~(1 << b);
         }
         if (!ok) break;
@@ -368,6 +367,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       mbar_arrive(&qfull[b]);
     };
     int k = 0, n = 0, units = 0;  // tiles; of this group: tiles and units
+    const bool out16 = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.ldo * 2)) & 15) == 0;  // rows in 16-byte pieces
     bool alive = true;
     if (cut.count > 0) {
       if constexpr (kWide) {
@@ -658,9 +658,18 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
                 h[i] = *reinterpret_cast<const uint32_t*>(&z);
               }
             }
-            uint2* to_out = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + off + ch);
+            uint16_t* to_out = reinterpret_cast<uint16_t*>(a.out) + off + ch;
+            if (zero) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) to_out[i / 2] = zero ? make_uint2(0u, 0u) : make_uint2(h[i], h[i + 1]);
+              for (int i = 0; i < 16; ++i) h[i] = 0u;
+            }
+            if (out16) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) reinterpret_cast<uint4*>(to_out)[i / 4] = make_uint4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) reinterpret_cast<uint2*>(to_out)[i / 2] = make_uint2(h[i], h[i + 1]);
+            }
           }
           __syncwarp();
         }
