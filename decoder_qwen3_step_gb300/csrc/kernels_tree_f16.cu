@@ -34,7 +34,8 @@ struct F16Smem {
   static constexpr int kStages = D == 128 ? 3 : D == 64 ? 6 : 8;
   static constexpr int kQPitch = D * 2 + 16;                   // bytes; rows fall into different banks
   static constexpr int kQ = kStages * kStage;                  // the queries, at a unit's end the warps' outputs
-  static constexpr int kRed = 4 * R * 16 * 4;
+  static constexpr int kRedPitch = 40;                         // floats of a row's 32 channels: rows fall into different banks
+  static constexpr int kRed = 4 * R * kRedPitch * 4;
   static constexpr int kML = kQ + (R * kQPitch > kRed ? R * kQPitch : kRed);  // float [4][R] maxima, [4][R] sums
   static constexpr int kFac = kML + 2 * 4 * R * 4;             // float [R]: the rows' score factors
   static constexpr int kBar = kFac + R * 4;
@@ -318,22 +319,22 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
       float* own = reinterpret_cast<float*>(dsm);
       const int j0 = max(t0 * kTreeKeys - u.ctx, 0), j1 = min(t1 * kTreeKeys - u.ctx, u.nodes);
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {  // 16 channels at a time
+      for (int j = 0; j < D / 32; ++j) {  // 32 channels at a time
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int z = 0; z < 2; ++z)
-              *reinterpret_cast<float2*>(red + (warp * R + i * 16 + z * 8 + (lane >> 2)) * 16 + n * 8 + 2 * (lane & 3)) =
-                  make_float2(o[i][2 * j + n][2 * z], o[i][2 * j + n][2 * z + 1]);
+              *reinterpret_cast<float2*>(red + (warp * R + i * 16 + z * 8 + (lane >> 2)) * SM::kRedPitch + n * 8 + 2 * (lane & 3)) =
+                  make_float2(o[i][4 * j + n][2 * z], o[i][4 * j + n][2 * z + 1]);
         group_bar();
-        for (int i = threadIdx.x; i < rows * 4; i += 128) {
-          const int r = i >> 2, x = (i & 3) * 4, row = u.row_tile * R + r, node = u.node0 + (row >> gs);
+        for (int i = threadIdx.x; i < rows * 8; i += 128) {
+          const int r = i >> 3, x = (i & 7) * 4, row = u.row_tile * R + r, node = u.node0 + (row >> gs);
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const float4 y = *reinterpret_cast<const float4*>(red + (w * R + r) * 16 + x);
+            const float4 y = *reinterpret_cast<const float4*>(red + (w * R + r) * SM::kRedPitch + x);
             v.x += y.x;
             v.y += y.y;
             v.z += y.z;
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
             for (int n = j0; n < j1; ++n) {
               if (!tree_sees(a.m, node, n)) continue;
               const int p = u.ctx + n;
-              const float4 y = tree_load4(a.kv, kTreeF16, kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D) + j * 16 + x);
+              const float4 y = tree_load4(a.kv, kTreeF16, kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D) + j * 32 + x);
               if (!isfinite(y.x)) v.x += y.x;
               if (!isfinite(y.y)) v.y += y.y;
               if (!isfinite(y.z)) v.z += y.z;
@@ -359,9 +360,9 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
             const bool zero = L == 0.f || __ldg(a.m.pos + node) < 0;
             const float inv = 1.0f / L;
             v = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            tree_store4(a.out, a.out_type, node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D + j * 16 + x, v);
+            tree_store4(a.out, a.out_type, node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D + j * 32 + x, v);
           } else {
-            *reinterpret_cast<float4*>((follow ? own : rec) + r * D + j * 16 + x) = v;
+            *reinterpret_cast<float4*>((follow ? own : rec) + r * D + j * 32 + x) = v;
           }
         }
         group_bar();
