@@ -57,13 +57,27 @@ __device__ __forceinline__ void tma_box_5d(void* dst, const CUtensorMap* map, in
       : "memory");
 }
 
-// D (TMEM) += A (TMEM, f16 pairs per column) B (shared memory)
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+// One MMA, operands' descriptors as halves: along K only the low one moves (its
+// address field, in 16-byte units), so a step is one 32-bit addition each.
+// D (TMEM) += A (shared memory) B (shared memory)
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// D (TMEM) += A (TMEM, f16 pairs per column) B (shared memory)
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 
@@ -238,57 +252,56 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
     uint32_t leader;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
     const uint32_t td = uni(tmem), smem0 = uni(smem_u32(dsm));
-    // a step along K only moves the descriptors' start addresses (their low bits, in 16-byte units)
     const uint64_t q_desc = sw128_desc(smem0 + SM::kQ), ring_desc = sw128_desc(smem0 + SM::kRing);
     const uint64_t v_desc = sw128_mn_desc(smem0 + SM::kRing, SM::kPanel);
-    // scores of tile k into group b's S, from query tile q
-    auto scores = [&](int k, int b, int q, bool last) -> bool {
-      const int li = 2 * k, slot = li % kS;
-      if (!wait(&full[slot], li / kS)) return false;
-      tc_fence_after();
-      const uint64_t qd = q_desc + q * (SM::kTile >> 4), kd = ring_desc + slot * (SM::kTile >> 4);
+    const uint32_t hi = (uint32_t)(ring_desc >> 32), q_lo = (uint32_t)q_desc, k_lo = (uint32_t)ring_desc, v_lo = (uint32_t)v_desc;
+    // the copies of load li (K of tile k: 2 k, V: 2 k + 1) have landed
+    auto landed = [&](int li) { return wait(&full[li % kS], li / kS); };
+    // scores of tile k (landed) into group b's S, from query tile q
+    auto scores = [&](int k, int b, int q, bool last) {
+      const int slot = 2 * k % kS;
+      const uint32_t qd = q_lo + q * (SM::kTile >> 4), kd = k_lo + slot * (SM::kTile >> 4);
       if (leader) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint32_t off = ((i >> 2) * SM::kPanel + (i & 3) * 32) >> 4;
-          tc_mma(td + b * 128, qd + off, kd + off, id_s, i != 0);
+          mma_ss(td + b * 128, qd + off, kd + off, hi, id_s, i != 0);
         }
-        if (last) tc_commit(&empty[slot]);
         tc_commit(&sfull[b]);
+        if (last) tc_commit(&empty[slot]);
       }
-      __syncwarp();
-      return true;
     };
-    // weights (tile n of group b) times values of tile k
+    // weights (tile n of group b) times values of tile k (landed)
     auto values = [&](int k, int b, int n, bool fresh, bool last) -> bool {
-      const int li = 2 * k + 1, slot = li % kS;
-      if (!wait(&full[slot], li / kS) || !wait(&pfull[b], n)) return false;
+      const int slot = (2 * k + 1) % kS;
+      const uint32_t vd = v_lo + slot * (SM::kTile >> 4);
+      if (!wait(&pfull[b], n)) return false;
       tc_fence_after();
-      const uint64_t vd = v_desc + slot * (SM::kTile >> 4);
       if (leader) {
 #pragma unroll
         for (int i = 0; i < kTK / 16; ++i)
-          tc_mma_ts(td + 256 + b * D, td + b * 128 + i * 8, vd + i * (2048 >> 4), id_o, i != 0 || !fresh);
+          mma_ts(td + 256 + b * D, td + b * 128 + i * 8, vd + i * (2048 >> 4), hi, id_o, i != 0 || !fresh);
         if (last) tc_commit(&empty[slot]);
       }
-      __syncwarp();
       return true;
     };
     const int count = uni(cut.count);
     int k = 0;
     if constexpr (!kWide) {
-      auto first_scores = [&](int x, int unit, bool first) -> bool {
-        if (first && !wait(&qfull[unit & 1], unit >> 1)) return false;
-        return scores(x, x & 1, unit & 1, true);
+      auto tile_scores = [&](int x, int unit, bool first) -> bool {
+        if (!landed(2 * x) || (first && !wait(&qfull[unit & 1], unit >> 1))) return false;
+        tc_fence_after();
+        scores(x, x & 1, unit & 1, true);
+        return true;
       };
-      bool ok = count == 0 || first_scores(0, 0, true);
+      bool ok = count == 0 || tile_scores(0, 0, true);
       for (int left = count; ok && left > 0; ++n_unit) {
         const int tiles = uni(min(u.tiles - tile, left));
         int fresh = 3;  // groups whose O this unit has not written yet
         for (int t = 0; ok && t < tiles; ++t, ++k) {
           const int b = k & 1;
           // the next tile's scores first: of this unit, or of the next one; O once the unit before has been read out of it
-          ok = (k + 1 >= count || first_scores(k + 1, n_unit + (t + 1 == tiles), t + 1 == tiles)) &&
+          ok = (k + 1 >= count || tile_scores(k + 1, n_unit + (t + 1 == tiles), t + 1 == tiles)) && landed(2 * k + 1) &&
                (t > 0 || n_unit == 0 || wait(&oempty[0], n_unit - 1)) && values(k, b, k >> 1, (fresh >> b) & 1, true);
           fresh &= ~(1 << b);
         }
@@ -304,8 +317,14 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       bool ok = true;
       // the scores of a unit's first tile
       auto first_scores = [&](int x) -> bool {
-        if (!wait(&qfull[0], units0) || !scores(x, 0, 0, groups == 1)) return false;
-        return groups == 1 || (wait(&qfull[1], units1) && scores(x, 1, 1, true));
+        if (!landed(2 * x) || !wait(&qfull[0], units0)) return false;
+        tc_fence_after();
+        scores(x, 0, 0, groups == 1);
+        if (groups == 1) return true;
+        if (!wait(&qfull[1], units1)) return false;
+        tc_fence_after();
+        scores(x, 1, 1, true);
+        return true;
       };
       if (count > 0) ok = first_scores(0);
       for (int left = count; ok && left > 0;) {
@@ -314,13 +333,16 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
         if (groups == 2 && units1 > 0) ok = ok && wait(&oempty[1], units1 - 1);
         for (int t = 0; ok && t < tiles; ++t, ++k) {
           const bool more = t + 1 < tiles;
-          ok = values(k, 0, n0++, t == 0, groups == 1);
-          if (ok && more) ok = scores(k + 1, 0, 0, groups == 1);
-          if (ok && !more && leader) tc_commit(&ofull[0]);
+          // both copies are waited for ahead of the weights: from there to a group's next scores nothing else is in the way
+          ok = landed(2 * k + 1) && (!more || landed(2 * k + 2)) && values(k, 0, n0++, t == 0, groups == 1);
+          if (!ok) break;
+          if (more) scores(k + 1, 0, 0, groups == 1);
+          else if (leader) tc_commit(&ofull[0]);
           if (groups == 1) continue;
-          ok = ok && values(k, 1, n1++, t == 0, true);
-          if (ok && more) ok = scores(k + 1, 1, 1, true);
-          if (ok && !more && leader) tc_commit(&ofull[1]);
+          ok = values(k, 1, n1++, t == 0, true);
+          if (!ok) break;
+          if (more) scores(k + 1, 1, 1, true);
+          else if (leader) tc_commit(&ofull[1]);
         }
         if (!ok) break;
         ++units0;
