@@ -445,9 +445,10 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
 #pragma unroll
             for (int p = 0; p < SM::kPanels; ++p) {
               uint4* at = reinterpret_cast<uint4*>(dsm + SM::kRing + slot * SM::kTile + p * SM::kPanel + q * 128 + (st & 7) * 16);
-              uint4 x = key0 + q < end ? *at : make_uint4(0u, 0u, 0u, 0u);
-              bool change = key0 + q >= end;
+              uint4 x = *at;
               uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+              bool change = key0 + q >= end && (w[0] | w[1] | w[2] | w[3]) != 0u;
+              if (change) x = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
               for (int z = 0; z < 4; ++z) {
                 const uint32_t mk = ((w[z] & 0x7C00u) == 0x7C00u ? 0xFFFFu : 0u) |
