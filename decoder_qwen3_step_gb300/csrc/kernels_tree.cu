@@ -115,7 +115,8 @@ cudaError_t append_u(const TreeAppendArgs& a, cudaStream_t s) {
 }
 template <int D>
 cudaError_t append_d(const TreeAppendArgs& a, cudaStream_t s) {
-  // a head per lane group while that leaves SMs idle
+  // a head per lane group while that leaves SMs idle: at 16:8 heads x 128, 16 nodes 1.8 us against 3.0 with four, 200 nodes
+  // 3.4 with either, 1000 nodes 9.7 against 7.0
   const int64_t rows = (int64_t)a.m.N * ((a.q ? a.d.H : 0) + (a.k ? 2 * a.d.Hkv : 0));
   return rows <= 4 * 152 * (256 / (D / 4)) ? append_u<D, 1>(a, s) : append_u<D, 4>(a, s);
 }
@@ -268,9 +269,9 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
   }
 }
 template <int D>
-cudaError_t merge_rows(const TreeAttendArgs& a, int n_merges, cudaStream_t s) {
-  // few units share their keys among many CTAs
-  if (n_merges < 64) return launch_pdl(k_tree_merge<D, 4>, n_merges * a.m.row_tile, 128, 0, s, a);
+cudaError_t merge_rows(const TreeAttendArgs& a, int n_merges, int parts, cudaStream_t s) {
+  // 1 sequence x 8 nodes over 4000 keys (38 parts a unit): 13.9 us against 20.0; 16 x 8 over 1000 (3 parts): 23.9 against 22.4
+  if (parts >= 8) return launch_pdl(k_tree_merge<D, 4>, n_merges * a.m.row_tile, 128, 0, s, a);
   return launch_pdl(k_tree_merge<D, 1>, n_merges * (a.m.row_tile / 4), 128, 0, s, a);
 }
 
@@ -354,11 +355,11 @@ __global__ void __launch_bounds__(128 * kG) k_tree_merge_wide(const __grid_const
 }
 
 template <int D>
-cudaError_t merge_wide(const TreeAttendArgs& a, int n_merges, cudaStream_t s) {
-  // few units share their keys among many CTAs: four channels and four record groups per block, or too few loads are in
-  // flight for all those records
+cudaError_t merge_wide(const TreeAttendArgs& a, int n_merges, int parts, cudaStream_t s) {
+  // many parts: four channels and four record groups per block, or too few loads are in flight for all those records
+  // (1 sequence x 64 nodes over 8000 keys, 19 parts: 19 us against 31; 4 x 64 over 4000, 5 parts: 33 against 30)
   const int halves = a.m.row_tile / 128;
-  if (n_merges < 64) return launch_pdl(k_tree_merge_wide<D, 4, 4>, n_merges * halves * (D / 4), 512, 0, s, a);
+  if (parts >= 8) return launch_pdl(k_tree_merge_wide<D, 4, 4>, n_merges * halves * (D / 4), 512, 0, s, a);
   return launch_pdl(k_tree_merge_wide<D, 16, 1>, n_merges * halves * (D / 16), 128, 0, s, a);
 }
 
@@ -384,15 +385,15 @@ cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s) {
   return launch_pdl(k_tree_commit, a.m.S * per, kCommitThreads, 0, s, a, cols, per);
 }
 
-cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, cudaStream_t s) {
+cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, int parts, cudaStream_t s) {
   // a replayed call may meet a plan with more merges than at its capture: the blocks loop
   if (a.m.row_tile >= 128) {
-    return a.d.D == 128 ? merge_wide<128>(a, max(n_merges, 1), s) : merge_wide<64>(a, max(n_merges, 1), s);
+    return a.d.D == 128 ? merge_wide<128>(a, max(n_merges, 1), parts, s) : merge_wide<64>(a, max(n_merges, 1), parts, s);
   }
   switch (a.d.D) {
-    case 32: return merge_rows<32>(a, max(n_merges, 1), s);
-    case 64: return merge_rows<64>(a, max(n_merges, 1), s);
-    case 128: return merge_rows<128>(a, max(n_merges, 1), s);
+    case 32: return merge_rows<32>(a, max(n_merges, 1), parts, s);
+    case 64: return merge_rows<64>(a, max(n_merges, 1), parts, s);
+    case 128: return merge_rows<128>(a, max(n_merges, 1), parts, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -45,12 +45,15 @@ struct TreeLayout {
 };
 
 // Which attention kernel takes a batch whose widest sequence has max_rows rows
-// (nodes x query heads per KV head).
+// (nodes x query heads per KV head).  Measured at 32 sequences over 1024-2048
+// keys, 16:8 heads x 128: 16 rows 40.5 us on mma.sync against 50 on tcgen05; 32
+// rows 83 (its accumulators spill at two row tiles a warp) against 51; at 8
+// sequences over 8000 keys with 512 rows, narrow units 211 us, wide ones 118.
 TreeVariant variant_for(bool f16, int D, int max_rows) {
-  if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2};
-  if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, 4};
-  if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, 4};
-  return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2};
+  if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2, 60};
+  if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, 4, 25};
+  if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, 4, 25};
+  return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2, 60};
 }
 // Records of the attention kernels: two per CTA; rows of all of them, per SM.
 constexpr int kRecordRows = 2 * 256;
@@ -102,7 +105,7 @@ struct dec_tree {
   // the plan that was set last
   bool set;
   TreeMeta meta;
-  int kernel, max_nodes, max_position, ctas, n_merges;
+  int kernel, max_nodes, max_position, ctas, n_merges, max_parts;
 };
 
 namespace {
@@ -192,9 +195,9 @@ int check_trees(const dec_pool* pool, const dec_tree_batch* b) {
 // second reader finds it in L2.  The gangs of a class cut its (sequence, head)
 // list into equal runs, a unit's start and end counted as unit_cost tiles.
 // *join: few CTAs share a unit, and the one that starts it joins the others'
-// parts by itself (cuts' follow is set); else they are merges.
+// parts by itself (cuts' follow is set); else they are merges, of up to *parts.
 int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVariant& var, int grid, int max_gang, TreeCut* cut,
-               TreeMerge* mrg, bool* join) {
+               TreeMerge* mrg, bool* join, int* parts) {
   const int G = c.n_heads / c.n_kv_heads, R = var.row_tile, K = var.tile_keys, Hkv = c.n_kv_heads;
   auto row_tiles = [&](const TreeSeq& s) { return (s.nodes * G + R - 1) / R; };
   auto tiles = [&](const TreeSeq& s) { return (s.ctx + s.nodes + K - 1) / K; };
@@ -241,8 +244,10 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
     // cuts as (unit, tile); near a unit's border the cut moves there, where that costs less than another piece
     const int n = gangs[g];
     const double run = cost / n;
-    // short units that all have a gang of their own stay whole: joining parts costs more than a tile or two
-    const bool split = (int)units.size() > n || longest * var.tile_keys > 128;
+    // short units that all have a gang of their own stay whole: joining parts costs more than up to three tiles one after
+    // the other (1 sequence x 5 nodes over 100 keys: 8.0 us against 10.3; 8 x 40 over 340: 11.7 against 14.9; four tiles of
+    // 64 keys: 9.5 against 9.2)
+    const bool split = (int)units.size() > n || longest > 3;
     const int snap = (int)std::min(var.unit_cost / 2.0, run / 8);
     std::vector<std::pair<int, int>> at;  // distinct, ascending
     size_t x = 0;
@@ -297,11 +302,15 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
     mrg[i].c1 += idle;
   }
   // Joining costs a fence, a flag's round trip and the reads behind it, some 5 us at the end of the call; a second kernel
-  // costs about 3 us where the records are few or small (1 sequence x 5 nodes over 500 keys: 9.3 us against 11.8), and
-  // more with the records of a full batch (32 x 64 nodes at 1024-2048: 61 us against 56; at most two parts to join there).
-  *join = true;
-  for (int i = 0; i < n_mrg; ++i)
-    if ((mrg[i].c1 - mrg[i].c0) / mrg[i].stride > 2) *join = false;
+  // costs about 3 us where few units are shared (1 sequence x 5 nodes over 180 keys: 8.8 us against 10.6; 16 x 8 over
+  // 1000-1400: 22.4 against 24.3) and more with the records of a full batch (32 x 8 over 1024-2048: 42.1 against 40.5; 16 x
+  // 64 over 2000: 41.2 against 38.2; 8 x 256 over 8000: 124 against 118; at most two parts to join there).
+  *join = n_mrg * 100 >= grid * var.join;
+  *parts = 0;
+  for (int i = 0; i < n_mrg; ++i) {
+    *parts = std::max(*parts, (mrg[i].c1 - mrg[i].c0) / mrg[i].stride + 1);
+    if (*parts > 3) *join = false;
+  }
   if (!*join) return n_mrg;
   for (int i = 0; i < n_mrg; ++i) cut[mrg[i].c0].follow = (mrg[i].c1 - mrg[i].c0) / mrg[i].stride;
   return 0;
@@ -354,7 +363,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   // only the wide kernel has the rows of a sequence walk the keys side by side; at most 1024 rows: gangs of four
   bool join = false;
   const int n_mrg = distribute(c, seqs, var, grid, var.kernel == kTreeTcWide ? 4 : 1, reinterpret_cast<TreeCut*>(H + h_cut),
-                               reinterpret_cast<TreeMerge*>(H + h_mrg), &join);
+                               reinterpret_cast<TreeMerge*>(H + h_mrg), &join, &t->max_parts);
   std::fill(H + h_flags, H + h_flags + t->sms * kTreeMaxCtasPerSm, 0);
   std::copy(seqs.begin(), seqs.end(), reinterpret_cast<TreeSeq*>(H + h_seqs));
   std::fill(H + h_hdr, H + h_hdr + kHdrInts, 0);
@@ -692,7 +701,7 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
   // nothing to join: no second launch, unless a replay may meet a plan that has something
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (t->n_merges == 0) TREE_CUDA(cudaStreamIsCapturing(st, &cap));
-  if (t->n_merges > 0 || cap != cudaStreamCaptureStatusNone) TREE_CUDA(launch_tree_merge(a, t->n_merges, st));
+  if (t->n_merges > 0 || cap != cudaStreamCaptureStatusNone) TREE_CUDA(launch_tree_merge(a, t->n_merges, t->max_parts, st));
   return DEC_OK;
 }
 

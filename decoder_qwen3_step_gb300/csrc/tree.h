@@ -97,12 +97,13 @@ enum TreeKernel { kTreeFfma = 0, kTreeMma, kTreeTc, kTreeTcWide };
 struct TreeVariant {
   int kernel, row_tile, tile_keys, ctas_per_sm;
   int unit_cost;  // what starting and finishing a unit costs a CTA, in key tiles
+  int join;       // shared units per hundred CTAs from which on joining in place beats a second kernel
 };
 constexpr int kTreeMaxCtasPerSm = 3;
 cudaError_t launch_tree_attend_f32(const TreeAttendArgs& a, int ctas, cudaStream_t s);
 cudaError_t launch_tree_attend_f16(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s);
 cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, bool wide, cudaStream_t s);
-cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, cudaStream_t s);
+cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, int parts, cudaStream_t s);
 
 struct TreeCommitArgs {
   TreeMeta m;
