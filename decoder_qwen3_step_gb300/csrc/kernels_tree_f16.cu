@@ -312,12 +312,31 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
           o[i >> 1][j][(i & 1) * 2 + 1] *= f;
         }
       }
+      // the rows are final here, or this CTA's part of a shared unit: a record, or where it joins the others' parts the ring,
+      // which is idle (the unit is its last)
       const bool whole = t0 == 0 && t1 == u.tiles;
-      float* rec = tree_record(a, here, t0 == 0);
       const int follow = !whole && t0 == 0 ? cut.follow : 0;  // CTAs whose parts are joined here
-      // to join, this CTA's part goes to the ring, which is idle: the unit is its last
       float* own = reinterpret_cast<float*>(dsm);
-      const int j0 = max(t0 * kTreeKeys - u.ctx, 0), j1 = min(t1 * kTreeKeys - u.ctx, u.nodes);
+      float* part = follow ? own : tree_record(a, here, t0 == 0);
+      if (threadIdx.x < rows) {
+        const int r = threadIdx.x;
+        const float M = fmaxf(fmaxf(ml[r], ml[R + r]), fmaxf(ml[2 * R + r], ml[3 * R + r]));
+        float L = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) L += M == -INFINITY ? 0.f : ml[(4 + w) * R + r] * ex2(ml[w * R + r] - M);
+        if (whole) {
+          const bool zero = L == 0.f || __ldg(a.m.pos + u.node0 + ((u.row_tile * R + r) >> gs)) < 0;
+          fac[r] = zero ? 0.f : 1.0f / L;
+        } else {
+          fac[r] = 1.f;
+          part[R * D + r] = M;
+          part[R * D + R + r] = L;
+        }
+      }
+      auto out_at = [&](int r) {  // element of the output's first channel of row r
+        const int row = u.row_tile * R + r;
+        return (u.node0 + (row >> gs)) * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D;
+      };
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {  // 32 channels at a time
 #pragma unroll
@@ -329,8 +348,9 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
               *reinterpret_cast<float2*>(red + (warp * R + i * 16 + z * 8 + (lane >> 2)) * SM::kRedPitch + n * 8 + 2 * (lane & 3)) =
                   make_float2(o[i][4 * j + n][2 * z], o[i][4 * j + n][2 * z + 1]);
         group_bar();
+#pragma unroll 1
         for (int i = threadIdx.x; i < rows * 8; i += 128) {
-          const int r = i >> 3, x = (i & 7) * 4, row = u.row_tile * R + r, node = u.node0 + (row >> gs);
+          const int r = i >> 3, x = (i & 7) * 4;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -340,43 +360,32 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
             v.z += y.z;
             v.w += y.w;
           }
-          if (odd) {  // rare: the values that were taken out, for the rows that see them
-            const int32_t* table = a.m.tables + u.tab;
-            for (int n = j0; n < j1; ++n) {
-              if (!tree_sees(a.m, node, n)) continue;
-              const int p = u.ctx + n;
-              const float4 y = tree_load4(a.kv, kTreeF16, kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D) + j * 32 + x);
-              if (!isfinite(y.x)) v.x += y.x;
-              if (!isfinite(y.y)) v.y += y.y;
-              if (!isfinite(y.z)) v.z += y.z;
-              if (!isfinite(y.w)) v.w += y.w;
-            }
-          }
-          if (whole) {
-            const float M = fmaxf(fmaxf(ml[r], ml[R + r]), fmaxf(ml[2 * R + r], ml[3 * R + r]));
-            float L = 0.f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) L += M == -INFINITY ? 0.f : ml[(4 + w) * R + r] * ex2(ml[w * R + r] - M);
-            const bool zero = L == 0.f || __ldg(a.m.pos + node) < 0;
-            const float inv = 1.0f / L;
-            v = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            tree_store4(a.out, a.out_type, node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D + j * 32 + x, v);
-          } else {
-            *reinterpret_cast<float4*>((follow ? own : rec) + r * D + j * 32 + x) = v;
+          const float f = fac[r];
+          if (!whole) *reinterpret_cast<float4*>(part + r * D + j * 32 + x) = v;
+          else tree_store4(a.out, a.out_type, out_at(r) + j * 32 + x, f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+        }
+        group_bar();
+      }
+      if (odd) {  // rare: the values that were taken out, for the rows that see them
+        const int32_t* table = a.m.tables + u.tab;
+        const int j0 = max(t0 * kTreeKeys - u.ctx, 0), j1 = min(t1 * kTreeKeys - u.ctx, u.nodes);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < rows * D; i += 128) {
+          const int r = i / D, node = u.node0 + ((u.row_tile * R + r) >> gs);
+          if (fac[r] == 0.f) continue;  // padding, or nothing seen
+#pragma unroll 1
+          for (int n = j0; n < j1; ++n) {
+            if (!tree_sees(a.m, node, n)) continue;
+            const int p = u.ctx + n;
+            const float z = __half2float(reinterpret_cast<const __half*>(
+                a.kv)[kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D) + i % D]);
+            if (isfinite(z)) continue;
+            if (whole) tree_store(a.out, a.out_type, out_at(r) + i % D, tree_load(a.out, a.out_type, out_at(r) + i % D) + z);
+            else part[i] += z;
           }
         }
         group_bar();
       }
-      if (!whole)
-        for (int r = threadIdx.x; r < rows; r += 128) {
-          const float M = fmaxf(fmaxf(ml[r], ml[R + r]), fmaxf(ml[2 * R + r], ml[3 * R + r]));
-          float L = 0.f;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) L += M == -INFINITY ? 0.f : ml[(4 + w) * R + r] * ex2(ml[w * R + r] - M);
-          float* to = follow ? own : rec;
-          to[R * D + r] = M;
-          to[R * D + R + r] = L;
-        }
       if (follow) {
         // every part's maxima and sums in one round trip, then the sums of the parts; a thread has the four channels 4 c ..
         // of kRows rows and up to 16 loads in flight
@@ -419,11 +428,11 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
         }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-          const int r = threadIdx.x / kLanes + i * (128 / kLanes), row = u.row_tile * R + r, node = u.node0 + (row >> gs);
+          const int r = threadIdx.x / kLanes + i * (128 / kLanes);
           if (r >= rows) continue;
-          const bool zero = L[i] == 0.f || __ldg(a.m.pos + node) < 0;
+          const bool zero = L[i] == 0.f || __ldg(a.m.pos + u.node0 + ((u.row_tile * R + r) >> gs)) < 0;
           const float inv = 1.0f / L[i];
-          tree_store4(a.out, a.out_type, node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D + c * 4,
+          tree_store4(a.out, a.out_type, out_at(r) + c * 4,
                       zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v[i].x * inv, v[i].y * inv, v[i].z * inv, v[i].w * inv));
         }
       } else if (!whole && t0 > 0) {
