@@ -82,36 +82,38 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
   const int here = tree_place();
   const TreeCut cut = a.m.cuts[here];
   const bool ok_shape = tree_shape_ok(a.m, true);
+  TreeUnit u = tree_unit_first(a.m, cut);
+  int tile = cut.tile, k = 0;
+  // a lane's block of the eight tiles from t on, of the current unit up to tile t1
+  auto entries = [&](int t, int t1) {
+    const int b = t * 4 + lane;
+    int blk = b < (u.ctx + u.nodes + 15) >> 4 && b < t1 * 4 ? __ldg(a.m.tables + u.tab + b) : 0;
+#ifdef DEC_DEBUG
+    if ((unsigned)blk >= (unsigned)a.d.n_blocks) {
+      atomicOr(a.m.err, kErrBounds);
+      blk = 0;
+    }
+#endif
+    return blk;
+  };
+  int nxt = warp == 4 && ok_shape && cut.count > 0 ? entries(tile, min(u.tiles, tile + cut.count)) : 0;
   __syncthreads();
   pdl_wait_prev();
   pdl_launch_next();
   if (!ok_shape) return;
   volatile int* abort_flag = flags;
   const int gs = a.d.gs, G = 1 << gs;
-  TreeUnit u = tree_unit_first(a.m, cut);
-  int tile = cut.tile, k = 0;
 
   if (warp == 4) {
     // ---- producer: lanes 0..3 copy one block each; table entries come 8 tiles at a time ----
     for (int left = cut.count; left > 0;) {
       const int t0 = tile, t1 = min(u.tiles, tile + left), blocks = (u.ctx + u.nodes + 15) >> 4;
-      const int32_t* table = a.m.tables + u.tab;
-      auto entries = [&](int t) {
-        const int b = t * 4 + lane;
-        int blk = b < blocks && b < t1 * 4 ? __ldg(table + b) : 0;
-#ifdef DEC_DEBUG
-        if ((unsigned)blk >= (unsigned)a.d.n_blocks) {
-          atomicOr(a.m.err, kErrBounds);
-          blk = 0;
-        }
-#endif
-        return blk;
-      };
-      int cur = 0, nxt = entries(t0);
+      if (left < cut.count) nxt = entries(t0, t1);  // the first unit's are there
+      int cur = 0;
       for (int t = t0; t < t1; ++t, ++k) {
         if (((t - t0) & 7) == 0) {
           cur = nxt;
-          nxt = entries(t + 8);
+          nxt = entries(t + 8, t1);
         }
         const int blk = __shfl_sync(0xffffffffu, cur, (((t - t0) & 7) << 2) + (lane & 3));
         const int slot = k % kS;
@@ -164,6 +166,15 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
 
       for (int t = t0; t < t1; ++t, ++k) {
         const int slot = k % kS, key0 = t * kTreeKeys + warp * 16, nkeys = min(16, end - key0);
+        const bool drafted = nkeys > 0 && key0 + nkeys > u.ctx;  // some key of the block is a node
+        uint32_t sees[2 * MT];  // this lane's rows, bit = key of the block; read ahead of the wait
+        if (drafted) {
+#pragma unroll
+          for (int i = 0; i < 2 * MT; ++i) {
+            const int row = u.row_tile * R + (i >> 1) * 16 + (i & 1) * 8 + (lane >> 2);
+            sees[i] = tree_window(a.m, a.m.anc + (size_t)(u.node0 + min(row >> gs, u.nodes - 1)) * a.m.words, key0 - u.ctx);
+          }
+        }
         alive = __all_sync(0xffffffffu, alive && mbar_wait(&full[slot], (k / kS) & 1, abort_flag, a.m.err));
         if (alive && nkeys > 0) {
           uint8_t* Kb = dsm + slot * SM::kStage + warp * 2 * SM::kSlab;
@@ -186,7 +197,6 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
               af_mma_f16(s[i][1], A, B[2], B[3]);
             }
           }
-          const bool drafted = key0 + nkeys > u.ctx;  // some key of the block is a node
           float mx[2 * MT];
 #pragma unroll
           for (int i = 0; i < 2 * MT; ++i) {
@@ -199,15 +209,11 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
               x[n][e + 1] *= c[i];
             }
             if (drafted) {
-              const int row = u.row_tile * R + (i >> 1) * 16 + (i & 1) * 8 + (lane >> 2);
-              const int node = u.node0 + min((row >> gs), u.nodes - 1);
 #pragma unroll
               for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const int j = key0 + n * 8 + 2 * (lane & 3) + z - u.ctx;
-                  if (j >= 0 && (j >= u.nodes || !tree_sees(a.m, node, j))) x[n][e + z] = -INFINITY;
-                }
+                for (int z = 0; z < 2; ++z)
+                  if (!((sees[i] >> (n * 8 + 2 * (lane & 3) + z)) & 1u)) x[n][e + z] = -INFINITY;
             }
             mx[i] = fmaxf(fmaxf(x[0][e], x[0][e + 1]), fmaxf(x[1][e], x[1][e + 1]));
             mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
@@ -246,8 +252,9 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
           if (drafted) {
             // value rows past the end hold anything: zero them; a node's value that is not finite must not meet
             // another branch's zero weights: zero it too, its descendants get it back at the unit's end
-            bool odd = false;
-            for (int i = lane; i < 16 * (D / 8); i += 32) {
+            bool odd = false, changed = false;
+#pragma unroll 4
+            for (int i = max(u.ctx - key0, 0) * (D / 8) + lane; i < 16 * (D / 8); i += 32) {
               const int r = i / (D / 8);
               uint4* p = reinterpret_cast<uint4*>(Vb + slab_at<D>(r, (i % (D / 8)) * 8));
               uint4 x = *p;
@@ -258,7 +265,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
                 if (r >= nkeys) {
                   change |= w[z] != 0u;
                   w[z] = 0u;
-                } else if (key0 + r >= u.ctx) {
+                } else {
                   const uint32_t mk = ((w[z] & 0x7C00u) == 0x7C00u ? 0xFFFFu : 0u) |
                                       ((w[z] & 0x7C000000u) == 0x7C000000u ? 0xFFFF0000u : 0u);
                   if (mk) {
@@ -268,11 +275,14 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
                 }
               }
               if (change) *p = x;
+              changed |= change;
             }
-            if (__any_sync(0xffffffffu, odd) && lane == 0) flags[1] = 1;
-            // the slot is refilled by the async proxy later: order these stores before it
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
+            if (__any_sync(0xffffffffu, changed)) {
+              if (__any_sync(0xffffffffu, odd) && lane == 0) flags[1] = 1;
+              // the slot is refilled by the async proxy later: order these stores before it
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+            }
           }
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {

@@ -52,6 +52,15 @@ __device__ __forceinline__ bool tree_sees(const TreeMeta& m, int node, int j) {
   return (__ldg(m.anc + (size_t)node * m.words + (j >> 5)) >> (j & 31)) & 1u;
 }
 
+// Which of the nodes j .. j + 31 of its sequence a row of the mask (m.words words) sees, bit 0 node j; j > -32, and
+// negative numbers are cached tokens, which every row sees.  Two loads without a branch: a branch and a load per key cost
+// the tile that holds the nodes 2 us of serial latency.
+__device__ __forceinline__ uint32_t tree_window(const TreeMeta& m, const uint32_t* row, int j) {
+  const int w = j >> 5;
+  const uint32_t a = __ldg(row + min(max(w, 0), m.words - 1)), b = __ldg(row + min(w + 1, m.words - 1));
+  return __funnelshift_r(w < 0 ? 0xffffffffu : w < m.words ? a : 0u, w + 1 < m.words ? b : 0u, j & 31);
+}
+
 // The two 16-bit elements of a word as fp32 (both conversions are exact).
 template <typename T>
 __device__ __forceinline__ float2 tree_pair(uint32_t w);
