@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(256, D == 128 ? 2 : 3) k_tree_attend_f32(const
         rec[R * D + R + r] = l[i];
       }
     }
-    if (!final && t0 > 0) {
+    if (t0 > 0 && cut.awaited) {
       __syncthreads();
       if (tid == 0) tree_publish(a.m, here);
     }

@@ -359,9 +359,18 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
     if (leader) tc_commit(mma_done);
     __syncwarp();
   } else if (warp >= 10) {
-    // ---- queries one unit ahead (the first unit's by the softmax warps, which have nothing else to do yet) ----
+    // ---- Queries one unit ahead (the first unit's by the softmax warps, which have nothing else to do yet).
+    // One of these warps also publishes the part of a shared unit that this CTA begins with: the fence takes up to 3 us
+    // under load, and the softmax warps have the next unit to go on with.  ----
+    bool publish = warp == 11 && cut.awaited;
+    auto published = [&]() {
+      asm volatile("bar.sync 4, 288;" ::: "memory");
+      if (lane == 0) tree_publish(a.m, here);
+      publish = false;
+    };
     for (int left = kWide ? 0 : cut.count; left > 0; ++n_unit) {
       const int b = n_unit & 1;
+      if (publish && n_unit == 2) published();  // the first two units' queries are on their way
       if (!__all_sync(0xffffffffu, n_unit < 2 || mbar_wait(&qempty[b], ((n_unit >> 1) - 1) & 1, abort_flag, a.m.err))) break;
       if (n_unit > 0)
         tree_load_queries<D, kTR, 2, 4>(a, u, u.row_tile * kTR, warp - 10, reinterpret_cast<float*>(dsm + SM::kFac) + b * kTR, [&](int q, int x, uint4 h) {
@@ -373,6 +382,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       tile = 0;
       if (left > 0) tree_unit_next(a.m, gs, kR, a.d.Hkv, u);
     }
+    if (publish) published();
   } else {
     // ---- softmax ----
     const int b = warp >> 2, wr = (warp & 3) * 32, r = wr + lane, st = threadIdx.x & 127;
@@ -723,10 +733,8 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
         mbar_arrive(&oempty[kWide ? b : 0]);  // O may be written again
         ++units;
       }
-      if (!whole && t0 > 0) {  // a part for another CTA: both groups have written it (a group that sat out has nothing to)
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (threadIdx.x == 0) tree_publish(a.m, here);
-      }
+      if (t0 > 0 && cut.awaited)  // a part for another CTA (a group that sat out has nothing of it)
+        asm volatile("bar.arrive 4, 288;" ::: "memory");
       left -= t1 - t0;
       tile = 0;
       u = nu;

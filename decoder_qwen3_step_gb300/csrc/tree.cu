@@ -312,7 +312,10 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
     if (*parts > 3) *join = false;
   }
   if (!*join) return n_mrg;
-  for (int i = 0; i < n_mrg; ++i) cut[mrg[i].c0].follow = (mrg[i].c1 - mrg[i].c0) / mrg[i].stride;
+  for (int i = 0; i < n_mrg; ++i) {
+    cut[mrg[i].c0].follow = (mrg[i].c1 - mrg[i].c0) / mrg[i].stride;
+    for (int c = mrg[i].c0 + mrg[i].stride; c <= mrg[i].c1; c += mrg[i].stride) cut[c].awaited = 1;
+  }
   return 0;
 }
 

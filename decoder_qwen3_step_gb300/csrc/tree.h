@@ -33,7 +33,7 @@ struct alignas(16) TreeCut {
   int32_t q, head, row_tile, tile;
   int32_t count, step;
   int32_t follow;  // CTAs cta + step, cta + 2 step, .. that finish this one's last unit, for this one to join
-  int32_t pad;
+  int32_t awaited; // its first unit's part is joined by the CTA that starts that unit
   TreeSeq s;  // seqs[q]: a CTA starts with a single read
 };
 // A unit (sequence, KV head, row tile) that CTAs c0, c0 + stride, .., c1 share.
