@@ -265,23 +265,13 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
               uint4* p = reinterpret_cast<uint4*>(Vb + slab_at<D>(r, (i % (D / 8)) * 8));
               uint4 x = *p;
               uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-              bool change = false;
+              if (r < nkeys ? tree_not_finite(x) : (w[0] | w[1] | w[2] | w[3])) {
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                if (r >= nkeys) {
-                  change |= w[z] != 0u;
-                  w[z] = 0u;
-                } else {
-                  const uint32_t mk = ((w[z] & 0x7C00u) == 0x7C00u ? 0xFFFFu : 0u) |
-                                      ((w[z] & 0x7C000000u) == 0x7C000000u ? 0xFFFF0000u : 0u);
-                  if (mk) {
-                    w[z] &= ~mk;
-                    change = odd = true;
-                  }
-                }
+                for (int z = 0; z < 4; ++z) w[z] = r < nkeys ? tree_finite_or_0(w[z]) : 0u;
+                *p = x;
+                odd |= r < nkeys;
+                changed = true;
               }
-              if (change) *p = x;
-              changed |= change;
             }
             if (__any_sync(0xffffffffu, changed)) {
               if (__any_sync(0xffffffffu, odd) && lane == 0) flags[1] = 1;

@@ -52,6 +52,16 @@ __device__ __forceinline__ bool tree_sees(const TreeMeta& m, int node, int j) {
   return (__ldg(m.anc + (size_t)node * m.words + (j >> 5)) >> (j & 31)) & 1u;
 }
 
+// Whether any of eight halves is infinite or NaN (its exponent bits, all ones, carry into the sign's place), and a pair of
+// halves with those set to 0.
+__device__ __forceinline__ uint32_t tree_not_finite(uint4 x) {
+  return (((x.x & 0x7C007C00u) + 0x04000400u) | ((x.y & 0x7C007C00u) + 0x04000400u) | ((x.z & 0x7C007C00u) + 0x04000400u) |
+          ((x.w & 0x7C007C00u) + 0x04000400u)) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t tree_finite_or_0(uint32_t w) {
+  return w & ~(((w & 0x7C00u) == 0x7C00u ? 0xFFFFu : 0u) | ((w & 0x7C000000u) == 0x7C000000u ? 0xFFFF0000u : 0u));
+}
+
 // Which of the nodes j .. j + 31 of its sequence a row of the mask (m.words words) sees, bit 0 node j; j > -32, and
 // negative numbers are cached tokens, which every row sees.  Two loads without a branch: a branch and a load per key cost
 // the tile that holds the nodes 2 us of serial latency.
