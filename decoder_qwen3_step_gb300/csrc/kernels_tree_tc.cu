@@ -7,9 +7,11 @@
 //                 in TMEM: thread = row = TMEM lane.  S is read from TMEM, the
 //                 weights go back as f16 over the first half of its columns; a
 //                 row's maximum and sum never leave their thread
-//   warp 8        TMA producer: K and V tiles as 64-channel panels of 128 keys
-//                 in 128-byte swizzled rows (one box per block and panel), into
-//                 a ring of tile slots, K and V of a tile one after the other
+//   warp 8        TMA producer: K and V tiles of 128 keys, 128-byte swizzled
+//                 rows of 64 channels, the panels of eight keys side by side
+//                 (one box of 4 KB per block: with one per block and panel the
+//                 copies' issue alone took 0.75 us for 32 KB: 32 x 64 53.8 us, now 50.9),
+//                 into a ring of tile slots, K and V of a tile in turn
 //   warp 9        issues S = Q K^T (both operands K-major in shared memory) and
 //                 O += P V (P from TMEM, V as a channel-major operand: its
 //                 panels are read transposed by the MMA itself), always with a
@@ -38,7 +40,8 @@ constexpr uint32_t kTmemCols = 512;  // S of the two groups: columns 0, 128; O: 
 template <int D>
 struct TcSmem {
   static constexpr int kPanels = D / 64;
-  static constexpr int kPanel = kTK * 128;            // bytes of 64 channels of 128 keys (or rows)
+  static constexpr int kPanel = kTR * 128;            // bytes of 64 channels of 128 queries
+  static constexpr int kGroup = kPanels * 1024;       // bytes of eight keys
   static constexpr int kTile = kPanels * kPanel;
   static constexpr int kSlots = D == 128 ? 5 : 10;    // of the ring; at least K, V, K are in use at once
   static constexpr int kQ = 0;                        // two tiles: the units' in turn (narrow), the groups' (wide)
@@ -49,25 +52,25 @@ struct TcSmem {
   static constexpr int kBytes = kBar + kBars * 8 + 32;
 };
 
-__device__ __forceinline__ void tma_box_5d(void* dst, const CUtensorMap* map, int y, int half, int is_v, int z, uint64_t* bar) {
+__device__ __forceinline__ void tma_box_5d(void* dst, const CUtensorMap* map, int group, int z, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
-      "[%7];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(0), "r"(y), "r"(half), "r"(is_v), "r"(z), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(0), "r"(group), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
 
 // One MMA, operands' descriptors as halves: along K only the low one moves (its
 // address field, in 16-byte units), so a step is one 32-bit addition each.
 // D (TMEM) += A (shared memory) B (shared memory)
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t a_hi, uint32_t b_hi, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
       "mov.b64 a, {%1, %3};\n\t"
-      "mov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+      "mov.b64 b, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 // D (TMEM) += A (TMEM, f16 pairs per column) B (shared memory)
@@ -85,9 +88,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// MN-major operand, 128-byte swizzle: 64-element atoms `panel` bytes apart, groups of 8 along K 1024 bytes apart.
-__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t panel) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+// 128-byte swizzled operand in groups of 8 keys, `group` bytes apart.  Keys along N (K-major): the first 64 channels, more
+// of them a panel's 1024 bytes on.  Keys along K (MN-major): panels of 64 channels 1024 bytes apart.
+__device__ __forceinline__ uint64_t keys_desc(uint32_t saddr, uint32_t group, bool mn) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(mn ? 1024 >> 4 : 1) << 16) | ((uint64_t)(group >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
@@ -176,6 +180,21 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   const int here = tree_place();
   const TreeCut cut = a.m.cuts[here];
   const bool ok_shape = tree_shape_ok(a.m, true);
+  TreeUnit u = tree_unit_first(a.m, cut);
+  int tile = cut.tile, n_unit = 0;
+  // a lane's block of tile t, if that is in front of t1
+  auto entry = [&](int t, int t1) {
+    const int b = t * 8 + (lane & 7);
+    int blk = b < (u.ctx + u.nodes + 15) >> 4 && t < t1 ? __ldg(a.m.tables + u.tab + b) : 0;
+#ifdef DEC_DEBUG
+    if ((unsigned)blk >= (unsigned)a.d.n_blocks) {
+      atomicOr(a.m.err, kErrBounds);
+      blk = 0;
+    }
+#endif
+    return blk;
+  };
+  int nxt = warp == 8 && ok_shape && cut.count > 0 ? entry(tile, min(u.tiles, tile + cut.count)) : 0;
   __syncthreads();
   pdl_wait_prev();
   pdl_launch_next();
@@ -191,34 +210,20 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags + 1);
   volatile int* abort_flag = flags;
   const int gs = a.d.gs, G = 1 << gs;
-  TreeUnit u = tree_unit_first(a.m, cut);
-  int tile = cut.tile, n_unit = 0;
   // a wide unit with at most 128 rows leaves the second group out
   auto both = [&](const TreeUnit& x) { return (x.nodes << gs) - x.row_tile * kR > kTR; };
 
   if (warp == 8) {
-    // ---- producer: lane = (panel, block) for K, then for V ----
+    // ---- producer: lanes 0..7 copy a block each, K, then V ----
     int li = 0;  // loads so far: K of tile k is load 2k, V is 2k + 1
     for (int left = cut.count; left > 0;) {
       const int t0 = tile, t1 = min(u.tiles, tile + left), blocks = (u.ctx + u.nodes + 15) >> 4;
-      const int32_t* table = a.m.tables + u.tab;
-      auto entry = [&](int t) {
-        const int b = t * 8 + (lane & 7);
-        int blk = b < blocks && t < t1 ? __ldg(table + b) : 0;
-#ifdef DEC_DEBUG
-        if ((unsigned)blk >= (unsigned)a.d.n_blocks) {
-          atomicOr(a.m.err, kErrBounds);
-          blk = 0;
-        }
-#endif
-        return blk;
-      };
-      int nxt = entry(t0);
+      if (left < cut.count) nxt = entry(t0, t1);  // the first unit's is there
       for (int t = t0; t < t1; ++t) {
         const int here = min(8, blocks - t * 8), blk = nxt;
-        nxt = entry(t + 1);
+        nxt = entry(t + 1, t1);
         const uint32_t bytes = here * SM::kPanels * 2048;
-        const int z = a.layer * a.d.n_blocks + blk, panel = lane >> 3;
+        const int z = (a.layer * a.d.n_blocks + blk) * 2;
 #pragma unroll
         for (int is_v = 0; is_v < 2; ++is_v, ++li) {
           const int slot = li % kS;
@@ -230,9 +235,8 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
             flags[2] = li + 1;
           }
           __syncwarp();
-          if (panel < SM::kPanels && (lane & 7) < here)
-            tma_box_5d(dsm + SM::kRing + slot * SM::kTile + panel * SM::kPanel + (lane & 7) * 2048, &tm, u.head * 16,
-                       panel, is_v, z, &full[slot]);
+          if (lane < here)
+            tma_box_5d(dsm + SM::kRing + slot * SM::kTile + lane * 2 * SM::kGroup, &tm, u.head * 2, z + is_v, &full[slot]);
           __syncwarp();
         }
       }
@@ -252,9 +256,10 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
     uint32_t leader;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
     const uint32_t td = uni(tmem), smem0 = uni(smem_u32(dsm));
-    const uint64_t q_desc = sw128_desc(smem0 + SM::kQ), ring_desc = sw128_desc(smem0 + SM::kRing);
-    const uint64_t v_desc = sw128_mn_desc(smem0 + SM::kRing, SM::kPanel);
-    const uint32_t hi = (uint32_t)(ring_desc >> 32), q_lo = (uint32_t)q_desc, k_lo = (uint32_t)ring_desc, v_lo = (uint32_t)v_desc;
+    const uint64_t q_desc = sw128_desc(smem0 + SM::kQ);
+    const uint64_t k_desc = keys_desc(smem0 + SM::kRing, SM::kGroup, false), v_desc = keys_desc(smem0 + SM::kRing, SM::kGroup, true);
+    const uint32_t q_hi = (uint32_t)(q_desc >> 32), q_lo = (uint32_t)q_desc;
+    const uint32_t hi = (uint32_t)(k_desc >> 32), k_lo = (uint32_t)k_desc, v_lo = (uint32_t)v_desc;  // V's high half is K's
     // the copies of load li (K of tile k: 2 k, V: 2 k + 1) have landed
     auto landed = [&](int li) { return wait(&full[li % kS], li / kS); };
     // scores of tile k (landed) into group b's S, from query tile q
@@ -264,8 +269,8 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       if (leader) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = ((i >> 2) * SM::kPanel + (i & 3) * 32) >> 4;
-          mma_ss(td + b * 128, qd + off, kd + off, hi, id_s, i != 0);
+          const uint32_t in = (i & 3) * 32;
+          mma_ss(td + b * 128, qd + (((i >> 2) * SM::kPanel + in) >> 4), kd + (((i >> 2) * 1024 + in) >> 4), q_hi, hi, id_s, i != 0);
         }
         tc_commit(&sfull[b]);
         if (last) tc_commit(&empty[slot]);
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       if (leader) {
 #pragma unroll
         for (int i = 0; i < kTK / 16; ++i)
-          mma_ts(td + 256 + b * D, td + b * 128 + i * 8, vd + i * (2048 >> 4), hi, id_o, i != 0 || !fresh);
+          mma_ts(td + 256 + b * D, td + b * 128 + i * 8, vd + i * (2 * SM::kGroup >> 4), hi, id_o, i != 0 || !fresh);
         if (last) tc_commit(&empty[slot]);
       }
       return true;
@@ -458,7 +463,8 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           for (int q = max(u.ctx - key0, 0) + (st >> 3); alive && q < kTK; q += 16) {
 #pragma unroll
             for (int p = 0; p < SM::kPanels; ++p) {
-              uint4* at = reinterpret_cast<uint4*>(dsm + SM::kRing + slot * SM::kTile + p * SM::kPanel + q * 128 + (st & 7) * 16);
+              uint4* at = reinterpret_cast<uint4*>(dsm + SM::kRing + slot * SM::kTile + (q >> 3) * SM::kGroup + p * 1024 +
+                                                   (q & 7) * 128 + (st & 7) * 16);
               uint4 x = *at;
               uint32_t* w = reinterpret_cast<uint32_t*>(&x);
               if (key0 + q >= end) {

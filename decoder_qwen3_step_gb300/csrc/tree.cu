@@ -101,7 +101,7 @@ struct dec_tree {
   cudaEvent_t stage_ev[kStages];
   int stage_next;
   bool f16;
-  CUtensorMap tm, tm_panel;  // boxes of a whole block (K and V), and of one 64-channel panel of K or V
+  CUtensorMap tm, tm_groups;  // boxes of a block: K and V row by row, and K or V by groups of eight rows
   // the plan that was set last
   bool set;
   TreeMeta meta;
@@ -110,11 +110,14 @@ struct dec_tree {
 
 namespace {
 
-// The pool's tensor map for the f16 attention: [64 channels][rows of a slab]
-// [halves of the head][K, V][layer and block]; one box is the K and V of one
-// KV head of one block (panel: 64 channels of K or V), in 128-byte (64-byte
-// for head_dim 32) swizzled rows.
-bool pool_map(CUtensorMap* out, const dec_pool* p, bool panel) {
+// The pool's tensor maps for the f16 attention, in 128-byte (64-byte for
+// head_dim 32) swizzled rows.  [64 channels][rows of a slab][halves of the
+// head][K, V][layer and block]: one box is the K and V of one KV head of one
+// block.  groups: [64 channels][8 rows][halves][groups of 8 rows][layer, block,
+// K or V]: one box is the K or the V of one KV head of one block, the halves of
+// eight rows next to each other, so that the groups of a tile of many blocks
+// lie evenly apart, as the tensor cores want them.
+bool pool_map(CUtensorMap* out, const dec_pool* p, bool groups) {
   typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -129,9 +132,15 @@ bool pool_map(CUtensorMap* out, const dec_pool* p, bool panel) {
   if (!fn) return false;
   const dec_config& c = p->cfg;
   const cuuint64_t D = c.head_dim, bd = D >= 64 ? 64 : D, slab = (cuuint64_t)c.n_kv_heads * 16 * D * 2;
-  cuuint64_t dims[5] = {bd, (cuuint64_t)c.n_kv_heads * 16, D / bd, 2, (cuuint64_t)c.n_layers * p->n_blocks};
+  const cuuint64_t n = (cuuint64_t)c.n_layers * p->n_blocks, h = D / bd;
+  cuuint64_t dims[5] = {bd, (cuuint64_t)c.n_kv_heads * 16, h, 2, n};
   cuuint64_t strides[4] = {D * 2, bd * 2, slab, 2 * slab};
-  cuuint32_t box[5] = {(cuuint32_t)bd, 16, panel ? 1 : (cuuint32_t)(D / bd), panel ? 1u : 2u, 1};
+  cuuint32_t box[5] = {(cuuint32_t)bd, 16, (cuuint32_t)h, 2, 1};
+  if (groups) {
+    dims[1] = 8, dims[3] = (cuuint64_t)c.n_kv_heads * 2, dims[4] = 2 * n;
+    strides[2] = 8 * D * 2, strides[3] = slab;
+    box[1] = 8;
+  }
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return fn(out, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, p->slabs, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             bd == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -557,7 +566,7 @@ int dec_tree_create(const dec_pool* pool, int32_t max_seqs, int32_t max_tokens, 
   if (e == cudaSuccess) e = cudaMemset(t->ws, 0, 256);
   if (e != cudaSuccess) {
     rc = fail(DEC_ECUDA, "dec_tree_create: %s", cudaGetErrorString(e));
-  } else if (t->f16 && !(pool_map(&t->tm, pool, false) && pool_map(&t->tm_panel, pool, true))) {
+  } else if (t->f16 && !(pool_map(&t->tm, pool, false) && pool_map(&t->tm_groups, pool, true))) {
     rc = fail(DEC_ECUDA, "tensor map of the KV pool failed");
   }
   if (rc) {
@@ -700,7 +709,7 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
   cudaStream_t st = (cudaStream_t)stream;
   TREE_CUDA(t->kernel == kTreeFfma  ? launch_tree_attend_f32(a, t->ctas, st)
             : t->kernel == kTreeMma ? launch_tree_attend_f16(a, &t->tm, t->ctas, st)
-                                    : launch_tree_attend_tc(a, &t->tm_panel, t->ctas, t->kernel == kTreeTcWide, st));
+                                    : launch_tree_attend_tc(a, &t->tm_groups, t->ctas, t->kernel == kTreeTcWide, st));
   // nothing to join: no second launch, unless a replay may meet a plan that has something
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (t->n_merges == 0) TREE_CUDA(cudaStreamIsCapturing(st, &cap));
