@@ -48,7 +48,7 @@ struct TcSmem {
   static constexpr int kRing = 2 * kTile, kFac = kRing + kSlots * kTile;  // fac: float [2][kTR], as the queries
   static constexpr int kBar = kFac + 2 * kTR * 4;
   // barriers: full, empty [slots]; Q full, Q empty, S full, P full, O full, O empty [2]; MMA done
-  static constexpr int kBars = 2 * kSlots + 13;
+  static constexpr int kBars = 2 * kSlots + 15;
   static constexpr int kBytes = kBar + kBars * 8 + 32;
 };
 
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   extern __shared__ __align__(1024) uint8_t dsm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(dsm + SM::kBar);
   uint64_t *full = bars, *empty = bars + kS, *qfull = bars + 2 * kS, *qempty = qfull + 2, *sfull = qfull + 4,
-           *pfull = qfull + 6, *ofull = qfull + 8, *oempty = qfull + 10, *mma_done = qfull + 12;
+           *pfull = qfull + 6, *ofull = qfull + 8, *oempty = qfull + 10, *mma_done = qfull + 12, *phalf = qfull + 13;
   // [0] abort, [1] TMEM base, [2] slots filled, [4 + i] 1 + the unit (of parity i) that met a value that is not finite
   int* flags = reinterpret_cast<int*>(bars + SM::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       mbar_init(&qempty[i], 256);
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 128);
+      mbar_init(&phalf[i], 128);
       mbar_init(&ofull[i], 1);
       mbar_init(&oempty[i], kWide ? 128 : 256);
     }
@@ -280,11 +281,23 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
     auto values = [&](int k, int b, int n, bool fresh, bool last) -> bool {
       const int slot = (2 * k + 1) % kS;
       const uint32_t vd = v_lo + slot * (SM::kTile >> 4);
+      constexpr int kHalf = kWide ? 0 : kTK / 32;
+      if constexpr (!kWide) {  // the first half of the keys while the second's weights are worked on (32 x 64: 50.9 to 50.5 us; wide 114 to 134,
+                              // the issuer then waits for one group when the other one is ready)
+        if (!wait(&phalf[b], n)) return false;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i)
+            mma_ts(td + 256 + b * D, td + b * 128 + i * 8, vd + i * (2 * SM::kGroup >> 4), hi, id_o, i != 0 || !fresh);
+        }
+        __syncwarp();
+      }
       if (!wait(&pfull[b], n)) return false;
       tc_fence_after();
       if (leader) {
 #pragma unroll
-        for (int i = 0; i < kTK / 16; ++i)
+        for (int i = kHalf; i < kTK / 16; ++i)
           mma_ts(td + 256 + b * D, td + b * 128 + i * 8, vd + i * (2 * SM::kGroup >> 4), hi, id_o, i != 0 || !fresh);
         if (last) tc_commit(&empty[slot]);
       }
@@ -579,11 +592,18 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
             tc_wait32(sb);
             if (j == 0) tc_ld32_async(ts + 64, sa);
             weights(sb, j + 1);
+            if (!kWide && j == 0) {
+              tc_wait_st();
+              tc_fence_before();
+              mbar_arrive(&phalf[b]);
+            }
           }
           const float2 lx = unpack2(add2(l2[0], l2[1]));
           l += lx.x + lx.y;
           tc_wait_st();
           tc_fence_before();
+        } else if constexpr (!kWide) {
+          mbar_arrive(&phalf[b]);
         }
         first = false;
         mbar_arrive(&pfull[b]);
