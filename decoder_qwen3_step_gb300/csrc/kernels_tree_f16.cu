@@ -58,7 +58,7 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-constexpr int kF16Threads = 192;  // consumers, producer, publisher
+constexpr int kF16Threads = 160;
 
 template <int D, int R>
 __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid_constant__ CUtensorMap tm,
@@ -132,12 +132,6 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
       if (left > 0) tree_unit_next(a.m, gs, R, a.d.Hkv, u);
     }
   produced:;
-  } else if (warp == 5) {
-    // ---- publisher: the fence behind a record took the consumers 0.8 us on an idle device and 3 to 4 us under load ----
-    if (cut.awaited) {
-      asm volatile("bar.sync 2, 160;" ::: "memory");
-      if (lane == 0) tree_publish(a.m, here);
-    }
   } else {
     // ---- consumers: warp w folds block w of every tile ----
     uint8_t* Qs = dsm + SM::kQ;
@@ -318,12 +312,9 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
           o[i >> 1][j][(i & 1) * 2 + 1] *= f;
         }
       }
-      // the rows are final here, or this CTA's part of a shared unit: a record, or where it joins the others' parts the ring,
-      // which is idle (the unit is its last)
+      // the rows are final here, or this CTA's part of a shared unit: a record
       const bool whole = t0 == 0 && t1 == u.tiles;
-      const int follow = !whole && t0 == 0 ? cut.follow : 0;  // CTAs whose parts are joined here
-      float* own = reinterpret_cast<float*>(dsm);
-      float* part = follow ? own : tree_record(a, here, t0 == 0);
+      float* part = tree_record(a, here, t0 == 0);
       if (threadIdx.x < rows) {
         const int r = threadIdx.x;
         const float M = fmaxf(fmaxf(ml[r], ml[R + r]), fmaxf(ml[2 * R + r], ml[3 * R + r]));
@@ -392,58 +383,6 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
         }
         group_bar();
       }
-      if (follow) {
-        // every part's maxima and sums in one round trip, then the sums of the parts; a thread has the four channels 4 c ..
-        // of kRows rows and up to 16 loads in flight
-        float* mm = own + R * (D + 2);  // [follow + 1][R] maxima, own first, and as many sums behind them
-        float* ll = mm + (follow + 1) * R;
-        if (threadIdx.x < follow) tree_await(a.m, here + (threadIdx.x + 1) * cut.step);
-        group_bar();
-        for (int x = threadIdx.x; x < (follow + 1) * R; x += 128) {
-          const float* p = x < R ? own : tree_record(a, here + x / R * cut.step, false);
-          mm[x] = x < R ? p[R * D + x] : __ldcg(p + R * D + x % R);
-          ll[x] = x < R ? p[R * D + R + x] : __ldcg(p + R * D + R + x % R);
-        }
-        group_bar();
-        constexpr int kLanes = D / 4, kRows = R * kLanes / 128;
-        const int c = threadIdx.x % kLanes;
-        float M[kRows], L[kRows];
-        float4 v[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int r = threadIdx.x / kLanes + i * (128 / kLanes);
-          M[i] = -INFINITY;
-          for (int x = 0; x <= follow; ++x) M[i] = fmaxf(M[i], mm[x * R + r]);
-          if (M[i] == -INFINITY) M[i] = 0.f;
-          const float f = ex2(mm[r] - M[i]);
-          L[i] = ll[r] * f;
-          const float4 y = *reinterpret_cast<const float4*>(own + r * D + c * 4);
-          v[i] = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
-        }
-#pragma unroll 4
-        for (int x = 1; x <= follow; ++x) {
-          const float* p = tree_record(a, here + x * cut.step, false);
-#pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            const int r = threadIdx.x / kLanes + i * (128 / kLanes);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + min(r, rows - 1) * D + c * 4));
-            const float f = ex2(mm[x * R + r] - M[i]);
-            L[i] = fmaf(ll[x * R + r], f, L[i]);
-            v[i] = make_float4(fmaf(y.x, f, v[i].x), fmaf(y.y, f, v[i].y), fmaf(y.z, f, v[i].z), fmaf(y.w, f, v[i].w));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int r = threadIdx.x / kLanes + i * (128 / kLanes);
-          if (r >= rows) continue;
-          const bool zero = L[i] == 0.f || __ldg(a.m.pos + u.node0 + ((u.row_tile * R + r) >> gs)) < 0;
-          const float inv = 1.0f / L[i];
-          tree_store4(a.out, a.out_type, out_at(r) + c * 4,
-                      zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v[i].x * inv, v[i].y * inv, v[i].z * inv, v[i].w * inv));
-        }
-      } else if (t0 > 0 && cut.awaited) {
-        asm volatile("bar.arrive 2, 160;" ::: "memory");
-      }
       if (threadIdx.x == 0) flags[1] = 0;
       group_bar();  // the statistics and the flag are free again
       left -= t1 - t0;
@@ -452,7 +391,6 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
     }
   }
   __syncthreads();
-  if (threadIdx.x < cut.follow) a.m.flags[here + (threadIdx.x + 1) * cut.step] = 0;
   // after an abort, let the copies still in flight land before the CTA exits
   if (warp == 4 && lane == 0 && *abort_flag) {
     const uint64_t w0 = global_ns();

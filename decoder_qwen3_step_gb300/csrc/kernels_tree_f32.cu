@@ -212,10 +212,6 @@ __global__ void __launch_bounds__(256, D == 128 ? 2 : 3) k_tree_attend_f32(const
     // the unit's rows: final, or this CTA's record of a shared unit
     const bool whole = t0 == 0 && t1 == u.tiles;
     float* rec = tree_record(a, here, t0 == 0);
-    const int follow = !whole && t0 == 0 ? cut.follow : 0;  // CTAs whose parts are joined here
-    if (tid < follow) tree_await(a.m, here + (tid + 1) * cut.step);
-    if (follow) __syncthreads();
-    const bool final = whole || follow;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
 #pragma unroll
@@ -239,65 +235,31 @@ __global__ void __launch_bounds__(256, D == 128 ? 2 : 3) k_tree_attend_f32(const
             }
         }
       }
-      if (follow) {
-        float M = m[i];
-#pragma unroll 4
-        for (int x = 1; x <= follow; ++x) M = fmaxf(M, __ldcg(tree_record(a, here + x * cut.step, false) + R * D + r));
-        if (M == -INFINITY) M = 0.f;
-        const float own = ex2(m[i] - M);
-        l[i] *= own;
-#pragma unroll
-        for (int c = 0; c < kVec; ++c)
-#pragma unroll
-          for (int e = 0; e < kW; ++e) o[i][c][e] *= own;
-#pragma unroll 4
-        for (int x = 1; x <= follow; ++x) {
-          const float* p = tree_record(a, here + x * cut.step, false);
-          const float f = ex2(__ldcg(p + R * D + r) - M);
-          l[i] = fmaf(__ldcg(p + R * D + R + r), f, l[i]);
-#pragma unroll
-          for (int c = 0; c < kVec; ++c)
-#pragma unroll
-            for (int e = 0; e < kW; e += 2) {
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(p + r * D + c * 64 + tx * kW + e));
-              o[i][c][e] = fmaf(v.x, f, o[i][c][e]);
-              o[i][c][e + 1] = fmaf(v.y, f, o[i][c][e + 1]);
-            }
-        }
-      }
       const bool zero = __ldg(a.m.pos + node) < 0 || l[i] == 0.f;
-      const float f = final ? 1.0f / l[i] : 1.f;
+      const float f = whole ? 1.0f / l[i] : 1.f;
       const int64_t off = node * a.ldo + (int64_t)(u.head * G + (row & (G - 1))) * D;
 #pragma unroll
       for (int c = 0; c < kVec; ++c) {
         const int d = c * 64 + tx * kW;
         float v[kW];
 #pragma unroll
-        for (int e = 0; e < kW; ++e) v[e] = final && zero ? 0.f : o[i][c][e] * f;
+        for (int e = 0; e < kW; ++e) v[e] = whole && zero ? 0.f : o[i][c][e] * f;
         if constexpr (kW == 4) {
           const float4 w = make_float4(v[0], v[1], v[2], v[3]);
-          if (final) tree_store4(a.out, a.out_type, off + d, w);
+          if (whole) tree_store4(a.out, a.out_type, off + d, w);
           else *reinterpret_cast<float4*>(rec + r * D + d) = w;
         } else {
 #pragma unroll
           for (int e = 0; e < kW; ++e) {
-            if (final) tree_store(a.out, a.out_type, off + d + e, v[e]);
+            if (whole) tree_store(a.out, a.out_type, off + d + e, v[e]);
             else rec[r * D + d + e] = v[e];
           }
         }
       }
-      if (!final && tx == 0) {
+      if (!whole && tx == 0) {
         rec[R * D + r] = m[i];
         rec[R * D + R + r] = l[i];
       }
-    }
-    if (t0 > 0 && cut.awaited) {
-      __syncthreads();
-      if (tid == 0) tree_publish(a.m, here);
-    }
-    if (follow) {  // every thread is past its wait
-      __syncthreads();
-      if (tid < follow) a.m.flags[here + (tid + 1) * cut.step] = 0;
     }
     left -= t1 - t0;
     tile = 0;

@@ -50,10 +50,10 @@ struct TreeLayout {
 // rows 83 (its accumulators spill at two row tiles a warp) against 51; at 8
 // sequences over 8000 keys with 512 rows, narrow units 211 us, wide ones 118.
 TreeVariant variant_for(bool f16, int D, int max_rows) {
-  if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2, 60};
-  if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, 4, 25};
+  if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2, 0};
+  if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, 4, 50};
   if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, 4, 25};
-  return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2, 60};
+  return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2, 0};
 }
 // Records of the attention kernels: two per CTA; rows of all of them, per SM.
 constexpr int kRecordRows = 2 * 256;
@@ -310,11 +310,14 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
     mrg[i].c0 += idle;
     mrg[i].c1 += idle;
   }
-  // Joining costs a fence, a flag's round trip and the reads behind it, some 5 us at the end of the call; a second kernel
-  // costs about 3 us where few units are shared (1 sequence x 5 nodes over 180 keys: 8.8 us against 10.6; 16 x 8 over
-  // 1000-1400: 22.4 against 24.3) and more with the records of a full batch (32 x 8 over 1024-2048: 42.1 against 40.5; 16 x
-  // 64 over 2000: 41.2 against 38.2; 8 x 256 over 8000: 124 against 118; at most two parts to join there).
-  *join = n_mrg * 100 >= grid * var.join;
+  // Joining costs a flag's round trip and the reads behind it at the end of the call, a second kernel its launch and the
+  // records of all shared units.  The tcgen05 kernels' large records are better joined, once enough units are shared
+  // (joined, second kernel: 32 x 64 over 1024-2048 51.9 us, 56.4; 16 x 64 over 2000 35.9, 40.5; 8 x 64 over 2000 29.1, 29.4;
+  // wide: 8 x 256 over 8000 114, 119; 5 x 256 over 4000, 53 units per hundred CTAs, 57.3, 59.2; 4 x 256 there, 42 per
+  // hundred, 51.0, 50.6; 8 x 128 over 1000, 42 per hundred, 34.0, 30.4).  The small ones of 16 rows are not (mma.sync: 32 x
+  // 8 over 1024-2048 39.4, 38.7; 64 x 4 over 500-1500 49.2, 47.8; 24 x 8 over 3000-4000 60.5, 58.5; an f32 cache: 16 x 4
+  // over 1000-1400 108.6, 106.2; 40 x 8 over 300-600 102.8, 104.8).
+  *join = var.join > 0 && n_mrg * 100 >= grid * var.join;
   *parts = 0;
   for (int i = 0; i < n_mrg; ++i) {
     *parts = std::max(*parts, (mrg[i].c1 - mrg[i].c0) / mrg[i].stride + 1);

@@ -97,7 +97,7 @@ enum TreeKernel { kTreeFfma = 0, kTreeMma, kTreeTc, kTreeTcWide };
 struct TreeVariant {
   int kernel, row_tile, tile_keys, ctas_per_sm;
   int unit_cost;  // what starting and finishing a unit costs a CTA, in key tiles
-  int join;       // shared units per hundred CTAs from which on joining in place beats a second kernel
+  int join;       // shared units per hundred CTAs from which on joining in place beats a second kernel; 0: never
 };
 constexpr int kTreeMaxCtasPerSm = 3;
 cudaError_t launch_tree_attend_f32(const TreeAttendArgs& a, int ctas, cudaStream_t s);

@@ -137,7 +137,8 @@ __device__ __forceinline__ float* tree_record(const TreeAttendArgs& a, int cta, 
 // ---- joining shared units without a second launch -------------------------------
 // The CTA that starts a unit (and whose run ends in it) joins the parts of the
 // CTAs that finish it: each of those publishes its record, the first thing of
-// its run, with a flag, and the joining CTA waits for the flags at its own end
+// its run, with a flag (from a warp that has nothing else to do: the fence took
+// the softmax warps up to 3 us), and the joining CTA waits for the flags at its own end
 // and clears them at its exit.  What a CTA waits for lies behind its place, and
 // the last place is the first block's, so it waits only for blocks that were
 // started before it (a place from an atomic ticket instead cost 3 us of a 9 us
