@@ -10,13 +10,15 @@
 //   warp 8        TMA producer: K and V tiles of 128 keys, 128-byte swizzled
 //                 rows of 64 channels, the panels of eight keys side by side
 //                 (one box of 4 KB per block: with one per block and panel the
-//                 copies' issue alone took 0.75 us for 32 KB: 32 x 64 53.8 us, now 50.9),
+//                 copies' issue alone took 0.75 us for 32 KB: 32 x 64 nodes over
+//                 1024-2048 keys took 53.8 us, now 50.9),
 //                 into a ring of tile slots, K and V of a tile in turn
 //   warp 9        issues S = Q K^T (both operands K-major in shared memory) and
 //                 O += P V (P from TMEM, V as a channel-major operand: its
 //                 panels are read transposed by the MMA itself), always with a
 //                 group's next S queued while the other group's softmax runs
-//   warps 10, 11  narrow: the next unit's queries into the other of two buffers
+//   warps 10, 11  narrow: the next unit's queries into the other of two buffers;
+//                 11: publishes the part of a unit that another CTA joins
 // Narrow (up to 128 rows): the groups take the key tiles of the same rows in
 // turn and join their halves at the unit's end, each for half of the channels.
 // Wide: group b takes rows 128 b .. 128 b + 127 of every tile, so a tile's bytes
@@ -282,8 +284,9 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       const int slot = (2 * k + 1) % kS;
       const uint32_t vd = v_lo + slot * (SM::kTile >> 4);
       constexpr int kHalf = kWide ? 0 : kTK / 32;
-      if constexpr (!kWide) {  // the first half of the keys while the second's weights are worked on (32 x 64: 50.9 to 50.5 us; wide 114 to 134,
-                              // the issuer then waits for one group when the other one is ready)
+      // narrow: the first half of the keys while the second's weights are worked on (32 x 64: 50.9 us, so 50.5; 8 x 256 took
+      // 134 us with it instead of 114: the issuer then waits for one group while the other one is ready)
+      if constexpr (!kWide) {
         if (!wait(&phalf[b], n)) return false;
         tc_fence_after();
         if (leader) {
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
         for (int t = 0; ok && t < tiles; ++t, ++k) {
           const int b = k & 1;
           // the unit's next scores first; O once the unit before has been read out of it.  (The next unit's first scores
-          // wait for keys that may be far off: ahead of this unit's last values they held up its end, 32 x 64 took 54.4 us, now 53.8)
+          // wait for keys that may be far off: ahead of this unit's last values they held up its end, 54.4 us against 53.8)
           ok = (t + 1 == tiles || tile_scores(k + 1, n_unit, false)) && landed(2 * k + 1) &&
                (t > 0 || n_unit == 0 || wait(&oempty[0], n_unit - 1)) && values(k, b, k >> 1, (fresh >> b) & 1, true);
           fresh &= ~(1 << b);

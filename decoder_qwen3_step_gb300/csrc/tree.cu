@@ -46,9 +46,9 @@ struct TreeLayout {
 
 // Which attention kernel takes a batch whose widest sequence has max_rows rows
 // (nodes x query heads per KV head).  Measured at 32 sequences over 1024-2048
-// keys, 16:8 heads x 128: 16 rows 40.5 us on mma.sync against 50 on tcgen05; 32
+// keys, 16:8 heads x 128: 16 rows 38.4 us on mma.sync against 46 on tcgen05; 32
 // rows 83 (its accumulators spill at two row tiles a warp) against 51; at 8
-// sequences over 8000 keys with 512 rows, narrow units 211 us, wide ones 118.
+// sequences over 8000 keys with 512 rows, narrow units 211 us, wide ones 114.
 TreeVariant variant_for(bool f16, int D, int max_rows) {
   if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2, 0};
   if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, 4, 50};
@@ -254,8 +254,8 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
     const int n = gangs[g];
     const double run = cost / n;
     // short units that all have a gang of their own stay whole: joining parts costs more than up to three tiles one after
-    // the other (1 sequence x 5 nodes over 100 keys: 8.0 us against 10.3; 8 x 40 over 340: 11.7 against 14.9; four tiles of
-    // 64 keys: 9.5 against 9.2)
+    // the other (4 sequences x 64 nodes over 300 keys, three tiles: 11.4 us against 14.3 with cuts from two tiles on; 1 x 5
+    // over 180: 6.5 against 6.4; 1 x 64 over 500, five tiles: 13.5 whole, 13.9 cut; four tiles of 64 keys: 9.5 whole, 9.2 cut)
     const bool split = (int)units.size() > n || longest > 3;
     const int snap = (int)std::min(var.unit_cost / 2.0, run / 8);
     std::vector<std::pair<int, int>> at;  // distinct, ascending
