@@ -198,6 +198,30 @@ def test_values_in_slots_that_a_node_does_not_see_change_nothing(shape, cache):
     w.close()
 
 
+@pytest.mark.parametrize("cache, seqs, nodes, ctx", [("f32", 1, 20, 3000), ("f16", 1, 6, 3000), ("f16", 30, 7, 900), ("f16", 2, 60, 3000),
+                                                     ("f16", 30, 50, 900), ("f16", 2, 250, 1500), ("f16", 10, 200, 900)])
+def test_values_that_are_not_finite_in_units_that_share_their_keys(cache, seqs, nodes, ctx):
+    """Contexts that several CTAs divide, their parts put together by a second kernel or by one of them."""
+    w = Setup("16:8x128", cache, [ctx + 3 * i for i in range(seqs)], [random_tree(nodes, i) for i in range(seqs)], seed=4)
+    q = w.rand(w.N, w.H, w.D)
+    clean = w.trees.attend(0, q).clone()
+    check(w, clean, 0, q, sorted(random.Random(3).sample(range(w.N), min(w.N, 20))))
+    for value in (float("nan"), float("inf")):
+        for s, i in ((0, 2), (seqs - 1, nodes // 2)):
+            b, r = w.where(s, w.ctx[s] + i)
+            keep = w.slab[0, b, 1, :, r].clone()
+            below = torch.tensor([nodes * s + j for j in range(nodes) if w.ctx[s] + i in w.seen(s, j)], device="cuda")
+            rest = torch.ones(w.N, dtype=torch.bool, device="cuda")
+            rest[below] = False
+            w.slab[0, b, 1, :, r] = value
+            got = w.trees.attend(0, q)
+            assert torch.equal(got[rest], clean[rest]), (value, s, i)
+            assert not bool(torch.isfinite(got[below]).any()), (value, s, i)
+            w.slab[0, b, 1, :, r] = keep
+    assert torch.equal(w.trees.attend(0, q), clean)
+    w.close()
+
+
 @pytest.mark.parametrize("cache", ["f16", "f32"])
 @pytest.mark.parametrize("in_type", [torch.float32, torch.bfloat16, torch.float16])
 def test_types_strides_and_rows_behind_the_last(in_type, cache):
