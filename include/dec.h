@@ -635,7 +635,9 @@ int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* str
  * for the tensor cores and statistics and sums are fp32.  out must not overlap
  * q.  A node's result does not depend on what is cached in slots it does not see (infinities and
  * NaN included); it may differ in its last bits with the rest of the batch,
- * which decides how the keys are split over the GPU. */
+ * which decides how the keys are split over the GPU, and between a direct call
+ * and a replay of one captured with another plan (the split's parts are then
+ * added in another order). */
 int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, int64_t ldq, void* out, int32_t out_type,
                     int64_t ldo, void* stream);
 /* Accept drafted tokens.  DEVICE int32: draft [N] the nodes' tokens, target

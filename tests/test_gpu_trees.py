@@ -614,6 +614,41 @@ def test_captured_calls_follow_the_plan():
     w.close()
 
 
+@pytest.mark.parametrize("seqs, nodes", [(30, 7), (30, 50), (10, 200)])
+def test_a_captured_call_over_plans_divided_in_other_ways(seqs, nodes):
+    """The same nodes over contexts whose units stay whole, are joined in place, or go through the merge kernel."""
+    trees = [random_tree(nodes, i) for i in range(seqs)]
+    w = Setup("16:8x128", "f16", [1700 + i for i in range(seqs)], trees, seed=5)
+    q = w.rand(w.N, w.H, w.D)
+    tables, out = w.tables, torch.empty((w.N, w.H * w.D), dtype=torch.float16, device="cuda")
+    plans = [[1700 + i for i in range(seqs)], [10 + i for i in range(seqs)], [900] * seqs, [0] * (seqs - 1) + [1700 + seqs - 1]]
+    for first in (0, 1):
+        w.ctx = plans[first]
+        w.trees.set(w.ctx, w.parents, tables)
+        w.trees.attend(0, q, out=out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            w.trees.attend(0, q, out=out)
+        for w.ctx in plans + plans[::-1]:
+            w.trees.set(w.ctx, w.parents, tables)
+            out.fill_(float("nan"))
+            graph.replay()
+            graph.replay()
+            got = out.clone()
+            w.trees.attend(0, q, out=out)
+            # the same parts, but a merge kernel that was chosen at the capture may add them in another order: fp32 sums of up
+            # to 64 parts of values of about 1 (64 half steps), and then up to one step of the output apart
+            off = (got.float() - out.float()).abs()
+            assert bool((off <= 2 * 2.0 ** -11 * out.float().abs() + 64 * 2.0 ** -24).all())
+        for w.ctx in plans:
+            w.trees.set(w.ctx, w.parents, tables)
+            graph.replay()
+            check(w, out, 0, q, sorted(random.Random(4).sample(range(w.N), 20)))
+        del graph
+    w.close()
+
+
 def test_a_replay_that_outgrows_its_rotary_table_says_so():
     w = Setup("8:4x64", "f16", [10], [4], seed=3, extra_blocks=0)
     rope = RopeTable(64, 14)
