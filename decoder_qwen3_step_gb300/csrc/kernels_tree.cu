@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(128) k_tree_merge(const __grid_constant__ Tree
 }
 template <int D>
 cudaError_t merge_rows(const TreeAttendArgs& a, int n_merges, int parts, cudaStream_t s) {
-  // 1 sequence x 8 nodes over 4000 keys (38 parts a unit): 13.9 us against 20.0; 16 x 8 over 1000 (3 parts): 23.9 against 22.4
+  // four warps a row, or one: 1 sequence x 8 nodes over 4000 keys (38 parts a unit) 11.7 us, 18.0; 4 x 8 over 2000 (10 parts)
+  // 12.4, 13.5; 16 x 8 over 1000 (3 parts) 19.1, 17.3; 32 x 8 over 1024-2048 (2 parts) 42.2, 38.1
   if (parts >= 8) return launch_pdl(k_tree_merge<D, 4>, n_merges * a.m.row_tile, 128, 0, s, a);
   return launch_pdl(k_tree_merge<D, 1>, n_merges * (a.m.row_tile / 4), 128, 0, s, a);
 }
@@ -357,7 +358,8 @@ __global__ void __launch_bounds__(128 * kG) k_tree_merge_wide(const __grid_const
 template <int D>
 cudaError_t merge_wide(const TreeAttendArgs& a, int n_merges, int parts, cudaStream_t s) {
   // many parts: four channels and four record groups per block, or too few loads are in flight for all those records
-  // (1 sequence x 64 nodes over 8000 keys, 19 parts: 19 us against 31; 4 x 64 over 4000, 5 parts: 33 against 30)
+  // (1 sequence x 64 nodes over 8000 keys, 19 parts: 18.8 us against 30.9; 2 x 64 over 4000, 10 parts: 21.9 against 26.2; 4 x
+  // 64 over 4000, 5 parts: 32.8 against 29.5)
   const int halves = a.m.row_tile / 128;
   if (parts >= 8) return launch_pdl(k_tree_merge_wide<D, 4, 4>, n_merges * halves * (D / 4), 512, 0, s, a);
   return launch_pdl(k_tree_merge_wide<D, 16, 1>, n_merges * halves * (D / 16), 128, 0, s, a);
