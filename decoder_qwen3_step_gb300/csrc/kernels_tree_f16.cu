@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
       for (int i = 0; i < 2 * MT; ++i) {  // this warp's factor to the common maximum
         const int r = (i >> 1) * 16 + (i & 1) * 8 + (lane >> 2);
         const float M = fmaxf(fmaxf(ml[r], ml[R + r]), fmaxf(ml[2 * R + r], ml[3 * R + r]));
-        const float f = M == -INFINITY ? 0.f : ex2(m[i] - M);
+        const float f = ex2(m[i] - (M == -INFINITY ? 0.f : M));  // 0 where the row saw nothing
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {
           o[i >> 1][j][(i & 1) * 2] *= f;
@@ -318,9 +318,11 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
       if (threadIdx.x < rows) {
         const int r = threadIdx.x;
         const float M = fmaxf(fmaxf(ml[r], ml[R + r]), fmaxf(ml[2 * R + r], ml[3 * R + r]));
+        // no maximum: the row saw nothing (its sums are 0), or every score of it was NaN (so is a sum, and the output)
+        const float mu = M == -INFINITY ? 0.f : M;
         float L = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) L += M == -INFINITY ? 0.f : ml[(4 + w) * R + r] * ex2(ml[w * R + r] - M);
+        for (int w = 0; w < 4; ++w) L += ml[(4 + w) * R + r] * ex2(ml[w * R + r] - mu);
         if (whole) {
           const bool zero = L == 0.f || __ldg(a.m.pos + u.node0 + ((u.row_tile * R + r) >> gs)) < 0;
           fac[r] = zero ? 0.f : 1.0f / L;
