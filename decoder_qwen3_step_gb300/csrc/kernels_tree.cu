@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(256, U == 4 && sizeof(T) == 4 ? 5 : 4) k_tree_
     }
     if (a.rope) {
       if (a.interleaved) {
-        y = make_float4(y.x * c0.x - y.y * c0.y, y.y * c0.x + y.x * c0.y, y.z * c0.z - y.w * c0.w, y.w * c0.z + y.z * c0.w);
+        if (turn)  // a product with sin = 0 would carry a channel that is not finite into its neighbour
+          y = make_float4(y.x * c0.x - y.y * c0.y, y.y * c0.x + y.x * c0.y, y.z * c0.z - y.w * c0.w, y.w * c0.z + y.z * c0.w);
       } else {
         float4 p;
         p.x = __shfl_sync(0xffffffffu, y.x, other, kLanes);
