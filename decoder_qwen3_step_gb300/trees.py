@@ -21,6 +21,7 @@ import numpy as np
 import torch
 
 from . import dec
+from .inputs import BLOCK_TOKENS
 from .runtime import _i32, _ptr, make_config
 
 _empty, _raw_stream = torch.empty, torch._C._cuda_getCurrentRawStream
@@ -99,6 +100,8 @@ def tree_batch(ctx, parents, tables):
     tab = np.zeros((max(len(tables), 1), width), dtype=np.int32)
     for i, t in enumerate(tables):
         tab[i, :len(t)] = t
+        if len(t) < width and len(t) * BLOCK_TOKENS < ctx[i] + len(nodes[i]):
+            tab[i, len(t):] = -1  # the library refuses the table: a filled-up one would name somebody's block
     flat = np.concatenate(nodes + [np.zeros(1, dtype=np.int32)])  # never empty
     arrays = (start, _i32(ctx if len(ctx) else [0]), flat, tab)
     return dec.dec_tree_batch(len(nodes), int(start[-1]), *(_ptr(a) for a in arrays), width), arrays
