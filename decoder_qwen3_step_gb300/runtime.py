@@ -67,8 +67,12 @@ class Batch:
         self.n_tokens = int(self.seq_start[-1])
         self.max_blocks = max(1, max(len(s[2]) for s in seqs))
         tab = np.zeros((S, self.max_blocks), dtype=np.int32)
+        self.short = -1  # the first sequence whose table ends before its last slot: filled up it would name somebody's block
         for i, s in enumerate(seqs):
-            tab[i, : len(s[2])] = s[2]
+            n = len(s[2])
+            tab[i, :n] = s[2]
+            if n < self.max_blocks and n * BLOCK_TOKENS < s[1] + lens[i] and self.short < 0:
+                self.short = i
         self.tables = tab
         self.device_ids = device_ids
         st = dec.dec_batch()
@@ -81,6 +85,12 @@ class Batch:
         st.block_table = _ptr(self.tables)
         st.max_blocks = self.max_blocks
         self.struct = st
+
+    def checked(self):
+        """Refuse a table that is too short beside longer ones: the library sees the longest table's length alone."""
+        if self.short >= 0:
+            raise ValueError(f"block table of sequence {self.short} too short for its last position")
+        return self
 
 
 class Decoder:
@@ -196,7 +206,7 @@ class Decoder:
     def prefill(self, seqs, rows: int = dec.DEC_ROWS_ALL, logits: bool = True, device_ids=None,
                 out=None):
         """seqs: list of (ids, start, block_table).  Returns (logits [R,V] fp32 | None, argmax [R] int32)."""
-        b = Batch(seqs, device_ids)
+        b = Batch(seqs, device_ids).checked()
         R = b.n_tokens if rows == dec.DEC_ROWS_ALL else b.n_seqs
         lg, am = self._outputs(R, logits, out)
         dec.check(self.L.dec_prefill(self.handle, self.pool, C.byref(b.struct), rows,
@@ -205,7 +215,7 @@ class Decoder:
         return lg, am
 
     def decode(self, seqs, logits: bool = True, device_ids=None, out=None):
-        b = Batch(seqs, device_ids)
+        b = Batch(seqs, device_ids).checked()
         lg, am = self._outputs(b.n_seqs, logits, out)
         dec.check(self.L.dec_decode(self.handle, self.pool, C.byref(b.struct),
                                     C.c_void_p(lg.data_ptr()) if lg is not None else None,

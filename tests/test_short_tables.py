@@ -9,7 +9,7 @@ import pytest
 pytest.importorskip("torch")
 
 from decoder_qwen3_step_gb300 import dec, inputs, trees  # noqa: E402
-from decoder_qwen3_step_gb300.runtime import make_config  # noqa: E402
+from decoder_qwen3_step_gb300.runtime import Batch, Decoder, make_config  # noqa: E402
 
 
 @pytest.fixture()
@@ -40,3 +40,33 @@ def test_tree_tables(pool, ctx, nodes, tables, taken):
     b, keep = trees.tree_batch(ctx, nodes, tables)
     code = L.dec_tree_check(p, C.byref(b))
     assert code == dec.DEC_OK if taken else code in (dec.DEC_EBLOCK, dec.DEC_ERANGE)
+
+
+@pytest.mark.parametrize("seqs, taken", [
+    ([([1], 18, [5]), ([1], 33, [6, 7, 8])], False),
+    ([([1], 15, [5]), ([1], 33, [6, 7, 8])], True),
+    ([([1, 2], 15, [5]), ([1], 33, [6, 7, 8])], False),
+    ([([1] * 20, 0, [5, 9]), ([1] * 48, 0, [6, 7, 8])], True),
+    ([([1] * 33, 0, [5, 9]), ([1] * 48, 0, [6, 7, 8])], False),
+    ([([1], 40, []), ([1], 33, [6, 7, 8])], False),
+])
+def test_step_tables(pool, seqs, taken):
+    """Decoder.prefill and Decoder.decode marshal their step through Batch(...).checked()."""
+    L, p = pool
+    if taken:
+        assert L.dec_batch_check(p, C.byref(Batch(seqs).checked().struct), 0) == dec.DEC_OK
+    else:
+        with pytest.raises(ValueError):
+            Batch(seqs).checked()
+
+
+def test_a_decoder_refuses_short_tables():
+    class Library:
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} called")
+
+    m = Decoder.__new__(Decoder)
+    m.L, m.pool, m.handle = Library(), None, None
+    for step in (m.prefill, m.decode):
+        with pytest.raises(ValueError):
+            step([([1], 18, [5]), ([1], 33, [6, 7, 8])])
