@@ -366,7 +366,21 @@ cudaError_t merge_wide(const TreeAttendArgs& a, int n_merges, int parts, cudaStr
   return launch_pdl(k_tree_merge_wide<D, 16, 1>, n_merges * halves * (D / 16), 128, 0, s, a);
 }
 
+// ---- test of the joins' flags --------------------------------------------------------
+// Both sides of the flag of place 0 in one thread: the part first, or the wait until it runs out.
+__global__ void k_tree_join_test(TreeMeta m, int late, uint64_t limit_ns) {
+  if (!late) tree_publish(m, 0);
+  tree_await(m, 0, limit_ns);
+  tree_retire(m, 0);
+  if (late) tree_publish(m, 0);
+}
+
 }  // namespace
+
+cudaError_t launch_tree_join_test(const TreeMeta& m, int late, uint64_t limit_ns, cudaStream_t s) {
+  k_tree_join_test<<<1, 1, 0, s>>>(m, late, limit_ns);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t s) {
   k_rope_table<<<(a.positions * a.pairs + 255) / 256, 256, 0, s>>>(a);

@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       while (!mbar_try(&full[i % kS], (i / kS) & 1) && global_ns() - w0 < kWaitLimitNs) {
       }
   __syncthreads();
-  if (threadIdx.x < cut.follow) a.m.flags[here + (threadIdx.x + 1) * cut.step] = 0;
+  if (threadIdx.x < cut.follow) tree_retire(a.m, here + (threadIdx.x + 1) * cut.step);
   if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");

@@ -630,6 +630,22 @@ int dec_tree_status(dec_tree* t, void* stream, uint32_t* flags) {
   return DEC_OK;
 }
 
+int dec_debug_tree_join(dec_tree* t, int32_t late, uint64_t limit_ns, int32_t* left, void* stream) {
+  int rc = check_ready(t, 0);
+  if (rc) return rc;
+  if (!left) return fail(DEC_EINVAL, "NULL argument");
+  if (limit_ns < 1000 || limit_ns > 1000000000ull) return fail(DEC_EINVAL, "the test limit must lie between 1 us and 1 s");
+  DeviceGuard g(t->device);
+  if (!g.ok) return fail(DEC_ECUDA, "the plan's device cannot be made current");
+  cudaStream_t st = (cudaStream_t)stream;
+  TREE_CUDA(launch_tree_join_test(t->meta, late, limit_ns, st));
+  int32_t v = 0;
+  TREE_CUDA(cudaMemcpyAsync(&v, t->meta.flags, 4, cudaMemcpyDeviceToHost, st));
+  TREE_CUDA(cudaStreamSynchronize(st));
+  *left = v;
+  return DEC_OK;
+}
+
 int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* stream) {
   int rc = check_ready(t, layer);
   if (rc) return rc;

@@ -55,7 +55,7 @@ struct TreeMeta {
   const TreeMerge* merges;   // [hdr[kHdrMerges]]
   const int32_t* tables;     // pool block ids, sequence after sequence
   uint32_t* err;             // device error word
-  uint32_t* flags;           // a word per place: its part of a shared unit is there
+  uint32_t* flags;           // a word per place, 1: its part of a shared unit is there; 0 between calls
   int S, N, words, row_tile; // the shape the launch was made for (checked against hdr)
   int tile_keys;             // keys per attention tile
 };
@@ -114,6 +114,8 @@ struct TreeCommitArgs {
   int kv_bytes;
 };
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s);
+
+cudaError_t launch_tree_join_test(const TreeMeta& m, int late, uint64_t limit_ns, cudaStream_t s);
 
 constexpr int kRopeMaxPairs = 64;
 struct RopeTableArgs {

@@ -137,35 +137,39 @@ __device__ __forceinline__ float* tree_record(const TreeAttendArgs& a, int cta, 
 // ---- joining shared units without a second launch -------------------------------
 // The CTA that starts a unit (and whose run ends in it) joins the parts of the
 // CTAs that finish it: each of those publishes its record, the first thing of
-// its run, with a flag (from a warp that has nothing else to do: the fence took
-// the softmax warps up to 3 us), and the joining CTA waits for the flags at its own end
-// and clears them at its exit.  What a CTA waits for lies behind its place, and
-// the last place is the first block's, so it waits only for blocks that were
-// started before it (a place from an atomic ticket instead cost 3 us of a 9 us
-// call).
+// its run, by adding 1 to its flag (from a warp that has nothing else to do: the
+// fence took the softmax warps up to 3 us), and the joining CTA waits for the
+// flags at its own end and subtracts the 1 at its exit.  Both happen in every
+// call, in whichever order once a wait has run out, so a flag is 0 again when
+// the call has ended and a part that came too late is never taken for the next
+// call's.  What a CTA waits for lies behind its place, and the last place is
+// the first block's, so it waits only for blocks that were started before it (a
+// place from an atomic ticket instead cost 3 us of a 9 us call).
 __device__ __forceinline__ int tree_place() { return gridDim.x - 1 - blockIdx.x; }
 // After a barrier behind the record's stores; one thread.
 __device__ __forceinline__ void tree_publish(const TreeMeta& m, int place) {
   __threadfence();
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(m.flags + place), "r"(1u) : "memory");
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(m.flags + place), "r"(1u) : "memory");
 }
-// Wait for the record of `place` (one thread; a barrier then spreads it).  Gives up after a second.
-__device__ __forceinline__ void tree_await(const TreeMeta& m, int place) {
+// Wait for the record of `place` (one thread; a barrier then spreads it).  Gives up after limit_ns.
+__device__ __forceinline__ void tree_await(const TreeMeta& m, int place, uint64_t limit_ns = 1000000000ull) {
   uint64_t t0 = 0;
   while (true) {
     uint32_t v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(m.flags + place) : "memory");
-    if (v) break;
+    if (v == 1u) break;
     uint64_t now;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
     if (!t0) t0 = now;
-    if (now - t0 > 1000000000ull) {
+    if (now - t0 > limit_ns) {
       atomicOr(m.err, kErrTimeout);
       break;
     }
   }
   __threadfence();
 }
+// The joining CTA is done with the record of `place`; one thread, after every wait for it.
+__device__ __forceinline__ void tree_retire(const TreeMeta& m, int place) { atomicSub(m.flags + place, 1u); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -42,7 +42,7 @@ EXPORTS = (
     "dec_quantize_int4", "dec_batch_check", "dec_attend_noalloc_status", "dec_debug_wait_timeout",
     "dec_build_flags", "dec_debug_poison_table", "dec_rope_table_bytes", "dec_rope_table", "dec_tree_check",
     "dec_tree_workspace_bytes", "dec_tree_create", "dec_tree_destroy", "dec_tree_set", "dec_tree_status",
-    "dec_tree_append", "dec_tree_attend", "dec_tree_commit",
+    "dec_tree_append", "dec_tree_attend", "dec_tree_commit", "dec_debug_tree_join",
 )
 KERNEL_CLASSES = ("embed", "qkv", "qkv_post", "attn", "attn_merge", "oproj", "gateup", "down", "lmhead", "argmax",
                   "step")
@@ -178,6 +178,7 @@ def lib() -> C.CDLL:
             "dec_tree_append": (I, [V, C.c_int32, C.POINTER(dec_tree_qkv), V]),
             "dec_tree_attend": (I, [V, C.c_int32, V, C.c_int32, I64, V, C.c_int32, I64, V]),
             "dec_tree_commit": (I, [V, V, V, V, V, V, V, V]),
+            "dec_debug_tree_join": (I, [V, I, C.c_uint64, C.POINTER(C.c_int32), V]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)

@@ -653,6 +653,12 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
  * layer; the slots behind hold nothing of use. */
 int dec_tree_commit(dec_tree* t, const int32_t* draft, const int32_t* target, const int32_t* prior, int32_t* accepted,
                     int32_t* path, int32_t* next, void* stream);
+/* Test hook for the bounded waits of dec_tree_attend's joins: one wait of at
+ * most limit_ns (1 us .. 1 s) for a part that comes before it, or, with late
+ * != 0, after it has run out (DEC_DEV_TIMEOUT in the plan's error word).
+ * *left: the part's flag afterwards, 0 as every call has to leave it.  Needs a
+ * plan; synchronises `stream`. */
+int dec_debug_tree_join(dec_tree* t, int32_t late, uint64_t limit_ns, int32_t* left, void* stream);
 
 /* Library version string. */
 const char* dec_version(void);
