@@ -102,6 +102,7 @@ struct dec_tree {
   int stage_next;
   bool f16;
   CUtensorMap tm, tm_groups;  // boxes of a block: K and V row by row, and K or V by groups of eight rows
+  bool cleared;               // the error word has been
   // the plan that was set last
   bool set;
   TreeMeta meta;
@@ -566,7 +567,6 @@ int dec_tree_create(const dec_pool* pool, int32_t max_seqs, int32_t max_tokens, 
     e = cudaMallocHost((void**)&t->stage[i], t->lay.meta_ints * 4);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&t->stage_ev[i], cudaEventDisableTiming);
   }
-  if (e == cudaSuccess) e = cudaMemset(t->ws, 0, 256);
   if (e != cudaSuccess) {
     rc = fail(DEC_ECUDA, "dec_tree_create: %s", cudaGetErrorString(e));
   } else if (t->f16 && !(pool_map(&t->tm, pool, false) && pool_map(&t->tm_groups, pool, true))) {
@@ -611,6 +611,10 @@ int dec_tree_set(dec_tree* t, const dec_tree_batch* b, void* stream) {
   } catch (const std::bad_alloc&) {
     return fail(DEC_ECAPACITY, "out of host memory");
   }
+  if (!t->cleared) {  // the error word, once, in the order of the stream that the plan is first used on
+    TREE_CUDA(cudaMemsetAsync(t->ws, 0, 256, st));
+    t->cleared = true;
+  }
   TREE_CUDA(cudaMemcpyAsync(t->ws + t->lay.meta, t->stage[slot], ints * 4, cudaMemcpyHostToDevice, st));
   TREE_CUDA(cudaEventRecord(t->stage_ev[slot], st));
   t->set = true;
@@ -623,8 +627,10 @@ int dec_tree_status(dec_tree* t, void* stream, uint32_t* flags) {
   if (!g.ok) return fail(DEC_ECUDA, "the plan's device cannot be made current");
   cudaStream_t st = (cudaStream_t)stream;
   uint32_t v = 0;
-  TREE_CUDA(cudaMemcpyAsync(&v, t->ws, 4, cudaMemcpyDeviceToHost, st));
-  TREE_CUDA(cudaMemsetAsync(t->ws, 0, 4, st));
+  if (t->cleared) {  // else no call has been made
+    TREE_CUDA(cudaMemcpyAsync(&v, t->ws, 4, cudaMemcpyDeviceToHost, st));
+    TREE_CUDA(cudaMemsetAsync(t->ws, 0, 4, st));
+  }
   TREE_CUDA(cudaStreamSynchronize(st));
   *flags = v;
   return DEC_OK;

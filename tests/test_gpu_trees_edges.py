@@ -8,6 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from decoder_qwen3_step_gb300 import dec  # noqa: E402
+from decoder_qwen3_step_gb300.trees import tree_batch  # noqa: E402
 
 from .test_gpu_trees import Setup, random_tree  # noqa: E402
 
@@ -33,4 +34,32 @@ def test_a_part_that_comes_too_late_is_not_taken_for_the_next_calls():
     for limit in (0, 999, 1_000_000_001):
         assert L.dec_debug_tree_join(t.handle, 1, limit, C.byref(left), stream) == dec.DEC_EINVAL
     assert L.dec_debug_tree_join(t.handle, 1, 1000, None, stream) == dec.DEC_EINVAL
+    w.close()
+
+
+def test_the_status_belongs_to_the_plan_alone():
+    """What an earlier owner of the workspace still writes on the plan's stream is no status of the plan's."""
+    w = Setup("8:4x64", "f16", [40], [9], seed=1)
+    L, size, h, flags = w.trees.L, C.c_size_t(), C.c_void_p(), C.c_uint32(9)
+    assert L.dec_tree_workspace_bytes(w.pool.pool, 1, 9, 8, C.byref(size)) == 0
+    buf = torch.zeros(size.value + 256, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        buf.fill_(255)  # the earlier owner's last write
+    assert L.dec_tree_create(w.pool.pool, 1, 9, 8, C.c_void_p((buf.data_ptr() + 255) & ~255), size.value, C.byref(h)) == 0
+    assert L.dec_tree_status(h, C.c_void_p(s.cuda_stream), C.byref(flags)) == 0 and flags.value == 0  # before any call
+    b, keep = tree_batch(w.ctx, w.parents, w.tables)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        buf.fill_(255)
+    assert L.dec_tree_set(h, C.byref(b), C.c_void_p(s.cuda_stream)) == 0
+    q = w.rand(w.N, w.H, w.D)
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.empty((w.N, w.H * w.D), dtype=torch.bfloat16, device="cuda")
+    assert L.dec_tree_attend(h, 0, q.data_ptr(), dec.DEC_T_F32, w.H * w.D, out.data_ptr(), dec.DEC_T_BF16, w.H * w.D, C.c_void_p(s.cuda_stream)) == 0
+    assert L.dec_tree_status(h, C.c_void_p(s.cuda_stream), C.byref(flags)) == 0 and flags.value == 0
+    assert torch.equal(out, w.trees.attend(0, q))
+    L.dec_tree_destroy(h)
     w.close()
