@@ -107,8 +107,21 @@ def tree_batch(ctx, parents, tables):
     return dec.dec_tree_batch(len(nodes), int(start[-1]), *(_ptr(a) for a in arrays), width), arrays
 
 
+def _used_on(stream, *tensors):
+    """Tensors that a call on a given stream reads or writes: their memory is not reused before it has."""
+    for x in tensors:
+        if x is not None:
+            x.record_stream(stream)
+
+
 class DraftTrees:
-    """The plan of a step's draft trees over one pool (a KvPool or a Decoder)."""
+    """The plan of a step's draft trees over one pool (a KvPool or a Decoder).
+
+    Calls run on the current stream, or on `stream`.  Either way the caller
+    orders them behind the work that fills their inputs; the tensors given to
+    a call with `stream` may be dropped right after it.  What a captured graph
+    uses (this plan, its pool, the tensors of the calls) has to be kept for as
+    long as the graph is replayed."""
 
     def __init__(self, pool, max_seqs: int, max_tokens: int, max_blocks: int):
         self.L = dec.lib()
@@ -125,6 +138,7 @@ class DraftTrees:
                                              C.byref(h)), "dec_tree_create")
         self.handle = h
         self.n_tokens = self.n_seqs = 0
+        self._streams = set()  # that calls were made on
         self._heads, self._kv_heads, self._dim = self.cfg.n_heads, self.cfg.n_kv_heads, self.cfg.head_dim
         # a step makes these calls for every layer: the lookups are done once
         self._append, self._attend, self._commit = self.L.dec_tree_append, self.L.dec_tree_attend, self.L.dec_tree_commit
@@ -132,7 +146,13 @@ class DraftTrees:
         self._out_type = torch.float32 if self.cfg.mode == dec.DEC_FP32 else torch.bfloat16
 
     def _stream(self, stream):
-        return stream.cuda_stream if stream is not None else _raw_stream(self._index)
+        raw = stream.cuda_stream if stream is not None else _raw_stream(self._index)
+        if raw not in self._streams:  # the plan's memory and the pool's must not be given away while this stream reads them
+            s = stream if stream is not None else torch.cuda.current_stream(self._index)
+            for x in (self.workspace, self.pool.slabs):
+                x.record_stream(s)
+            self._streams.add(raw)
+        return raw
 
     def _new(self, shape, dtype, stream):
         """An output that lives on the stream its kernel runs on."""
@@ -195,6 +215,8 @@ class DraftTrees:
         elif q is not None:
             out = self._new((self.n_tokens, self._heads, self._dim), q_type, stream)
             x.q_out, x.ldqo, x.q_type = out.data_ptr(), self._heads * self._dim, _TYPES[q_type]
+        if stream is not None:
+            _used_on(stream, q, k, v, q_norm, k_norm, out, rope and rope.table)
         code = self._append(self.handle, layer, x, self._stream(stream))
         if code:
             dec.check(code, "dec_tree_append")
@@ -217,6 +239,8 @@ class DraftTrees:
             po, ldo, kind_o = out.data_ptr(), self._heads * self._dim, _TYPES[out_type]
         else:
             po, ldo, kind_o = self._rows(out, "out", self._heads)
+        if stream is not None:
+            _used_on(stream, q, out)
         code = self._attend(self.handle, layer, p, kind, ld, po, kind_o, ldo, self._stream(stream))
         if code:
             dec.check(code, "dec_tree_attend")
@@ -237,6 +261,8 @@ class DraftTrees:
             a, p, x = out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr()
         else:
             a, p, x = self._ids(out[0], "accepted", s), self._ids(out[1], "path", n), self._ids(out[2], "next", s)
+        if stream is not None:
+            _used_on(stream, draft, target, prior, *out)
         code = self._commit(self.handle, *ids, a, p, x, self._stream(stream))
         if code:
             dec.check(code, "dec_tree_commit")

@@ -8,7 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from decoder_qwen3_step_gb300 import dec  # noqa: E402
-from decoder_qwen3_step_gb300.trees import tree_batch  # noqa: E402
+from decoder_qwen3_step_gb300.trees import DraftTrees, KvPool, RopeTable, tree_batch  # noqa: E402
 
 from .test_gpu_trees import Setup, random_tree  # noqa: E402
 
@@ -62,4 +62,44 @@ def test_the_status_belongs_to_the_plan_alone():
     assert L.dec_tree_status(h, C.c_void_p(s.cuda_stream), C.byref(flags)) == 0 and flags.value == 0
     assert torch.equal(out, w.trees.attend(0, q))
     L.dec_tree_destroy(h)
+    w.close()
+
+
+def test_tensors_of_calls_on_another_stream_may_be_dropped():
+    """Inputs, and a plan with its pool, that are dropped while a call's stream has not come to it yet."""
+    w = Setup("16:8x128", "f16", [300, 40], [20, 9], seed=2)
+    q, k, v = w.rand(w.N, w.H, w.D), w.rand(w.N, w.Hkv, w.D), w.rand(w.N, w.Hkv, w.D)
+    gain = 1 + 0.1 * w.rand(w.D)
+    rope = RopeTable(64, 400)
+    want_q = w.trees.append(0, q, k, v, rope=rope, q_norm=gain, k_norm=gain)
+    want = w.trees.attend(0, want_q).clone()
+    draft = torch.arange(w.N, dtype=torch.int32, device="cuda")
+    before, blocks, tables, ctx, parents = w.slab.clone(), w.blocks, w.tables, w.ctx, w.parents
+    s = torch.cuda.Stream()
+    pool = KvPool(w.shape, w.pool.mode, blocks, max_positions=40960, slabs=before)
+    pool.alloc(blocks)
+    trees = DraftTrees(pool, 2, w.N, 30)
+    torch.cuda.synchronize()
+
+    def overwrite(*sizes):
+        """Whatever the allocator hands out again is written on the current stream, ahead of s."""
+        for n in sizes:
+            for _ in range(6):
+                torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+
+    sizes = [x.numel() * x.element_size() for x in (q, k, gain, draft, rope.table, before, trees.workspace, want)]
+    trees.set(ctx, parents, tables, stream=s)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(400_000_000)
+    got_q = trees.append(0, q.clone(), k.clone(), v.clone(), rope=RopeTable(64, 400), q_norm=gain.clone(), k_norm=gain.clone(), stream=s)
+    got = trees.attend(0, got_q, stream=s)
+    copies = [draft.clone(), draft.clone()]
+    acc, path, nxt = trees.commit(*copies, stream=s)
+    assert not s.query()  # the calls are still waiting, so the copies that were made above have been made
+    del copies, trees, pool, before
+    overwrite(*sizes)
+    s.synchronize()
+    assert torch.equal(got_q, want_q) and torch.equal(got, want)
+    assert acc.tolist() == [1, 1] and nxt.tolist() == [0, 20]
     w.close()
