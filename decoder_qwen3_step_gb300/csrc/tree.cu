@@ -664,6 +664,8 @@ int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* str
   if (x->q) {
     if ((rc = check_rows(x->q, x->ldq, c.n_heads, D, x->in_type, "q"))) return rc;
     if ((rc = check_rows(x->q_out, x->ldqo, c.n_heads, D, x->q_type, "q_out"))) return rc;
+    if (x->q_out == x->q && (x->q_type != x->in_type || x->ldqo != x->ldq))
+      return fail(DEC_EINVAL, "queries in place need one type and one row stride: other rows are still to be read");
   }
   if (x->k) {
     if ((rc = check_rows(x->k, x->ldk, c.n_kv_heads, D, x->in_type, "k"))) return rc;

@@ -623,7 +623,8 @@ typedef struct dec_tree_qkv {
     const dec_rope* rope;     /* HOST, read during the call; NULL: no rotation */
     const float* rope_table;  /* DEVICE, from dec_rope_table with the same dec_rope */
     int32_t rope_positions;   /* its n_positions: above the largest position of the trees (DEC_ERANGE) */
-    void* q_out;              /* DEVICE [N, n_heads, head_dim]; may be q itself if types and strides agree */
+    void* q_out;              /* DEVICE [N, n_heads, head_dim]; may be q itself if types and strides agree
+                                 (DEC_EINVAL if they do not), must not overlap the inputs otherwise */
     int64_t ldqo;
 } dec_tree_qkv;
 /* Norm, rotate, and write the keys and values of all nodes to their slots of

@@ -103,3 +103,24 @@ def test_tensors_of_calls_on_another_stream_may_be_dropped():
     assert torch.equal(got_q, want_q) and torch.equal(got, want)
     assert acc.tolist() == [1, 1] and nxt.tolist() == [0, 20]
     w.close()
+
+
+def test_queries_in_place_of_another_type_or_stride_are_refused():
+    w = Setup("8:4x64", "f16", [20], [6], seed=1)
+    ld = w.H * w.D
+    buf = w.rand(w.N, 2 * ld)
+    keep = buf.clone()
+    x = dec.dec_tree_qkv(q=buf.data_ptr(), ldq=2 * ld, in_type=dec.DEC_T_F32, q_type=dec.DEC_T_F32, q_out=buf.data_ptr(), ldqo=2 * ld)
+    stream = C.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def append(**change):
+        y = dec.dec_tree_qkv.from_buffer_copy(x)
+        for k, v in change.items():
+            setattr(y, k, v)
+        return w.trees.L.dec_tree_append(w.trees.handle, 0, C.byref(y), stream)
+
+    assert append(q_type=dec.DEC_T_BF16) == append(ldqo=ld) == append(q_type=dec.DEC_T_F16, ldqo=ld) == dec.DEC_EINVAL
+    assert append() == dec.DEC_OK and torch.equal(buf, keep)  # nothing to do to them
+    with pytest.raises(dec.DecError):
+        w.trees.append(0, buf[:, :ld], None, None, out=buf.view(-1, ld)[: w.N])
+    w.close()
