@@ -515,10 +515,13 @@ int dec_debug_df_exp(const double* x, double* y, int64_t n, void* stream);
  * every layer's calls.  A plan's calls share its workspace: order them on one
  * stream (or by events); two plans are independent.  dec_tree_append,
  * dec_tree_attend and dec_tree_commit can be captured into a CUDA graph; a
- * replay uses the plan that is set then, as long as dec_tree_set (outside the
- * graph, ordered before the replay) got the same seq_start as at the capture:
- * pad with DEC_TREE_PAD nodes.  A replay on a plan with other counts of
- * sequences or nodes, or another longest sequence, does nothing and sets
+ * replay follows the plan that is set then (by dec_tree_set outside the graph,
+ * ordered before the replay) if its shape is the capture's: the same n_seqs,
+ * n_tokens and ceil(longest / 32), longest the most nodes of a sequence, and
+ * for dec_tree_attend longest * (n_heads / n_kv_heads) on the same side of 16
+ * and, with an f16 cache and head_dim 64 or 128, of 128.  How the nodes are
+ * divided among the sequences may differ (DEC_TREE_PAD nodes fill a batch up).
+ * A replay on a plan of another shape does nothing and sets
  * DEC_DEV_SHAPE.  Calls run on the device that was current at
  * dec_tree_create, whichever device is current then. */
 

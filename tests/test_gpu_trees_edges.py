@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 from decoder_qwen3_step_gb300 import dec  # noqa: E402
 from decoder_qwen3_step_gb300.trees import DraftTrees, KvPool, RopeTable, tree_batch  # noqa: E402
 
-from .test_gpu_trees import Setup, random_tree  # noqa: E402
+from .test_gpu_trees import Setup, check, random_tree  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -123,4 +123,54 @@ def test_queries_in_place_of_another_type_or_stride_are_refused():
     assert append() == dec.DEC_OK and torch.equal(buf, keep)  # nothing to do to them
     with pytest.raises(dec.DecError):
         w.trees.append(0, buf[:, :ld], None, None, out=buf.view(-1, ld)[: w.N])
+    w.close()
+
+
+@pytest.mark.parametrize("shape, cache", [("16:8x128", "f16"), ("8:4x64", "f32"), ("4:2x32", "f16")])
+def test_replays_over_nodes_divided_among_the_sequences_in_other_ways(shape, cache):
+    """15 nodes of two sequences: a replay follows any division whose longest tree has the captured one's row tile."""
+    w = Setup(shape, cache, [40, 70], [15, 15], seed=3)  # room for either to take all of them
+    w.ctx, tables = [40, 70], w.tables
+    w.N, w.parents = 15, [random_tree(8, 1), random_tree(7, 2)]
+    w.trees.set(w.ctx, w.parents, tables)
+    q, k, v = w.rand(15, w.H, w.D), w.rand(15, w.Hkv, w.D), w.rand(15, w.Hkv, w.D)
+    qr, out = torch.empty_like(q), torch.empty((15, w.H * w.D), dtype=torch.bfloat16 if cache == "f16" else torch.float32, device="cuda")
+    draft = torch.arange(15, dtype=torch.int32, device="cuda")
+    outs = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (2, 15, 2)]
+    rope = RopeTable(w.D, 200)
+
+    def calls():
+        w.trees.append(1, q, k, v, rope=rope, out=qr)
+        w.trees.attend(1, qr, out=out)
+        w.trees.commit(draft, draft, out=outs)
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    slab = w.slab.clone()
+    for a in (8, 7, 8):  # 16 rows at most: the capture's row tile
+        w.parents = [random_tree(a, a), random_tree(15 - a, 20 + a)]
+        w.trees.set(w.ctx, w.parents, tables)
+        w.slab.copy_(slab)
+        out.fill_(float("nan"))
+        graph.replay()
+        check(w, out, 1, qr)
+        got = [x.clone() for x in (qr, w.slab, *outs)]
+        w.slab.copy_(slab)
+        calls()
+        assert all(torch.equal(x, y) for x, y in zip(got, (qr, w.slab, *outs)))
+        assert w.trees.status() == 0 and outs[2].tolist() == [0, a]
+    for a in (9, 14, 1):  # more rows: attention does nothing and says so, append and commit follow
+        w.parents = [random_tree(a, a), random_tree(15 - a, 20 + a)]
+        w.trees.set(w.ctx, w.parents, tables)
+        out.fill_(7.0)
+        graph.replay()
+        assert w.trees.status() == dec.DEC_DEV_SHAPE
+        assert bool((out == 7.0).all()) and outs[2].tolist() == [0, a]
+        want = w.trees.append(1, q, k, v, rope=rope)
+        assert torch.equal(qr, want)
+    w.trees.set(w.ctx, [8, 7], tables)
+    del graph
     w.close()
