@@ -92,7 +92,9 @@ bool type_ok(int t) { return t == kTreeF32 || t == kTreeF16 || t == kTreeBf16; }
 }  // namespace
 
 struct dec_tree {
-  const dec_pool* pool;
+  const dec_pool* pool;  // its block bookkeeping, read by dec_tree_set alone
+  void* slabs;           // what the kernels need of the pool
+  int n_blocks;
   dec_config cfg;
   int device, sms, max_seqs, max_tokens, max_blocks;
   char* ws;
@@ -419,7 +421,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
 TreePoolDims pool_dims(const dec_tree* t) {
   const dec_config& c = t->cfg;
   const int G = c.n_heads / c.n_kv_heads;
-  return {c.n_heads, c.n_kv_heads, c.head_dim, c.n_layers, t->pool->n_blocks, G == 4 ? 2 : G - 1, (float)c.rms_eps};
+  return {c.n_heads, c.n_kv_heads, c.head_dim, c.n_layers, t->n_blocks, G == 4 ? 2 : G - 1, (float)c.rms_eps};
 }
 
 int check_rope(const dec_rope* r) {
@@ -554,6 +556,8 @@ int dec_tree_create(const dec_pool* pool, int32_t max_seqs, int32_t max_tokens, 
   dec_tree* t = new (std::nothrow) dec_tree();
   if (!t) return fail(DEC_ECAPACITY, "out of host memory");
   t->pool = pool;
+  t->slabs = pool->slabs;
+  t->n_blocks = pool->n_blocks;
   t->cfg = pool->cfg;
   t->max_seqs = max_seqs;
   t->max_tokens = max_tokens;
@@ -702,7 +706,7 @@ int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* str
   a.q_type = x->q_type;
   a.kv_f16 = t->f16;
   a.layer = layer;
-  a.kv = t->pool->slabs;
+  a.kv = t->slabs;
   TREE_CUDA(launch_tree_append(a, (cudaStream_t)stream));
   return DEC_OK;
 }
@@ -730,7 +734,7 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
   a.q_type = q_type;
   a.out_type = out_type;
   a.layer = layer;
-  a.kv = t->pool->slabs;
+  a.kv = t->slabs;
   a.part = (float*)(t->ws + t->lay.part);
   a.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)c.head_dim));
   cudaStream_t st = (cudaStream_t)stream;
@@ -760,7 +764,7 @@ int dec_tree_commit(dec_tree* t, const int32_t* draft, const int32_t* target, co
   a.accepted = accepted;
   a.path = path;
   a.next = next;
-  a.kv = t->pool->slabs;
+  a.kv = t->slabs;
   a.kv_bytes = t->f16 ? 2 : 4;
   TREE_CUDA(launch_tree_commit(a, (cudaStream_t)stream));
   return DEC_OK;

@@ -173,6 +173,8 @@ class DraftTrees:
 
     def set(self, ctx, parents, tables, stream=None) -> None:
         """This step's trees: cached tokens, parents (an int n: a chain of n) and block table of every sequence."""
+        if not self.pool.pool:
+            raise ValueError("the pool is closed")
         b, keep = tree_batch(ctx, parents, tables)
         dec.check(self.L.dec_tree_set(self.handle, C.byref(b), self._stream(stream)), "dec_tree_set")
         self.n_seqs, self.n_tokens = b.n_seqs, b.n_tokens

@@ -559,8 +559,9 @@ int dec_tree_check(const dec_pool* pool, const dec_tree_batch* b);
 int dec_tree_workspace_bytes(const dec_pool* pool, int32_t max_seqs, int32_t max_tokens, int32_t max_blocks,
                              size_t* bytes);
 /* workspace: caller-owned device memory, 256-byte aligned, not to be touched
- * while the plan lives; pool must outlive the plan.  Nothing is written to it
- * before the first dec_tree_set, in the order of that call's stream.  The plan
+ * while the plan lives; the pool has to live for every dec_tree_set, its memory
+ * for every call.  Nothing is written to the workspace before the first
+ * dec_tree_set, in the order of that call's stream.  The plan
  * owns only host memory (a small pinned staging ring). */
 int dec_tree_create(const dec_pool* pool, int32_t max_seqs, int32_t max_tokens, int32_t max_blocks, void* workspace,
                     size_t bytes, dec_tree** out);

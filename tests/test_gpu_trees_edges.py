@@ -174,3 +174,20 @@ def test_replays_over_nodes_divided_among_the_sequences_in_other_ways(shape, cac
     w.trees.set(w.ctx, [8, 7], tables)
     del graph
     w.close()
+
+
+def test_a_plan_outlives_the_pools_bookkeeping():
+    """A closed KvPool keeps its memory: the plan that is set works on, another one is refused."""
+    w = Setup("8:4x64", "f16", [20], [6], seed=1)
+    q, k = w.rand(w.N, w.H, w.D), w.rand(w.N, w.Hkv, w.D)
+    w.trees.append(0, None, k, k)
+    want = w.trees.attend(0, q).clone()
+    w.pool.close()
+    others = [KvPool(w.shape, w.pool.mode, 3) for _ in range(20)]  # host memory of the closed one is used again
+    w.trees.append(0, None, k, k)
+    assert torch.equal(w.trees.attend(0, q), want)
+    with pytest.raises(ValueError):
+        w.trees.set(w.ctx, w.parents, w.tables)
+    assert torch.equal(w.trees.attend(0, q), want)
+    del others
+    w.close()
