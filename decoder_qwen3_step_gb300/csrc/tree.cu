@@ -55,6 +55,9 @@ TreeVariant variant_for(bool f16, int D, int max_rows) {
   if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, 4, 25};
   return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2, 0};
 }
+// The rows of a sequence walk the keys side by side in the wide kernel alone, a CTA for each of its row tiles.
+constexpr int kWideGang = 4;
+static_assert(kTreeMaxNodes * 4 <= kWideGang * 256, "at most four query heads per KV head");
 // Records of the attention kernels: two per CTA; rows of all of them, per SM.
 constexpr int kRecordRows = 2 * 256;
 
@@ -62,7 +65,7 @@ TreeLayout tree_layout(const dec_config& c, int max_seqs, int max_tokens, int ma
   TreeLayout L{};
   const size_t S = max_seqs, N = max_tokens, P = (size_t)sms * kTreeMaxCtasPerSm;
   // header, flags, seq_start, seqs, pos, dst, parents, mask, cuts, merges, tables (each piece 16-byte aligned)
-  L.meta_ints = kHdrInts + P + (S + 1) + 8 * S + 3 * N + N * (kTreeMaxNodes / 32) + P * 24 + S * (size_t)max_blocks + 16 * 4;
+  L.meta_ints = kHdrInts + P + (S + 1) + 4 * S + 3 * N + N * (kTreeMaxNodes / 32) + P * 20 + S * (size_t)max_blocks + 16 * 4;
   L.meta = 256;
   L.part = up256(L.meta + L.meta_ints * 4);
   L.total = up256(L.part + (size_t)sms * kRecordRows * (size_t)(c.head_dim + 2) * 4);
@@ -206,10 +209,10 @@ int check_trees(const dec_pool* pool, const dec_tree_batch* b) {
 // `max_gang`) that walk the same keys at the same time, so that a tile's
 // second reader finds it in L2.  The gangs of a class cut its (sequence, head)
 // list into equal runs, a unit's start and end counted as unit_cost tiles.
-// *join: few CTAs share a unit, and the one that starts it joins the others'
-// parts by itself (cuts' follow is set); else they are merges, of up to *parts.
+// Returns the merges, of up to *parts, that a second kernel is needed for: none
+// where the CTAs that start shared units join the others' parts (cuts' follow).
 int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVariant& var, int grid, int max_gang, TreeCut* cut,
-               TreeMerge* mrg, bool* join, int* parts) {
+               TreeMerge* mrg, int* parts) {
   const int G = c.n_heads / c.n_kv_heads, R = var.row_tile, K = var.tile_keys, Hkv = c.n_kv_heads;
   auto row_tiles = [&](const TreeSeq& s) { return (s.nodes * G + R - 1) / R; };
   auto tiles = [&](const TreeSeq& s) { return (s.ctx + s.nodes + K - 1) / K; };
@@ -238,18 +241,18 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
     const int g = gang(seqs[q0]);
     size_t q1 = q0;
     while (q1 < seqs.size() && gang(seqs[q1]) == g) ++q1;
-    // the class as a line of units: of the row tiles i, i + g, .. of a (sequence, head) for gang member i.  Members run in
-    // step, so every member's line has the length of the first one's; a unit that a member lacks is no work to it
+    // the class as a line of units: (sequence, head, row tile) for a gang of one, (sequence, head) for a larger one, whose
+    // members have a row tile each (a gang is as large as its sequences have row tiles, if it may be larger than one)
     struct Unit {
-      int q, head, pass, tiles;
+      int q, head, row_tile, tiles;  // the first member's
     };
     std::vector<Unit> units;
     double cost = 0;
     int longest = 0;
     for (size_t q = q0; q < q1; ++q)
       for (int h = 0; h < Hkv; ++h)
-        for (int pass = 0; pass * g < row_tiles(seqs[q]); ++pass) {
-          units.push_back({(int)q, h, pass, tiles(seqs[q])});
+        for (int rt = 0; rt < row_tiles(seqs[q]); rt += g) {
+          units.push_back({(int)q, h, rt, tiles(seqs[q])});
           cost += tiles(seqs[q]) + var.unit_cost;
           longest = std::max(longest, tiles(seqs[q]));
         }
@@ -278,15 +281,13 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
     at.push_back({(int)units.size(), 0});
     for (int i = 0; i < used; ++i)
       for (int member = 0; member < g; ++member) {
-        // this member's first unit in the run: its row tile may not exist in the first one
         TreeCut& o = cut[cta + i * g + member];
         o = {};
         for (int y = at[i].first; y <= at[i + 1].first && y < (int)units.size(); ++y) {
           const Unit& w = units[y];
           const int t0 = y == at[i].first ? at[i].second : 0, t1 = y == at[i + 1].first ? at[i + 1].second : w.tiles;
-          const int rt = w.pass * g + member;
-          if (t1 <= t0 || rt >= row_tiles(seqs[w.q])) continue;
-          if (o.count == 0) o = {w.q, w.head, rt, t0, 0, g, 0, 0, seqs[w.q]};
+          if (t1 <= t0) continue;
+          if (o.count == 0) o = {w.q, w.head, w.row_tile + member, t0, 0, g, 0, 0, seqs[w.q]};
           o.count += t1 - t0;
         }
       }
@@ -297,9 +298,7 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
       int last = i;
       while (last + 1 < used && at[last + 1].first == at[i].first) ++last;
       for (int member = 0; member < g; ++member) {
-        const int rt = w.pass * g + member;
-        if (rt >= row_tiles(seqs[w.q])) continue;
-        mrg[n_mrg++] = {w.head, rt, cta + (i - 1) * g + member, cta + last * g + member, g, seqs[w.q].node0, seqs[w.q].nodes, 0};
+        mrg[n_mrg++] = {w.head, w.row_tile + member, cta + (i - 1) * g + member, cta + last * g + member, g, seqs[w.q].node0, seqs[w.q].nodes, 0};
       }
     }
     cta += used * g;
@@ -320,13 +319,13 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
   // hundred, 51.0, 50.6; 8 x 128 over 1000, 42 per hundred, 34.0, 30.4).  The small ones of 16 rows are not (mma.sync: 32 x
   // 8 over 1024-2048 39.4, 38.7; 64 x 4 over 500-1500 49.2, 47.8; 24 x 8 over 3000-4000 60.5, 58.5; an f32 cache: 16 x 4
   // over 1000-1400 108.6, 106.2; 40 x 8 over 300-600 102.8, 104.8).
-  *join = var.join > 0 && n_mrg * 100 >= grid * var.join;
+  bool join = var.join > 0 && n_mrg * 100 >= grid * var.join;
   *parts = 0;
   for (int i = 0; i < n_mrg; ++i) {
     *parts = std::max(*parts, (mrg[i].c1 - mrg[i].c0) / mrg[i].stride + 1);
-    if (*parts > 3) *join = false;
+    if (*parts > 3) join = false;
   }
-  if (!*join) return n_mrg;
+  if (!join) return n_mrg;
   for (int i = 0; i < n_mrg; ++i) {
     cut[mrg[i].c0].follow = (mrg[i].c1 - mrg[i].c0) / mrg[i].stride;
     for (int c = mrg[i].c0 + mrg[i].stride; c <= mrg[i].c1; c += mrg[i].stride) cut[c].awaited = 1;
@@ -346,15 +345,15 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   const int W = std::max((max_nodes + 31) / 32, 1);
   const TreeVariant var = variant_for(t->f16, c.head_dim, max_nodes * G);
   const int grid = t->sms * var.ctas_per_sm;
-  const size_t h_hdr = take(kHdrInts), h_flags = take((size_t)t->sms * kTreeMaxCtasPerSm), h_start = take(S + 1), h_seqs = take((size_t)S * 8), h_pos = take(N), h_dst = take(N),
-               h_par = take(N), h_anc = take((size_t)N * W), h_cut = take((size_t)grid * 16), h_mrg = take((size_t)grid * 8),
+  const size_t h_hdr = take(kHdrInts), h_flags = take((size_t)t->sms * kTreeMaxCtasPerSm), h_start = take(S + 1), h_seqs = take((size_t)S * 4), h_pos = take(N), h_dst = take(N),
+               h_par = take(N), h_anc = take((size_t)N * W), h_cut = take((size_t)grid * 12), h_mrg = take((size_t)grid * 8),
                h_tables = o;
   std::vector<TreeSeq> seqs;
   for (int s = 0; s < S; ++s) {
     const int a0 = b->seq_start[s], T = b->seq_start[s + 1] - a0, ctx = b->ctx[s];
     H[h_start + s] = a0;
     if (T == 0) continue;
-    seqs.push_back({a0, T, ctx, (int32_t)(o - h_tables), s, 0, 0, 0});
+    seqs.push_back({a0, T, ctx, (int32_t)(o - h_tables)});
     const int32_t* row = b->block_table + (size_t)s * b->max_blocks;
     const int nb = (ctx + T + 15) / 16;
     std::copy(row, row + nb, H + o);
@@ -378,10 +377,9 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
     }
   }
   H[h_start + S] = N;
-  // only the wide kernel has the rows of a sequence walk the keys side by side; at most 1024 rows: gangs of four
-  bool join = false;
-  const int n_mrg = distribute(c, seqs, var, grid, var.kernel == kTreeTcWide ? 4 : 1, reinterpret_cast<TreeCut*>(H + h_cut),
-                               reinterpret_cast<TreeMerge*>(H + h_mrg), &join, &t->max_parts);
+  static_assert(sizeof(TreeSeq) == 16 && sizeof(TreeCut) == 48 && sizeof(TreeMerge) == 32, "as the pieces are measured above");
+  const int n_mrg = distribute(c, seqs, var, grid, var.kernel == kTreeTcWide ? kWideGang : 1, reinterpret_cast<TreeCut*>(H + h_cut),
+                               reinterpret_cast<TreeMerge*>(H + h_mrg), &t->max_parts);
   std::fill(H + h_flags, H + h_flags + t->sms * kTreeMaxCtasPerSm, 0);
   std::copy(seqs.begin(), seqs.end(), reinterpret_cast<TreeSeq*>(H + h_seqs));
   std::fill(H + h_hdr, H + h_hdr + kHdrInts, 0);
@@ -390,7 +388,6 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   H[h_hdr + kHdrWords] = W;
   H[h_hdr + kHdrRowTile] = var.row_tile;
   H[h_hdr + kHdrMerges] = n_mrg;
-  H[h_hdr + kHdrJoin] = join;
   int32_t* d = reinterpret_cast<int32_t*>(t->ws + t->lay.meta);
   TreeMeta& m = t->meta;
   m.hdr = d + h_hdr;

@@ -18,12 +18,11 @@ constexpr uint32_t kErrShape = 16u; // a captured call met a plan of another sha
 enum TreeType { kTreeF32 = 0, kTreeF16 = 1, kTreeBf16 = 2 };
 
 // Header words of the uploaded plan.
-enum TreeHdr { kHdrSeqs = 0, kHdrTokens, kHdrWords, kHdrRowTile, kHdrMerges, kHdrJoin, kHdrInts = 16 };
+enum TreeHdr { kHdrSeqs = 0, kHdrTokens, kHdrWords, kHdrRowTile, kHdrMerges, kHdrInts = 16 };
 
-// A sequence with nodes, as the attention kernels read it (two 16-byte loads).
+// A sequence with nodes, as the attention kernels read it (one 16-byte load).
 struct alignas(16) TreeSeq {
   int32_t node0, nodes, ctx, tab;  // first node, nodes, cached tokens, first entry in tables
-  int32_t seq, pad0, pad1, pad2;
 };
 // Attention work of one CTA: `count` key tiles in the order (entry of seqs, KV
 // head, row tile, key tile), from `tile` of this unit on.  A row tile is
