@@ -1,6 +1,7 @@
 // kernels_tree.cu - draft trees over the paged KV cache: rotary tables, the
 // rotated append, the commit of an accepted path, and the merge of split
-// attention.  (Attention itself: kernels_tree_f32.cu, kernels_tree_f16.cu.)
+// attention.  (Attention itself: kernels_tree_f32.cu, kernels_tree_f16.cu,
+// kernels_tree_tc.cu.)
 #include <limits.h>
 
 #include "tree_common.cuh"
@@ -119,7 +120,7 @@ cudaError_t append_d(const TreeAppendArgs& a, cudaStream_t s) {
   // a head per lane group while that leaves SMs idle: at 16:8 heads x 128, 16 nodes 1.8 us against 3.0 with four, 200 nodes
   // 3.4 with either, 1000 nodes 9.7 against 7.0
   const int64_t rows = (int64_t)a.m.N * ((a.q ? a.d.H : 0) + (a.k ? 2 * a.d.Hkv : 0));
-  return rows <= 4 * 152 * (256 / (D / 4)) ? append_u<D, 1>(a, s) : append_u<D, 4>(a, s);
+  return rows <= 4ll * a.sms * (256 / (D / 4)) ? append_u<D, 1>(a, s) : append_u<D, 4>(a, s);
 }
 
 // ---- commit ----------------------------------------------------------------------

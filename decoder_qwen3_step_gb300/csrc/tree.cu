@@ -702,6 +702,7 @@ int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* str
   a.in_type = x->in_type;
   a.q_type = x->q_type;
   a.kv_f16 = t->f16;
+  a.sms = t->sms;
   a.layer = layer;
   a.kv = t->slabs;
   TREE_CUDA(launch_tree_append(a, (cudaStream_t)stream));

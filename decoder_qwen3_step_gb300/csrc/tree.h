@@ -76,6 +76,7 @@ struct TreeAppendArgs {
   void* q_out;
   int in_type, q_type, kv_f16, layer;
   void* kv;
+  int sms;  // of the plan's device
 };
 cudaError_t launch_tree_append(const TreeAppendArgs& a, cudaStream_t s);
 
