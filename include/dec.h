@@ -639,8 +639,10 @@ int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* str
  * an fp32 cache, which is computed in fp32 throughout; DEC_T_F16 or
  * DEC_T_BF16 for an f16 cache, where queries and weights are rounded to f16
  * for the tensor cores and statistics and sums are fp32.  out must not overlap
- * q.  A node's result does not depend on what is cached in slots it does not see (infinities and
- * NaN included); it may differ in its last bits with the rest of the batch,
+ * q.  A node's result does not depend on what is cached in slots it does not
+ * see (infinities and NaN included); a query, or a key that it sees, that is NaN
+ * gives NaN; scores that are all -inf give zeros, as for a node that sees
+ * nothing.  The result may differ in its last bits with the rest of the batch,
  * which decides how the keys are split over the GPU, and between a direct call
  * and a replay of one captured with another plan (the split's parts are then
  * added in another order). */

@@ -83,3 +83,16 @@ def test_channels_that_are_not_turned_are_copied(shape, rot, cache, nodes, layou
         assert same(w.slab[1, b, 0, :, r, rot:], k2[n, :, rot:].to(w.cache))
         assert same(w.slab[1, b, 1, :, r], v2[n].to(w.cache))
     w.close()
+
+
+@pytest.mark.parametrize("cache, nodes", [("f16", 4), ("f16", 40), ("f16", 200), ("f32", 4)])
+def test_scores_that_are_all_minus_infinity_give_zeros(cache, nodes):
+    w = Setup("16:8x128", cache, [0, 30], [random_tree(nodes, 1), 2], seed=2)
+    q = w.rand(w.N, w.H, w.D)
+    b, r = w.where(0, 0)
+    w.slab[0, b, 0, :, r, 5] = -1.0  # the root's key, the only one that it sees
+    q[0, :, 5] = float("inf")
+    out = w.trees.attend(0, q)
+    assert not bool(out[0].any())
+    check(w, out, 0, q, sorted(random.Random(3).sample(range(1, w.N), min(w.N - 1, 30))))
+    w.close()
