@@ -13,10 +13,10 @@
 // leaves the result exact: numerator and denominator use the same maximum.
 //
 // Rounded to f16: the queries, each row scaled by a power of two to [1, 2)
-// first so that no magnitude overflows (2^-12 relative per channel, as the
-// cached keys have it already), and the weights P (2^-12 relative each; they
-// are at most 2^8 and the row's largest at least 1).  Statistics and
-// accumulators are fp32.
+// first so that no magnitude overflows (off by at most 2^-11 of the row's
+// largest channel; the cached keys are f16 already), and the weights P (2^-11
+// relative each, or 2^-25 where that is more; they are at most 2^8 and the
+// row's largest at least 1).  Statistics and accumulators are fp32.
 #include "attn_fold.cuh"
 #include "tc_common.cuh"
 #include "tree_common.cuh"

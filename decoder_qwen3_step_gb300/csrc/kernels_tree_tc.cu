@@ -557,8 +557,8 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           }
           const float mu = m == -INFINITY ? 0.f : m;
           uint64_t c2 = pack2(c, c), m2 = pack2(-mu, -mu), l2[2] = {0ull, 0ull};
-          // s c - m in one rounding while that is small against the weights' own (2^-12 at 2^12); far out the product is
-          // rounded as the maximum was, or the largest score would miss it by its own last place
+          // s c - m in one rounding while the maximum's own (2^-13 up to 2^12) is small against the weights' (2^-11); far out
+          // the product is rounded as the maximum was, or the largest score would miss it by its own last place
           if (__any_sync(0xffffffffu, !(fabsf(mu) <= 4096.f))) {
             tc_wait32(sa);
 #pragma unroll 1

@@ -317,8 +317,8 @@ int distribute(const dec_config& c, std::vector<TreeSeq>& seqs, const TreeVarian
   // (joined, second kernel: 32 x 64 over 1024-2048 51.9 us, 56.4; 16 x 64 over 2000 35.9, 40.5; 8 x 64 over 2000 29.1, 29.4;
   // wide: 8 x 256 over 8000 114, 119; 5 x 256 over 4000, 53 units per hundred CTAs, 57.3, 59.2; 4 x 256 there, 42 per
   // hundred, 51.0, 50.6; 8 x 128 over 1000, 42 per hundred, 34.0, 30.4).  The small ones of 16 rows are not (mma.sync: 32 x
-  // 8 over 1024-2048 39.4, 38.7; 64 x 4 over 500-1500 49.2, 47.8; 24 x 8 over 3000-4000 60.5, 58.5; an f32 cache: 16 x 4
-  // over 1000-1400 108.6, 106.2; 40 x 8 over 300-600 102.8, 104.8).
+  // 8 over 1024-2048 39.4, 38.7; 64 x 4 over 500-1500 49.2, 47.8; 24 x 8 over 3000-4000 60.5, 58.5).  An fp32 cache has it
+  // either way (16 x 4 over 1000-1400 108.6, 106.2; 40 x 8 over 300-600 102.8, 104.8) and does without.
   bool join = var.join > 0 && n_mrg * 100 >= grid * var.join;
   *parts = 0;
   for (int i = 0; i < n_mrg; ++i) {

@@ -184,7 +184,7 @@ __device__ __forceinline__ float ex2(float x) {
 // branch and no division per row: a first version with both, one row per warp
 // and step, took 0.7 us a row on instruction latency alone.
 // Each row is scaled by a power of two so that its largest magnitude lies in
-// [1, 2): f16 then rounds every channel by at most 2^-12 of that, whatever the
+// [1, 2): f16 then rounds every channel by at most 2^-11 of that, whatever the
 // queries' range; fac[r] takes the row's score factor.  put(r, channel / 8,
 // eight halves).  Rows past the last are zeros.
 template <int D, int R, int W, int kMaxU, typename T, typename F>
