@@ -732,26 +732,69 @@ int dec_pool_bytes(const dec_config* cfg, int32_t n_blocks, size_t* bytes) {
   return DEC_OK;
 }
 
+static int pool_new(const dec_config* cfg, int kv_type, size_t scales, int32_t n_blocks, void* slabs, size_t bytes,
+                    size_t need, dec_pool** out) {
+  if (!slabs || !out) return fail(DEC_EINVAL, "NULL argument");
+  if (bytes < need) return fail(DEC_EINVAL, "slab buffer too small: %zu < %zu", bytes, need);
+  if ((uintptr_t)slabs & 255) return fail(DEC_EINVAL, "slab buffer must be 256-byte aligned");
+  dec_pool* p = nullptr;
+  try {
+    p = new dec_pool();
+    p->cfg = *cfg;
+    p->n_blocks = n_blocks;
+    p->slabs = slabs;
+    p->kv_type = kv_type;
+    p->scales = scales;
+    p->refs.assign(n_blocks, 0);
+    p->fill.assign(n_blocks, 0);
+    p->registered.assign(n_blocks, 0);
+    p->key.assign(n_blocks, 0);
+    p->lru_pos.assign(n_blocks, p->lru.end());
+    p->free_list.resize(n_blocks);
+    for (int i = 0; i < n_blocks; ++i) p->free_list[i] = n_blocks - 1 - i;
+  } catch (const std::bad_alloc&) {
+    delete p;
+    return fail(DEC_ECAPACITY, "out of host memory");
+  }
+  *out = p;
+  return DEC_OK;
+}
+
 int dec_pool_create(const dec_config* cfg, int32_t n_blocks, void* slabs, size_t bytes, dec_pool** out) {
   size_t need = 0;
   int rc = dec_pool_bytes(cfg, n_blocks, &need);
   if (rc) return rc;
-  if (!slabs || !out) return fail(DEC_EINVAL, "NULL argument");
-  if (bytes < need) return fail(DEC_EINVAL, "slab buffer too small: %zu < %zu", bytes, need);
-  if ((uintptr_t)slabs & 255) return fail(DEC_EINVAL, "slab buffer must be 256-byte aligned");
-  dec_pool* p = new dec_pool();
-  p->cfg = *cfg;
-  p->n_blocks = n_blocks;
-  p->slabs = slabs;
-  p->refs.assign(n_blocks, 0);
-  p->fill.assign(n_blocks, 0);
-  p->registered.assign(n_blocks, 0);
-  p->key.assign(n_blocks, 0);
-  p->lru_pos.assign(n_blocks, p->lru.end());
-  p->free_list.resize(n_blocks);
-  for (int i = 0; i < n_blocks; ++i) p->free_list[i] = n_blocks - 1 - i;
-  *out = p;
+  return pool_new(cfg, cfg->mode == DEC_FP32 ? DEC_T_F32 : DEC_T_F16, 0, n_blocks, slabs, bytes, need, out);
+}
+
+// Codes of one byte, then the scales.
+static int pool_q8_layout(const dec_config* cfg, int32_t kv_type, int32_t n_blocks, size_t* scales, size_t* bytes) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  if (kv_type != DEC_T_E4M3 && kv_type != DEC_T_I8) return fail(DEC_EINVAL, "8-bit element types are DEC_T_E4M3 and DEC_T_I8, not %d", kv_type);
+  if (cfg->mode == DEC_FP32) return fail(DEC_EINVAL, "a cache in 8 bits needs a serving mode: its attention rounds weights to f16");
+  if (n_blocks <= 0) return fail(DEC_EINVAL, "a pool needs at least one block");
+  const size_t pages = (size_t)n_blocks * cfg->n_layers * 2 * cfg->n_kv_heads;
+  *scales = align256(pages * cfg->block_tokens * cfg->head_dim);
+  *bytes = *scales + pages * sizeof(float);
   return DEC_OK;
+}
+
+int dec_pool_q8_bytes(const dec_config* cfg, int32_t kv_type, int32_t n_blocks, size_t* bytes) {
+  size_t scales = 0, need = 0;
+  int rc = pool_q8_layout(cfg, kv_type, n_blocks, &scales, &need);
+  if (rc) return rc;
+  if (!bytes) return fail(DEC_EINVAL, "bytes is NULL");
+  *bytes = need;
+  return DEC_OK;
+}
+
+int dec_pool_q8_create(const dec_config* cfg, int32_t kv_type, int32_t n_blocks, void* slabs, size_t bytes,
+                       dec_pool** out) {
+  size_t scales = 0, need = 0;
+  int rc = pool_q8_layout(cfg, kv_type, n_blocks, &scales, &need);
+  if (rc) return rc;
+  return pool_new(cfg, kv_type, scales, n_blocks, slabs, bytes, need, out);
 }
 
 void dec_pool_destroy(dec_pool* p) { delete p; }
@@ -826,6 +869,18 @@ int dec_kv_offset(const dec_pool* p, const int32_t* table, int32_t n_table, int3
   if (blk < 0 || blk >= p->n_blocks) return fail(DEC_EBLOCK, "block id %d outside the pool", blk);
   *offset = kv_offset(layer, blk, is_v, kv_head, pos % c.block_tokens, p->n_blocks, c.n_kv_heads, c.block_tokens,
                       c.head_dim);
+  return DEC_OK;
+}
+
+int dec_kv_scale_offset(const dec_pool* p, const int32_t* table, int32_t n_table, int32_t pos, int32_t layer,
+                        int32_t kv_head, int32_t is_v, int64_t* offset) {
+  int64_t at = 0;
+  if (!offset) return fail(DEC_EINVAL, "NULL argument");
+  int rc = dec_kv_offset(p, table, n_table, pos, layer, kv_head, is_v, &at);
+  if (rc) return rc;
+  if (!pool_q8(p)) return fail(DEC_EINVAL, "the pool has no scales");
+  const int blk = table[pos / p->cfg.block_tokens];
+  *offset = (int64_t)p->scales + ((((int64_t)layer * p->n_blocks + blk) * p->cfg.n_kv_heads + kv_head) * 2 + is_v) * 4;
   return DEC_OK;
 }
 
@@ -1220,6 +1275,7 @@ static int launch_decode_graph(dec_model* m, const StepPlan& sp, cudaStream_t st
 // written position of the batch.
 static int check_batch(const dec_config& c, const dec_pool* pool, const dec_batch* b, bool decode) {
   if (!b) return fail(DEC_EINVAL, "NULL argument");
+  if (pool_q8(pool)) return fail(DEC_EINVAL, "the decoder does not run on a pool held in 8 bits: dec_tree_* does");
   const int S = b->n_seqs, N = b->n_tokens;
   if (S < 1 || N < 1) return fail(DEC_EINVAL, "empty step: %d sequences, %d tokens", S, N);
   if (decode && N != S) return fail(DEC_EINVAL, "decode takes exactly one token per sequence");

@@ -46,6 +46,7 @@ AttendLayout attend_layout(const dec_config& c, int S, int max_ctx, int max_bloc
 int attend_check(const dec_pool* pool, int32_t layer, int32_t n_seqs, const float* q, const int32_t* ctx,
                  const int32_t* block_table, int32_t max_blocks, const void* out, int* max_ctx) {
   if (!pool || !q || !ctx || !block_table || !out) return fail_msg(DEC_EINVAL, "NULL argument");
+  if (pool_q8(pool)) return fail_msg(DEC_EINVAL, "a pool held in 8 bits is read by dec_tree_attend");
   const dec_config& c = pool->cfg;
   if (layer < 0 || layer >= c.n_layers) return fail_msg(DEC_EINVAL, "layer outside the model");
   if (n_seqs < 1) return fail_msg(DEC_EINVAL, "n_seqs must be at least 1");

@@ -17,6 +17,8 @@ struct dec_pool {
   dec_config cfg;
   int n_blocks;
   void* slabs;
+  int kv_type;     // DEC_T_* of its elements
+  size_t scales;   // 8-bit elements: byte offset of the scales
   std::vector<int32_t> refs;
   std::vector<int32_t> free_list;
   std::vector<int32_t> fill;
@@ -28,6 +30,8 @@ struct dec_pool {
 };
 
 namespace dec {
+// Whether a pool holds 8-bit codes and scales.
+inline bool pool_q8(const dec_pool* p) { return p->kv_type == DEC_T_E4M3 || p->kv_type == DEC_T_I8; }
 // Record `msg` as the thread's last error and return `code`.
 int set_error(int code, const char* msg);
 // Look up the device address of dec_attend_noalloc's array on the current

@@ -2,8 +2,6 @@
 // rotated append, the commit of an accepted path, and the merge of split
 // attention.  (Attention itself: kernels_tree_f32.cu, kernels_tree_f16.cu,
 // kernels_tree_tc.cu.)
-#include <limits.h>
-
 #include "tree_common.cuh"
 
 namespace dec {
@@ -101,7 +99,7 @@ __global__ void __launch_bounds__(256, U == 4 && sizeof(T) == 4 ? 5 : 4) k_tree_
       tree_store4(a.q_out, a.q_type, node * a.ldo + (h0 + u) * D + el, pad ? make_float4(0.f, 0.f, 0.f, 0.f) : y);
     } else if (!pad) {
       const int64_t off = kv_offset(a.layer, dst >> 4, is_v, h0 + u, dst & 15, a.d.n_blocks, a.d.Hkv, 16, D);
-      tree_store4(a.kv, a.kv_f16 ? kTreeF16 : kTreeF32, off + el, y);
+      tree_store4(a.kv, a.kv_type, off + el, y);
     }
   }
 }
@@ -141,33 +139,8 @@ __global__ void __launch_bounds__(kCommitThreads) k_tree_commit(const __grid_con
   const int s = blockIdx.x / blocks_per_seq, part = blockIdx.x % blocks_per_seq;
   const bool ok = tree_shape_ok(a.m);  // the plan is older than the kernels before this one
   const int b = __ldg(a.m.seq_start + s), T = min(__ldg(a.m.seq_start + s + 1) - b, kTreeMaxNodes);
-  for (int i = threadIdx.x; i <= T; i += kCommitThreads) child[i] = INT_MAX;
-  pdl_wait_prev();
-  pdl_launch_next();
-  if (!ok) return;
-  __syncthreads();
-  for (int i = threadIdx.x; i < T; i += kCommitThreads) {
-    const int p = __ldg(a.m.parents + b + i);
-    if (p < -1) continue;  // padding
-    const bool ok = p >= 0 ? a.draft[b + i] == a.target[b + p] : !a.prior || a.draft[b + i] == a.prior[s];
-    if (ok) atomicMin(&child[p + 1], i);
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int n = 0;
-    for (int at = child[0]; at != INT_MAX; at = child[at + 1]) path[n++] = at;
-    n_path = n;
-  }
-  __syncthreads();
-  const int n = n_path;
-  if (part == 0) {
-    for (int i = threadIdx.x; i < T; i += kCommitThreads) a.path[b + i] = i < n ? path[i] : -1;
-    if (threadIdx.x == 0) {
-      a.accepted[s] = n;
-      a.next[s] = n ? a.target[b + path[n - 1]] : a.prior ? a.prior[s] : -1;
-    }
-  }
-  const int row_chunks = a.d.D * a.kv_bytes / 16;  // 16-byte pieces of a head row
+  const int n = tree_walk<kCommitThreads>(a, s, b, T, ok, part == 0, child, path, &n_path);
+  const int row_chunks = a.d.D * (a.kv_type == kTreeF16 ? 2 : 4) / 16;  // 16-byte pieces of a head row
   const int col = part * kCommitThreads + threadIdx.x;
   if (col >= cols) return;
   const int c = col % row_chunks, h = col / row_chunks % a.d.Hkv, lv = col / row_chunks / a.d.Hkv;
@@ -398,7 +371,7 @@ cudaError_t launch_tree_append(const TreeAppendArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s) {
-  const int cols = a.d.n_layers * 2 * a.d.Hkv * (a.d.D * a.kv_bytes / 16);
+  const int cols = a.d.n_layers * 2 * a.d.Hkv * (a.d.D * (a.kv_type == kTreeF16 ? 2 : 4) / 16);
   const int per = (cols + kCommitThreads - 1) / kCommitThreads;
   return launch_pdl(k_tree_commit, a.m.S * per, kCommitThreads, 0, s, a, cols, per);
 }

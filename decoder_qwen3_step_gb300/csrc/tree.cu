@@ -49,8 +49,9 @@ struct TreeLayout {
 // keys, 16:8 heads x 128: 16 rows 38.4 us on mma.sync against 46 on tcgen05; 32
 // rows 83 (its accumulators spill at two row tiles a warp) against 51; at 8
 // sequences over 8000 keys with 512 rows, narrow units 211 us, wide ones 114.
-TreeVariant variant_for(bool f16, int D, int max_rows) {
-  if (!f16) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2, 0};
+TreeVariant variant_for(int kv_type, int D, int max_rows) {
+  if (kv_type == kTreeE4m3 || kv_type == kTreeI8) return {kTreeMmaQ8, 16, 64, 3, 2, 0};
+  if (kv_type == kTreeF32) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2, 0};
   if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, 4, 50};
   if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, 4, 25};
   return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2, 0};
@@ -61,11 +62,12 @@ static_assert(kTreeMaxNodes * 4 <= kWideGang * 256, "at most four query heads pe
 // Records of the attention kernels: two per CTA; rows of all of them, per SM.
 constexpr int kRecordRows = 2 * 256;
 
-TreeLayout tree_layout(const dec_config& c, int max_seqs, int max_tokens, int max_blocks, int sms) {
+TreeLayout tree_layout(const dec_config& c, bool q8, int max_seqs, int max_tokens, int max_blocks, int sms) {
   TreeLayout L{};
   const size_t S = max_seqs, N = max_tokens, P = (size_t)sms * kTreeMaxCtasPerSm;
-  // header, flags, seq_start, seqs, pos, dst, parents, mask, cuts, merges, tables (each piece 16-byte aligned)
-  L.meta_ints = kHdrInts + P + (S + 1) + 4 * S + 3 * N + N * (kTreeMaxNodes / 32) + P * 20 + S * (size_t)max_blocks + 16 * 4;
+  // header, flags, seq_start, seqs, pos, dst, parents, mask, cuts, merges, reads, pages (a node at least in each), tables
+  // (each piece 16-byte aligned)
+  L.meta_ints = kHdrInts + P + (S + 1) + 4 * S + 3 * N + N * (kTreeMaxNodes / 32) + P * 20 + 8 * (S + 1) + (q8 ? 4 * N : 0) + S * (size_t)max_blocks + 16 * 4;
   L.meta = 256;
   L.part = up256(L.meta + L.meta_ints * 4);
   L.total = up256(L.part + (size_t)sms * kRecordRows * (size_t)(c.head_dim + 2) * 4);
@@ -105,13 +107,16 @@ struct dec_tree {
   int32_t* stage[kStages];
   cudaEvent_t stage_ev[kStages];
   int stage_next;
-  bool f16;
+  bool f16, q8;  // f16: computed on the f16 tensor cores (f16 and 8-bit caches)
+  int kv_type;
+  float* scales;  // of an 8-bit cache
   CUtensorMap tm, tm_groups;  // boxes of a block: K and V row by row, and K or V by groups of eight rows
   bool cleared;               // the error word has been
   // the plan that was set last
   bool set;
   TreeMeta meta;
-  int kernel, max_nodes, max_position, ctas, n_merges, max_parts;
+  int kernel, max_nodes, max_position, ctas, n_merges, max_parts, n_pages, read_blocks[2];
+  int64_t read_rows[2];
 };
 
 namespace {
@@ -122,7 +127,8 @@ namespace {
 // block.  groups: [64 channels][8 rows][halves][groups of 8 rows][layer, block,
 // K or V]: one box is the K or the V of one KV head of one block, the halves of
 // eight rows next to each other, so that the groups of a tile of many blocks
-// lie evenly apart, as the tensor cores want them.
+// lie evenly apart, as the tensor cores want them.  8-bit codes: a box as the
+// first, rows of the whole head (128, 64 or 32 bytes, swizzled as wide).
 bool pool_map(CUtensorMap* out, const dec_pool* p, bool groups) {
   typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -148,6 +154,15 @@ bool pool_map(CUtensorMap* out, const dec_pool* p, bool groups) {
     box[1] = 8;
   }
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  if (pool_q8(p)) {
+    const cuuint64_t codes = (cuuint64_t)c.n_kv_heads * 16 * D, d8[4] = {D, (cuuint64_t)c.n_kv_heads * 16, 2, n}, s8[3] = {D, codes, 2 * codes};
+    const cuuint32_t b8[4] = {(cuuint32_t)D, 16, 2, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p->slabs, d8, s8, b8, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              D == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+              : D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                        : CU_TENSOR_MAP_SWIZZLE_32B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
   return fn(out, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, p->slabs, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             bd == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -343,21 +358,37 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   int max_nodes = 0, max_position = 0;
   for (int s = 0; s < S; ++s) max_nodes = std::max(max_nodes, b->seq_start[s + 1] - b->seq_start[s]);
   const int W = std::max((max_nodes + 31) / 32, 1);
-  const TreeVariant var = variant_for(t->f16, c.head_dim, max_nodes * G);
+  const TreeVariant var = variant_for(t->kv_type, c.head_dim, max_nodes * G);
   const int grid = t->sms * var.ctas_per_sm;
   const size_t h_hdr = take(kHdrInts), h_flags = take((size_t)t->sms * kTreeMaxCtasPerSm), h_start = take(S + 1), h_seqs = take((size_t)S * 4), h_pos = take(N), h_dst = take(N),
                h_par = take(N), h_anc = take((size_t)N * W), h_cut = take((size_t)grid * 12), h_mrg = take((size_t)grid * 8),
-               h_tables = o;
+               h_reads = take((size_t)(S + 1) * 8), h_pages = take(t->q8 ? (size_t)N * 4 : 0), h_tables = o;
   std::vector<TreeSeq> seqs;
+  TreePage* pages = reinterpret_cast<TreePage*>(H + h_pages);
+  TreeReadSeq read{};
+  int n_pages = 0;
   for (int s = 0; s < S; ++s) {
     const int a0 = b->seq_start[s], T = b->seq_start[s + 1] - a0, ctx = b->ctx[s];
     H[h_start + s] = a0;
+    read.tab = (int32_t)(o - h_tables);
+    read.ctx = ctx;
+    read.nodes = T;
+    reinterpret_cast<TreeReadSeq*>(H + h_reads)[s] = read;
     if (T == 0) continue;
+    read.blocks[0] += (ctx + T + 15) / 16;
+    read.blocks[1] += (ctx + T + 15) / 16 - ctx / 16;
+    read.rows[0] += ctx + T;
+    read.rows[1] += ctx % 16 + T;
     seqs.push_back({a0, T, ctx, (int32_t)(o - h_tables)});
     const int32_t* row = b->block_table + (size_t)s * b->max_blocks;
     const int nb = (ctx + T + 15) / 16;
     std::copy(row, row + nb, H + o);
     o += nb;
+    for (int i = 0; t->q8 && i < T;) {
+      const int slot = (ctx + i) & 15, in = std::min(T - i, 16 - slot);
+      pages[n_pages++] = {row[(ctx + i) >> 4], a0 + i, slot, in};
+      i += in;
+    }
     uint32_t* anc = reinterpret_cast<uint32_t*>(H + h_anc + (size_t)a0 * W);
     for (int i = 0; i < T; ++i) {
       const int p = b->parents ? b->parents[a0 + i] : i - 1;
@@ -377,7 +408,8 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
     }
   }
   H[h_start + S] = N;
-  static_assert(sizeof(TreeSeq) == 16 && sizeof(TreeCut) == 48 && sizeof(TreeMerge) == 32, "as the pieces are measured above");
+  reinterpret_cast<TreeReadSeq*>(H + h_reads)[S] = read;
+  static_assert(sizeof(TreeSeq) == 16 && sizeof(TreeCut) == 48 && sizeof(TreeMerge) == 32 && sizeof(TreePage) == 16 && sizeof(TreeReadSeq) == 32, "as the pieces are measured above");
   const int n_mrg = distribute(c, seqs, var, grid, var.kernel == kTreeTcWide ? kWideGang : 1, reinterpret_cast<TreeCut*>(H + h_cut),
                                reinterpret_cast<TreeMerge*>(H + h_mrg), &t->max_parts);
   std::fill(H + h_flags, H + h_flags + t->sms * kTreeMaxCtasPerSm, 0);
@@ -388,6 +420,9 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   H[h_hdr + kHdrWords] = W;
   H[h_hdr + kHdrRowTile] = var.row_tile;
   H[h_hdr + kHdrMerges] = n_mrg;
+  H[h_hdr + kHdrPages] = n_pages;
+  H[h_hdr + kHdrRows] = read.rows[0];
+  H[h_hdr + kHdrRows + 1] = read.rows[1];
   int32_t* d = reinterpret_cast<int32_t*>(t->ws + t->lay.meta);
   TreeMeta& m = t->meta;
   m.hdr = d + h_hdr;
@@ -399,6 +434,8 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   m.anc = reinterpret_cast<const uint32_t*>(d + h_anc);
   m.cuts = reinterpret_cast<const TreeCut*>(d + h_cut);
   m.merges = reinterpret_cast<const TreeMerge*>(d + h_mrg);
+  m.pages = reinterpret_cast<const TreePage*>(d + h_pages);
+  m.reads = reinterpret_cast<const TreeReadSeq*>(d + h_reads);
   m.tables = d + h_tables;
   m.err = reinterpret_cast<uint32_t*>(t->ws);
   m.flags = reinterpret_cast<uint32_t*>(d + h_flags);
@@ -412,6 +449,11 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   t->max_position = max_position;
   t->ctas = grid;
   t->n_merges = n_mrg;
+  t->n_pages = n_pages;
+  for (int i = 0; i < 2; ++i) {
+    t->read_blocks[i] = read.blocks[i];
+    t->read_rows[i] = read.rows[i];
+  }
   return o;
 }
 
@@ -525,7 +567,7 @@ int dec_tree_workspace_bytes(const dec_pool* pool, int32_t max_seqs, int32_t max
   int dev = 0, sms = 0;
   TREE_CUDA(cudaGetDevice(&dev));
   TREE_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  *bytes = tree_layout(pool->cfg, max_seqs, max_tokens, max_blocks, sms).total;
+  *bytes = tree_layout(pool->cfg, pool_q8(pool), max_seqs, max_tokens, max_blocks, sms).total;
   return DEC_OK;
 }
 
@@ -561,16 +603,19 @@ int dec_tree_create(const dec_pool* pool, int32_t max_seqs, int32_t max_tokens, 
   t->max_blocks = max_blocks;
   t->ws = (char*)workspace;
   t->f16 = pool->cfg.mode != DEC_FP32;
+  t->q8 = pool_q8(pool);
+  t->kv_type = pool->kv_type;
+  t->scales = t->q8 ? reinterpret_cast<float*>(reinterpret_cast<char*>(pool->slabs) + pool->scales) : nullptr;
   cudaError_t e = cudaGetDevice(&t->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&t->sms, cudaDevAttrMultiProcessorCount, t->device);
-  t->lay = tree_layout(t->cfg, max_seqs, max_tokens, max_blocks, t->sms);
+  t->lay = tree_layout(t->cfg, t->q8, max_seqs, max_tokens, max_blocks, t->sms);
   for (int i = 0; i < kStages && e == cudaSuccess; ++i) {
     e = cudaMallocHost((void**)&t->stage[i], t->lay.meta_ints * 4);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&t->stage_ev[i], cudaEventDisableTiming);
   }
   if (e != cudaSuccess) {
     rc = fail(DEC_ECUDA, "dec_tree_create: %s", cudaGetErrorString(e));
-  } else if (t->f16 && !(pool_map(&t->tm, pool, false) && pool_map(&t->tm_groups, pool, true))) {
+  } else if (t->f16 && !(pool_map(&t->tm, pool, false) && (t->q8 || pool_map(&t->tm_groups, pool, true)))) {
     rc = fail(DEC_ECUDA, "tensor map of the KV pool failed");
   }
   if (rc) {
@@ -701,11 +746,13 @@ int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* str
   a.q_out = x->q_out;
   a.in_type = x->in_type;
   a.q_type = x->q_type;
-  a.kv_f16 = t->f16;
+  a.kv_type = t->kv_type;
+  a.scales = t->scales;
+  a.n_pages = t->n_pages;
   a.sms = t->sms;
   a.layer = layer;
   a.kv = t->slabs;
-  TREE_CUDA(launch_tree_append(a, (cudaStream_t)stream));
+  TREE_CUDA(t->q8 ? launch_tree_append_q8(a, (cudaStream_t)stream) : launch_tree_append(a, (cudaStream_t)stream));
   return DEC_OK;
 }
 
@@ -719,7 +766,7 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
   if ((rc = check_rows(out, ldo, c.n_heads, c.head_dim, out_type, "out"))) return rc;
   if (q == out) return fail(DEC_EINVAL, "the output must not be the queries: other units still read them");
   if (t->f16 && out_type == DEC_T_F32)
-    return fail(DEC_EINVAL, "an f16 cache gives f16 or bf16 outputs (its weights are rounded to f16)");
+    return fail(DEC_EINVAL, "an f16 or 8-bit cache gives f16 or bf16 outputs (its weights are rounded to f16)");
   DeviceGuard g(t->device);
   if (!g.ok) return fail(DEC_ECUDA, "the plan's device cannot be made current");
   TreeAttendArgs a{};
@@ -733,10 +780,12 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
   a.out_type = out_type;
   a.layer = layer;
   a.kv = t->slabs;
+  a.scales = t->scales;
   a.part = (float*)(t->ws + t->lay.part);
   a.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)c.head_dim));
   cudaStream_t st = (cudaStream_t)stream;
   TREE_CUDA(t->kernel == kTreeFfma  ? launch_tree_attend_f32(a, t->ctas, st)
+            : t->kernel == kTreeMmaQ8 ? launch_tree_attend_q8(a, t->kv_type, &t->tm, t->ctas, st)
             : t->kernel == kTreeMma ? launch_tree_attend_f16(a, &t->tm, t->ctas, st)
                                     : launch_tree_attend_tc(a, &t->tm_groups, t->ctas, t->kernel == kTreeTcWide, st));
   // nothing to join: no second launch, unless a replay may meet a plan that has something
@@ -763,8 +812,56 @@ int dec_tree_commit(dec_tree* t, const int32_t* draft, const int32_t* target, co
   a.path = path;
   a.next = next;
   a.kv = t->slabs;
-  a.kv_bytes = t->f16 ? 2 : 4;
-  TREE_CUDA(launch_tree_commit(a, (cudaStream_t)stream));
+  a.kv_type = t->kv_type;
+  a.scales = t->scales;
+  TREE_CUDA(t->q8 ? launch_tree_commit_q8(a, (cudaStream_t)stream) : launch_tree_commit(a, (cudaStream_t)stream));
+  return DEC_OK;
+}
+
+int dec_tree_read_rows(const dec_tree* t, int32_t part, int64_t* rows) {
+  int rc = check_ready(t, 0);
+  if (rc) return rc;
+  if (!rows) return fail(DEC_EINVAL, "NULL argument");
+  if (part != DEC_READ_ALL && part != DEC_READ_PAGES) return fail(DEC_EINVAL, "unknown part %d", part);
+  *rows = t->read_rows[part];
+  return DEC_OK;
+}
+
+int dec_tree_read(dec_tree* t, int32_t layer, int32_t n_layers, int32_t part, int64_t rows, int32_t out_type, void* k,
+                  void* v, int64_t ld, int64_t layer_stride, void* stream) {
+  int64_t have = 0;
+  int rc = check_ready(t, layer);
+  if (rc || (rc = dec_tree_read_rows(t, part, &have))) return rc;
+  const dec_config& c = t->cfg;
+  if (n_layers < 1 || n_layers > c.n_layers - layer) return fail(DEC_EINVAL, "%d layers from layer %d on are not all of the model", n_layers, layer);
+  if (rows != have) return fail(DEC_EINVAL, "%lld rows asked for, the plan has %lld", (long long)rows, (long long)have);
+  if (!k && !v) return fail(DEC_EINVAL, "neither keys nor values");
+  for (const void* p : {k, v}) {
+    if (p && (rc = check_rows(p, ld, c.n_kv_heads, c.head_dim, out_type, p == k ? "k" : "v"))) return rc;
+  }
+  if (k == v) return fail(DEC_EINVAL, "keys and values must not overlap");
+  // layers must not run into each other; one alone has no stride
+  if (n_layers > 1 && (layer_stride % 4 || layer_stride < (rows - 1) * ld + (int64_t)c.n_kv_heads * c.head_dim))
+    return fail(DEC_EINVAL, "layers of %lld rows overlap at a stride of %lld, or it is no multiple of 4", (long long)rows, (long long)layer_stride);
+  DeviceGuard g(t->device);
+  if (!g.ok) return fail(DEC_ECUDA, "the plan's device cannot be made current");
+  TreeReadArgs a{};
+  a.m = t->meta;
+  a.d = pool_dims(t);
+  a.kv = t->slabs;
+  a.scales = t->scales;
+  a.kv_type = t->kv_type;
+  a.out_type = out_type;
+  a.layer = layer;
+  a.n_layers = n_layers;
+  a.part = part;
+  a.rows = rows;
+  a.ld = ld;
+  a.layer_stride = n_layers > 1 ? layer_stride : 0;
+  a.k = k;
+  a.v = v;
+  a.n_blocks = t->read_blocks[part];
+  TREE_CUDA(launch_tree_read(a, (cudaStream_t)stream));
   return DEC_OK;
 }
 

@@ -14,11 +14,13 @@ namespace dec {
 constexpr int kTreeMaxNodes = 256;  // nodes per sequence (a row of the ancestor mask is at most 8 words)
 constexpr uint32_t kErrShape = 16u; // a captured call met a plan of another shape (mirrors DEC_DEV_SHAPE)
 
-// Element types of the callers' tensors (mirror DEC_T_*).
-enum TreeType { kTreeF32 = 0, kTreeF16 = 1, kTreeBf16 = 2 };
+constexpr uint32_t kErrNonFinite = 32u;  // a value that is not finite was quantised (mirrors DEC_DEV_NONFINITE)
+
+// Element types of the callers' tensors and of the cache (mirror DEC_T_*).
+enum TreeType { kTreeF32 = 0, kTreeF16 = 1, kTreeBf16 = 2, kTreeE4m3 = 3, kTreeI8 = 4 };
 
 // Header words of the uploaded plan.
-enum TreeHdr { kHdrSeqs = 0, kHdrTokens, kHdrWords, kHdrRowTile, kHdrMerges, kHdrInts = 16 };
+enum TreeHdr { kHdrSeqs = 0, kHdrTokens, kHdrWords, kHdrRowTile, kHdrMerges, kHdrPages, kHdrRows, kHdrInts = 16 };  // two row counts
 
 // A sequence with nodes, as the attention kernels read it (one 16-byte load).
 struct alignas(16) TreeSeq {
@@ -40,6 +42,16 @@ struct alignas(16) TreeMerge {
   int32_t head, row_tile, c0, c1;
   int32_t stride, node0, nodes, pad;
 };
+// A block that nodes lie in: `nodes` of them from node0 on in its slots from slot0 on (slots in front of slot0: cached tokens).
+struct alignas(16) TreePage {
+  int32_t block, node0, slot0, nodes;
+};
+// What dec_tree_read goes by, for every sequence: its tables, slots, and by part (all slots; from the first node's block on)
+// the blocks and rows of the sequences before it (the entry behind the last has the sums).
+struct alignas(16) TreeReadSeq {
+  int32_t tab, ctx, nodes, pad;
+  int32_t blocks[2], rows[2];
+};
 
 // The plan on the device: one upload, arrays back to back.
 struct TreeMeta {
@@ -52,6 +64,8 @@ struct TreeMeta {
   const uint32_t* anc;       // [N, words] bit j: the node sees node j (itself included)
   const TreeCut* cuts;       // [CTAs]
   const TreeMerge* merges;   // [hdr[kHdrMerges]]
+  const TreePage* pages;     // [hdr[kHdrPages]] (8-bit caches)
+  const TreeReadSeq* reads;  // [S+1]
   const int32_t* tables;     // pool block ids, sequence after sequence
   uint32_t* err;             // device error word
   uint32_t* flags;           // a word per place, 1: its part of a shared unit is there; 0 between calls
@@ -74,11 +88,14 @@ struct TreeAppendArgs {
   const float* rope;  // [positions, rot/2, 2] (cos, sin); null: no rotation
   int rot, interleaved, rope_positions;
   void* q_out;
-  int in_type, q_type, kv_f16, layer;
+  int in_type, q_type, kv_type, layer;
   void* kv;
+  float* scales;  // of an 8-bit cache: [layers][blocks][Hkv][2]
+  int n_pages;    // of the plan that is set (a replay may meet another number)
   int sms;  // of the plan's device
 };
 cudaError_t launch_tree_append(const TreeAppendArgs& a, cudaStream_t s);
+cudaError_t launch_tree_append_q8(const TreeAppendArgs& a, cudaStream_t s);
 
 struct TreeAttendArgs {
   TreeMeta m;
@@ -88,12 +105,13 @@ struct TreeAttendArgs {
   void* out;
   int q_type, out_type, layer;
   const void* kv;
+  const float* scales;  // of an 8-bit cache
   float* part;  // [CTAs, 2, row_tile, D + 2] records
   float scale_log2;  // log2(e) / sqrt(D)
 };
 // The attention kernel for sequences of up to max_rows (nodes x query heads
 // per KV head) rows, and its tiles.
-enum TreeKernel { kTreeFfma = 0, kTreeMma, kTreeTc, kTreeTcWide };
+enum TreeKernel { kTreeFfma = 0, kTreeMma, kTreeTc, kTreeTcWide, kTreeMmaQ8 };
 struct TreeVariant {
   int kernel, row_tile, tile_keys, ctas_per_sm;
   int unit_cost;  // what starting and finishing a unit costs a CTA, in key tiles
@@ -103,6 +121,7 @@ constexpr int kTreeMaxCtasPerSm = 3;
 cudaError_t launch_tree_attend_f32(const TreeAttendArgs& a, int ctas, cudaStream_t s);
 cudaError_t launch_tree_attend_f16(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s);
 cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, bool wide, cudaStream_t s);
+cudaError_t launch_tree_attend_q8(const TreeAttendArgs& a, int kv_type, const CUtensorMap* tm, int ctas, cudaStream_t s);
 cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, int parts, cudaStream_t s);
 
 struct TreeCommitArgs {
@@ -111,9 +130,23 @@ struct TreeCommitArgs {
   const int32_t *draft, *target, *prior;
   int32_t *accepted, *path, *next;
   void* kv;
-  int kv_bytes;
+  int kv_type;
+  float* scales;
 };
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s);
+cudaError_t launch_tree_commit_q8(const TreeCommitArgs& a, cudaStream_t s);
+
+struct TreeReadArgs {
+  TreeMeta m;
+  TreePoolDims d;
+  const void* kv;
+  const float* scales;
+  int kv_type, out_type, layer, n_layers, part;
+  int64_t rows, ld, layer_stride;
+  void *k, *v;
+  int n_blocks;  // of the sequences, of the plan that is set
+};
+cudaError_t launch_tree_read(const TreeReadArgs& a, cudaStream_t s);
 
 cudaError_t launch_tree_join_test(const TreeMeta& m, int late, uint64_t limit_ns, cudaStream_t s);
 

@@ -1,6 +1,8 @@
 // tree_common.cuh - device helpers shared by the draft-tree attention kernels.
 #pragma once
 
+#include <limits.h>
+
 #include "common.cuh"
 #include "tree.h"
 
@@ -126,6 +128,42 @@ __device__ __forceinline__ void tree_store4(void* p, int type, int64_t i, float4
     u = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
   *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + i) = u;
+}
+
+// ---- the walk of a commit ---------------------------------------------------------
+// From the root of sequence s (taken as certain, or as prior chose) down to the child whose token is the one the model
+// chose at its parent, the lowest such node, until there is none.  The nodes are b .. b + T - 1; a block of kThreads threads
+// fills path[] (shared, as child[] and n_path) and returns its length, 0 where the plan does not fit the launch (!ok); `tell`:
+// this block writes the call's outputs.  Waits for the kernels before.
+template <int kThreads>
+__device__ __forceinline__ int tree_walk(const TreeCommitArgs& a, int s, int b, int T, bool ok, bool tell, int* child, int* path, int* n_path) {
+  for (int i = threadIdx.x; i <= T; i += kThreads) child[i] = INT_MAX;
+  pdl_wait_prev();
+  pdl_launch_next();
+  if (!ok) return 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < T; i += kThreads) {
+    const int p = __ldg(a.m.parents + b + i);
+    if (p < -1) continue;  // padding
+    const bool good = p >= 0 ? a.draft[b + i] == a.target[b + p] : !a.prior || a.draft[b + i] == a.prior[s];
+    if (good) atomicMin(&child[p + 1], i);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int n = 0;
+    for (int at = child[0]; at != INT_MAX; at = child[at + 1]) path[n++] = at;
+    *n_path = n;
+  }
+  __syncthreads();
+  const int n = *n_path;
+  if (tell) {
+    for (int i = threadIdx.x; i < T; i += kThreads) a.path[b + i] = i < n ? path[i] : -1;
+    if (threadIdx.x == 0) {
+      a.accepted[s] = n;
+      a.next[s] = n ? a.target[b + path[n - 1]] : a.prior ? a.prior[s] : -1;
+    }
+  }
+  return n;
 }
 
 // Slot of a CTA's record: its first unit when that began in an earlier CTA, or

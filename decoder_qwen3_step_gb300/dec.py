@@ -16,11 +16,12 @@ LIB_PATH = os.path.join(_HERE, "libdec_debug.so" if os.environ.get("DEC_DEBUG") 
 DEC_OK, DEC_EINVAL, DEC_ECAPACITY, DEC_EBLOCK, DEC_ERANGE, DEC_EVOCAB, DEC_ECUDA, DEC_EDEVICE = range(8)
 DEC_FP32, DEC_BF16_F16KV, DEC_INT4_F16KV = 0, 1, 2
 DEC_ROWS_ALL, DEC_ROWS_LAST = 0, 1
-DEC_DEV_BAD_ID, DEC_DEV_TIMEOUT, DEC_DEV_CAPACITY, DEC_DEV_BOUNDS, DEC_DEV_SHAPE = 1, 2, 4, 8, 16
+DEC_DEV_BAD_ID, DEC_DEV_TIMEOUT, DEC_DEV_CAPACITY, DEC_DEV_BOUNDS, DEC_DEV_SHAPE, DEC_DEV_NONFINITE = 1, 2, 4, 8, 16, 32
 DEC_BUILD_DEBUG = 1
 DEC_PURPOSE_SAMPLE = 4
 DEC_SAMPLE_BAD_ID, DEC_SAMPLE_BAD_LOGIT, DEC_SAMPLE_NO_FINITE, DEC_SAMPLE_OVERFLOW = 1, 2, 4, 8
-DEC_T_F32, DEC_T_F16, DEC_T_BF16 = 0, 1, 2
+DEC_T_F32, DEC_T_F16, DEC_T_BF16, DEC_T_E4M3, DEC_T_I8 = 0, 1, 2, 3, 4
+DEC_READ_ALL, DEC_READ_PAGES = 0, 1
 DEC_TREE_PAD, DEC_TREE_MAX_NODES = -2, 256
 DEC_ROPE_HALF, DEC_ROPE_INTERLEAVED = 0, 1
 DEC_ROPE_PLAIN, DEC_ROPE_LINEAR, DEC_ROPE_YARN, DEC_ROPE_BANDS = 0, 1, 2, 3
@@ -42,7 +43,8 @@ EXPORTS = (
     "dec_quantize_int4", "dec_batch_check", "dec_attend_noalloc_status", "dec_debug_wait_timeout",
     "dec_build_flags", "dec_debug_poison_table", "dec_rope_table_bytes", "dec_rope_table", "dec_tree_check",
     "dec_tree_workspace_bytes", "dec_tree_create", "dec_tree_destroy", "dec_tree_set", "dec_tree_status",
-    "dec_tree_append", "dec_tree_attend", "dec_tree_commit", "dec_debug_tree_join",
+    "dec_tree_append", "dec_tree_attend", "dec_tree_commit", "dec_debug_tree_join", "dec_pool_q8_bytes", "dec_pool_q8_create",
+    "dec_kv_scale_offset", "dec_tree_read_rows", "dec_tree_read",
 )
 KERNEL_CLASSES = ("embed", "qkv", "qkv_post", "attn", "attn_merge", "oproj", "gateup", "down", "lmhead", "argmax",
                   "step")
@@ -178,6 +180,11 @@ def lib() -> C.CDLL:
             "dec_tree_append": (I, [V, C.c_int32, C.POINTER(dec_tree_qkv), V]),
             "dec_tree_attend": (I, [V, C.c_int32, V, C.c_int32, I64, V, C.c_int32, I64, V]),
             "dec_tree_commit": (I, [V, V, V, V, V, V, V, V]),
+            "dec_pool_q8_bytes": (I, [cfgp, C.c_int32, C.c_int32, C.POINTER(SZ)]),
+            "dec_pool_q8_create": (I, [cfgp, C.c_int32, C.c_int32, V, SZ, C.POINTER(V)]),
+            "dec_kv_scale_offset": (I, [V, _I32P, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.POINTER(I64)]),
+            "dec_tree_read_rows": (I, [V, C.c_int32, C.POINTER(I64)]),
+            "dec_tree_read": (I, [V, C.c_int32, C.c_int32, C.c_int32, I64, C.c_int32, V, V, I64, I64, V]),
             "dec_debug_tree_join": (I, [V, I, C.c_uint64, C.POINTER(C.c_int32), V]),
         }
         for name, (res, args) in sig.items():

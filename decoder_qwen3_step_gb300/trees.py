@@ -30,22 +30,26 @@ _TYPES = {torch.float32: dec.DEC_T_F32, torch.float16: dec.DEC_T_F16, torch.bflo
 
 class KvPool:
     """A paged KV pool without a model: the slab buffer (allocated here, or
-    the caller's) and libdec's block bookkeeping."""
+    the caller's) and libdec's block bookkeeping.  kv_type: DEC_T_I8 or
+    DEC_T_E4M3 for a cache held in 8 bits (a scale per page behind the codes,
+    see dec_pool_q8_create), None for the mode's own type."""
 
     def __init__(self, shape: dict, mode: int, n_blocks: int, max_positions: int = 4096, device: str = "cuda:0",
-                 slabs: torch.Tensor | None = None):
+                 slabs: torch.Tensor | None = None, kv_type: int | None = None):
         self.L = dec.lib()
         self.shape, self.mode, self.n_blocks = dict(shape), mode, n_blocks
         self.cfg = make_config(shape, mode, max_positions)
         size = C.c_size_t()
-        dec.check(self.L.dec_pool_bytes(C.byref(self.cfg), n_blocks, C.byref(size)), "dec_pool_bytes")
+        self.kv_type, what = kv_type, () if kv_type is None else (kv_type,)
+        sized, made = ("dec_pool_bytes", "dec_pool_create") if kv_type is None else ("dec_pool_q8_bytes", "dec_pool_q8_create")
+        dec.check(getattr(self.L, sized)(C.byref(self.cfg), *what, n_blocks, C.byref(size)), sized)
         if slabs is None:
             slabs = torch.zeros(size.value, dtype=torch.uint8, device=device)
         assert slabs.is_cuda and slabs.is_contiguous()
         self.slabs, self.device = slabs, slabs.device
         h = C.c_void_p()
-        dec.check(self.L.dec_pool_create(C.byref(self.cfg), n_blocks, C.c_void_p(slabs.data_ptr()),
-                                         slabs.numel() * slabs.element_size(), C.byref(h)), "dec_pool_create")
+        dec.check(getattr(self.L, made)(C.byref(self.cfg), *what, n_blocks, C.c_void_p(slabs.data_ptr()),
+                                        slabs.numel() * slabs.element_size(), C.byref(h)), made)
         self.pool = h
 
     def alloc(self, n: int) -> list:
@@ -138,6 +142,7 @@ class DraftTrees:
                                              C.byref(h)), "dec_tree_create")
         self.handle = h
         self.n_tokens = self.n_seqs = 0
+        self._rows_of = (0, 0)
         self._streams = set()  # that calls were made on
         self._heads, self._kv_heads, self._dim = self.cfg.n_heads, self.cfg.n_kv_heads, self.cfg.head_dim
         # a step makes these calls for every layer: the lookups are done once
@@ -178,6 +183,12 @@ class DraftTrees:
         b, keep = tree_batch(ctx, parents, tables)
         dec.check(self.L.dec_tree_set(self.handle, C.byref(b), self._stream(stream)), "dec_tree_set")
         self.n_seqs, self.n_tokens = b.n_seqs, b.n_tokens
+        self._rows_of = tuple(self._read_rows(part) for part in (dec.DEC_READ_ALL, dec.DEC_READ_PAGES))
+
+    def _read_rows(self, part):
+        n = C.c_int64()
+        dec.check(self.L.dec_tree_read_rows(self.handle, part, C.byref(n)), "dec_tree_read_rows")
+        return n.value
 
     def append(self, layer: int, q, k, v, rope: RopeTable | None = None, q_norm=None, k_norm=None, q_type=torch.float32,
                out=None, stream=None):
@@ -268,6 +279,32 @@ class DraftTrees:
         code = self._commit(self.handle, *ids, a, p, x, self._stream(stream))
         if code:
             dec.check(code, "dec_tree_commit")
+        return out
+
+    def read(self, layer: int, part: int = dec.DEC_READ_ALL, out_type=torch.bfloat16, layers: int | None = None, out=None,
+             stream=None):
+        """Keys and values back from the cache: two tensors [rows, kv_heads, head_dim],
+        or with `layers` [layers, rows, kv_heads, head_dim] of that many layers from
+        `layer` on.  Rows: the sequences' slots one after the other, all of them or
+        (DEC_READ_PAGES) from the block on that holds the sequence's first node.
+        out: two such tensors, contiguous, or None in the place of one that is not wanted."""
+        rows = self._rows_of[part] if part in (0, 1) else 0  # an unknown part is the library's to refuse
+        shape = (rows, self._kv_heads, self._dim) if layers is None else (layers, rows, self._kv_heads, self._dim)
+        if out is None:
+            if layers is not None and layers < 1:
+                raise ValueError("layers: at least one")
+            out = self._new(shape, out_type, stream), self._new(shape, out_type, stream)
+        given = [x for x in out if x is not None]
+        for x in given:
+            if x.shape != shape or x.dtype is not given[0].dtype or x.dtype not in _TYPES or not x.is_contiguous() or x.get_device() != self._index:
+                raise ValueError(f"out: need contiguous {shape} tensors of one type, f32, f16 or bf16, on cuda:{self._index}")
+        if stream is not None:
+            _used_on(stream, *out)
+        width = self._kv_heads * self._dim
+        code = self.L.dec_tree_read(self.handle, layer, 1 if layers is None else layers, part, rows, _TYPES[given[0].dtype] if given else 0,
+                                    *(None if x is None else x.data_ptr() for x in out), width, rows * width, self._stream(stream))
+        if code:
+            dec.check(code, "dec_tree_read")
         return out
 
     def status(self, stream=None) -> int:

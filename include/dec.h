@@ -142,6 +142,7 @@ const char* dec_last_error(void);
                                every build: a replayed call met a position past its rotary table) */
 #define DEC_DEV_SHAPE   16u /* a captured dec_tree_* call was replayed on a plan of another shape: it
                                did nothing */
+#define DEC_DEV_NONFINITE 32u /* dec_tree_append met an infinity or a NaN on its way into an 8-bit cache */
 
 /* ---- model ---------------------------------------------------------------- */
 /* Check a config; DEC_OK if the decoder can run it. */
@@ -200,6 +201,38 @@ int dec_pool_retain(dec_pool* p, int32_t id);  /* refcount + 1; DEC_EBLOCK if no
 int dec_pool_release(dec_pool* p, int32_t id);
 int dec_pool_free_blocks(const dec_pool* p, int32_t* n);   /* free, not counting cached blocks */
 int dec_pool_refcount(const dec_pool* p, int32_t id, int32_t* refs);
+
+/* ---- pools held in 8 bits ---------------------------------------------------
+ * A pool whose K/V are 8-bit codes with a scale for each page, a page being the
+ * K or the V of the 16 slots of one KV head of one block: a value is
+ * code * 2^e.  It serves draft trees (dec_tree_*: a decode step is a tree of one
+ * node, a chunk of a prompt a chain) at half the bytes of an f16 cache; block
+ * bookkeeping and the prefix cache are those of any pool.  dec_prefill,
+ * dec_decode and dec_attend refuse it (DEC_EINVAL).
+ *
+ * Codes (kv_type): DEC_T_I8, whole numbers -127 .. 127 (Q = 127), or DEC_T_E4M3
+ * (4 exponent and 3 mantissa bits, no infinities, Q = 448).  The scale is a
+ * power of two, e in -40 .. 40: the smallest with |x| <= Q 2^e for what the page
+ * was given.  So every value is exact in bf16 and fp32, a scale depends on what
+ * was written and not on how it was divided into calls, and when it rises the
+ * codes that are rounded again lose less than one step of the new scale in all.
+ * (amax / Q itself as the scale would give i8 half a bit more on average, but
+ * each of up to 15 rises within a page would cost half a step.)
+ *
+ * Layout: codes as in a pool of any type, one byte an element; then, from the
+ * next multiple of 256 bytes on, fp32 scales [layers][blocks][KV heads][2] (K,
+ * V).  cfg->mode: DEC_BF16_F16KV or DEC_INT4_F16KV (the attention is that of the
+ * serving modes). */
+#define DEC_T_E4M3 3
+#define DEC_T_I8   4
+int dec_pool_q8_bytes(const dec_config* cfg, int32_t kv_type, int32_t n_blocks, size_t* bytes);
+int dec_pool_q8_create(const dec_config* cfg, int32_t kv_type, int32_t n_blocks, void* slabs, size_t bytes,
+                       dec_pool** out);
+/* Byte offset within the slab buffer of the scale of the page that holds
+ * position pos (arguments and errors as dec_kv_offset; DEC_EINVAL for a pool
+ * without scales). */
+int dec_kv_scale_offset(const dec_pool* p, const int32_t* table, int32_t n_table, int32_t pos, int32_t layer,
+                        int32_t kv_head, int32_t is_v, int64_t* offset);
 
 /* ---- prefix cache in the pool (KvPool's hash index and LRU, tinyllm L10.1
  * sections 1 and 4; its boundary tests kv_pool_bounds_and_cache_lifecycle) ---
@@ -519,13 +552,13 @@ int dec_debug_df_exp(const double* x, double* y, int64_t n, void* stream);
  * ordered before the replay) if its shape is the capture's: the same n_seqs,
  * n_tokens and ceil(longest / 32), longest the most nodes of a sequence, and
  * for dec_tree_attend longest * (n_heads / n_kv_heads) on the same side of 16
- * and, with an f16 cache and head_dim 64 or 128, of 128.  How the nodes are
+ * and, with an f16 or 8-bit cache and head_dim 64 or 128, of 128.  How the nodes are
  * divided among the sequences may differ (DEC_TREE_PAD nodes fill a batch up).
  * A replay on a plan of another shape does nothing and sets
  * DEC_DEV_SHAPE.  Calls run on the device that was current at
  * dec_tree_create, whichever device is current then. */
 
-/* Element types. */
+/* Element types of the caller's tensors. */
 #define DEC_T_F32  0
 #define DEC_T_F16  1
 #define DEC_T_BF16 2
@@ -571,7 +604,7 @@ void dec_tree_destroy(dec_tree* t);
  * previous plan in place.  The blocks must stay allocated while it is used. */
 int dec_tree_set(dec_tree* t, const dec_tree_batch* b, void* stream);
 /* Synchronise `stream`, then read and clear the plan's device error word
- * (DEC_DEV_TIMEOUT, DEC_DEV_BOUNDS, DEC_DEV_SHAPE). */
+ * (DEC_DEV_TIMEOUT, DEC_DEV_BOUNDS, DEC_DEV_SHAPE, DEC_DEV_NONFINITE). */
 int dec_tree_status(dec_tree* t, void* stream, uint32_t* flags);
 
 /* Rotary positions.  Pair j of the first rot_dim channels of a head turns by
@@ -632,13 +665,20 @@ typedef struct dec_tree_qkv {
     int64_t ldqo;
 } dec_tree_qkv;
 /* Norm, rotate, and write the keys and values of all nodes to their slots of
- * `layer` (f16 caches: round to nearest even).  Computed in fp32. */
+ * `layer` (f16 caches: round to nearest even).  Computed in fp32.
+ * A cache held in 8 bits: a page's e becomes the smallest that the rows written
+ * to it by this call need (padding nodes do not count) and, where it holds
+ * cached tokens, at least what it was; if it rises, the cached tokens' codes are
+ * rounded again.  Codes round to nearest even.  Infinities become the page's
+ * largest code and NaN 0, neither counts for e, and DEC_DEV_NONFINITE is
+ * raised.  Magnitudes above Q 2^40 are cut to that. */
 int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* stream);
 /* Attention of all nodes.  q DEVICE [N, n_heads, head_dim] after norm and
  * rotation, any DEC_T_*; out DEVICE [N, n_heads * head_dim]: any DEC_T_* for
  * an fp32 cache, which is computed in fp32 throughout; DEC_T_F16 or
  * DEC_T_BF16 for an f16 cache, where queries and weights are rounded to f16
- * for the tensor cores and statistics and sums are fp32.  out must not overlap
+ * for the tensor cores and statistics and sums are fp32; so is a cache held in 8
+ * bits, whose codes are exact in f16.  out must not overlap
  * q.  A node's result does not depend on what is cached in slots it does not
  * see (infinities and NaN included); a query, or a key that it sees, that is NaN
  * gives NaN; scores that are all -inf give zeros, as for a node that sees
@@ -661,6 +701,22 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
  * layer; the slots behind hold nothing of use. */
 int dec_tree_commit(dec_tree* t, const int32_t* draft, const int32_t* target, const int32_t* prior, int32_t* accepted,
                     int32_t* path, int32_t* next, void* stream);
+/* Read keys and values back from `n_layers` layers from `layer` on: rows in the
+ * order of the sequences and of their slots, of whole sequences (cached tokens,
+ * then nodes) or of the slots from the first one of the block on that holds the
+ * sequence's first node (what dec_tree_append and dec_tree_commit change).
+ * Sequences without nodes have no rows.  k, v: DEVICE
+ * [n_layers, rows, n_kv_heads, head_dim] of any DEC_T_F32, F16, BF16 (rounded to
+ * nearest even from the cache's values; codes * 2^e above f16's range become
+ * infinite), rows ld elements and layers layer_stride elements apart, either
+ * may be NULL; k and v must not overlap.  Any pool.  rows: as
+ * dec_tree_read_rows gives it (DEC_EINVAL otherwise); a captured call replayed
+ * on a plan that has another number does nothing and sets DEC_DEV_SHAPE. */
+#define DEC_READ_ALL   0
+#define DEC_READ_PAGES 1
+int dec_tree_read_rows(const dec_tree* t, int32_t part, int64_t* rows);
+int dec_tree_read(dec_tree* t, int32_t layer, int32_t n_layers, int32_t part, int64_t rows, int32_t out_type, void* k,
+                  void* v, int64_t ld, int64_t layer_stride, void* stream);
 /* Test hook for the bounded waits of dec_tree_attend's joins: one wait of at
  * most limit_ns (1 us .. 1 s) for a part that comes before it, or, with late
  * != 0, after it has run out (DEC_DEV_TIMEOUT in the plan's error word).
