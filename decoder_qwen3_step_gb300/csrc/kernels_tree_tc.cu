@@ -1,5 +1,5 @@
-// kernels_tree_tc.cu - tree attention over an f16 cache for wide trees, on the
-// 5th-generation tensor cores (tcgen05, accumulators in TMEM).
+// kernels_tree_tc.cu - tree attention over an f16 or 8-bit cache for wide trees,
+// on the 5th-generation tensor cores (tcgen05, accumulators in TMEM).
 //
 // The same formula as kernels_tree_f16.cu with 128 keys and 128 or 256 rows
 // (nodes x query heads of one KV head) per step, one CTA per SM:
@@ -26,31 +26,46 @@
 // every key four times and ran at HBM speed, 211 us against 64 for the products.
 // O is rescaled in TMEM only when a row's scores exceed its maximum by 2^8
 // (exact: numerator and denominator share the maximum).  Warps whose rows are
-// all behind the last skip the softmax.  Roundings as in kernels_tree_f16.cu.
+// are all behind the last skip the softmax.  Roundings as in kernels_tree_f16.cu.
+//
+// 8-bit caches: the producer brings codes (a page is contiguous: one bulk copy)
+// into a ring of their own, and
+//   warps 12..15  turn them into f16 (exact) operand tiles of the layout above.
+// The MMAs work on codes; with the scales 2^a of K and 2^b of V of a block of 16
+// keys, the softmax takes s c 2^a + b as the logarithm of a weight for the value
+// codes (its running maximum is the reference, see kernels_tree_q8.cu) and sums
+// the weights times 2^-b.  A tile's 16 scales come through 64 bytes of shared
+// memory per softmax warp, a row's factors are one product per block.  Registers
+// are moved from the other warps to the softmax (512 threads have 128 each, it
+// needs up to 168).
 #include "attn_fold.cuh"
+#include "q8.cuh"
 #include "tc_common.cuh"
-#include "tree_common.cuh"
 
 namespace dec {
 
 namespace {
 
 constexpr int kTR = 128, kTK = 128;  // rows and keys of a step
-constexpr int kTcTreeThreads = 384;
+constexpr int kTcTreeThreads = 384, kTcTreeThreadsQ8 = 512;
 constexpr uint32_t kTmemCols = 512;  // S of the two groups: columns 0, 128; O: 256, 256 + D
 
-template <int D>
+template <int D, bool kQ8>
 struct TcSmem {
   static constexpr int kPanels = D / 64;
   static constexpr int kPanel = kTR * 128;            // bytes of 64 channels of 128 queries
   static constexpr int kGroup = kPanels * 1024;       // bytes of eight keys
   static constexpr int kTile = kPanels * kPanel;
-  static constexpr int kSlots = D == 128 ? 5 : 10;    // of the ring; at least K, V, K are in use at once
+  // operand tiles (at least K, V, K are in use at once) and, for 8 bits, slots for codes; else the copies land in the operands
+  static constexpr int kOps = kQ8 ? (D == 128 ? 3 : 6) : D == 128 ? 5 : 10;
+  static constexpr int kSlots = kQ8 ? (D == 128 ? 4 : 8) : kOps;
   static constexpr int kQ = 0;                        // two tiles: the units' in turn (narrow), the groups' (wide)
-  static constexpr int kRing = 2 * kTile, kFac = kRing + kSlots * kTile;  // fac: float [2][kTR], as the queries
-  static constexpr int kBar = kFac + 2 * kTR * 4;
-  // barriers: full, empty [slots]; Q full, Q empty, S full, P full, O full, O empty [2]; MMA done
-  static constexpr int kBars = 2 * kSlots + 15;
+  static constexpr int kRing = 2 * kTile, kCodes = kRing + kOps * kTile, kCodeTile = kTK * D;
+  static constexpr int kFac = kCodes + (kQ8 ? kSlots * kCodeTile : 0);  // float [2][kTR], as the queries
+  static constexpr int kScales = kFac + 2 * kTR * 4;                    // float2 [8 warps][2][8] (2^a, b) of a tile's blocks
+  static constexpr int kBar = kScales + (kQ8 ? 1024 : 0);
+  // barriers: full, empty [slots]; ready, used [operands] of 8 bits; Q full, Q empty, S full, P full, O full, O empty [2]; MMA done
+  static constexpr int kBars = 2 * kSlots + (kQ8 ? 2 * kOps : 0) + 15;
   static constexpr int kBytes = kBar + kBars * 8 + 32;
 };
 
@@ -149,14 +164,64 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
   return r;
 }
 
-template <int D, bool kWide>
-__global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __grid_constant__ CUtensorMap tm,
-                                                                      const __grid_constant__ TreeAttendArgs a) {
-  using SM = TcSmem<D>;
-  constexpr int kS = SM::kSlots, kR = kWide ? 2 * kTR : kTR;
+// A tile of 128 keys' codes (rows of D bytes) as an operand, by 128 threads.  Eight lanes of an access take four 16-byte
+// chunks of a row and the other four (D = 64: the same) of its neighbour, so that both sides touch every bank once.
+// odd: some rows may hold anything, codes that are no numbers become 0.
+template <int D, int kKind>
+__device__ __forceinline__ void tc_convert_load(const uint8_t* codes, int t, uint4 (&raw)[D / 16]) {
+  constexpr int kChunks = D / 16, kRowsPer = 128 / kChunks;  // rows of a round of all threads
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    int r, c;
+    if constexpr (D == 128) {
+      r = i * kRowsPer + (t >> 4) * 2 + ((t >> 2) & 1);
+      c = (t & 3) + 4 * (((t >> 2) ^ (t >> 3)) & 1);
+    } else {
+      r = i * kRowsPer + (t >> 2);
+      c = t & 3;
+    }
+    raw[i] = *reinterpret_cast<const uint4*>(codes + r * D + c * 16);
+  }
+}
+template <int D, int kKind>
+__device__ __forceinline__ void tc_convert_store(uint8_t* tile, int t, const uint4 (&raw)[D / 16], bool odd) {
+  constexpr int kChunks = D / 16, kRowsPer = 128 / kChunks, kGroup = D / 64 * 1024;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    int r, c;
+    if constexpr (D == 128) {
+      r = i * kRowsPer + (t >> 4) * 2 + ((t >> 2) & 1);
+      c = (t & 3) + 4 * (((t >> 2) ^ (t >> 3)) & 1);
+    } else {
+      r = i * kRowsPer + (t >> 2);
+      c = t & 3;
+    }
+    uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w}, h[8];
+    if (kKind == kTreeE4m3 && odd) {
+#pragma unroll
+      for (int z = 0; z < 4; ++z) w[z] = e4m3_numbers(w[z]);
+    }
+#pragma unroll
+    for (int z = 0; z < 4; ++z) q8_halves<kKind, false>(w[z], h[2 * z], h[2 * z + 1]);
+    uint8_t* at = tile + (r >> 3) * kGroup + (c >> 2) * 1024 + (r & 7) * 128;
+    const int x = (c & 3) * 2;
+    *reinterpret_cast<uint4*>(at + ((x ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(at + (((x + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+}
+
+template <int D, bool kWide, int kKind>
+__global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeThreadsQ8, 1)
+    k_tree_attend_tc(const __grid_constant__ CUtensorMap tm, const __grid_constant__ TreeAttendArgs a) {
+  constexpr bool kQ8 = kKind != kTreeF16;
+  using SM = TcSmem<D, kQ8>;
+  constexpr int kS = SM::kSlots, kOps = SM::kOps, kR = kWide ? 2 * kTR : kTR;
+  constexpr int kSoftmaxRegs = kWide ? 152 : 168;  // 256 threads with these, 256 with the rest of 256: 65,536, as launched
   extern __shared__ __align__(1024) uint8_t dsm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(dsm + SM::kBar);
-  uint64_t *full = bars, *empty = bars + kS, *qfull = bars + 2 * kS, *qempty = qfull + 2, *sfull = qfull + 4,
+  // ready, used: of the operands that the MMAs take (an f16 cache's copies are these)
+  uint64_t *full = bars, *empty = bars + kS, *ready = kQ8 ? bars + 2 * kS : full, *used = kQ8 ? ready + kOps : empty,
+           *qfull = kQ8 ? used + kOps : bars + 2 * kS, *qempty = qfull + 2, *sfull = qfull + 4,
            *pfull = qfull + 6, *ofull = qfull + 8, *oempty = qfull + 10, *mma_done = qfull + 12, *phalf = qfull + 13;
   // [0] abort, [1] TMEM base, [2] slots filled, [4 + i] 1 + the unit (of parity i) that met a value that is not finite
   int* flags = reinterpret_cast<int*>(bars + SM::kBars);
@@ -164,7 +229,11 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   if (threadIdx.x == 0) {
     for (int i = 0; i < kS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], kQ8 ? 4 : 1);
+    }
+    for (int i = 0; kQ8 && i < kOps; ++i) {
+      mbar_init(&ready[i], 4);
+      mbar_init(&used[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], kWide ? 128 : 320);
@@ -197,7 +266,17 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
 #endif
     return blk;
   };
-  int nxt = warp == 8 && ok_shape && cut.count > 0 ? entry(tile, min(u.tiles, tile + cut.count)) : 0;
+  // softmax of 8 bits: a lane's block of the group's four tiles from t on (narrow: every other tile)
+  auto entry4 = [&](int t, int t1) {
+    const int x = t + (lane >> 3) * (kWide ? 1 : 2);
+    return entry(x, t1);
+  };
+  int nxt = 0;
+  if (ok_shape && cut.count > 0) {
+    const int t1 = min(u.tiles, tile + cut.count);
+    if (warp == 8) nxt = entry(tile, t1);
+    else if (kQ8 && warp < 8) nxt = entry4(tile + (kWide ? 0 : warp >> 2), t1);  // tile k of the CTA is group k & 1's
+  }
   __syncthreads();
   pdl_wait_prev();
   pdl_launch_next();
@@ -212,6 +291,8 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags + 1);
   volatile int* abort_flag = flags;
+  // (the softmax warps raise theirs in their own branch: where branches meet the compiler counts on the fewest)
+  if (kQ8 && warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(256 - kSoftmaxRegs));
   const int gs = a.d.gs, G = 1 << gs;
   // a wide unit with at most 128 rows leaves the second group out
   auto both = [&](const TreeUnit& x) { return (x.nodes << gs) - x.row_tile * kR > kTR; };
@@ -225,7 +306,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       for (int t = t0; t < t1; ++t) {
         const int here = min(8, blocks - t * 8), blk = nxt;
         nxt = entry(t + 1, t1);
-        const uint32_t bytes = here * SM::kPanels * 2048;
+        const uint32_t bytes = here * (kQ8 ? 16 * D : SM::kPanels * 2048);
         const int z = (a.layer * a.d.n_blocks + blk) * 2;
 #pragma unroll
         for (int is_v = 0; is_v < 2; ++is_v, ++li) {
@@ -238,7 +319,11 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
             flags[2] = li + 1;
           }
           __syncwarp();
-          if (lane < here)
+          if constexpr (kQ8) {
+            if (lane < here)
+              bulk_g2s(dsm + SM::kCodes + slot * SM::kCodeTile + lane * 16 * D,
+                       reinterpret_cast<const uint8_t*>(a.kv) + kv_offset(a.layer, blk, is_v, u.head, 0, a.d.n_blocks, a.d.Hkv, 16, D), 16 * D, &full[slot]);
+          } else if (lane < here)
             tma_box_5d(dsm + SM::kRing + slot * SM::kTile + lane * 2 * SM::kGroup, &tm, u.head * 2, z + is_v, &full[slot]);
           __syncwarp();
         }
@@ -264,10 +349,10 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
     const uint32_t q_hi = (uint32_t)(q_desc >> 32), q_lo = (uint32_t)q_desc;
     const uint32_t hi = (uint32_t)(k_desc >> 32), k_lo = (uint32_t)k_desc, v_lo = (uint32_t)v_desc;  // V's high half is K's
     // the copies of load li (K of tile k: 2 k, V: 2 k + 1) have landed
-    auto landed = [&](int li) { return wait(&full[li % kS], li / kS); };
+    auto landed = [&](int li) { return wait(&ready[li % kOps], li / kOps); };
     // scores of tile k (landed) into group b's S, from query tile q
     auto scores = [&](int k, int b, int q, bool last) {
-      const int slot = 2 * k % kS;
+      const int slot = 2 * k % kOps;
       const uint32_t qd = q_lo + q * (SM::kTile >> 4), kd = k_lo + slot * (SM::kTile >> 4);
       if (leader) {
 #pragma unroll
@@ -276,12 +361,12 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           mma_ss(td + b * 128, qd + (((i >> 2) * SM::kPanel + in) >> 4), kd + (((i >> 2) * 1024 + in) >> 4), q_hi, hi, id_s, i != 0);
         }
         tc_commit(&sfull[b]);
-        if (last) tc_commit(&empty[slot]);
+        if (last) tc_commit(&used[slot]);
       }
     };
     // weights (tile n of group b) times values of tile k (landed)
     auto values = [&](int k, int b, int n, bool fresh, bool last) -> bool {
-      const int slot = (2 * k + 1) % kS;
+      const int slot = (2 * k + 1) % kOps;
       const uint32_t vd = v_lo + slot * (SM::kTile >> 4);
       constexpr int kHalf = kWide ? 0 : kTK / 32;
       // narrow: the first half of the keys while the second's weights are worked on (32 x 64: 50.9 us, so 50.5; 8 x 256 took
@@ -302,7 +387,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
 #pragma unroll
         for (int i = kHalf; i < kTK / 16; ++i)
           mma_ts(td + 256 + b * D, td + b * 128 + i * 8, vd + i * (2 * SM::kGroup >> 4), hi, id_o, i != 0 || !fresh);
-        if (last) tc_commit(&empty[slot]);
+        if (last) tc_commit(&used[slot]);
       }
       return true;
     };
@@ -383,6 +468,37 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
     }
     if (leader) tc_commit(mma_done);
     __syncwarp();
+  } else if (kQ8 && warp >= 12) {
+    // ---- codes to operands ----
+    const int ct = threadIdx.x - 384;
+    int li = 0;
+    for (int left = cut.count; left > 0;) {
+      const int t0 = tile, t1 = min(u.tiles, tile + left);
+      for (int t = t0; t < t1; ++t) {
+        const bool odd = t * kTK + kTK > u.ctx;  // rows of no token among them, perhaps
+#pragma unroll 1
+        for (int is_v = 0; is_v < 2; ++is_v, ++li) {
+          const int slot = li % kS, op = li % kOps;
+          uint4 raw[D / 16];
+          bool ok = mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err);
+          if (!__all_sync(0xffffffffu, ok)) goto converted;
+          tc_convert_load<D, kKind>(dsm + SM::kCodes + slot * SM::kCodeTile, ct, raw);
+          ok = li < kOps || mbar_wait(&used[op], ((li / kOps) - 1) & 1, abort_flag, a.m.err);
+          if (!__all_sync(0xffffffffu, ok)) goto converted;
+          tc_convert_store<D, kKind>(dsm + SM::kRing + op * SM::kTile, ct, raw, odd);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ready[op]);
+            mbar_arrive(&empty[slot]);
+          }
+        }
+      }
+      left -= t1 - t0;
+      tile = 0;
+      if (left > 0) tree_unit_next(a.m, gs, kR, a.d.Hkv, u);
+    }
+  converted:;
   } else if (warp >= 10) {
     // ---- Queries one unit ahead (the first unit's by the softmax warps, which have nothing else to do yet).
     // One of these warps also publishes the part of a shared unit that this CTA begins with: the fence takes up to 3 us
@@ -409,6 +525,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
     }
     if (publish) published();
   } else {
+    if constexpr (kQ8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax ----
     const int b = warp >> 2, wr = (warp & 3) * 32, r = wr + lane, st = threadIdx.x & 127;
     const int row_in = (kWide ? b * kTR : 0) + r;  // row of the unit
@@ -457,8 +574,35 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
         }
       }
       bool first = true;
+      // 8 bits: the scales of four of the group's tiles, a lane's block each; the next ones' on their way while these are used
+      const int ta = t0 + (kWide ? 0 : (k ^ b) & 1);  // the group's first tile of the unit
+      float2 sc = make_float2(0.f, 0.f), sc_next = sc;
+      int turn = 0;
+      auto scales_of = [&](int t, int blk) {
+        float2 y = make_float2(1.f, 1.f);
+        const int x = t + (lane >> 3) * (kWide ? 1 : 2);
+        if (x < t1 && x * 8 + (lane & 7) < (end + 15) >> 4) y = *reinterpret_cast<const float2*>(a.scales + q8_scale_at(a.d, a.layer, blk, u.head, 0));
+        return make_float2(q8_two(q8_exp(y.x)), (float)q8_exp(y.y));
+      };
+      if constexpr (kQ8) {
+        if (left < cut.count) nxt = entry4(ta, t1);
+        sc = scales_of(ta, nxt);
+        nxt = entry4(ta + (kWide ? 4 : 8), t1);
+      }
       for (int t = t0; t < t1; ++t, ++k) {
         if (!in || (!kWide && (k & 1) != b)) continue;
+        const float4* blocks = reinterpret_cast<const float4*>(dsm + SM::kScales + warp * 128 + (turn & 1) * 64);  // two blocks each
+        if constexpr (kQ8) {
+          if (turn == 4) {
+            turn = 0;
+            sc = sc_next;
+            nxt = entry4(t + (kWide ? 4 : 8), t1);
+          }
+          if (lane >> 3 == turn) *reinterpret_cast<float2*>(dsm + SM::kScales + warp * 128 + (turn & 1) * 64 + (lane & 7) * 8) = sc;
+          if (turn == 2) sc_next = scales_of(t + (kWide ? 2 : 4), nxt);
+          ++turn;
+          __syncwarp();
+        }
         const int key0 = t * kTK;
         const bool drafted = key0 + kTK > u.ctx;
         uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};  // keys of each 32 that this row sees
@@ -474,6 +618,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           // value rows past the end hold anything, a node's value that is not finite must not meet another branch's
           // zero weights: zero them; its descendants get it back at the unit's end.  Eight threads per row.  (Wide: both
           // groups do this for the tile, whichever comes first changes it)
+          if constexpr (!kQ8) {
           const int li = 2 * k + 1, slot = li % kS;
           alive = __all_sync(0xffffffffu, alive && mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err));
           for (int q = max(u.ctx - key0, 0) + (st >> 3); alive && q < kTK; q += 16) {
@@ -494,6 +639,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
         }
         alive = __all_sync(0xffffffffu, alive && mbar_wait(&sfull[b], n & 1, abort_flag, a.m.err));
         ++n;
@@ -518,7 +664,22 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           // loops: unrolled, the tile's code ran out of the instruction cache at every turn)
           uint32_t sa[32], sb[32];
           float mx = -INFINITY;
-          auto largest = [&](const uint32_t (&x)[32]) {
+          // 8 bits: a block's score factor for this row, kept off 0 and infinity (hidden scores are -inf) and its exponent
+          auto factors = [&](int j) {
+            float4 z = blocks[j];
+            z.x = fminf(fmaxf(z.x * c, 1.17549435e-38f), 3.40282347e38f);
+            z.z = fminf(fmaxf(z.z * c, 1.17549435e-38f), 3.40282347e38f);
+            return z;
+          };
+          auto largest = [&](const uint32_t (&x)[32], int j) {
+            if constexpr (kQ8) {
+              float y[2] = {-INFINITY, -INFINITY};  // of each block
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) y[i / 16] = fmaxf(fmaxf(y[i / 16], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+              const float4 z = factors(j);
+              mx = fmaxf(mx, fmaxf(__fadd_rn(__fmul_rn(y[0], z.x), z.y), __fadd_rn(__fmul_rn(y[1], z.z), z.w)));
+              return;
+            }
             float y[2] = {mx, mx};
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
@@ -532,12 +693,12 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           for (int j = 0; j < 4; j += 2) {
             tc_wait32(sa);
             tc_ld32_async(ts + j * 32 + 32, sb);
-            largest(sa);
+            largest(sa, j);
             tc_wait32(sb);
             tc_ld32_async(ts + ((j * 32 + 64) & 127), sa);  // at the end the first columns again, for the weights
-            largest(sb);
+            largest(sb, j + 1);
           }
-          mx *= c;
+          if constexpr (!kQ8) mx *= c;
           if (__any_sync(0xffffffffu, mx > m + 8.f)) {
             const float mn = fmaxf(m, mx), f = mn == m ? 1.f : ex2(m - mn);
             m = mn;
@@ -559,14 +720,22 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           uint64_t c2 = pack2(c, c), m2 = pack2(-mu, -mu), l2[2] = {0ull, 0ull};
           // s c - m in one rounding while the maximum's own (2^-13 up to 2^12) is small against the weights' (2^-11); far out
           // the product is rounded as the maximum was, or the largest score would miss it by its own last place
-          if (__any_sync(0xffffffffu, !(fabsf(mu) <= 4096.f))) {
+          const bool far = __any_sync(0xffffffffu, !(fabsf(mu) <= 4096.f));
+          if (far) {
             tc_wait32(sa);
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
               uint32_t s[32];
               tc_ld32(ts + j * 32, s);
+              if constexpr (kQ8) {
+                const float4 z = factors(j);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), c), -mu));
+                for (int i = 0; i < 32; ++i)
+                  s[i] = __float_as_uint(__fadd_rn(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), i < 16 ? z.x : z.z), i < 16 ? z.y : z.w), -mu));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), c), -mu));
+              }
               tc_st16(ts + j * 32, s);
               tc_st16(ts + j * 32 + 16, s + 16);
             }
@@ -577,14 +746,33 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
           }
           auto weights = [&](const uint32_t (&x)[32], int j) {
             uint32_t p[16];
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if constexpr (kQ8) {
+              f = factors(j);
+              c2 = far ? pack2(1.f, 1.f) : pack2(f.x, f.x);
+              m2 = far ? 0ull : pack2(f.y - mu, f.y - mu);
+              l2[0] = l2[1] = 0ull;
+            }
+            // 2^-b of the block that the sum so far belongs to
+            auto add_block = [&](float e) {
+              const float2 x = unpack2(add2(l2[0], l2[1]));
+              l = fmaf(x.x + x.y, __uint_as_float(__float_as_uint(8388735.f - e) << 23), l);
+            };
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
+              if (kQ8 && i == 8) {
+                add_block(f.y);
+                c2 = far ? c2 : pack2(f.z, f.z);
+                m2 = far ? m2 : pack2(f.w - mu, f.w - mu);
+                l2[0] = l2[1] = 0ull;
+              }
               const float2 z = unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, m2));
               const float ex = ex2(z.x), ey = ex2(z.y);
               l2[i & 1] = add2(l2[i & 1], pack2(ex, ey));
               const __half2 hh = __floats2half2_rn(ex, ey);
               p[i] = *reinterpret_cast<const uint32_t*>(&hh);
             }
+            if constexpr (kQ8) add_block(f.w);
             tc_st16(ts + j * 16, p);  // over scores that this thread has read
           };
 #pragma unroll 1
@@ -601,8 +789,10 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
               mbar_arrive(&phalf[b]);
             }
           }
-          const float2 lx = unpack2(add2(l2[0], l2[1]));
-          l += lx.x + lx.y;
+          if constexpr (!kQ8) {
+            const float2 lx = unpack2(add2(l2[0], l2[1]));
+            l += lx.x + lx.y;
+          }
           tc_wait_st();
           tc_fence_before();
         } else if constexpr (!kWide) {
@@ -647,7 +837,7 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
       }
       if (in && alive && mine) {
         tc_fence_after();
-        const bool odd = reinterpret_cast<volatile int*>(flags)[4 + (n_unit & 1)] == n_unit + 1;
+        const bool odd = !kQ8 && reinterpret_cast<volatile int*>(flags)[4 + (n_unit & 1)] == n_unit + 1;
         const bool valid = row < all_rows;
         float* rec = tree_record(a, here, t0 == 0);
         const int j0 = max(t0 * kTK - u.ctx, 0), j1 = min(t1 * kTK - u.ctx, u.nodes);
@@ -787,22 +977,29 @@ __global__ void __launch_bounds__(kTcTreeThreads, 1) k_tree_attend_tc(const __gr
   }
 }
 
-template <int D, bool kWide>
+template <int D, bool kWide, int kKind>
 cudaError_t one(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
   static SmemOptIn opt;
-  constexpr int smem = TcSmem<D>::kBytes;
+  constexpr bool kQ8 = kKind != kTreeF16;
+  constexpr int smem = TcSmem<D, kQ8>::kBytes;
   static_assert(smem <= 232448, "one CTA per SM");
-  cudaError_t e = opt.ensure(k_tree_attend_tc<D, kWide>, smem);
+  cudaError_t e = opt.ensure(k_tree_attend_tc<D, kWide, kKind>, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_tree_attend_tc<D, kWide>, ctas, kTcTreeThreads, smem, s, *tm, a);
+  return launch_pdl(k_tree_attend_tc<D, kWide, kKind>, ctas, kQ8 ? kTcTreeThreadsQ8 : kTcTreeThreads, smem, s, *tm, a);
+}
+template <int D, bool kWide>
+cudaError_t kinds(const TreeAttendArgs& a, int kv_type, const CUtensorMap* tm, int ctas, cudaStream_t s) {
+  return kv_type == kTreeF16    ? one<D, kWide, kTreeF16>(a, tm, ctas, s)
+         : kv_type == kTreeE4m3 ? one<D, kWide, kTreeE4m3>(a, tm, ctas, s)
+                                : one<D, kWide, kTreeI8>(a, tm, ctas, s);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, bool wide, cudaStream_t s) {
+cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, int kv_type, const CUtensorMap* tm, int ctas, bool wide, cudaStream_t s) {
   switch (a.d.D) {
-    case 64: return wide ? one<64, true>(a, tm, ctas, s) : one<64, false>(a, tm, ctas, s);
-    case 128: return wide ? one<128, true>(a, tm, ctas, s) : one<128, false>(a, tm, ctas, s);
+    case 64: return wide ? kinds<64, true>(a, kv_type, tm, ctas, s) : kinds<64, false>(a, kv_type, tm, ctas, s);
+    case 128: return wide ? kinds<128, true>(a, kv_type, tm, ctas, s) : kinds<128, false>(a, kv_type, tm, ctas, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -71,6 +71,33 @@ __device__ __forceinline__ float4 q8_unpack(uint32_t w) {
   }
 }
 
+// Two pairs of codes of a word as f16: bytes (0, 1), (2, 3), or the even and the odd ones.
+template <int kKind, bool kEvenOdd>
+__device__ __forceinline__ void q8_halves(uint32_t w, uint32_t& x, uint32_t& y) {
+  if constexpr (Q8<kKind>::kInt) {
+    const uint32_t u = w ^ 0x80808080u, bias = 0x64806480u;  // 1152
+    const uint32_t p = __byte_perm(u, 0x64u, kEvenOdd ? 0x4240 : 0x4140), q = __byte_perm(u, 0x64u, kEvenOdd ? 0x4341 : 0x4342);
+    const __half2 b = *reinterpret_cast<const __half2*>(&bias);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&p), b), g = __hsub2(*reinterpret_cast<const __half2*>(&q), b);
+    x = *reinterpret_cast<const uint32_t*>(&h);
+    y = *reinterpret_cast<const uint32_t*>(&g);
+  } else {
+    const uint32_t u = kEvenOdd ? __byte_perm(w, 0u, 0x3120) : w;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(x), "=r"(y)
+        : "r"(u));
+  }
+}
+
+// Codes that are no numbers (memory that no call has written) as 0.
+__device__ __forceinline__ uint32_t e4m3_numbers(uint32_t w) {
+  const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  return w & ~((nan >> 7) * 0xFFu);
+}
+
 // Index of a page's scale: [layers][blocks][KV heads][K, V].
 __device__ __forceinline__ int64_t q8_scale_at(const TreePoolDims& d, int layer, int block, int head, int is_v) {
   return (((int64_t)layer * d.n_blocks + block) * d.Hkv + head) * 2 + is_v;

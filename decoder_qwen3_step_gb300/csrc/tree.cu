@@ -50,10 +50,10 @@ struct TreeLayout {
 // rows 83 (its accumulators spill at two row tiles a warp) against 51; at 8
 // sequences over 8000 keys with 512 rows, narrow units 211 us, wide ones 114.
 TreeVariant variant_for(int kv_type, int D, int max_rows) {
-  if (kv_type == kTreeE4m3 || kv_type == kTreeI8) return {kTreeMmaQ8, 16, 64, 3, 2, 0};
   if (kv_type == kTreeF32) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2, 0};
   if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, 4, 50};
   if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, 4, 25};
+  if (kv_type != kTreeF16) return {kTreeMmaQ8, 16, 64, 3, 2, 0};
   return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2, 0};
 }
 // The rows of a sequence walk the keys side by side in the wide kernel alone, a CTA for each of its row tiles.
@@ -787,7 +787,7 @@ int dec_tree_attend(dec_tree* t, int32_t layer, const void* q, int32_t q_type, i
   TREE_CUDA(t->kernel == kTreeFfma  ? launch_tree_attend_f32(a, t->ctas, st)
             : t->kernel == kTreeMmaQ8 ? launch_tree_attend_q8(a, t->kv_type, &t->tm, t->ctas, st)
             : t->kernel == kTreeMma ? launch_tree_attend_f16(a, &t->tm, t->ctas, st)
-                                    : launch_tree_attend_tc(a, &t->tm_groups, t->ctas, t->kernel == kTreeTcWide, st));
+                                    : launch_tree_attend_tc(a, t->kv_type, t->q8 ? &t->tm : &t->tm_groups, t->ctas, t->kernel == kTreeTcWide, st));
   // nothing to join: no second launch, unless a replay may meet a plan that has something
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (t->n_merges == 0) TREE_CUDA(cudaStreamIsCapturing(st, &cap));

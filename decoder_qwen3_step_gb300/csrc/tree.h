@@ -120,7 +120,7 @@ struct TreeVariant {
 constexpr int kTreeMaxCtasPerSm = 3;
 cudaError_t launch_tree_attend_f32(const TreeAttendArgs& a, int ctas, cudaStream_t s);
 cudaError_t launch_tree_attend_f16(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s);
-cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, bool wide, cudaStream_t s);
+cudaError_t launch_tree_attend_tc(const TreeAttendArgs& a, int kv_type, const CUtensorMap* tm, int ctas, bool wide, cudaStream_t s);
 cudaError_t launch_tree_attend_q8(const TreeAttendArgs& a, int kv_type, const CUtensorMap* tm, int ctas, cudaStream_t s);
 cudaError_t launch_tree_merge(const TreeAttendArgs& a, int n_merges, int parts, cudaStream_t s);
 
