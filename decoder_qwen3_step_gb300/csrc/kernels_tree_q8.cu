@@ -12,15 +12,22 @@
 //
 // The division of the work and the roundings are those of kernels_tree_f16.cu:
 // a producer warp streams 64 keys (4 pool blocks, K and V, one TMA box per
-// block) into a ring, warp w of four folds block w of every tile for 16 rows.
+// block) into a ring, warp w of four folds block w of every tile for 8 or 16
+// rows.  Half the bytes a key leave half the time for it, so keys and channels
+// take the 16 rows of the MMAs and the few query rows their 8 columns:
+//   S^T = K Q^T, O^T += V^T P^T
+// with half the MMAs of the other way round where 8 rows are enough (a decode
+// step has 1 to 4), the queries in registers for a whole unit, and a maximum
+// that is only formed when some weight would pass 2^8 (one vote a block).
 //
 // Codes to f16 without moving them between lanes: a dot product does not mind
-// the order of its channels, so the queries lie in shared memory in the order in
-// which a lane's word of four codes comes out of ldmatrix (channels 4j, 4j + 1 |
-// 4j + 2, 4j + 3 instead of 2j, 2j + 1 | 8 + 2j, ..).  Values are read transposed
-// in pairs of channels, so a word holds two channels of two keys: its even bytes
-// are an operand of channels 0, 2, .., its odd ones of channels 1, 3, .. of 16;
-// the outputs of the two products are four channels in a row.
+// the order of its channels, so a lane's word of four codes, as it comes out of
+// ldmatrix, is four channels in a row of one key, and the lane's queries the same
+// four channels.  Values are read transposed in pairs of channels, a word holds
+// two channels of two keys: its even bytes are an operand row of an even channel
+// (rows 0 .. 7 of V^T's 16), its odd ones of an odd channel (rows 8 .. 15).
+// Weights come as [key][row] and are needed as [row][key]: one 8 x 8 transpose
+// (movmatrix) per 8 keys.
 // i8: the byte, its sign flipped, under an exponent of 2^10 is 1024 + 128 + c in
 // f16, one subtraction gives c: 5 instructions for four codes.
 #include "attn_fold.cuh"
@@ -32,21 +39,21 @@ namespace dec {
 namespace {
 
 constexpr int kQ8Keys = 64;  // keys per tile: 4 pool blocks
-constexpr int kQ8Rows = 16;
 constexpr int kQ8Threads = 160;
 
-template <int D>
+template <int D, int R>
 struct Q8Smem {
   static constexpr int kSlab = 16 * D;                         // K (or V) of one block
   static constexpr int kStage = 4 * 2 * kSlab;
-  static constexpr int kStages = D == 128 ? 4 : D == 64 ? 8 : 16;
+  static constexpr int kCtas = D == 128 && R == 16 ? 2 : 3;    // per SM: with 16 rows of 128 channels a lane needs 160 registers
+  static constexpr int kStages = D == 128 ? (kCtas == 2 ? 6 : 4) : D == 64 ? 8 : 16;
   static constexpr int kQPitch = D * 2 + 16;                   // bytes; rows fall into different banks
   static constexpr int kQ = kStages * kStage;                  // the queries, at a unit's end the warps' outputs
   static constexpr int kRedPitch = 40;                         // floats of a row's 32 channels: rows fall into different banks
-  static constexpr int kRed = 4 * kQ8Rows * kRedPitch * 4;
-  static constexpr int kML = kQ + (kQ8Rows * kQPitch > kRed ? kQ8Rows * kQPitch : kRed);  // float [4][R] maxima, [4][R] sums
-  static constexpr int kFac = kML + 2 * 4 * kQ8Rows * 4;       // float [R]: the rows' score factors
-  static constexpr int kBar = kFac + kQ8Rows * 4;
+  static constexpr int kRed = 4 * R * kRedPitch * 4;
+  static constexpr int kML = kQ + (R * kQPitch > kRed ? R * kQPitch : kRed);  // float [4][R] maxima, [4][R] sums
+  static constexpr int kFac = kML + 2 * 4 * R * 4;       // float [R]: the rows' score factors
+  static constexpr int kBar = kFac + R * 4;
   static constexpr int kBytes = kBar + 2 * kStages * 8 + 16;
   static_assert(kML % 16 == 0 && kBar % 8 == 0, "alignment");
 };
@@ -65,11 +72,18 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-template <int D, int kKind>
-__global__ void __launch_bounds__(kQ8Threads, 3) k_tree_attend_q8(const __grid_constant__ CUtensorMap tm,
+// Transpose of an 8 x 8 matrix of halves: a lane holds two of a row, before and after.
+__device__ __forceinline__ uint32_t q8_transpose(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, int R, int kKind>
+__global__ void __launch_bounds__(kQ8Threads, Q8Smem<D, R>::kCtas) k_tree_attend_q8(const __grid_constant__ CUtensorMap tm,
                                                                   const __grid_constant__ TreeAttendArgs a) {
-  using SM = Q8Smem<D>;
-  constexpr int R = kQ8Rows, kS = SM::kStages;
+  using SM = Q8Smem<D, R>;
+  constexpr int kN = R / 8, kS = SM::kStages;  // column tiles of 8 rows
   extern __shared__ __align__(1024) uint8_t dsm[];
   uint64_t* full = reinterpret_cast<uint64_t*>(dsm + SM::kBar);
   uint64_t* empty = full + kS;
@@ -161,28 +175,29 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_tree_attend_q8(const __grid_c
       };
       float2 sc = scales_of(t0, nxt), sc_next = sc;
       nxt = entries(t0 + 32, t1);
-      // eight channels of a row, in the order that the codes' words have
-      auto put = [&](int r, int x, uint4 h) {
-        uint8_t* at = Qs + r * SM::kQPitch + (x >> 1) * 32 + (x & 1) * 8;
-        *reinterpret_cast<uint2*>(at) = make_uint2(h.x, h.z);
-        *reinterpret_cast<uint2*>(at + 16) = make_uint2(h.y, h.w);
-      };
-      if constexpr (R / 4 >= 32 / (D / 8)) {
-        tree_load_queries<D, R, 4, 4>(a, u, u.row_tile * R, warp, fac, put);
-      } else if (warp < 2) {  // D = 32: a warp reads eight rows at a time
-        tree_load_queries<D, R, 2, 4>(a, u, u.row_tile * R, warp, fac, put);
-      }
+      auto put = [&](int r, int x, uint4 h) { *reinterpret_cast<uint4*>(Qs + r * SM::kQPitch + x * 16) = h; };
+      constexpr int kLoaders = R * (D / 8) / 32 < 4 ? R * (D / 8) / 32 : 4;  // a warp reads 32 / (D / 8) rows at a time
+      if (warp < kLoaders) tree_load_queries<D, R, kLoaders, 4>(a, u, u.row_tile * R, warp, fac, put);
       group_bar();
-      const uint32_t qb = smem_u32(Qs) + (lane & 15) * SM::kQPitch + (lane >> 4) * 16;
-      float c[2], m[2], l[2], o[D / 8][4];
+      // the lane's rows n * 8 + (lane >> 2) as operands, and n * 8 + 2 * (lane & 3), + 1 as columns of scores and outputs
+      uint32_t q[kN][D / 16][2];
+      float c[kN][2], m[kN][2], l[kN][2], o[kN][D / 16][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        c[i] = fac[i * 8 + (lane >> 2)];
-        m[i] = -INFINITY;
-        l[i] = 0.f;
+      for (int n = 0; n < kN; ++n) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint2 x = *reinterpret_cast<const uint2*>(Qs + (n * 8 + (lane >> 2)) * SM::kQPitch + i * 32 + (lane & 3) * 8);
+          q[n][i][0] = x.x;
+          q[n][i][1] = x.y;
+          o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+        }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          c[n][z] = fac[n * 8 + 2 * (lane & 3) + z];
+          m[n][z] = -INFINITY;
+          l[n][z] = 0.f;
+        }
       }
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
       for (int t = t0; t < t1; ++t, ++k) {
         const int turn = (t - t0) & 31;
@@ -194,81 +209,80 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_tree_attend_q8(const __grid_c
         const float sk = __shfl_sync(0xffffffffu, sc.x, turn), ev = __shfl_sync(0xffffffffu, sc.y, turn);
         const int slot = k % kS, key0 = t * kQ8Keys + warp * 16, nkeys = min(16, end - key0);
         const bool drafted = nkeys > 0 && key0 + nkeys > u.ctx;  // some key of the block is a node
-        uint32_t sees[2];  // this lane's rows, bit = key of the block; read ahead of the wait
+        uint32_t sees[kN][2];  // this lane's columns, bit = key of the block; read ahead of the wait
         if (drafted) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int row = u.row_tile * R + i * 8 + (lane >> 2);
-            sees[i] = tree_window(a.m, a.m.anc + (size_t)(u.node0 + min(row >> gs, u.nodes - 1)) * a.m.words, key0 - u.ctx);
-          }
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int row = u.row_tile * R + n * 8 + 2 * (lane & 3) + z;
+              sees[n][z] = tree_window(a.m, a.m.anc + (size_t)(u.node0 + min(row >> gs, u.nodes - 1)) * a.m.words, key0 - u.ctx);
+            }
         }
         alive = __all_sync(0xffffffffu, alive && mbar_wait(&full[slot], (k / kS) & 1, abort_flag, a.m.err));
         if (alive && nkeys > 0) {
           const uint32_t kb = smem_u32(dsm) + slot * SM::kStage + warp * 2 * SM::kSlab, vb = kb + SM::kSlab;
-          float s[2][4];
+          float s[kN][2][4];  // in two chains
 #pragma unroll
-          for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) s[n][z][0] = s[n][z][1] = s[n][z][2] = s[n][z][3] = 0.f;
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk) {
             uint32_t w[4];
             af_ldsm4(kb + slab_at<D>(key, kk * 2 + kc), w);
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-              uint32_t A[4], b0, b1;
-              af_ldsm4(qb + (kk * 2 + z) * 32, A);
-              q8_halves<kKind, false>(w[z], b0, b1);
-              af_mma_f16(s[0], A, b0, b1);
-              q8_halves<kKind, false>(w[2 + z], b0, b1);
-              af_mma_f16(s[1], A, b0, b1);
+              uint32_t A[4];
+              q8_halves<kKind, false>(w[z], A[0], A[2]);
+              q8_halves<kKind, false>(w[2 + z], A[1], A[3]);
+#pragma unroll
+              for (int n = 0; n < kN; ++n) af_mma_f16(s[n][z], A, q[n][2 * kk + z][0], q[n][2 * kk + z][1]);
             }
           }
-          float mx[2];
+          // scores of keys lane >> 2 and + 8: x[0], x[2] of the first column, x[1], x[3] of the second
+          float x[kN][4];
+          bool raise = false;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int e = i * 2;
-            const float f = c[i] * sk;
+          for (int n = 0; n < kN; ++n) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              s[n][e] *= f;
-              s[n][e + 1] *= f;
+            for (int i = 0; i < 4; ++i) {
+              x[n][i] = (s[n][0][i] + s[n][1][i]) * fminf(c[n][i & 1] * sk, 3.40282347e38f);
+              if (drafted && !((sees[n][i & 1] >> ((lane >> 2) + (i >> 1) * 8)) & 1u)) x[n][i] = -INFINITY;
             }
-            if (drafted) {
-#pragma unroll
-              for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int z = 0; z < 2; ++z)
-                  if (!((sees[i] >> (n * 8 + 2 * (lane & 3) + z)) & 1u)) s[n][e + z] = -INFINITY;
-            }
-            mx[i] = fmaxf(fmaxf(s[0][e], s[0][e + 1]), fmaxf(s[1][e], s[1][e + 1]));
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2)) + ev;
+            raise |= fmaxf(x[n][0], x[n][2]) + ev > m[n][0] + 8.f || fmaxf(x[n][1], x[n][3]) + ev > m[n][1] + 8.f;
           }
-          if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+          if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float mn = fmaxf(m[i], mx[i]);
-              const float f = mn == m[i] ? 1.f : ex2(m[i] - mn);
-              m[i] = mn;
-              l[i] *= f;
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
-              for (int j = 0; j < D / 8; ++j) {
-                o[j][i * 2] *= f;
-                o[j][i * 2 + 1] *= f;
+              for (int z = 0; z < 2; ++z) {
+                float mx = fmaxf(x[n][z], x[n][z + 2]);
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                const float mn = fmaxf(m[n][z], mx + ev);
+                const float f = mn == m[n][z] ? 1.f : ex2(m[n][z] - mn);
+                m[n][z] = mn;
+                l[n][z] *= f;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                  o[n][j][z] *= f;
+                  o[n][j][z + 2] *= f;
+                }
               }
-            }
           }
           const float sv = q8_two((int)ev);
-          uint32_t P[4];
+          uint32_t P[kN][2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int e = i * 2;
-            const float mu = m[i] == -INFINITY ? 0.f : m[i];  // nothing seen so far: every weight is 0
+          for (int n = 0; n < kN; ++n) {
+            float p[4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const float p0 = ex2(s[n][e] - mu), p1 = ex2(s[n][e + 1] - mu);
-              l[i] += p0 + p1;
-              P[2 * n + i] = af_pack_half(p0 * sv, p1 * sv);
+            for (int i = 0; i < 4; ++i) {
+              p[i] = ex2(x[n][i] - (m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1]));  // nothing seen so far: every weight is 0
+              l[n][i & 1] += p[i];
             }
+            P[n][0] = q8_transpose(af_pack_half(p[0] * sv, p[1] * sv));
+            P[n][1] = q8_transpose(af_pack_half(p[2] * sv, p[3] * sv));
           }
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
@@ -280,11 +294,11 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_tree_attend_q8(const __grid_c
             }
 #pragma unroll
             for (int z = 0; z < 2; ++z) {  // 16 channels: keys 0 .. 7 and 8 .. 15
-              uint32_t x0, x1, y0, y1;
-              q8_halves<kKind, true>(w[2 * z], x0, y0);
-              q8_halves<kKind, true>(w[2 * z + 1], x1, y1);
-              af_mma_f16(o[(2 * j + z) * 2], P, x0, x1);
-              af_mma_f16(o[(2 * j + z) * 2 + 1], P, y0, y1);
+              uint32_t A[4];
+              q8_halves<kKind, true>(w[2 * z], A[0], A[1]);
+              q8_halves<kKind, true>(w[2 * z + 1], A[2], A[3]);
+#pragma unroll
+              for (int n = 0; n < kN; ++n) af_mma_f16(o[n][2 * j + z], A, P[n][0], P[n][1]);
             }
           }
         }
@@ -293,27 +307,31 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_tree_attend_q8(const __grid_c
       }
       // ---- the unit's end: the four warps' states in warp order ----
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        if ((lane & 3) == 0) {
-          const int r = i * 8 + (lane >> 2);
-          ml[warp * R + r] = m[i];
-          ml[(4 + warp) * R + r] = l[i];
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) l[n][z] += __shfl_xor_sync(0xffffffffu, l[n][z], d);
+          if (lane < 4) {
+            const int r = n * 8 + 2 * lane + z;
+            ml[warp * R + r] = m[n][z];
+            ml[(4 + warp) * R + r] = l[n][z];
+          }
         }
-      }
       group_bar();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {  // this warp's factor to the common maximum
-        const int r = i * 8 + (lane >> 2);
-        const float M = fmaxf(fmaxf(ml[r], ml[R + r]), fmaxf(ml[2 * R + r], ml[3 * R + r]));
-        const float f = ex2(m[i] - (M == -INFINITY ? 0.f : M));  // 0 where the row saw nothing
+      for (int n = 0; n < kN; ++n)
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          o[j][i * 2] *= f;
-          o[j][i * 2 + 1] *= f;
+        for (int z = 0; z < 2; ++z) {  // this warp's factor to the common maximum
+          const int r = n * 8 + 2 * (lane & 3) + z;
+          const float M = fmaxf(fmaxf(ml[r], ml[R + r]), fmaxf(ml[2 * R + r], ml[3 * R + r]));
+          const float f = ex2(m[n][z] - (M == -INFINITY ? 0.f : M));  // 0 where the row saw nothing
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            o[n][j][z] *= f;
+            o[n][j][z + 2] *= f;
+          }
         }
-      }
       // the rows are final here, or this CTA's part of a shared unit: a record
       const bool whole = t0 == 0 && t1 == u.tiles;
       float* part = tree_record(a, here, t0 == 0);
@@ -336,13 +354,13 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_tree_attend_q8(const __grid_c
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {  // 32 channels at a time
 #pragma unroll
-        for (int z = 0; z < 2; ++z)
+        for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float(&x)[4] = o[(2 * j + z) * 2], (&y)[4] = o[(2 * j + z) * 2 + 1];  // channels 4 q, + 2 and 4 q + 1, + 3
-            *reinterpret_cast<float4*>(red + (warp * R + i * 8 + (lane >> 2)) * SM::kRedPitch + z * 16 + 4 * (lane & 3)) =
-                make_float4(x[2 * i], y[2 * i], x[2 * i + 1], y[2 * i + 1]);
-          }
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int z = 0; z < 2; ++z)  // channels 2 (lane >> 2), + 1 of 16
+              *reinterpret_cast<float2*>(red + (warp * R + n * 8 + 2 * (lane & 3) + z) * SM::kRedPitch + i * 16 + 2 * (lane >> 2)) =
+                  make_float2(o[n][2 * j + i][z], o[n][2 * j + i][z + 2]);
         group_bar();
         for (int i = threadIdx.x; i < rows * 8; i += 128) {
           const int r = i >> 3, x = (i & 7) * 4;
@@ -381,18 +399,19 @@ __global__ void __launch_bounds__(kQ8Threads, 3) k_tree_attend_q8(const __grid_c
   }
 }
 
-template <int D, int kKind>
+template <int D, int R, int kKind>
 cudaError_t one(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
   static SmemOptIn opt;
-  constexpr int smem = Q8Smem<D>::kBytes;
-  static_assert(smem <= 76 * 1024, "three CTAs per SM");
-  cudaError_t e = opt.ensure(k_tree_attend_q8<D, kKind>, smem);
+  constexpr int smem = Q8Smem<D, R>::kBytes;
+  static_assert(smem <= (Q8Smem<D, R>::kCtas == 2 ? 113 : 76) * 1024, "CTAs per SM");
+  cudaError_t e = opt.ensure(k_tree_attend_q8<D, R, kKind>, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_tree_attend_q8<D, kKind>, ctas, kQ8Threads, smem, s, *tm, a);
+  return launch_pdl(k_tree_attend_q8<D, R, kKind>, ctas, kQ8Threads, smem, s, *tm, a);
 }
 template <int D>
 cudaError_t kinds(const TreeAttendArgs& a, int kv_type, const CUtensorMap* tm, int ctas, cudaStream_t s) {
-  return kv_type == kTreeI8 ? one<D, kTreeI8>(a, tm, ctas, s) : one<D, kTreeE4m3>(a, tm, ctas, s);
+  if (a.m.row_tile == 8) return kv_type == kTreeI8 ? one<D, 8, kTreeI8>(a, tm, ctas, s) : one<D, 8, kTreeE4m3>(a, tm, ctas, s);
+  return kv_type == kTreeI8 ? one<D, 16, kTreeI8>(a, tm, ctas, s) : one<D, 16, kTreeE4m3>(a, tm, ctas, s);
 }
 
 }  // namespace

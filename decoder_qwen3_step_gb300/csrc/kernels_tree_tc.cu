@@ -112,8 +112,8 @@ __device__ __forceinline__ uint64_t keys_desc(uint32_t saddr, uint32_t group, bo
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// A load that runs on: its values are there after the next tc_wait32 on them.
-__device__ __forceinline__ void tc_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
+// A load that runs on: its values are there after the next tc_wait on them.
+__device__ __forceinline__ void tc_ld_async(uint32_t taddr, uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -123,13 +123,33 @@ __device__ __forceinline__ void tc_ld32_async(uint32_t taddr, uint32_t (&v)[32])
         "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tc_wait32(uint32_t (&v)[32]) {
+__device__ __forceinline__ void tc_wait(uint32_t (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
                  "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
                  "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
                  "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
                :
+               : "memory");
+}
+// The same for 16 columns.
+__device__ __forceinline__ void tc_ld_async(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tc_wait(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* v) {
@@ -216,6 +236,7 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
   constexpr bool kQ8 = kKind != kTreeF16;
   using SM = TcSmem<D, kQ8>;
   constexpr int kS = SM::kSlots, kOps = SM::kOps, kR = kWide ? 2 * kTR : kTR;
+  constexpr int kC = kQ8 ? 16 : 32;  // columns of S that a softmax thread works on at a time
   constexpr int kSoftmaxRegs = kWide ? 152 : 168;  // 256 threads with these, 256 with the rest of 256: 65,536, as launched
   extern __shared__ __align__(1024) uint8_t dsm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(dsm + SM::kBar);
@@ -574,9 +595,9 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
         }
       }
       bool first = true;
-      // 8 bits: the scales of four of the group's tiles, a lane's block each; the next ones' on their way while these are used
+      // 8 bits: the scales of four of the group's tiles, a lane's block each
       const int ta = t0 + (kWide ? 0 : (k ^ b) & 1);  // the group's first tile of the unit
-      float2 sc = make_float2(0.f, 0.f), sc_next = sc;
+      float2 sc = make_float2(0.f, 0.f);
       int turn = 0;
       auto scales_of = [&](int t, int blk) {
         float2 y = make_float2(1.f, 1.f);
@@ -591,16 +612,14 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
       }
       for (int t = t0; t < t1; ++t, ++k) {
         if (!in || (!kWide && (k & 1) != b)) continue;
-        const float4* blocks = reinterpret_cast<const float4*>(dsm + SM::kScales + warp * 128 + (turn & 1) * 64);  // two blocks each
+        const float2* blocks = reinterpret_cast<const float2*>(dsm + SM::kScales + warp * 128 + (turn & 1) * 64);
         if constexpr (kQ8) {
-          if (turn == 4) {
-            turn = 0;
-            sc = sc_next;
-            nxt = entry4(t + (kWide ? 4 : 8), t1);
-          }
           if (lane >> 3 == turn) *reinterpret_cast<float2*>(dsm + SM::kScales + warp * 128 + (turn & 1) * 64 + (lane & 7) * 8) = sc;
-          if (turn == 2) sc_next = scales_of(t + (kWide ? 2 : 4), nxt);
-          ++turn;
+          if (turn == 3) {  // the last of these four: the next ones' scales are on their way while it is worked on
+            sc = scales_of(t + (kWide ? 1 : 2), nxt);
+            nxt = entry4(t + (kWide ? 5 : 10), t1);
+          }
+          turn = (turn + 1) & 3;
           __syncwarp();
         }
         const int key0 = t * kTK;
@@ -660,42 +679,40 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
             }
             tc_wait_st();
           }
-          // two passes over S, 32 columns at a time, the next ones on their way while these are worked on (the loops stay
-          // loops: unrolled, the tile's code ran out of the instruction cache at every turn)
-          uint32_t sa[32], sb[32];
+          // two passes over S, 32 columns (8 bits: 16, a block) at a time, the next ones on their way while these are worked
+          // on (the loops stay loops: unrolled, the tile's code ran out of the instruction cache at every turn)
+          uint32_t sa[kC], sb[kC];
           float mx = -INFINITY;
-          // 8 bits: a block's score factor for this row, kept off 0 and infinity (hidden scores are -inf) and its exponent
+          // 8 bits: block j's score factor for this row, kept off 0 and infinity (hidden scores are -inf), and the exponent of
+          // its values
           auto factors = [&](int j) {
-            float4 z = blocks[j];
+            float2 z = blocks[j];
             z.x = fminf(fmaxf(z.x * c, 1.17549435e-38f), 3.40282347e38f);
-            z.z = fminf(fmaxf(z.z * c, 1.17549435e-38f), 3.40282347e38f);
             return z;
           };
-          auto largest = [&](const uint32_t (&x)[32], int j) {
-            if constexpr (kQ8) {
-              float y[2] = {-INFINITY, -INFINITY};  // of each block
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) y[i / 16] = fmaxf(fmaxf(y[i / 16], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-              const float4 z = factors(j);
-              mx = fmaxf(mx, fmaxf(__fadd_rn(__fmul_rn(y[0], z.x), z.y), __fadd_rn(__fmul_rn(y[1], z.z), z.w)));
-              return;
-            }
+          auto largest = [&](const uint32_t (&x)[kC], int j) {
             float y[2] = {mx, mx};
+            if constexpr (kQ8) y[0] = y[1] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
+            for (int i = 0; i < kC; i += 4) {
               y[0] = fmaxf(fmaxf(y[0], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
               y[1] = fmaxf(fmaxf(y[1], __uint_as_float(x[i + 2])), __uint_as_float(x[i + 3]));
             }
-            mx = fmaxf(y[0], y[1]);
+            if constexpr (kQ8) {
+              const float2 z = factors(j);
+              mx = fmaxf(mx, __fadd_rn(__fmul_rn(fmaxf(y[0], y[1]), z.x), z.y));
+            } else {
+              mx = fmaxf(y[0], y[1]);
+            }
           };
-          tc_ld32_async(ts, sa);
+          tc_ld_async(ts, sa);
 #pragma unroll 1
-          for (int j = 0; j < 4; j += 2) {
-            tc_wait32(sa);
-            tc_ld32_async(ts + j * 32 + 32, sb);
+          for (int j = 0; j < kTK / kC; j += 2) {
+            tc_wait(sa);
+            tc_ld_async(ts + (j + 1) * kC, sb);
             largest(sa, j);
-            tc_wait32(sb);
-            tc_ld32_async(ts + ((j * 32 + 64) & 127), sa);  // at the end the first columns again, for the weights
+            tc_wait(sb);
+            tc_ld_async(ts + (((j + 2) * kC) & 127), sa);  // at the end the first columns again, for the weights
             largest(sb, j + 1);
           }
           if constexpr (!kQ8) mx *= c;
@@ -704,7 +721,7 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
             m = mn;
             l *= f;
             if (!first) {  // this group's products so far have run: its S was issued behind them
-              tc_wait32(sa);
+              tc_wait(sa);
 #pragma unroll 1
               for (int j = 0; j < D / 32; ++j) {
                 uint32_t o[32];
@@ -722,16 +739,16 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
           // the product is rounded as the maximum was, or the largest score would miss it by its own last place
           const bool far = __any_sync(0xffffffffu, !(fabsf(mu) <= 4096.f));
           if (far) {
-            tc_wait32(sa);
+            tc_wait(sa);
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
               uint32_t s[32];
               tc_ld32(ts + j * 32, s);
               if constexpr (kQ8) {
-                const float4 z = factors(j);
+                const float2 y = factors(2 * j), z = factors(2 * j + 1);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                  s[i] = __float_as_uint(__fadd_rn(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), i < 16 ? z.x : z.z), i < 16 ? z.y : z.w), -mu));
+                  s[i] = __float_as_uint(__fadd_rn(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), i < 16 ? y.x : z.x), i < 16 ? y.y : z.y), -mu));
               } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), c), -mu));
@@ -740,50 +757,48 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
               tc_st16(ts + j * 32 + 16, s + 16);
             }
             tc_wait_st();
-            tc_ld32_async(ts, sa);
+            tc_ld_async(ts, sa);
             c2 = pack2(1.f, 1.f);
             m2 = 0ull;
           }
-          auto weights = [&](const uint32_t (&x)[32], int j) {
-            uint32_t p[16];
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+          auto weights = [&](const uint32_t (&x)[kC], int j) {
+            uint32_t p[kC / 2];
+            float e = 0.f;
             if constexpr (kQ8) {
-              f = factors(j);
-              c2 = far ? pack2(1.f, 1.f) : pack2(f.x, f.x);
-              m2 = far ? 0ull : pack2(f.y - mu, f.y - mu);
+              const float2 z = factors(j);
+              e = z.y;
+              if (!far) {
+                c2 = pack2(z.x, z.x);
+                m2 = pack2(e - mu, e - mu);
+              }
               l2[0] = l2[1] = 0ull;
             }
-            // 2^-b of the block that the sum so far belongs to
-            auto add_block = [&](float e) {
-              const float2 x = unpack2(add2(l2[0], l2[1]));
-              l = fmaf(x.x + x.y, __uint_as_float(__float_as_uint(8388735.f - e) << 23), l);
-            };
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (kQ8 && i == 8) {
-                add_block(f.y);
-                c2 = far ? c2 : pack2(f.z, f.z);
-                m2 = far ? m2 : pack2(f.w - mu, f.w - mu);
-                l2[0] = l2[1] = 0ull;
-              }
+            for (int i = 0; i < kC / 2; ++i) {
               const float2 z = unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, m2));
               const float ex = ex2(z.x), ey = ex2(z.y);
               l2[i & 1] = add2(l2[i & 1], pack2(ex, ey));
               const __half2 hh = __floats2half2_rn(ex, ey);
               p[i] = *reinterpret_cast<const uint32_t*>(&hh);
             }
-            if constexpr (kQ8) add_block(f.w);
-            tc_st16(ts + j * 16, p);  // over scores that this thread has read
+            // over scores that this thread has read
+            if constexpr (kQ8) {
+              tc_st8(ts + j * 8, p);
+              const float2 y = unpack2(add2(l2[0], l2[1]));
+              l = fmaf(y.x + y.y, __uint_as_float(__float_as_uint(8388735.f - e) << 23), l);  // times 2^-e
+            } else {
+              tc_st16(ts + j * 16, p);
+            }
           };
 #pragma unroll 1
-          for (int j = 0; j < 4; j += 2) {
-            tc_wait32(sa);
-            tc_ld32_async(ts + j * 32 + 32, sb);
+          for (int j = 0; j < kTK / kC; j += 2) {
+            tc_wait(sa);
+            tc_ld_async(ts + (j + 1) * kC, sb);
             weights(sa, j);
-            tc_wait32(sb);
-            if (j == 0) tc_ld32_async(ts + 64, sa);
+            tc_wait(sb);
+            if (j + 2 < kTK / kC) tc_ld_async(ts + (j + 2) * kC, sa);
             weights(sb, j + 1);
-            if (!kWide && j == 0) {
+            if (!kWide && (j + 2) * kC == 64) {
               tc_wait_st();
               tc_fence_before();
               mbar_arrive(&phalf[b]);

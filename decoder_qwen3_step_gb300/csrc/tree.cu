@@ -53,7 +53,7 @@ TreeVariant variant_for(int kv_type, int D, int max_rows) {
   if (kv_type == kTreeF32) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2, 0};
   if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, 4, 50};
   if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, 4, 25};
-  if (kv_type != kTreeF16) return {kTreeMmaQ8, 16, 64, 3, 2, 0};
+  if (kv_type != kTreeF16) return {kTreeMmaQ8, max_rows <= 8 ? 8 : 16, 64, D == 128 && max_rows > 8 ? 2 : 3, 2, 0};
   return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2, 0};
 }
 // The rows of a sequence walk the keys side by side in the wide kernel alone, a CTA for each of its row tiles.

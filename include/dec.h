@@ -551,8 +551,9 @@ int dec_debug_df_exp(const double* x, double* y, int64_t n, void* stream);
  * replay follows the plan that is set then (by dec_tree_set outside the graph,
  * ordered before the replay) if its shape is the capture's: the same n_seqs,
  * n_tokens and ceil(longest / 32), longest the most nodes of a sequence, and
- * for dec_tree_attend longest * (n_heads / n_kv_heads) on the same side of 16
- * and, with an f16 or 8-bit cache and head_dim 64 or 128, of 128.  How the nodes are
+ * for dec_tree_attend longest * (n_heads / n_kv_heads) on the same side of 16,
+ * with an f16 or 8-bit cache and head_dim 64 or 128 of 128, and with an 8-bit
+ * cache of 8.  How the nodes are
  * divided among the sequences may differ (DEC_TREE_PAD nodes fill a batch up).
  * A replay on a plan of another shape does nothing and sets
  * DEC_DEV_SHAPE.  Calls run on the device that was current at
