@@ -26,18 +26,21 @@
 // every key four times and ran at HBM speed, 211 us against 64 for the products.
 // O is rescaled in TMEM only when a row's scores exceed its maximum by 2^8
 // (exact: numerator and denominator share the maximum).  Warps whose rows are
-// are all behind the last skip the softmax.  Roundings as in kernels_tree_f16.cu.
+// all behind the last skip the softmax.  Roundings as in kernels_tree_f16.cu.
 //
 // 8-bit caches: the producer brings codes (a page is contiguous: one bulk copy)
 // into a ring of their own, and
-//   warps 12..15  turn them into f16 (exact) operand tiles of the layout above.
-// The MMAs work on codes; with the scales 2^a of K and 2^b of V of a block of 16
-// keys, the softmax takes s c 2^a + b as the logarithm of a weight for the value
-// codes (its running maximum is the reference, see kernels_tree_q8.cu) and sums
-// the weights times 2^-b.  A tile's 16 scales come through 64 bytes of shared
-// memory per softmax warp, a row's factors are one product per block.  Registers
-// are moved from the other warps to the softmax (512 threads have 128 each, it
-// needs up to 168).
+//   warps 12..15  turn them into f16 operand tiles of the layout above.
+// A tile of 128 keys takes 2^A, the largest K scale of its eight blocks, out of
+// its keys, and 2^B of V's out of its values: an operand is code * 2^(a - A), one
+// fused multiply-add on the way from i8 to f16 (exact down to 2^-24: a page may
+// be 2^24 smaller than its neighbours before its codes lose bits, and then by
+// less than 2^-25 of the neighbours' step).  So the softmax has one factor c 2^A
+// and one exponent B a tile: weights are 2^(s + B - m), l adds 2^-B times their
+// sum (the reference m as in kernels_tree_q8.cu).  With a factor for each block
+// in the softmax it took 1.3 us a tile in place of 0.85.
+// Registers are moved from the other warps to the softmax (512 threads have 128
+// each).
 #include "attn_fold.cuh"
 #include "q8.cuh"
 #include "tc_common.cuh"
@@ -48,6 +51,8 @@ namespace {
 
 constexpr int kTR = 128, kTK = 128;  // rows and keys of a step
 constexpr int kTcTreeThreads = 384, kTcTreeThreadsQ8 = 512;
+constexpr int kScaleRing = 8;  // tiles whose (2^A, B) are kept: the conversion is at most two ahead of the softmax
+constexpr int kOps8 = 3, kSlots8 = 4;  // of 128 channels
 constexpr uint32_t kTmemCols = 512;  // S of the two groups: columns 0, 128; O: 256, 256 + D
 
 template <int D, bool kQ8>
@@ -57,13 +62,13 @@ struct TcSmem {
   static constexpr int kGroup = kPanels * 1024;       // bytes of eight keys
   static constexpr int kTile = kPanels * kPanel;
   // operand tiles (at least K, V, K are in use at once) and, for 8 bits, slots for codes; else the copies land in the operands
-  static constexpr int kOps = kQ8 ? (D == 128 ? 3 : 6) : D == 128 ? 5 : 10;
-  static constexpr int kSlots = kQ8 ? (D == 128 ? 4 : 8) : kOps;
+  static constexpr int kOps = kQ8 ? (D == 128 ? kOps8 : 2 * kOps8) : D == 128 ? 5 : 10;
+  static constexpr int kSlots = kQ8 ? (D == 128 ? kSlots8 : 2 * kSlots8) : kOps;
   static constexpr int kQ = 0;                        // two tiles: the units' in turn (narrow), the groups' (wide)
   static constexpr int kRing = 2 * kTile, kCodes = kRing + kOps * kTile, kCodeTile = kTK * D;
   static constexpr int kFac = kCodes + (kQ8 ? kSlots * kCodeTile : 0);  // float [2][kTR], as the queries
-  static constexpr int kScales = kFac + 2 * kTR * 4;                    // float2 [8 warps][2][8] (2^a, b) of a tile's blocks
-  static constexpr int kBar = kScales + (kQ8 ? 1024 : 0);
+  static constexpr int kScales = kFac + 2 * kTR * 4;                    // float2 [kScaleRing]
+  static constexpr int kBar = kScales + (kQ8 ? kScaleRing * 8 : 0);
   // barriers: full, empty [slots]; ready, used [operands] of 8 bits; Q full, Q empty, S full, P full, O full, O empty [2]; MMA done
   static constexpr int kBars = 2 * kSlots + (kQ8 ? 2 * kOps : 0) + 15;
   static constexpr int kBytes = kBar + kBars * 8 + 32;
@@ -112,8 +117,8 @@ __device__ __forceinline__ uint64_t keys_desc(uint32_t saddr, uint32_t group, bo
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// A load that runs on: its values are there after the next tc_wait on them.
-__device__ __forceinline__ void tc_ld_async(uint32_t taddr, uint32_t (&v)[32]) {
+// A load that runs on: its values are there after the next tc_wait32 on them.
+__device__ __forceinline__ void tc_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -123,33 +128,13 @@ __device__ __forceinline__ void tc_ld_async(uint32_t taddr, uint32_t (&v)[32]) {
         "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tc_wait(uint32_t (&v)[32]) {
+__device__ __forceinline__ void tc_wait32(uint32_t (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
                  "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
                  "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
                  "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
                :
-               : "memory");
-}
-// The same for 16 columns.
-__device__ __forceinline__ void tc_ld_async(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tc_wait(uint32_t (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
-                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* v) {
@@ -184,49 +169,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
   return r;
 }
 
-// A tile of 128 keys' codes (rows of D bytes) as an operand, by 128 threads.  Eight lanes of an access take four 16-byte
-// chunks of a row and the other four (D = 64: the same) of its neighbour, so that both sides touch every bank once.
-// odd: some rows may hold anything, codes that are no numbers become 0.
-template <int D, int kKind>
-__device__ __forceinline__ void tc_convert_load(const uint8_t* codes, int t, uint4 (&raw)[D / 16]) {
-  constexpr int kChunks = D / 16, kRowsPer = 128 / kChunks;  // rows of a round of all threads
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    int r, c;
-    if constexpr (D == 128) {
-      r = i * kRowsPer + (t >> 4) * 2 + ((t >> 2) & 1);
-      c = (t & 3) + 4 * (((t >> 2) ^ (t >> 3)) & 1);
-    } else {
-      r = i * kRowsPer + (t >> 2);
-      c = t & 3;
-    }
-    raw[i] = *reinterpret_cast<const uint4*>(codes + r * D + c * 16);
-  }
-}
-template <int D, int kKind>
-__device__ __forceinline__ void tc_convert_store(uint8_t* tile, int t, const uint4 (&raw)[D / 16], bool odd) {
-  constexpr int kChunks = D / 16, kRowsPer = 128 / kChunks, kGroup = D / 64 * 1024;
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    int r, c;
-    if constexpr (D == 128) {
-      r = i * kRowsPer + (t >> 4) * 2 + ((t >> 2) & 1);
-      c = (t & 3) + 4 * (((t >> 2) ^ (t >> 3)) & 1);
-    } else {
-      r = i * kRowsPer + (t >> 2);
-      c = t & 3;
-    }
-    uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w}, h[8];
-    if (kKind == kTreeE4m3 && odd) {
-#pragma unroll
-      for (int z = 0; z < 4; ++z) w[z] = e4m3_numbers(w[z]);
-    }
-#pragma unroll
-    for (int z = 0; z < 4; ++z) q8_halves<kKind, false>(w[z], h[2 * z], h[2 * z + 1]);
-    uint8_t* at = tile + (r >> 3) * kGroup + (c >> 2) * 1024 + (r & 7) * 128;
-    const int x = (c & 3) * 2;
-    *reinterpret_cast<uint4*>(at + ((x ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(at + (((x + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+// A tile of 128 keys' codes (rows of D bytes) as an operand, by 128 threads: thread t's row and 16-byte chunk of round i.
+// Eight lanes of an access take four chunks of a row and the other four (D = 64: the same) of its neighbour, so that reads
+// and writes touch every bank once.  The rows of a round lie in one block (D = 64: a warp's).
+template <int D>
+__device__ __forceinline__ void tc_chunk(int i, int t, int& r, int& c) {
+  if constexpr (D == 128) {
+    r = i * 16 + (t >> 4) * 2 + ((t >> 2) & 1);
+    c = (t & 3) + 4 * (((t >> 2) ^ (t >> 3)) & 1);
+  } else {
+    r = i * 32 + (t >> 2);
+    c = t & 3;
   }
 }
 
@@ -236,8 +189,7 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
   constexpr bool kQ8 = kKind != kTreeF16;
   using SM = TcSmem<D, kQ8>;
   constexpr int kS = SM::kSlots, kOps = SM::kOps, kR = kWide ? 2 * kTR : kTR;
-  constexpr int kC = kQ8 ? 16 : 32;  // columns of S that a softmax thread works on at a time
-  constexpr int kSoftmaxRegs = kWide ? 152 : 168;  // 256 threads with these, 256 with the rest of 256: 65,536, as launched
+  constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;  // of 8 bits: 256 threads each, in all the 512 x 128 of the launch
   extern __shared__ __align__(1024) uint8_t dsm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(dsm + SM::kBar);
   // ready, used: of the operands that the MMAs take (an f16 cache's copies are these)
@@ -259,7 +211,7 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
     for (int i = 0; i < 2; ++i) {
       mbar_init(&qfull[i], kWide ? 128 : 320);
       mbar_init(&qempty[i], 256);
-      mbar_init(&sfull[i], 1);
+      mbar_init(&sfull[i], kQ8 ? 2 : 1);
       mbar_init(&pfull[i], 128);
       mbar_init(&phalf[i], 128);
       mbar_init(&ofull[i], 1);
@@ -287,22 +239,17 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
 #endif
     return blk;
   };
-  // softmax of 8 bits: a lane's block of the group's four tiles from t on (narrow: every other tile)
-  auto entry4 = [&](int t, int t1) {
-    const int x = t + (lane >> 3) * (kWide ? 1 : 2);
-    return entry(x, t1);
-  };
+  // a lane's block of the four tiles from t on
+  auto entry4 = [&](int t, int t1) { return entry(t + (lane >> 3), t1); };
   int nxt = 0;
   if (ok_shape && cut.count > 0) {
     const int t1 = min(u.tiles, tile + cut.count);
     if (warp == 8) nxt = entry(tile, t1);
-    else if (kQ8 && warp < 8) nxt = entry4(tile + (kWide ? 0 : warp >> 2), t1);  // tile k of the CTA is group k & 1's
+    else if (kQ8 && warp >= 12) nxt = entry4(tile, t1);
   }
   __syncthreads();
-  pdl_wait_prev();
-  pdl_launch_next();
-  if (!ok_shape) return;
-  if (warp == 9) {
+  // the tensor memory, too, before the wait
+  if (warp == 9 && ok_shape) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(flags + 1)), "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -310,10 +257,13 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait_prev();
+  pdl_launch_next();
+  if (!ok_shape) return;
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(flags + 1);
   volatile int* abort_flag = flags;
   // (the softmax warps raise theirs in their own branch: where branches meet the compiler counts on the fewest)
-  if (kQ8 && warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(256 - kSoftmaxRegs));
+  if (kQ8 && warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   const int gs = a.d.gs, G = 1 << gs;
   // a wide unit with at most 128 rows leaves the second group out
   auto both = [&](const TreeUnit& x) { return (x.nodes << gs) - x.row_tile * kR > kTR; };
@@ -383,6 +333,7 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
         }
         tc_commit(&sfull[b]);
         if (last) tc_commit(&used[slot]);
+        if constexpr (kQ8) mbar_arrive(&sfull[b]);  // the tile's scales, which this warp has acquired with the operand
       }
     };
     // weights (tile n of group b) times values of tile k (landed)
@@ -494,24 +445,81 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
     const int ct = threadIdx.x - 384;
     int li = 0;
     for (int left = cut.count; left > 0;) {
-      const int t0 = tile, t1 = min(u.tiles, tile + left);
+      const int t0 = tile, t1 = min(u.tiles, tile + left), blocks = (u.ctx + u.nodes + 15) >> 4;
+      if (left < cut.count) nxt = entry4(t0, t1);  // the first unit's are there
+      // exponents of K and V of a lane's block of four tiles (behind the last block: the least), minus their tile's largest,
+      // and that; the next tiles' are loaded before the last of these is worked on
+      int2 e, top;
+      auto exponents = [&](int t, int blk) {
+        const int x = t + (lane >> 3);
+        e = make_int2(kExpMin, kExpMin);
+        if (x < t1 && x * 8 + (lane & 7) < blocks) {
+          const float2 y = *reinterpret_cast<const float2*>(a.scales + q8_scale_at(a.d, a.layer, blk, u.head, 0));
+          e = make_int2(q8_exp(y.x), q8_exp(y.y));
+        }
+      };
+      exponents(t0, nxt);
       for (int t = t0; t < t1; ++t) {
+        const int turn = (t - t0) & 3;
+        if (turn == 0) {
+          nxt = entry4(t + 4, t1);
+          top = e;
+#pragma unroll
+          for (int d = 1; d < 8; d *= 2) {
+            top.x = max(top.x, __shfl_xor_sync(0xffffffffu, top.x, d));
+            top.y = max(top.y, __shfl_xor_sync(0xffffffffu, top.y, d));
+          }
+          e.x -= top.x;
+          e.y -= top.y;
+        }
+        // 2^(a - A) of f16, down to 2^-24 (below, 0)
+        auto half_two = [](int d) { return d >= -14 ? (uint32_t)(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u; };
+        const int2 here = top;
+        const uint32_t fk = half_two(e.x) * 0x10001u, fv = half_two(e.y) * 0x10001u;
+        const int2 tile_top = make_int2(__shfl_sync(0xffffffffu, here.x, turn * 8), __shfl_sync(0xffffffffu, here.y, turn * 8));
+        if (turn == 3) exponents(t + 1, nxt);
         const bool odd = t * kTK + kTK > u.ctx;  // rows of no token among them, perhaps
 #pragma unroll 1
         for (int is_v = 0; is_v < 2; ++is_v, ++li) {
           const int slot = li % kS, op = li % kOps;
-          uint4 raw[D / 16];
           bool ok = mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err);
           if (!__all_sync(0xffffffffu, ok)) goto converted;
-          tc_convert_load<D, kKind>(dsm + SM::kCodes + slot * SM::kCodeTile, ct, raw);
           ok = li < kOps || mbar_wait(&used[op], ((li / kOps) - 1) & 1, abort_flag, a.m.err);
           if (!__all_sync(0xffffffffu, ok)) goto converted;
-          tc_convert_store<D, kKind>(dsm + SM::kRing + op * SM::kTile, ct, raw, odd);
+          const uint32_t f = is_v ? fv : fk;
+          int r, c;
+          tc_chunk<D>(0, ct, r, c);
+          // a round's rows lie 16 (D = 64: 32) below the last one's: the same place in their group, two (four) groups on
+          const uint8_t* from = dsm + SM::kCodes + slot * SM::kCodeTile + r * D + c * 16;
+          uint8_t* to8 = dsm + SM::kRing + op * SM::kTile + (r >> 3) * SM::kGroup + (c >> 2) * 1024 + (r & 7) * 128;
+          const int x0 = ((c & 3) * 2 ^ (r & 7)) << 4, x1 = (((c & 3) * 2 + 1) ^ (r & 7)) << 4;
+          constexpr int kRows = D == 128 ? 16 : 32, kU = 4;
+#pragma unroll 1
+          for (int i = 0; i < D / 16; i += kU) {
+            uint4 raw[kU];
+#pragma unroll
+            for (int y = 0; y < kU; ++y) raw[y] = *reinterpret_cast<const uint4*>(from + (i + y) * kRows * D);
+#pragma unroll
+            for (int y = 0; y < kU; ++y) {
+              const uint32_t two = __shfl_sync(0xffffffffu, f, turn * 8 + (D == 128 ? i + y : (i + y) * 2 + (ct >> 6)));
+              uint32_t w[4] = {raw[y].x, raw[y].y, raw[y].z, raw[y].w}, h[8];
+              if (kKind == kTreeE4m3 && odd) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) w[z] = e4m3_numbers(w[z]);
+              }
+#pragma unroll
+              for (int z = 0; z < 4; ++z) q8_halves_times<kKind>(w[z], two, h[2 * z], h[2 * z + 1]);
+              uint8_t* at = to8 + (i + y) * (kRows / 8) * SM::kGroup;
+              *reinterpret_cast<uint4*>(at + x0) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(at + x1) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+          }
+          if (ct == 0 && !is_v) reinterpret_cast<float2*>(dsm + SM::kScales)[(li >> 1) % kScaleRing] = make_float2(q8_two(tile_top.x), (float)tile_top.y);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&ready[op]);
             mbar_arrive(&empty[slot]);
+            mbar_arrive(&ready[op]);
           }
         }
       }
@@ -595,33 +603,8 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
         }
       }
       bool first = true;
-      // 8 bits: the scales of four of the group's tiles, a lane's block each
-      const int ta = t0 + (kWide ? 0 : (k ^ b) & 1);  // the group's first tile of the unit
-      float2 sc = make_float2(0.f, 0.f);
-      int turn = 0;
-      auto scales_of = [&](int t, int blk) {
-        float2 y = make_float2(1.f, 1.f);
-        const int x = t + (lane >> 3) * (kWide ? 1 : 2);
-        if (x < t1 && x * 8 + (lane & 7) < (end + 15) >> 4) y = *reinterpret_cast<const float2*>(a.scales + q8_scale_at(a.d, a.layer, blk, u.head, 0));
-        return make_float2(q8_two(q8_exp(y.x)), (float)q8_exp(y.y));
-      };
-      if constexpr (kQ8) {
-        if (left < cut.count) nxt = entry4(ta, t1);
-        sc = scales_of(ta, nxt);
-        nxt = entry4(ta + (kWide ? 4 : 8), t1);
-      }
       for (int t = t0; t < t1; ++t, ++k) {
         if (!in || (!kWide && (k & 1) != b)) continue;
-        const float2* blocks = reinterpret_cast<const float2*>(dsm + SM::kScales + warp * 128 + (turn & 1) * 64);
-        if constexpr (kQ8) {
-          if (lane >> 3 == turn) *reinterpret_cast<float2*>(dsm + SM::kScales + warp * 128 + (turn & 1) * 64 + (lane & 7) * 8) = sc;
-          if (turn == 3) {  // the last of these four: the next ones' scales are on their way while it is worked on
-            sc = scales_of(t + (kWide ? 1 : 2), nxt);
-            nxt = entry4(t + (kWide ? 5 : 10), t1);
-          }
-          turn = (turn + 1) & 3;
-          __syncwarp();
-        }
         const int key0 = t * kTK;
         const bool drafted = key0 + kTK > u.ctx;
         uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};  // keys of each 32 that this row sees
@@ -636,7 +619,7 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
           }
           // value rows past the end hold anything, a node's value that is not finite must not meet another branch's
           // zero weights: zero them; its descendants get it back at the unit's end.  Eight threads per row.  (Wide: both
-          // groups do this for the tile, whichever comes first changes it)
+          // groups do this for the tile, whichever comes first changes it.  8 bits: operands are always finite)
           if constexpr (!kQ8) {
           const int li = 2 * k + 1, slot = li % kS;
           alive = __all_sync(0xffffffffu, alive && mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err));
@@ -664,6 +647,12 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
         ++n;
         if (alive && mine) {
           tc_fence_after();
+          float f = c, e = 0.f;  // this tile's score factor (8 bits: kept off 0 and infinity, hidden scores are -inf) and exponent
+          if constexpr (kQ8) {
+            const float2 z = reinterpret_cast<const float2*>(dsm + SM::kScales)[k % kScaleRing];
+            f = fminf(fmaxf(c * z.x, 1.17549435e-38f), 3.40282347e38f);
+            e = z.y;
+          }
           if (drafted) {  // rare: hide in place what the rows do not see
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
@@ -679,135 +668,99 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
             }
             tc_wait_st();
           }
-          // two passes over S, 32 columns (8 bits: 16, a block) at a time, the next ones on their way while these are worked
-          // on (the loops stay loops: unrolled, the tile's code ran out of the instruction cache at every turn)
-          uint32_t sa[kC], sb[kC];
+          // two passes over S, 32 columns at a time, the next ones on their way while these are worked on (the loops stay
+          // loops: unrolled, the tile's code ran out of the instruction cache at every turn)
+          uint32_t sa[32], sb[32];
           float mx = -INFINITY;
-          // 8 bits: block j's score factor for this row, kept off 0 and infinity (hidden scores are -inf), and the exponent of
-          // its values
-          auto factors = [&](int j) {
-            float2 z = blocks[j];
-            z.x = fminf(fmaxf(z.x * c, 1.17549435e-38f), 3.40282347e38f);
-            return z;
-          };
-          auto largest = [&](const uint32_t (&x)[kC], int j) {
+          auto largest = [&](const uint32_t (&x)[32]) {
             float y[2] = {mx, mx};
-            if constexpr (kQ8) y[0] = y[1] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kC; i += 4) {
+            for (int i = 0; i < 32; i += 4) {
               y[0] = fmaxf(fmaxf(y[0], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
               y[1] = fmaxf(fmaxf(y[1], __uint_as_float(x[i + 2])), __uint_as_float(x[i + 3]));
             }
-            if constexpr (kQ8) {
-              const float2 z = factors(j);
-              mx = fmaxf(mx, __fadd_rn(__fmul_rn(fmaxf(y[0], y[1]), z.x), z.y));
-            } else {
-              mx = fmaxf(y[0], y[1]);
-            }
+            mx = fmaxf(y[0], y[1]);
           };
-          tc_ld_async(ts, sa);
+          tc_ld32_async(ts, sa);
 #pragma unroll 1
-          for (int j = 0; j < kTK / kC; j += 2) {
-            tc_wait(sa);
-            tc_ld_async(ts + (j + 1) * kC, sb);
-            largest(sa, j);
-            tc_wait(sb);
-            tc_ld_async(ts + (((j + 2) * kC) & 127), sa);  // at the end the first columns again, for the weights
-            largest(sb, j + 1);
+          for (int j = 0; j < 4; j += 2) {
+            tc_wait32(sa);
+            tc_ld32_async(ts + j * 32 + 32, sb);
+            largest(sa);
+            tc_wait32(sb);
+            tc_ld32_async(ts + ((j * 32 + 64) & 127), sa);  // at the end the first columns again, for the weights
+            largest(sb);
           }
-          if constexpr (!kQ8) mx *= c;
+          mx = kQ8 ? __fadd_rn(__fmul_rn(mx, f), e) : mx * f;
           if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-            const float mn = fmaxf(m, mx), f = mn == m ? 1.f : ex2(m - mn);
+            const float mn = fmaxf(m, mx), g = mn == m ? 1.f : ex2(m - mn);
             m = mn;
-            l *= f;
+            l *= g;
             if (!first) {  // this group's products so far have run: its S was issued behind them
-              tc_wait(sa);
+              tc_wait32(sa);
 #pragma unroll 1
               for (int j = 0; j < D / 32; ++j) {
                 uint32_t o[32];
                 tc_ld32(to + j * 32, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * g);
                 tc_st16(to + j * 32, o);
                 tc_st16(to + j * 32 + 16, o + 16);
               }
             }
           }
           const float mu = m == -INFINITY ? 0.f : m;
-          uint64_t c2 = pack2(c, c), m2 = pack2(-mu, -mu), l2[2] = {0ull, 0ull};
+          uint64_t c2 = pack2(f, f), m2 = pack2(e - mu, e - mu), l2[2] = {0ull, 0ull};
           // s c - m in one rounding while the maximum's own (2^-13 up to 2^12) is small against the weights' (2^-11); far out
           // the product is rounded as the maximum was, or the largest score would miss it by its own last place
-          const bool far = __any_sync(0xffffffffu, !(fabsf(mu) <= 4096.f));
-          if (far) {
-            tc_wait(sa);
+          if (__any_sync(0xffffffffu, !(fabsf(mu) <= 4096.f))) {
+            tc_wait32(sa);
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
               uint32_t s[32];
               tc_ld32(ts + j * 32, s);
-              if constexpr (kQ8) {
-                const float2 y = factors(2 * j), z = factors(2 * j + 1);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  s[i] = __float_as_uint(__fadd_rn(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), i < 16 ? y.x : z.x), i < 16 ? y.y : z.y), -mu));
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), c), -mu));
+              for (int i = 0; i < 32; ++i) {
+                const float y = __fmul_rn(__uint_as_float(s[i]), f);
+                s[i] = __float_as_uint(__fadd_rn(kQ8 ? __fadd_rn(y, e) : y, -mu));
               }
               tc_st16(ts + j * 32, s);
               tc_st16(ts + j * 32 + 16, s + 16);
             }
             tc_wait_st();
-            tc_ld_async(ts, sa);
+            tc_ld32_async(ts, sa);
             c2 = pack2(1.f, 1.f);
             m2 = 0ull;
           }
-          auto weights = [&](const uint32_t (&x)[kC], int j) {
-            uint32_t p[kC / 2];
-            float e = 0.f;
-            if constexpr (kQ8) {
-              const float2 z = factors(j);
-              e = z.y;
-              if (!far) {
-                c2 = pack2(z.x, z.x);
-                m2 = pack2(e - mu, e - mu);
-              }
-              l2[0] = l2[1] = 0ull;
-            }
+          auto weights = [&](const uint32_t (&x)[32], int j) {
+            uint32_t p[16];
 #pragma unroll
-            for (int i = 0; i < kC / 2; ++i) {
+            for (int i = 0; i < 16; ++i) {
               const float2 z = unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, m2));
               const float ex = ex2(z.x), ey = ex2(z.y);
               l2[i & 1] = add2(l2[i & 1], pack2(ex, ey));
               const __half2 hh = __floats2half2_rn(ex, ey);
               p[i] = *reinterpret_cast<const uint32_t*>(&hh);
             }
-            // over scores that this thread has read
-            if constexpr (kQ8) {
-              tc_st8(ts + j * 8, p);
-              const float2 y = unpack2(add2(l2[0], l2[1]));
-              l = fmaf(y.x + y.y, __uint_as_float(__float_as_uint(8388735.f - e) << 23), l);  // times 2^-e
-            } else {
-              tc_st16(ts + j * 16, p);
-            }
+            tc_st16(ts + j * 16, p);  // over scores that this thread has read
           };
 #pragma unroll 1
-          for (int j = 0; j < kTK / kC; j += 2) {
-            tc_wait(sa);
-            tc_ld_async(ts + (j + 1) * kC, sb);
+          for (int j = 0; j < 4; j += 2) {
+            tc_wait32(sa);
+            tc_ld32_async(ts + j * 32 + 32, sb);
             weights(sa, j);
-            tc_wait(sb);
-            if (j + 2 < kTK / kC) tc_ld_async(ts + (j + 2) * kC, sa);
+            tc_wait32(sb);
+            if (j == 0) tc_ld32_async(ts + 64, sa);
             weights(sb, j + 1);
-            if (!kWide && (j + 2) * kC == 64) {
+            if (!kWide && j == 0) {
               tc_wait_st();
               tc_fence_before();
               mbar_arrive(&phalf[b]);
             }
           }
-          if constexpr (!kQ8) {
-            const float2 lx = unpack2(add2(l2[0], l2[1]));
-            l += lx.x + lx.y;
-          }
+          const float2 lx = unpack2(add2(l2[0], l2[1]));
+          // the weights carry the values' 2^e: take it out (2^-e, whose exponent field is 127 - e)
+          l = kQ8 ? fmaf(lx.x + lx.y, __uint_as_float(__float_as_uint(8388735.f - e) << 23), l) : l + (lx.x + lx.y);
           tc_wait_st();
           tc_fence_before();
         } else if constexpr (!kWide) {

@@ -29,9 +29,10 @@ struct Q8 {
 };
 
 __device__ __forceinline__ float q8_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-// e of a stored scale (of memory that no call has written: some e of the range).
+// e of a stored scale; the least one for memory that holds none.
 __device__ __forceinline__ int q8_exp(float scale) {
-  return min(max((int)((__float_as_uint(scale) >> 23) & 255u) - 127, kExpMin), kExpMax);
+  const int e = (int)(__float_as_uint(scale) >> 23) - 127;
+  return e < kExpMin || e > kExpMax ? kExpMin : e;
 }
 // need(amax), amax finite: 127 = (2 - 2^-6) 2^6, 448 = 1.75 2^8.
 template <int kKind>
@@ -90,6 +91,26 @@ __device__ __forceinline__ void q8_halves(uint32_t w, uint32_t& x, uint32_t& y) 
         : "=r"(x), "=r"(y)
         : "r"(u));
   }
+}
+
+// Bytes (0, 1) and (2, 3) as f16 times a power of two (in both halves of `two`), rounded once where that is subnormal.
+template <int kKind>
+__device__ __forceinline__ void q8_halves_times(uint32_t w, uint32_t two, uint32_t& x, uint32_t& y) {
+  const __half2 f = *reinterpret_cast<const __half2*>(&two);
+  __half2 h, g;
+  if constexpr (Q8<kKind>::kInt) {  // (1024 + 128 + c) f - 1152 f
+    const uint32_t u = w ^ 0x80808080u, bias = 0xE480E480u;  // -1152
+    const uint32_t p = __byte_perm(u, 0x64u, 0x4140), q = __byte_perm(u, 0x64u, 0x4342);
+    const __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&bias), f);
+    h = __hfma2(*reinterpret_cast<const __half2*>(&p), f, b);
+    g = __hfma2(*reinterpret_cast<const __half2*>(&q), f, b);
+  } else {
+    q8_halves<kKind, false>(w, x, y);
+    h = __hmul2(*reinterpret_cast<const __half2*>(&x), f);
+    g = __hmul2(*reinterpret_cast<const __half2*>(&y), f);
+  }
+  x = *reinterpret_cast<const uint32_t*>(&h);
+  y = *reinterpret_cast<const uint32_t*>(&g);
 }
 
 // Codes that are no numbers (memory that no call has written) as 0.
