@@ -142,11 +142,12 @@ class DraftTrees:
                                              C.byref(h)), "dec_tree_create")
         self.handle = h
         self.n_tokens = self.n_seqs = 0
-        self._rows_of = (0, 0)
         self._streams = set()  # that calls were made on
         self._heads, self._kv_heads, self._dim = self.cfg.n_heads, self.cfg.n_kv_heads, self.cfg.head_dim
+        self._kv_width = self._kv_heads * self._dim
+        self._read_of = ((0, 0, (0, self._kv_heads, self._dim)),) * 2  # by part: rows, elements of a layer, shape
         # a step makes these calls for every layer: the lookups are done once
-        self._append, self._attend, self._commit = self.L.dec_tree_append, self.L.dec_tree_attend, self.L.dec_tree_commit
+        self._append, self._attend, self._commit, self._read = self.L.dec_tree_append, self.L.dec_tree_attend, self.L.dec_tree_commit, self.L.dec_tree_read
         self._qkv = dec.dec_tree_qkv()
         self._out_type = torch.float32 if self.cfg.mode == dec.DEC_FP32 else torch.bfloat16
 
@@ -183,7 +184,8 @@ class DraftTrees:
         b, keep = tree_batch(ctx, parents, tables)
         dec.check(self.L.dec_tree_set(self.handle, C.byref(b), self._stream(stream)), "dec_tree_set")
         self.n_seqs, self.n_tokens = b.n_seqs, b.n_tokens
-        self._rows_of = tuple(self._read_rows(part) for part in (dec.DEC_READ_ALL, dec.DEC_READ_PAGES))
+        rows = (self._read_rows(part) for part in (dec.DEC_READ_ALL, dec.DEC_READ_PAGES))
+        self._read_of = tuple((n, n * self._kv_width, (n, self._kv_heads, self._dim)) for n in rows)
 
     def _read_rows(self, part):
         n = C.c_int64()
@@ -288,21 +290,30 @@ class DraftTrees:
         `layer` on.  Rows: the sequences' slots one after the other, all of them or
         (DEC_READ_PAGES) from the block on that holds the sequence's first node.
         out: two such tensors, contiguous, or None in the place of one that is not wanted."""
-        rows = self._rows_of[part] if part in (0, 1) else 0  # an unknown part is the library's to refuse
-        shape = (rows, self._kv_heads, self._dim) if layers is None else (layers, rows, self._kv_heads, self._dim)
-        if out is None:
-            if layers is not None and layers < 1:
+        # an unknown part is the library's to refuse
+        rows, span, shape = self._read_of[part] if part in (0, 1) else (0, 0, (0, self._kv_heads, self._dim))
+        n = 1
+        if layers is not None:
+            if layers < 1:
                 raise ValueError("layers: at least one")
-            out = self._new(shape, out_type, stream), self._new(shape, out_type, stream)
-        given = [x for x in out if x is not None]
-        for x in given:
-            if x.shape != shape or x.dtype is not given[0].dtype or x.dtype not in _TYPES or not x.is_contiguous() or x.get_device() != self._index:
-                raise ValueError(f"out: need contiguous {shape} tensors of one type, f32, f16 or bf16, on cuda:{self._index}")
-        if stream is not None:
-            _used_on(stream, *out)
-        width = self._kv_heads * self._dim
-        code = self.L.dec_tree_read(self.handle, layer, 1 if layers is None else layers, part, rows, _TYPES[given[0].dtype] if given else 0,
-                                    *(None if x is None else x.data_ptr() for x in out), width, rows * width, self._stream(stream))
+            n, shape = layers, (layers, *shape)
+        if out is None:
+            kind, raw = _TYPES[out_type], self._stream(stream)
+            if stream is None:  # last, as in append
+                out = _empty(shape, dtype=out_type, device=self.device), _empty(shape, dtype=out_type, device=self.device)
+            else:
+                out = self._new(shape, out_type, stream), self._new(shape, out_type, stream)
+                _used_on(stream, *out)
+            code = self._read(self.handle, layer, n, part, rows, kind, out[0].data_ptr(), out[1].data_ptr(), self._kv_width, span, raw)
+        else:
+            given = [x for x in out if x is not None]
+            for x in given:
+                if x.shape != shape or x.dtype is not given[0].dtype or x.dtype not in _TYPES or not x.is_contiguous() or x.get_device() != self._index:
+                    raise ValueError(f"out: need contiguous {shape} tensors of one type, f32, f16 or bf16, on cuda:{self._index}")
+            if stream is not None:
+                _used_on(stream, *out)
+            code = self._read(self.handle, layer, n, part, rows, _TYPES[given[0].dtype] if given else 0,
+                              *(None if x is None else x.data_ptr() for x in out), self._kv_width, span, self._stream(stream))
         if code:
             dec.check(code, "dec_tree_read")
         return out
