@@ -194,6 +194,27 @@ def test_memory_that_no_call_has_written_changes_nothing(shape, nodes, kind):
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("shape, nodes", [("16:8x128", 3), ("16:8x128", 40), ("16:8x128", 200), ("8:4x64", 40), ("8:2x128", 2), ("4:2x32", 20)])
+@pytest.mark.parametrize("spread", [4.0, 40.0, 1000.0])
+def test_scores_far_apart(spread, shape, nodes, kind):
+    """Scores that rise along the keys by tens to tens of thousands: a row's reference is raised again and again, within the
+    tiles, too, and one key takes nearly all the weight."""
+    ctx, parents = [700, 129], [random_tree(nodes, 1), nodes]
+    w = Setup8(shape, kind, ctx, parents, seed=11)
+    # the keys' first channel grows with the position, up or down by head; queries are large there
+    for s in range(2):
+        for slot in range(0, w.ctx[s] + len(w.parents[s])):
+            b, r = w.where(s, slot)
+            ramp = (slot % 128) / 128 if slot % 3 else 0.5
+            codes = codes_of(torch.full((w.Hkv,), ramp * 100, dtype=torch.float64), torch.zeros(w.Hkv, dtype=torch.float64), kind)
+            w.codes[0, b, 0, :, r, 0] = torch.where(torch.arange(w.Hkv) % 2 == 0, codes, codes_of(torch.full((w.Hkv,), 100 - ramp * 100, dtype=torch.float64), torch.zeros(w.Hkv, dtype=torch.float64), kind)).cuda()
+    q = w.rand(w.N, w.H, w.D)
+    q[..., 0] = spread * (1 + torch.rand(q[..., 0].shape, generator=w.g).cuda())
+    check(w, w.trees.attend(0, q), 0, q, set(range(0, w.N, max(w.N // 20, 1))))
+    w.close()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("scale", [1e30, 1e-30, 70000.0, 0.0])
 def test_queries_of_any_magnitude(scale, kind):
     for nodes in (3, 60):
