@@ -46,7 +46,7 @@ struct Q8Smem {
   static constexpr int kSlab = 16 * D;                         // K (or V) of one block
   static constexpr int kStage = 4 * 2 * kSlab;
   static constexpr int kCtas = D == 128 && R == 16 ? 2 : 3;    // per SM: with 16 rows of 128 channels a lane needs 160 registers
-  static constexpr int kStages = D == 128 ? (kCtas == 2 ? 6 : 4) : D == 64 ? 8 : 16;
+  static constexpr int kStages = D == 128 ? 4 : D == 64 ? 8 : 16;  // (two CTAs of 16 rows with six: 32 x 8 over 1500 36.0 us, with four 32.3)
   static constexpr int kQPitch = D * 2 + 16;                   // bytes; rows fall into different banks
   static constexpr int kQ = kStages * kStage;                  // the queries, at a unit's end the warps' outputs
   static constexpr int kRedPitch = 40;                         // floats of a row's 32 channels: rows fall into different banks
@@ -403,7 +403,7 @@ template <int D, int R, int kKind>
 cudaError_t one(const TreeAttendArgs& a, const CUtensorMap* tm, int ctas, cudaStream_t s) {
   static SmemOptIn opt;
   constexpr int smem = Q8Smem<D, R>::kBytes;
-  static_assert(smem <= (Q8Smem<D, R>::kCtas == 2 ? 113 : 76) * 1024, "CTAs per SM");
+  static_assert(smem <= 76 * 1024, "three CTAs per SM");
   cudaError_t e = opt.ensure(k_tree_attend_q8<D, R, kKind>, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_tree_attend_q8<D, R, kKind>, ctas, kQ8Threads, smem, s, *tm, a);

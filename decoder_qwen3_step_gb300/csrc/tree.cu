@@ -56,7 +56,9 @@ TreeVariant variant_for(int kv_type, int D, int max_rows) {
   const int unit = kv_type == kTreeF16 ? 4 : 2;
   if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, unit, 50};
   if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, unit, 25};
-  if (kv_type != kTreeF16) return {kTreeMmaQ8, max_rows <= 8 ? 8 : 16, 64, D == 128 && max_rows > 8 ? 2 : 3, 2, 0};
+  // Three CTAs per SM fill the GPU while the kernel before still drains: with 456 the last one or two found no place until
+  // others had ended, 12 us later (32 x 1 over 1024-2048: 27.0 us, with 448 23.1; over 6000: 83, 66.6)
+  if (kv_type != kTreeF16) return max_rows > 8 && D == 128 ? TreeVariant{kTreeMmaQ8, 16, 64, 2, 2, 0, 0} : TreeVariant{kTreeMmaQ8, max_rows > 8 ? 16 : 8, 64, 3, 2, 0, 8};
   return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2, 0};
 }
 // The rows of a sequence walk the keys side by side in the wide kernel alone, a CTA for each of its row tiles.
@@ -362,7 +364,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   for (int s = 0; s < S; ++s) max_nodes = std::max(max_nodes, b->seq_start[s + 1] - b->seq_start[s]);
   const int W = std::max((max_nodes + 31) / 32, 1);
   const TreeVariant var = variant_for(t->kv_type, c.head_dim, max_nodes * G);
-  const int grid = t->sms * var.ctas_per_sm;
+  const int grid = t->sms * var.ctas_per_sm - var.spare;
   const size_t h_hdr = take(kHdrInts), h_flags = take((size_t)t->sms * kTreeMaxCtasPerSm), h_start = take(S + 1), h_seqs = take((size_t)S * 4), h_pos = take(N), h_dst = take(N),
                h_par = take(N), h_anc = take((size_t)N * W), h_cut = take((size_t)grid * 12), h_mrg = take((size_t)grid * 8),
                h_reads = take((size_t)(S + 1) * 8), h_pages = take(t->q8 ? (size_t)N * 4 : 0), h_tables = o;
