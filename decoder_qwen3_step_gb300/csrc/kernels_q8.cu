@@ -20,13 +20,22 @@ namespace {
 // a warp.
 // HBM bounds the large calls, instructions not far behind (32 x 256 nodes: 82 us
 // with the rows in registers, every loop unrolled to 16 rows and 147 instructions
-// a row), so the loops go four steps of rows at a time, the next ones' loads in
-// flight: their sums of squares are reduced together (6 shuffles for 4 rows of 128
-// channels; the lanes end up with one row's each, so one root and quotient serve
-// four rows), and what is rare is looked for once a page (padding, values that are
-// not finite, e at its end).
+// a row), so a task's rows are copied to shared memory all at once (with four
+// steps of them in flight 56 us), and the loops go four steps at a time: their
+// sums of squares are reduced together (6 shuffles for 4 rows of 128 channels; the
+// lanes end up with one row's each, so one root and quotient serve four rows), and
+// what is rare is looked for once a page (padding, values that are not finite, e
+// at its end).
 // Cached tokens of a page are read and written only where its e rises.
 constexpr int kAppendSide = 4;  // steps of rows at a time
+
+// 8 or 16 bytes global -> shared, waited for by the thread that asked.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+  if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(src), "n"(kBytes) : "memory");
+}
 
 // Codes of four values times inv = 2^-e where the largest magnitude is known to fit.
 template <int kKind>
@@ -71,12 +80,11 @@ __global__ void __launch_bounds__(128, 5) k_append_q8(const __grid_constant__ Tr
     }
     const int64_t stride = is_q ? D : is_v ? a.ldv : a.ldk;  // between the task's rows
     const T* src = reinterpret_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) + node * (is_q ? a.ldq : stride) + h * D + el;
-    float4 next[kSide];
-    auto fetch = [&](int s0) {  // rows behind the last are the last again
-#pragma unroll
-      for (int j = 0; j < kSide; ++j) next[j] = tree_load4(src + min((s0 + j) * kRows + sub, n - 1) * stride);
-    };
-    fetch(0);
+    // every row of the task on its way to where its lane formed values go (four channels of a lane, no other lane's); rows
+    // behind the last are the last again
+#pragma unroll 4
+    for (int s = 0; s * kRows < (n + kSide * kRows - 1) / (kSide * kRows) * (kSide * kRows); ++s)
+      copy_async<4 * sizeof(T)>(rows + (s * kRows + sub) * kLanes, src + min(s * kRows + sub, n - 1) * stride);
     int pos_of = __ldg(a.m.pos + node + (is_q ? 0 : min(lane & 15, n - 1)));  // row lane & 15's position
     if (a.rope && pos_of >= a.rope_positions) {  // a replay whose plan outgrew the table of its capture
       atomicOr(a.m.err, kErrBounds);
@@ -112,16 +120,16 @@ __global__ void __launch_bounds__(128, 5) k_append_q8(const __grid_constant__ Tr
     const int out_row = D * (a.q_type == kTreeF32 ? 4 : 2);
     if (is_q) out = reinterpret_cast<char*>(a.q_out) + (node * a.ldo + (h + sub) * D + el) * (a.q_type == kTreeF32 ? 4 : 2);
     float amax = 0.f, bad = 0.f;  // bad: NaN once a value is not finite
+    asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
     for (int s0 = 0; s0 * kRows < n; s0 += kSide) {
       float4 x[kSide];
 #pragma unroll
-      for (int j = 0; j < kSide; ++j) x[j] = next[j];
+      for (int j = 0; j < kSide; ++j) x[j] = tree_load4(reinterpret_cast<const T*>(rows + ((s0 + j) * kRows + sub) * kLanes));
       if (rope && !is_q) {
 #pragma unroll
         for (int j = 0; j < kSide; ++j) angles(pos_at((s0 + j) * kRows + sub), c0[j], c1[j]);
       }
-      if ((s0 + kSide) * kRows < n) fetch(s0 + kSide);
       if (gain) {
         float ss[kSide];
 #pragma unroll
