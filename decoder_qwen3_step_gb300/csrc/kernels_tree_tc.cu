@@ -31,14 +31,20 @@
 // 8-bit caches: the producer brings codes (a page is contiguous: one bulk copy)
 // into a ring of their own, and
 //   warps 12..15  turn them into f16 operand tiles of the layout above.
-// A tile of 128 keys takes 2^A, the largest K scale of its eight blocks, out of
-// its keys, and 2^B of V's out of its values: an operand is code * 2^(a - A), one
-// fused multiply-add on the way from i8 to f16 (exact down to 2^-24: a page may
-// be 2^24 smaller than its neighbours before its codes lose bits, and then by
-// less than 2^-25 of the neighbours' step).  So the softmax has one factor c 2^A
+// A tile of 128 keys takes 2^A out of its keys, A near the largest K exponent of
+// its eight blocks, and 2^B of V's out of its values: an operand is code * 2^(a -
+// A), one fused multiply-add on the way from i8 to f16, exact down to 2^-24.  The
+// largest page keeps a factor of 2^5 (i8; e4m3: 2^7, f16's range allows that
+// much), so a page's scale may be 2^29 below its neighbours' before its codes lose
+// bits.  So the softmax has one factor c 2^A
 // and one exponent B a tile: weights are 2^(s + B - m), l adds 2^-B times their
 // sum (the reference m as in kernels_tree_q8.cu).  With a factor for each block
 // in the softmax it took 1.3 us a tile in place of 0.85.
+// The reference may then pass a row's true one, the largest s + b, by as much as
+// the V exponents of a tile differ (a page of large values whose weights are all
+// small).  Up to 2^8 that costs f16's weights nothing that counts; a tile whose
+// pages lie further apart takes its V codes as they are and each block's own b
+// into the scores, as kernels_tree_q8.cu does for all.
 // Registers are moved from the other warps to the softmax (512 threads have 128
 // each).
 #include "attn_fold.cuh"
@@ -51,7 +57,12 @@ namespace {
 
 constexpr int kTR = 128, kTK = 128;  // rows and keys of a step
 constexpr int kTcTreeThreads = 384, kTcTreeThreadsQ8 = 512;
-constexpr int kScaleRing = 8;  // tiles whose (2^A, B) are kept: the conversion is at most two ahead of the softmax
+// A tile's 2^A, B (infinite: pages far apart) and the b of its blocks; of how many tiles they are kept (the conversion is at
+// most four ahead of the softmax)
+struct TileScales {
+  float a, b, each[8];
+};
+constexpr int kScaleRing = 8, kApart = 8;
 constexpr int kOps8 = 3, kSlots8 = 4;  // of 128 channels
 constexpr uint32_t kTmemCols = 512;  // S of the two groups: columns 0, 128; O: 256, 256 + D
 
@@ -67,8 +78,8 @@ struct TcSmem {
   static constexpr int kQ = 0;                        // two tiles: the units' in turn (narrow), the groups' (wide)
   static constexpr int kRing = 2 * kTile, kCodes = kRing + kOps * kTile, kCodeTile = kTK * D;
   static constexpr int kFac = kCodes + (kQ8 ? kSlots * kCodeTile : 0);  // float [2][kTR], as the queries
-  static constexpr int kScales = kFac + 2 * kTR * 4;                    // float2 [kScaleRing]
-  static constexpr int kBar = kScales + (kQ8 ? kScaleRing * 8 : 0);
+  static constexpr int kScales = kFac + 2 * kTR * 4;                    // TileScales [kScaleRing]
+  static constexpr int kBar = kScales + (kQ8 ? kScaleRing * (int)sizeof(TileScales) : 0);
   // barriers: full, empty [slots]; ready, used [operands] of 8 bits; Q full, Q empty, S full, P full, O full, O empty [2]; MMA done
   static constexpr int kBars = 2 * kSlots + (kQ8 ? 2 * kOps : 0) + 15;
   static constexpr int kBytes = kBar + kBars * 8 + 32;
@@ -136,6 +147,16 @@ __device__ __forceinline__ void tc_wait32(uint32_t (&v)[32]) {
                  "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
                :
                : "memory");
+}
+// 16 columns, there when it returns.
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -442,41 +463,53 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
     __syncwarp();
   } else if (kQ8 && warp >= 12) {
     // ---- codes to operands ----
+    constexpr int kLift = kKind == kTreeI8 ? 5 : 7;  // 1152 2^5 and 448 2^7 are still f16
     const int ct = threadIdx.x - 384;
     int li = 0;
     for (int left = cut.count; left > 0;) {
       const int t0 = tile, t1 = min(u.tiles, tile + left), blocks = (u.ctx + u.nodes + 15) >> 4;
       if (left < cut.count) nxt = entry4(t0, t1);  // the first unit's are there
-      // exponents of K and V of a lane's block of four tiles (behind the last block: the least), minus their tile's largest,
-      // and that; the next tiles' are loaded before the last of these is worked on
-      int2 e, top;
+      // exponents of K and V of a lane's block of four tiles, if it is one; the next tiles' are loaded before the last of these
+      // is worked on
+      int2 e;
+      bool block = false;
       auto exponents = [&](int t, int blk) {
         const int x = t + (lane >> 3);
         e = make_int2(kExpMin, kExpMin);
-        if (x < t1 && x * 8 + (lane & 7) < blocks) {
+        block = x < t1 && x * 8 + (lane & 7) < blocks;
+        if (block) {
           const float2 y = *reinterpret_cast<const float2*>(a.scales + q8_scale_at(a.d, a.layer, blk, u.head, 0));
           e = make_int2(q8_exp(y.x), q8_exp(y.y));
         }
       };
       exponents(t0, nxt);
+      uint32_t fk = 0, fv = 0;  // the factors of the lane's block, in both halves
+      TileScales scales;        // of its tile (each[0]: the block's b)
       for (int t = t0; t < t1; ++t) {
         const int turn = (t - t0) & 3;
         if (turn == 0) {
           nxt = entry4(t + 4, t1);
-          top = e;
+          int ka = e.x, va = e.y, low = block ? e.y : kExpMax;
 #pragma unroll
           for (int d = 1; d < 8; d *= 2) {
-            top.x = max(top.x, __shfl_xor_sync(0xffffffffu, top.x, d));
-            top.y = max(top.y, __shfl_xor_sync(0xffffffffu, top.y, d));
+            ka = max(ka, __shfl_xor_sync(0xffffffffu, ka, d));
+            va = max(va, __shfl_xor_sync(0xffffffffu, va, d));
+            low = min(low, __shfl_xor_sync(0xffffffffu, low, d));
           }
-          e.x -= top.x;
-          e.y -= top.y;
+          const bool apart = va - low > kApart;
+          scales.a = q8_two(ka - kLift);
+          scales.b = apart ? INFINITY : (float)(va - kLift);
+          scales.each[0] = (float)e.y;
+          // 2^d in f16, down to 2^-24 (below, 0)
+          auto half_two = [](int d) { return (d >= -14 ? (uint32_t)(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u) * 0x10001u; };
+          fk = half_two(e.x - ka + kLift);
+          fv = half_two(apart ? 0 : e.y - va + kLift);
         }
-        // 2^(a - A) of f16, down to 2^-24 (below, 0)
-        auto half_two = [](int d) { return d >= -14 ? (uint32_t)(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u; };
-        const int2 here = top;
-        const uint32_t fk = half_two(e.x) * 0x10001u, fv = half_two(e.y) * 0x10001u;
-        const int2 tile_top = make_int2(__shfl_sync(0xffffffffu, here.x, turn * 8), __shfl_sync(0xffffffffu, here.y, turn * 8));
+        if (warp == 12 && lane >> 3 == turn) {
+          TileScales& to = reinterpret_cast<TileScales*>(dsm + SM::kScales)[(li >> 1) % kScaleRing];
+          to.each[lane & 7] = scales.each[0];
+          if ((lane & 7) == 0) to.a = scales.a, to.b = scales.b;
+        }
         if (turn == 3) exponents(t + 1, nxt);
         const bool odd = t * kTK + kTK > u.ctx;  // rows of no token among them, perhaps
 #pragma unroll 1
@@ -514,7 +547,6 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
               *reinterpret_cast<uint4*>(at + x1) = make_uint4(h[4], h[5], h[6], h[7]);
             }
           }
-          if (ct == 0 && !is_v) reinterpret_cast<float2*>(dsm + SM::kScales)[(li >> 1) % kScaleRing] = make_float2(q8_two(tile_top.x), (float)tile_top.y);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
@@ -648,10 +680,12 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
         if (alive && mine) {
           tc_fence_after();
           float f = c, e = 0.f;  // this tile's score factor (8 bits: kept off 0 and infinity, hidden scores are -inf) and exponent
+          const TileScales* scales = reinterpret_cast<const TileScales*>(dsm + SM::kScales) + k % kScaleRing;
+          bool apart = false;
           if constexpr (kQ8) {
-            const float2 z = reinterpret_cast<const float2*>(dsm + SM::kScales)[k % kScaleRing];
-            f = fminf(fmaxf(c * z.x, 1.17549435e-38f), 3.40282347e38f);
-            e = z.y;
+            f = fminf(fmaxf(c * scales->a, 1.17549435e-38f), 3.40282347e38f);
+            e = scales->b;
+            apart = e == INFINITY;
           }
           if (drafted) {  // rare: hide in place what the rows do not see
 #pragma unroll 1
@@ -667,6 +701,20 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
               tc_st16(ts + j * 32 + 16, s + 16);
             }
             tc_wait_st();
+          }
+          if (kQ8 && apart) {  // rare: s f + b of each block in place of the scores
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+              const float eb = scales->each[j];
+              uint32_t s[16];
+              tc_ld16(ts + j * 16, s);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), f), eb));
+              tc_st16(ts + j * 16, s);
+            }
+            tc_wait_st();
+            f = 1.f;
+            e = 0.f;
           }
           // two passes over S, 32 columns at a time, the next ones on their way while these are worked on (the loops stay
           // loops: unrolled, the tile's code ran out of the instruction cache at every turn)
@@ -711,6 +759,20 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
           }
           const float mu = m == -INFINITY ? 0.f : m;
           uint64_t c2 = pack2(f, f), m2 = pack2(e - mu, e - mu), l2[2] = {0ull, 0ull};
+          if (kQ8 && apart) {  // the sum, block by block
+            tc_wait32(sa);
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+              const float eb = scales->each[j];
+              uint32_t s[16];
+              tc_ld16(ts + j * 16, s);
+              float sum = 0.f;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum += ex2(__uint_as_float(s[i]) - mu);
+              l = fmaf(sum, q8_two(-(int)eb), l);
+            }
+            tc_ld32_async(ts, sa);
+          }
           // s c - m in one rounding while the maximum's own (2^-13 up to 2^12) is small against the weights' (2^-11); far out
           // the product is rounded as the maximum was, or the largest score would miss it by its own last place
           if (__any_sync(0xffffffffu, !(fabsf(mu) <= 4096.f))) {
@@ -760,7 +822,8 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
           }
           const float2 lx = unpack2(add2(l2[0], l2[1]));
           // the weights carry the values' 2^e: take it out (2^-e, whose exponent field is 127 - e)
-          l = kQ8 ? fmaf(lx.x + lx.y, __uint_as_float(__float_as_uint(8388735.f - e) << 23), l) : l + (lx.x + lx.y);
+          if constexpr (!kQ8) l += lx.x + lx.y;
+          else if (!apart) l = fmaf(lx.x + lx.y, __uint_as_float(__float_as_uint(8388735.f - e) << 23), l);
           tc_wait_st();
           tc_fence_before();
         } else if constexpr (!kWide) {

@@ -364,7 +364,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   for (int s = 0; s < S; ++s) max_nodes = std::max(max_nodes, b->seq_start[s + 1] - b->seq_start[s]);
   const int W = std::max((max_nodes + 31) / 32, 1);
   const TreeVariant var = variant_for(t->kv_type, c.head_dim, max_nodes * G);
-  const int grid = t->sms * var.ctas_per_sm - var.spare;
+  const int grid = std::max(t->sms * var.ctas_per_sm - var.spare, t->sms);
   const size_t h_hdr = take(kHdrInts), h_flags = take((size_t)t->sms * kTreeMaxCtasPerSm), h_start = take(S + 1), h_seqs = take((size_t)S * 4), h_pos = take(N), h_dst = take(N),
                h_par = take(N), h_anc = take((size_t)N * W), h_cut = take((size_t)grid * 12), h_mrg = take((size_t)grid * 8),
                h_reads = take((size_t)(S + 1) * 8), h_pages = take(t->q8 ? (size_t)N * 4 : 0), h_tables = o;

@@ -334,6 +334,44 @@ def test_append_is_the_formula(shape, rot, layout, in_type, kind):
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("shape, nodes", [("16:8x128", 3), ("8:4x64", 40), ("4:2x32", 256), ("12:3x32", 20)])
+def test_queries_in_place_and_parts_alone(shape, nodes, kind):
+    w = Setup8(shape, kind, [37, 5], [nodes, max(nodes // 3, 1)], seed=3)
+    rope = RopeTable(w.D, 400)
+    q, k, v = w.rand(w.N, w.H, w.D), w.rand(w.N, w.Hkv, w.D), w.rand(w.N, w.Hkv, w.D)
+    g = 1 + 0.1 * w.rand(w.D)
+    start = w.buf.clone()
+    both = w.trees.append(0, q, k, v, rope=rope, q_norm=g, k_norm=g)
+    whole = w.buf.clone()
+    w.buf.copy_(start)
+    w.trees.append(0, None, k, v, rope=rope, k_norm=g)
+    assert torch.equal(w.buf, whole)
+    assert torch.equal(w.trees.append(0, q, None, None, rope=rope, q_norm=g), both)
+    assert torch.equal(w.buf, whole)
+    same = q.clone()
+    w.trees.append(0, same, None, None, rope=rope, q_norm=g, out=same)
+    assert torch.equal(same, both)
+    w.close()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("nodes", [2, 20, 100])
+def test_a_page_next_to_one_with_a_far_larger_scale_keeps_its_values(nodes, kind):
+    """Scales 2^28 apart within 128 slots, the large page's weights as good as zero: rows are the small pages' values."""
+    w = Setup8("16:8x128", kind, [128 * 3], [nodes], seed=3)
+    q = w.rand(w.N, w.H, w.D)
+    q[..., 0] = 60.0
+    w.codes[0, :, 0, :, :, 0] = codes_of(torch.tensor(100.0, dtype=torch.float64), torch.tensor(0.0), kind).item()  # every score up
+    w.scales[0, :, :, 0] = 1.0
+    for p in (1, 9, 20):  # one page of each tile: hidden by low scores, its values 2^28 times the others'
+        b = w.tables[0][p]
+        w.codes[0, b, 0, :, :, 0] = codes_of(torch.tensor(-100.0, dtype=torch.float64), torch.tensor(0.0), kind).item()
+        w.scales[0, b, :, 1] *= 2.0 ** 28 / 2
+    check(w, w.trees.attend(0, q), 0, q, set(range(0, w.N, max(w.N // 20, 1))))
+    w.close()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
 def test_a_page_filled_token_by_token_loses_less_than_a_step(kind):
     """16 calls of one token, growing: every value ends within one step of its page's final scale, and e is that of one call."""
     w = Setup8("16:8x128", kind, [32], [1], seed=3, extra_blocks=2)
