@@ -21,7 +21,7 @@ namespace {
 // HBM bounds the large calls, instructions not far behind (32 x 256 nodes: 82 us
 // with the rows in registers, every loop unrolled to 16 rows and 147 instructions
 // a row), so a task's rows are copied to shared memory all at once (with four
-// steps of them in flight 56 us), and the loops go four steps at a time: their
+// steps of them in flight 56 us; now 50: 195 MB at 3.9 TB/s), and the loops go four steps at a time: their
 // sums of squares are reduced together (6 shuffles for 4 rows of 128 channels; the
 // lanes end up with one row's each, so one root and quotient serve four rows), and
 // what is rare is looked for once a page (padding, values that are not finite, e
@@ -266,7 +266,7 @@ cudaError_t append_d(const TreeAppendArgs& a, cudaStream_t s) {
 // rounded again; then the rows are written.  Rows from pages of the same scale keep
 // their codes (their values fit), a page that gets no others is a copy.
 // Latency bounds it, not the few bytes; instructions come next (with four codes a
-// lane, 16 steps a page, 32 sequences x 64 nodes over 28 layers took 24 us).
+// lane, 16 steps a page, 32 sequences x 64 nodes over 28 layers took 24 us, so 12).
 constexpr int kCommitThreads = 256;
 
 template <int D, int kKind>
@@ -368,14 +368,14 @@ cudaError_t commit_d(const TreeCommitArgs& a, cudaStream_t s) {
 }
 
 // ---- reading back ------------------------------------------------------------------
-// A block of threads per pool block and layer, a warp per page (KV head, K or V),
-// two at a time: 16 rows each in 16-byte loads, all in flight, then the values in
-// the output's type.  A block's warps fill whole rows of the output between them.
-// HBM bounds it, the output's bytes most of all.
+// A block of threads per pool block and layer, a warp per page (KV head, K or V):
+// its 16 rows in 16-byte loads, all in flight, then the values in the output's
+// type.  A block's warps fill whole rows of the output between them.  HBM bounds
+// it, the output's bytes most of all: 28 layers of 32 x 1024-2048 tokens from i8 to
+// f16 1328 us, 8.5 GB at 6.4 TB/s (with two pages a warp at a time 1728).
 template <int D, int kType>
 __global__ void __launch_bounds__(256) k_tree_read(const __grid_constant__ TreeReadArgs a, bool wide) {
   constexpr int kSize = kType == kTreeF32 ? 4 : kType == kTreeF16 ? 2 : 1, kE = 16 / kSize, kLoads = 16 * D / (32 * kE);
-  constexpr int kPages = 1;
   static_assert(kLoads >= 1, "a page is a load of every lane at least");
   const bool ok = tree_shape_ok(a.m);  // the plan is older than the kernels before this one
   const int S = a.m.S, nb = __ldg(&a.m.reads[S].blocks[a.part]);
@@ -407,62 +407,53 @@ __global__ void __launch_bounds__(256) k_tree_read(const __grid_constant__ TreeR
   for (int layer = blockIdx.y; layer < a.n_layers; layer += gridDim.y)
     for (int b = blockIdx.x; b < nb; b += gridDim.x) {
       if (gridDim.x < nb) place(b);
-      for (int i0 = threadIdx.x >> 5; i0 < pages; i0 += 8 * kPages) {
-        uint4 raw[kPages][kLoads];
-        float f[kPages];
+      for (int i = threadIdx.x >> 5; i < pages; i += 8) {
+        const int h = i % a.d.Hkv, is_v = a.k ? i >= a.d.Hkv : 1;
+        const uint8_t* page = reinterpret_cast<const uint8_t*>(a.kv) + kv_offset(a.layer + layer, block, is_v, h, 0, a.d.n_blocks, a.d.Hkv, 16, D) * kSize;
+        const float f = kSize == 1 ? a.scales[q8_scale_at(a.d, a.layer + layer, block, h, is_v)] : 1.f;
+        uint4 raw[kLoads];
 #pragma unroll
-        for (int y = 0; y < kPages; ++y) {
-          const int i = min(i0 + 8 * y, pages - 1), h = i % a.d.Hkv, is_v = a.k ? i >= a.d.Hkv : 1;
-          const uint8_t* page = reinterpret_cast<const uint8_t*>(a.kv) + kv_offset(a.layer + layer, block, is_v, h, 0, a.d.n_blocks, a.d.Hkv, 16, D) * kSize;
-          f[y] = kSize == 1 ? a.scales[q8_scale_at(a.d, a.layer + layer, block, h, is_v)] : 1.f;
+        for (int l = 0; l < kLoads; ++l) raw[l] = *reinterpret_cast<const uint4*>(page + (l * 32 + lane) * 16);
+        void* out = is_v ? a.v : a.k;
 #pragma unroll
-          for (int l = 0; l < kLoads; ++l) raw[y][l] = *reinterpret_cast<const uint4*>(page + (l * 32 + lane) * 16);
-        }
+        for (int l = 0; l < kLoads; ++l) {
+          const int e = (l * 32 + lane) * kE, r = e / D;
+          if (r >= rows) continue;
+          const uint32_t w[4] = {raw[l].x, raw[l].y, raw[l].z, raw[l].w};
+          float4 v[kE / 4];
 #pragma unroll
-        for (int y = 0; y < kPages; ++y) {
-          const int i = i0 + 8 * y, h = i % a.d.Hkv, is_v = a.k ? i >= a.d.Hkv : 1;
-          if (i >= pages) break;
-          void* out = is_v ? a.v : a.k;
-#pragma unroll
-          for (int l = 0; l < kLoads; ++l) {
-            const int e = (l * 32 + lane) * kE, r = e / D;
-            if (r >= rows) continue;
-            const uint32_t w[4] = {raw[y][l].x, raw[y][l].y, raw[y][l].z, raw[y][l].w};
-            float4 v[kE / 4];
-#pragma unroll
-            for (int j = 0; j < kE / 4; ++j) {
-              if constexpr (kType == kTreeF32) {
-                v[j] = make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
-              } else if constexpr (kType == kTreeF16) {
-                const float2 g = tree_pair<__half>(w[2 * j]), z = tree_pair<__half>(w[2 * j + 1]);
-                v[j] = make_float4(g.x, g.y, z.x, z.y);
-              } else {
-                const float4 c = q8_unpack<kType>(w[j]);
-                v[j] = make_float4(c.x * f[y], c.y * f[y], c.z * f[y], c.w * f[y]);
-              }
-            }
-            const int64_t at = layer * a.layer_stride + (row0 + r) * a.ld + h * D + e % D;
-            if (kE > 4 && wide && a.out_type != kTreeF32) {
-#pragma unroll
-              for (int j = 0; j + 1 < kE / 4; j += 2) {
-                const float z[8] = {v[j].x, v[j].y, v[j].z, v[j].w, v[j + 1].x, v[j + 1].y, v[j + 1].z, v[j + 1].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if (a.out_type == kTreeF16) {
-                    const __half2 x = __floats2half2_rn(z[2 * k], z[2 * k + 1]);
-                    o[k] = *reinterpret_cast<const uint32_t*>(&x);
-                  } else {
-                    const __nv_bfloat162 x = __floats2bfloat162_rn(z[2 * k], z[2 * k + 1]);
-                    o[k] = *reinterpret_cast<const uint32_t*>(&x);
-                  }
-                }
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(out) + at + j * 4) = make_uint4(o[0], o[1], o[2], o[3]);
-              }
+          for (int j = 0; j < kE / 4; ++j) {
+            if constexpr (kType == kTreeF32) {
+              v[j] = make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
+            } else if constexpr (kType == kTreeF16) {
+              const float2 g = tree_pair<__half>(w[2 * j]), z = tree_pair<__half>(w[2 * j + 1]);
+              v[j] = make_float4(g.x, g.y, z.x, z.y);
             } else {
-#pragma unroll
-              for (int j = 0; j < kE / 4; ++j) tree_store4(out, a.out_type, at + j * 4, v[j]);
+              const float4 c = q8_unpack<kType>(w[j]);
+              v[j] = make_float4(c.x * f, c.y * f, c.z * f, c.w * f);
             }
+          }
+          const int64_t at = layer * a.layer_stride + (row0 + r) * a.ld + h * D + e % D;
+          if (kE > 4 && wide && a.out_type != kTreeF32) {
+#pragma unroll
+            for (int j = 0; j + 1 < kE / 4; j += 2) {
+              const float z[8] = {v[j].x, v[j].y, v[j].z, v[j].w, v[j + 1].x, v[j + 1].y, v[j + 1].z, v[j + 1].w};
+              uint32_t o[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (a.out_type == kTreeF16) {
+                  const __half2 x = __floats2half2_rn(z[2 * k], z[2 * k + 1]);
+                  o[k] = *reinterpret_cast<const uint32_t*>(&x);
+                } else {
+                  const __nv_bfloat162 x = __floats2bfloat162_rn(z[2 * k], z[2 * k + 1]);
+                  o[k] = *reinterpret_cast<const uint32_t*>(&x);
+                }
+              }
+              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(out) + at + j * 4) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kE / 4; ++j) tree_store4(out, a.out_type, at + j * 4, v[j]);
           }
         }
       }

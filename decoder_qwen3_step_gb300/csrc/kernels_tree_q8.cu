@@ -30,6 +30,11 @@
 // (movmatrix) per 8 keys.
 // i8: the byte, its sign flipped, under an exponent of 2^10 is 1024 + 128 + c in
 // f16, one subtraction gives c: 5 instructions for four codes.
+//
+// 32 x 1 nodes over 1024-2048 keys, 16:8 heads x 128: 24.7 us, 102 MB at 4.1 TB/s;
+// 32 x 1 over 6000 66 us, 6.0 TB/s (f16: 117 us).  From 1500 to 6000 keys a key's
+// bytes go at 6.9 TB/s, so HBM bounds the long ones; some 9 us a call (the start,
+// the ends of units, the second kernel) do not depend on the length.
 #include "attn_fold.cuh"
 #include "q8.cuh"
 #include "tc_common.cuh"

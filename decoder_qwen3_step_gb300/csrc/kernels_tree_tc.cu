@@ -46,7 +46,10 @@
 // pages lie further apart takes its V codes as they are and each block's own b
 // into the scores, as kernels_tree_q8.cu does for all.
 // Registers are moved from the other warps to the softmax (512 threads have 128
-// each).
+// each).  32 x 64 nodes over 1024-2048 keys: 52.4 us, 119 MB at 2.3 TB/s; 8 x 256
+// over 8000: 136 us, 934 TFLOP/s.  Neither the codes' bytes nor the products bound
+// it but the steps of a tile, one after the other, with a conversion more than over
+// f16: there the same calls take up to a sixth less time.
 #include "attn_fold.cuh"
 #include "q8.cuh"
 #include "tc_common.cuh"
@@ -210,7 +213,9 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
   constexpr bool kQ8 = kKind != kTreeF16;
   using SM = TcSmem<D, kQ8>;
   constexpr int kS = SM::kSlots, kOps = SM::kOps, kR = kWide ? 2 * kTR : kTR;
-  constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;  // of 8 bits: 256 threads each, in all the 512 x 128 of the launch
+  // of 8 bits: 256 threads each, in all the 512 x 128 of the launch.  Narrow (152 / 104, 160 / 96): 32 x 64 nodes over
+  // 1024-2048 keys 53.5, 52.4 us, 1 x 64 over 40000 41.5, 40.9; wide: 8 x 256 over 8000 135.9, 140.3
+  constexpr int kSoftmaxRegs = kWide ? 152 : 160, kOtherRegs = 256 - kSoftmaxRegs;
   extern __shared__ __align__(1024) uint8_t dsm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(dsm + SM::kBar);
   // ready, used: of the operands that the MMAs take (an f16 cache's copies are these)
@@ -653,26 +658,26 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
           // zero weights: zero them; its descendants get it back at the unit's end.  Eight threads per row.  (Wide: both
           // groups do this for the tile, whichever comes first changes it.  8 bits: operands are always finite)
           if constexpr (!kQ8) {
-          const int li = 2 * k + 1, slot = li % kS;
-          alive = __all_sync(0xffffffffu, alive && mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err));
-          for (int q = max(u.ctx - key0, 0) + (st >> 3); alive && q < kTK; q += 16) {
+            const int li = 2 * k + 1, slot = li % kS;
+            alive = __all_sync(0xffffffffu, alive && mbar_wait(&full[slot], (li / kS) & 1, abort_flag, a.m.err));
+            for (int q = max(u.ctx - key0, 0) + (st >> 3); alive && q < kTK; q += 16) {
 #pragma unroll
-            for (int p = 0; p < SM::kPanels; ++p) {
-              uint4* at = reinterpret_cast<uint4*>(dsm + SM::kRing + slot * SM::kTile + (q >> 3) * SM::kGroup + p * 1024 +
-                                                   (q & 7) * 128 + (st & 7) * 16);
-              uint4 x = *at;
-              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-              if (key0 + q >= end) {
-                if (w[0] | w[1] | w[2] | w[3]) *at = make_uint4(0u, 0u, 0u, 0u);
-              } else if (tree_not_finite(x)) {
+              for (int p = 0; p < SM::kPanels; ++p) {
+                uint4* at = reinterpret_cast<uint4*>(dsm + SM::kRing + slot * SM::kTile + (q >> 3) * SM::kGroup + p * 1024 +
+                                                     (q & 7) * 128 + (st & 7) * 16);
+                uint4 x = *at;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+                if (key0 + q >= end) {
+                  if (w[0] | w[1] | w[2] | w[3]) *at = make_uint4(0u, 0u, 0u, 0u);
+                } else if (tree_not_finite(x)) {
 #pragma unroll
-                for (int z = 0; z < 4; ++z) w[z] = tree_finite_or_0(w[z]);
-                *at = x;
-                flags[4 + (n_unit & 1)] = n_unit + 1;
+                  for (int z = 0; z < 4; ++z) w[z] = tree_finite_or_0(w[z]);
+                  *at = x;
+                  flags[4 + (n_unit & 1)] = n_unit + 1;
+                }
               }
             }
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
         }
         alive = __all_sync(0xffffffffu, alive && mbar_wait(&sfull[b], n & 1, abort_flag, a.m.err));

@@ -51,8 +51,8 @@ struct TreeLayout {
 // sequences over 8000 keys with 512 rows, narrow units 211 us, wide ones 114.
 TreeVariant variant_for(int kv_type, int D, int max_rows) {
   if (kv_type == kTreeF32) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2, 0};
-  // a unit's start and end in tiles of 8-bit keys: 2 (8 x 256 over 8000: 132 us, with 4 135, with 6 137.5; 32 x 64 over
-  // 1024-2048: 50.6, 52.7, 55.5)
+  // a unit's start and end in tiles of 8-bit keys: 2 (before pages far apart had
+  // their own path: 8 x 256 over 8000 132 us, with 4 135, with 6 137.5; 32 x 64 over 1024-2048 50.6, 52.7, 55.5)
   const int unit = kv_type == kTreeF16 ? 4 : 2;
   if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, unit, 50};
   if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, unit, 25};

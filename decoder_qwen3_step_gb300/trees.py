@@ -11,6 +11,12 @@ A verification step of a program that runs its own projections::
         q = trees.append(layer, q_raw, k_raw, v_raw, rope=rope, q_norm=gq, k_norm=gk)
         o = trees.attend(layer, q)
     accepted, path, after = trees.commit(draft_ids, chosen_ids)
+
+A pool with ``kv_type=dec.DEC_T_I8`` or ``dec.DEC_T_E4M3`` holds 8-bit codes with a
+power-of-two scale per page and head: append quantises, attend and commit work on
+the codes, and ``trees.read(layer)`` gives the values back (from any pool)::
+
+    pool = KvPool(shape, dec.DEC_BF16_F16KV, n_blocks, kv_type=dec.DEC_T_I8)
 """
 
 from __future__ import annotations
