@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(128, 5) k_append_q8(const __grid_constant__ Tr
 #pragma unroll 4
     for (int s = 0; s * kRows < n; ++s) {  // each lane's own values
       const int r = s * kRows + sub;
-      if (r >= n || (pads && pos_at(r) < 0)) continue;
+      const bool pad = pads && pos_at(r) < 0;  // a shuffle: every lane, also those behind the last row
+      if (r >= n || pad) continue;
       const float4 y = rows[r * kLanes];
       *reinterpret_cast<uint32_t*>(page + r * D) = fits ? q8_pack_fit<kKind>(y, inv) : q8_pack<kKind>(make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
     }

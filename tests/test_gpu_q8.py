@@ -297,6 +297,27 @@ def test_append_without_rotation_gives_the_nearest_codes(batch, shape, kind):
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("shape", ["4:2x32", "12:3x32", "8:4x64", "16:8x128"])
+def test_append_with_padding_in_pages_of_any_number_of_rows(shape, kind):
+    """Pages of 1 .. 16 rows, at a page's start and at its end, padding first, everywhere but last, and anywhere."""
+    ctx, parents = [], []
+    rng = random.Random(7)
+    for n in range(1, 17):
+        for pads in ({0}, set(range(n - 1)), {i for i in range(n) if rng.random() < 0.5}):
+            for c in (32, 48 - n):
+                ctx.append(c)
+                parents.append([PAD if i in pads else -1 for i in range(n)])
+    w = Setup8(shape, kind, ctx, parents, seed=4)
+    k, v = w.rand(w.N, w.Hkv, w.D), w.rand(w.N, w.Hkv, w.D)
+    k *= torch.exp2(torch.randint(-3, 4, (w.N, w.Hkv, 1), generator=w.g).float()).cuda()
+    want = expected_pages(w, 0, torch.stack([k, v], 1).double())
+    w.trees.append(0, None, k, v)
+    assert torch.equal(log2(w.scales[0]).transpose(1, 2), want[1])
+    assert torch.equal(w.codes[0], want[0])
+    w.close()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("in_type", [torch.float32, torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("shape, rot, layout", [("4:2x32", 8, dec.DEC_ROPE_HALF), ("16:8x128", 128, dec.DEC_ROPE_HALF), ("16:8x128", 72, dec.DEC_ROPE_INTERLEAVED), ("8:4x64", 48, dec.DEC_ROPE_HALF),
                                                 ("5:5x64", 64, dec.DEC_ROPE_INTERLEAVED), ("8:2x128", 128, dec.DEC_ROPE_HALF)])
