@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(kCommitThreads, 4) k_commit_q8(const __grid_co
         f[t] = q8_two(q8_exp(f[t]));
         other |= f[t] != q8_two(was);
       }
-    if (!__any_sync(0xffffffffu, other)) {  // every lane's loads are behind it
+    __syncwarp();  // every lane's rows and scales are loaded before any of them is written over
+    if (!__any_sync(0xffffffffu, other)) {
 #pragma unroll
       for (int t = 0; t < kSteps; ++t)
         if (move >> t & 1u) *reinterpret_cast<uint4*>(page + (t * kRows + sub) * D) = w[t];

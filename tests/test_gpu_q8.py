@@ -511,6 +511,33 @@ def test_commit_walks_moves_and_quantises(shape, with_prior, kind):
     w.close()
 
 
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("shape", ["4:2x32", "8:4x64", "16:8x128"])
+@pytest.mark.parametrize("ctx", [0, 5, 16])
+def test_commit_between_pages_of_one_scale_copies_codes(ctx, shape, kind):
+    """Every code may move over one that another lane of the warp has to move on: chains that leave out every other node, or
+    all but the last ones, over pages of the same scale."""
+    step = [i - 2 if i > 1 else i - 1 for i in range(100)]  # 0, 2, 4, .. and 0, 1, 3, 5, ..
+    far = [-1] + [0] * 50 + list(range(50, 90))
+    w = Setup8(shape, kind, [ctx] * 3, [step, step, far], layers=4, seed=2)
+    w.scales[:] = 2.0 ** -4
+    ways = [list(range(0, 100, 2)), [0] + list(range(1, 100, 2)), [0] + list(range(50, 91))]
+    draft = torch.arange(w.N, dtype=torch.int32, device="cuda")
+    target = torch.full((w.N,), -1, dtype=torch.int32)
+    want, b = w.codes.clone(), 0
+    for s, way in enumerate(ways):
+        for x, y in zip(way, way[1:]):
+            target[b + x] = b + y
+        for i, x in enumerate(way):
+            (to, r), (frm, z) = w.where(s, ctx + i), w.where(s, ctx + x)
+            want[:, to, :, :, r] = w.codes[:, frm, :, :, z]
+        b += len(w.parents[s])
+    accepted, _, _ = w.trees.commit(draft, target.cuda())
+    assert accepted.tolist() == [len(x) for x in ways]
+    assert torch.equal(w.codes, want) and bool((w.scales == 2.0 ** -4).all())
+    w.close()
+
+
 # ---- read -----------------------------------------------------------------------------------------------------
 
 
