@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
           }
           bool raise = false;
 #pragma unroll
-          for (int i = 0; i < 2 * MT; ++i) raise |= mx[i] > m[i] + 8.f;
+          for (int i = 0; i < 2 * MT; ++i) raise |= mx[i] - m[i] > 8.f;  // (m + 8 could round up to the next score)
           if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i) {

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kQ8Threads, Q8Smem<D, R>::kCtas) k_tree_attend
               x[n][i] = (s[n][0][i] + s[n][1][i]) * fminf(c[n][i & 1] * sk, 3.40282347e38f);
               if (drafted && !((sees[n][i & 1] >> ((lane >> 2) + (i >> 1) * 8)) & 1u)) x[n][i] = -INFINITY;
             }
-            raise |= fmaxf(x[n][0], x[n][2]) + ev > m[n][0] + 8.f || fmaxf(x[n][1], x[n][3]) + ev > m[n][1] + 8.f;
+            raise |= fmaxf(x[n][0], x[n][2]) + ev - m[n][0] > 8.f || fmaxf(x[n][1], x[n][3]) + ev - m[n][1] > 8.f;  // (m + 8 could round up to the next score)
           }
           if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll

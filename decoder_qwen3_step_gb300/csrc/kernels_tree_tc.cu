@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
             largest(sb);
           }
           mx = kQ8 ? __fadd_rn(__fmul_rn(mx, f), e) : mx * f;
-          if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+          if (__any_sync(0xffffffffu, mx - m > 8.f)) {  // (m + 8 could round up to the next score)
             const float mn = fmaxf(m, mx), g = mn == m ? 1.f : ex2(m - mn);
             m = mn;
             l *= g;
