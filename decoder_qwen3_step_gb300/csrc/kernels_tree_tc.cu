@@ -24,8 +24,8 @@
 // Wide: group b takes rows 128 b .. 128 b + 127 of every tile, so a tile's bytes
 // serve 256 rows; with narrow units 8 x 256 nodes at contexts of 8000 read
 // every key four times and ran at HBM speed, 211 us against 64 for the products.
-// O is rescaled in TMEM only when a row's scores exceed its maximum by 2^8
-// (exact: numerator and denominator share the maximum).  Warps whose rows are
+// O is rescaled in TMEM only when a row's scores exceed its reference by 2^8, of
+// 8 bits 2^15 (exact: numerator and denominator share the reference).  Warps whose rows are
 // all behind the last skip the softmax.  Roundings as in kernels_tree_f16.cu.
 //
 // 8-bit caches: the producer brings codes (a page is contiguous: one bulk copy)
@@ -40,11 +40,14 @@
 // and one exponent B a tile: weights are 2^(s + B - m), l adds 2^-B times their
 // sum (the reference m as in kernels_tree_q8.cu).  With a factor for each block
 // in the softmax it took 1.3 us a tile in place of 0.85.
-// The reference may then pass a row's true one, the largest s + b, by as much as
-// the V exponents of a tile differ (a page of large values whose weights are all
-// small).  Up to 2^8 that costs f16's weights nothing that counts; a tile whose
-// pages lie further apart takes its V codes as they are and each block's own b
-// into the scores, as kernels_tree_q8.cu does for all.
+// The largest s + B may then pass a row's true one, the largest s + b, by as much
+// as the V exponents of a tile differ (a page of large values whose weights are
+// all small).  Up to 2^8 the reference makes up for it: it is set 2^8 below that
+// largest and raised once weights would pass 2^15 (f16 ends at 2^16), so a row's
+// largest true weight is 1 or more, as in kernels_tree_q8.cu, and weights down to
+// 2^-14 of it keep all their bits.  A tile whose pages lie further apart takes
+// each block's own b into the scores, and its V codes all times the power of two
+// that other tiles give to their largest page, so that B and b mean the same.
 // Registers are moved from the other warps to the softmax (512 threads have 128
 // each).  32 x 64 nodes over 1024-2048 keys: 52.4 us, 119 MB at 2.3 TB/s; 8 x 256
 // over 8000: 136 us, 934 TFLOP/s.  Neither the codes' bytes nor the products bound
@@ -60,12 +63,14 @@ namespace {
 
 constexpr int kTR = 128, kTK = 128;  // rows and keys of a step
 constexpr int kTcTreeThreads = 384, kTcTreeThreadsQ8 = 512;
-// A tile's 2^A, B (infinite: pages far apart) and the b of its blocks; of how many tiles they are kept (the conversion is at
-// most four ahead of the softmax)
+// A tile's 2^A, B (infinite: pages far apart) and its blocks' b, reckoned as B is; of how many tiles they are kept (the
+// conversion is at most four ahead of the softmax)
 struct TileScales {
   float a, b, each[8];
 };
 constexpr int kScaleRing = 8, kApart = 8;
+// Of 8 bits: how far below the largest score a reference is set, and how far above it scores may lie
+constexpr float kBelow8 = (float)kApart, kAbove8 = 15.f;
 constexpr int kOps8 = 3, kSlots8 = 4;  // of 128 channels
 constexpr uint32_t kTmemCols = 512;  // S of the two groups: columns 0, 128; O: 256, 256 + D
 
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
       };
       exponents(t0, nxt);
       uint32_t fk = 0, fv = 0;  // the factors of the lane's block, in both halves
-      TileScales scales;        // of its tile (each[0]: the block's b)
+      TileScales scales;        // of its tile (each[0]: the block's)
       for (int t = t0; t < t1; ++t) {
         const int turn = (t - t0) & 3;
         if (turn == 0) {
@@ -504,11 +509,11 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
           const bool apart = va - low > kApart;
           scales.a = q8_two(ka - kLift);
           scales.b = apart ? INFINITY : (float)(va - kLift);
-          scales.each[0] = (float)e.y;
+          scales.each[0] = (float)(e.y - kLift);
           // 2^d in f16, down to 2^-24 (below, 0)
           auto half_two = [](int d) { return (d >= -14 ? (uint32_t)(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u) * 0x10001u; };
           fk = half_two(e.x - ka + kLift);
-          fv = half_two(apart ? 0 : e.y - va + kLift);
+          fv = half_two(apart ? kLift : e.y - va + kLift);
         }
         if (warp == 12 && lane >> 3 == turn) {
           TileScales& to = reinterpret_cast<TileScales*>(dsm + SM::kScales)[(li >> 1) % kScaleRing];
@@ -745,8 +750,8 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
             largest(sb);
           }
           mx = kQ8 ? __fadd_rn(__fmul_rn(mx, f), e) : mx * f;
-          if (__any_sync(0xffffffffu, mx - m > 8.f)) {  // (m + 8 could round up to the next score)
-            const float mn = fmaxf(m, mx), g = mn == m ? 1.f : ex2(m - mn);
+          if (__any_sync(0xffffffffu, mx - m > (kQ8 ? kAbove8 : 8.f))) {  // (a sum with m could round up to the next score)
+            const float mn = fmaxf(m, kQ8 ? mx - kBelow8 : mx), g = mn == m ? 1.f : ex2(m - mn);
             m = mn;
             l *= g;
             if (!first) {  // this group's products so far have run: its S was issued behind them

@@ -14,6 +14,47 @@ from tests.test_gpu_trees import Setup  # noqa: E402
 pytestmark = pytest.mark.gpu
 
 
+def code(x, kind):
+    return codes_of(torch.tensor(float(x), dtype=torch.float64), torch.tensor(0.0), kind).item()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("gap", [3, 5, 8, 9, 12])
+@pytest.mark.parametrize("shape, seqs, nodes", [("8:4x64", 16, 30), ("16:8x128", 16, 20), ("8:4x64", 8, 200), ("16:8x128", 8, 70), ("16:8x128", 8, 4)])
+def test_many_small_weights_beside_a_page_of_larger_values(shape, seqs, nodes, gap, kind):
+    """Each of the first two tiles has one key with the largest score and a page that nobody looks at, its values 2^gap times
+    the others'; all other keys weigh 2^-15.5 of the largest each, which is no whole number of f16's smallest steps."""
+    ctx = 4000
+    w = Setup8(shape, kind, [ctx] * seqs, [[-1] * nodes] * seqs, layers=1, seed=gap)
+    w.scales[:] = 1.0
+    low, base, top = code(-64, kind), code(32, kind), code(64, kind)
+    w.codes[0, :, 0, :, :, 0] = base
+    w.codes[0, :, 1] = code(96, kind)
+    for s in range(seqs):
+        for tile in range(2):
+            b, r = w.where(s, tile * 128 + 40 + tile)
+            w.codes[0, b, 0, :, r, 0] = top
+            w.codes[0, b, 1, :, r] = code(-96, kind)
+            b, _ = w.where(s, tile * 128 + 80)
+            w.codes[0, b, 0, :, :, 0] = low
+            w.scales[0, b, :, 1] = 2.0 ** gap
+        for slot in range(ctx, ctx + nodes):
+            b, r = w.where(s, slot)
+            w.codes[0, b, 0, :, r, 0] = low
+    # exact in f16, as are the codes, so the scores are the formula's but for fp32
+    q0 = round(15.474 * math.sqrt(w.D) / 32 * math.log(2) * 256) / 256
+    q = torch.zeros((w.N, w.H, w.D), device="cuda")
+    q[..., 0] = q0
+    small, n = math.exp(-32 * q0 / math.sqrt(w.D)), ctx - 2 * 17
+    want = 96 * (n * small - 2) / (n * small + 2)  # what nobody looks at weighs 2^-30 in all
+    got = w.trees.attend(0, q, out_type=torch.float16).double()
+    # weights: half a step of f16 each, and of its subnormal numbers (2^-25 of a reference that is at most the largest);
+    # fp32: scores below 2^5 off by 3 half steps, 72 more for sums and the exponential; then the output's half step
+    allowed = 96 * (2.0 ** -11 + n * 2.0 ** -25 / (2 + n * small) + (3 * 32 + 72) * 2.0 ** -24) + 2.0 ** -11 * abs(want)
+    assert float((got - want).abs().max()) <= allowed
+    w.close()
+
+
 @pytest.mark.parametrize("cache", ["f16", *KINDS])
 @pytest.mark.parametrize("blocks", [4, 8, 16])  # a warp of the narrow kernels, a group of a wide unit, of a narrow one meet every such block
 @pytest.mark.parametrize("shape, nodes", [("8:4x64", 3), ("16:8x128", 8), ("16:8x128", 40), ("16:8x128", 100)])
