@@ -35,8 +35,8 @@
 // its eight blocks, and 2^B of V's out of its values: an operand is code * 2^(a -
 // A), one fused multiply-add on the way from i8 to f16, exact down to 2^-24.  The
 // largest page keeps a factor of 2^5 (i8; e4m3: 2^7, f16's range allows that
-// much), so a page's scale may be 2^29 below its neighbours' before its codes lose
-// bits.  So the softmax has one factor c 2^A
+// much), so operands are exact while K's scales lie within 2^29 (e4m3, whose codes
+// end at 2^-9: 2^22).  So the softmax has one factor c 2^A
 // and one exponent B a tile: weights are 2^(s + B - m), l adds 2^-B times their
 // sum (the reference m as in kernels_tree_q8.cu).  With a factor for each block
 // in the softmax it took 1.3 us a tile in place of 0.85.
@@ -45,9 +45,10 @@
 // all small).  Up to 2^8 the reference makes up for it: it is set 2^8 below that
 // largest and raised once weights would pass 2^15 (f16 ends at 2^16), so a row's
 // largest true weight is 1 or more, as in kernels_tree_q8.cu, and weights down to
-// 2^-14 of it keep all their bits.  A tile whose pages lie further apart takes
-// each block's own b into the scores, and its V codes all times the power of two
-// that other tiles give to their largest page, so that B and b mean the same.
+// 2^-14 of it keep all their bits.  A tile whose pages lie further apart (K's or
+// V's) takes each block's own 2^a and b into the scores, its K codes as they are,
+// and its V codes all times the power of two that other tiles give to their largest
+// page, so that B and b mean the same.
 // Registers are moved from the other warps to the softmax (512 threads have 128
 // each).  32 x 64 nodes over 1024-2048 keys: 52.4 us, 119 MB at 2.3 TB/s; 8 x 256
 // over 8000: 136 us, 934 TFLOP/s.  Neither the codes' bytes nor the products bound
@@ -63,10 +64,10 @@ namespace {
 
 constexpr int kTR = 128, kTK = 128;  // rows and keys of a step
 constexpr int kTcTreeThreads = 384, kTcTreeThreadsQ8 = 512;
-// A tile's 2^A, B (infinite: pages far apart) and its blocks' b, reckoned as B is; of how many tiles they are kept (the
-// conversion is at most four ahead of the softmax)
+// A tile's 2^A, B (infinite: pages far apart), its blocks' b, reckoned as B is, and their 2^a; of how many tiles they are
+// kept (the conversion is at most four ahead of the softmax)
 struct TileScales {
-  float a, b, each[8];
+  float a, b, each[8], keys[8];
 };
 constexpr int kScaleRing = 8, kApart = 8;
 // Of 8 bits: how far below the largest score a reference is set, and how far above it scores may lie
@@ -474,6 +475,8 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
   } else if (kQ8 && warp >= 12) {
     // ---- codes to operands ----
     constexpr int kLift = kKind == kTreeI8 ? 5 : 7;  // 1152 2^5 and 448 2^7 are still f16
+    // how far K's exponents may lie apart: codes are multiples of 1 (e4m3: 2^-9), f16 numbers of 2^-24
+    constexpr int kApartKeys = kLift + 24 - (kKind == kTreeI8 ? 0 : 9);
     const int ct = threadIdx.x - 384;
     int li = 0;
     for (int left = cut.count; left > 0;) {
@@ -499,25 +502,28 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
         const int turn = (t - t0) & 3;
         if (turn == 0) {
           nxt = entry4(t + 4, t1);
-          int ka = e.x, va = e.y, low = block ? e.y : kExpMax;
+          int ka = e.x, va = e.y, klow = block ? e.x : kExpMax, low = block ? e.y : kExpMax;
 #pragma unroll
           for (int d = 1; d < 8; d *= 2) {
             ka = max(ka, __shfl_xor_sync(0xffffffffu, ka, d));
             va = max(va, __shfl_xor_sync(0xffffffffu, va, d));
+            klow = min(klow, __shfl_xor_sync(0xffffffffu, klow, d));
             low = min(low, __shfl_xor_sync(0xffffffffu, low, d));
           }
-          const bool apart = va - low > kApart;
+          const bool apart = va - low > kApart || ka - klow > kApartKeys;
           scales.a = q8_two(ka - kLift);
           scales.b = apart ? INFINITY : (float)(va - kLift);
           scales.each[0] = (float)(e.y - kLift);
+          scales.keys[0] = q8_two(e.x);
           // 2^d in f16, down to 2^-24 (below, 0)
           auto half_two = [](int d) { return (d >= -14 ? (uint32_t)(d + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u) * 0x10001u; };
-          fk = half_two(e.x - ka + kLift);
+          fk = half_two(apart ? 0 : e.x - ka + kLift);
           fv = half_two(apart ? kLift : e.y - va + kLift);
         }
         if (warp == 12 && lane >> 3 == turn) {
           TileScales& to = reinterpret_cast<TileScales*>(dsm + SM::kScales)[(li >> 1) % kScaleRing];
           to.each[lane & 7] = scales.each[0];
+          to.keys[lane & 7] = scales.keys[0];
           if ((lane & 7) == 0) to.a = scales.a, to.b = scales.b;
         }
         if (turn == 3) exponents(t + 1, nxt);
@@ -690,10 +696,11 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
         if (alive && mine) {
           tc_fence_after();
           float f = c, e = 0.f;  // this tile's score factor (8 bits: kept off 0 and infinity, hidden scores are -inf) and exponent
+          auto kept = [](float x) { return fminf(fmaxf(x, 1.17549435e-38f), 3.40282347e38f); };
           const TileScales* scales = reinterpret_cast<const TileScales*>(dsm + SM::kScales) + k % kScaleRing;
           bool apart = false;
           if constexpr (kQ8) {
-            f = fminf(fmaxf(c * scales->a, 1.17549435e-38f), 3.40282347e38f);
+            f = kept(c * scales->a);
             e = scales->b;
             apart = e == INFINITY;
           }
@@ -715,11 +722,11 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
           if (kQ8 && apart) {  // rare: s f + b of each block in place of the scores
 #pragma unroll 1
             for (int j = 0; j < 8; ++j) {
-              const float eb = scales->each[j];
+              const float fb = kept(c * scales->keys[j]), eb = scales->each[j];
               uint32_t s[16];
               tc_ld16(ts + j * 16, s);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), f), eb));
+              for (int i = 0; i < 16; ++i) s[i] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(s[i]), fb), eb));
               tc_st16(ts + j * 16, s);
             }
             tc_wait_st();

@@ -683,8 +683,8 @@ int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* str
  * q.  A node's result does not depend on what is cached in slots it does not
  * see (infinities and NaN included; in 8 bits that is so of the codes, but the
  * values of a page share its scale, and where a sequence has more than 16 rows,
- * nodes x query heads per KV head, keys whose page's scale is more than 2^29
- * below the largest of the same 128 slots are rounded to 2^-29 of that); a query, or a key that it sees, that is NaN
+ * nodes x query heads per KV head, the scales of the pages of the same 128 slots
+ * may change its last bits); a query, or a key that it sees, that is NaN
  * gives NaN; scores that are all -inf give zeros, as for a node that sees
  * nothing.  The result may differ in its last bits with the rest of the batch,
  * which decides how the keys are split over the GPU, and between a direct call

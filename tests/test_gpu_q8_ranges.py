@@ -8,7 +8,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tests.q8_reference import KINDS, codes_of  # noqa: E402
-from tests.test_gpu_q8 import Setup8  # noqa: E402
+from tests.test_gpu_q8 import Setup8, check  # noqa: E402
 from tests.test_gpu_trees import Setup  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -52,6 +52,26 @@ def test_many_small_weights_beside_a_page_of_larger_values(shape, seqs, nodes, g
     # fp32: scores below 2^5 off by 3 half steps, 72 more for sums and the exponential; then the output's half step
     allowed = 96 * (2.0 ** -11 + n * 2.0 ** -25 / (2 + n * small) + (3 * 32 + 72) * 2.0 ** -24) + 2.0 ** -11 * abs(want)
     assert float((got - want).abs().max()) <= allowed
+    w.close()
+
+
+@pytest.mark.parametrize("gap", [20, 22, 23, 26, 29, 30, 31, 32, 33, 44])
+@pytest.mark.parametrize("shape, nodes", [("8:4x64", 60), ("16:8x128", 40), ("16:8x128", 200), ("8:4x64", 256), ("16:8x128", 5), ("4:2x32", 60)])
+@pytest.mark.parametrize("kind, fine", [("i8", False), ("e4m3", False), ("e4m3", True)])
+def test_keys_beside_a_page_of_far_larger_ones(kind, fine, shape, nodes, gap):
+    """Keys of a tile keep their bits whatever the scale of a page next to them, of nodes that the rows do not see; fine:
+    keys that are e4m3's smallest numbers."""
+    w = Setup8(shape, kind, [112], [[-1] * nodes], layers=1, seed=gap)
+    q = w.rand(w.N, w.H, w.D)
+    if fine:
+        k = w.codes[0, :, 0]
+        w.codes[0, :, 0] = torch.where(k & 0x7F != 0, (k & 0x87) | 1, k)  # up to 7 of the steps of 2^-9
+        q *= 2.0 ** 20
+    b, _ = w.where(0, 112)  # slots 112 .. 127 of the tile 0 .. 127: the first sixteen nodes
+    w.scales[0, :, :, 0] = 2.0 ** (-6 if fine else -9 if kind == "i8" else -10)
+    w.scales[0, b, :, 0] *= 2.0 ** gap
+    out = w.trees.attend(0, q)
+    check(w, out, 0, q, set(range(min(16, nodes - 1), w.N, max(w.N // 24, 1))) | {w.N - 1} if nodes > 16 else None)
     w.close()
 
 
