@@ -4,8 +4,10 @@
 // o_i = sum_j p_ij v_j / sum_j p_ij, p_ij = 2^(s_ij - m_i), s_ij = q_i . k_j *
 // log2(e) / sqrt(D), with k_j = 2^a c_j and v_j = 2^b d_j, a and b the exponents
 // of the pages that hold them.  The products run on the codes, which are exact
-// in f16; 2^a goes into the scores' factor, 2^b into the weights:
-//   O += (p_ij 2^b) d_j,   l += p_ij.
+// in f16; 2^a goes into the scores' factor, b is added to the scores:
+//   w_ij = 2^(s_ij + b - m_i),   O += w_ij d_j,   l += w_ij 2^-b.
+// (Weights and reference go by the same rounded s_ij + b: with 2^b as a factor of
+// p_ij, scores from 2^27 on, which have no place left for b, gave weights of 2^b.)
 // The reference m_i is a running maximum of s_ij + b (raised when a row exceeds
 // it by 2^8), so the rounded weights are at most 2^8 whatever the scales, and the
 // largest at least 1; l holds in fp32 for scales of 2^-40 .. 2^40.
@@ -245,17 +247,17 @@ __global__ void __launch_bounds__(kQ8Threads, Q8Smem<D, R>::kCtas) k_tree_attend
               for (int n = 0; n < kN; ++n) af_mma_f16(s[n][z], A, q[n][2 * kk + z][0], q[n][2 * kk + z][1]);
             }
           }
-          // scores of keys lane >> 2 and + 8: x[0], x[2] of the first column, x[1], x[3] of the second
+          // scores + ev of keys lane >> 2 and + 8: x[0], x[2] of the first column, x[1], x[3] of the second
           float x[kN][4];
           bool raise = false;
 #pragma unroll
           for (int n = 0; n < kN; ++n) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              x[n][i] = (s[n][0][i] + s[n][1][i]) * fminf(c[n][i & 1] * sk, 3.40282347e38f);
+              x[n][i] = fmaf(s[n][0][i] + s[n][1][i], fminf(c[n][i & 1] * sk, 3.40282347e38f), ev);
               if (drafted && !((sees[n][i & 1] >> ((lane >> 2) + (i >> 1) * 8)) & 1u)) x[n][i] = -INFINITY;
             }
-            raise |= fmaxf(x[n][0], x[n][2]) + ev - m[n][0] > 8.f || fmaxf(x[n][1], x[n][3]) + ev - m[n][1] > 8.f;  // (m + 8 could round up to the next score)
+            raise |= fmaxf(x[n][0], x[n][2]) - m[n][0] > 8.f || fmaxf(x[n][1], x[n][3]) - m[n][1] > 8.f;  // (m + 8 could round up to the next score)
           }
           if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kQ8Threads, Q8Smem<D, R>::kCtas) k_tree_attend
                 float mx = fmaxf(x[n][z], x[n][z + 2]);
 #pragma unroll
                 for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                const float mn = fmaxf(m[n][z], mx + ev);
+                const float mn = fmaxf(m[n][z], mx);
                 const float f = mn == m[n][z] ? 1.f : ex2(m[n][z] - mn);
                 m[n][z] = mn;
                 l[n][z] *= f;
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kQ8Threads, Q8Smem<D, R>::kCtas) k_tree_attend
                 }
               }
           }
-          const float sv = q8_two((int)ev);
+          const float out_of = q8_two(-(int)ev);
           uint32_t P[kN][2];
 #pragma unroll
           for (int n = 0; n < kN; ++n) {
@@ -284,10 +286,10 @@ __global__ void __launch_bounds__(kQ8Threads, Q8Smem<D, R>::kCtas) k_tree_attend
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               p[i] = ex2(x[n][i] - (m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1]));  // nothing seen so far: every weight is 0
-              l[n][i & 1] += p[i];
+              l[n][i & 1] = fmaf(p[i], out_of, l[n][i & 1]);
             }
-            P[n][0] = q8_transpose(af_pack_half(p[0] * sv, p[1] * sv));
-            P[n][1] = q8_transpose(af_pack_half(p[2] * sv, p[3] * sv));
+            P[n][0] = q8_transpose(af_pack_half(p[0], p[1]));
+            P[n][1] = q8_transpose(af_pack_half(p[2], p[3]));
           }
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {

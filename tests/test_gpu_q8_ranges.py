@@ -75,6 +75,35 @@ def test_keys_beside_a_page_of_far_larger_ones(kind, fine, shape, nodes, gap):
     w.close()
 
 
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("values", [-38, -20, 0, 20, 34])
+@pytest.mark.parametrize("size", [3e7, 1e8, 1e9, 1e15])
+@pytest.mark.parametrize("shape, nodes", [("8:4x64", 5), ("16:8x128", 3), ("16:8x128", 8), ("16:8x128", 40), ("8:4x64", 200)])
+def test_scores_past_the_last_place_of_a_values_exponent(shape, nodes, size, values, kind):
+    """Queries so large that one key takes all the weight and its score has no bits left for the exponent of a value's scale:
+    the output is that key's value."""
+    w = Setup8(shape, kind, [250, 40], [nodes, nodes], layers=1, seed=3)
+    w.scales[..., 1] *= 2.0 ** values
+    w.scales.clamp_(2.0 ** -40, 2.0 ** 40)
+    q = w.rand(w.N, w.H, w.D) * size
+    out = w.trees.attend(0, q).view(w.N, w.H, w.D).double()
+    assert bool(torch.isfinite(out).all())
+    G, rows = w.H // w.Hkv, 0
+    for n, s, i, _, _ in w.nodes():
+        k, v, _, _ = (x.repeat_interleave(G, 1) for x in w.rows(0, s, w.seen(s, i)))
+        sc = torch.einsum("hd,khd->hk", q[n].double(), k) / math.sqrt(w.D)
+        size_of = torch.einsum("hd,khd->hk", q[n].double().abs(), k.abs()) / math.sqrt(w.D)
+        first = sc.topk(2, -1)
+        # f16 queries: half a step of each product (2^-11) on both sides, and 100 so that nothing else weighs anything
+        clear = first.values[:, 0] - first.values[:, 1] > 2 * 2.0 ** -11 * 1.01 * size_of.amax(-1) + 100
+        for h in clear.nonzero()[:, 0].tolist():
+            want = v[first.indices[h, 0], h]
+            assert bool(((out[n, h] - want).abs() <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20) * want.abs()).all()), (n, h)
+            rows += 1
+    assert rows > w.N
+    w.close()
+
+
 @pytest.mark.parametrize("cache", ["f16", *KINDS])
 @pytest.mark.parametrize("blocks", [4, 8, 16])  # a warp of the narrow kernels, a group of a wide unit, of a narrow one meet every such block
 @pytest.mark.parametrize("shape, nodes", [("8:4x64", 3), ("16:8x128", 8), ("16:8x128", 40), ("16:8x128", 100)])
