@@ -371,6 +371,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   std::vector<TreeSeq> seqs;
   TreePage* pages = reinterpret_cast<TreePage*>(H + h_pages);
   TreeReadSeq read{};
+  int64_t read_rows[2] = {0, 0};  // sequences may share their cached blocks: more rows than the pool has slots
   int n_pages = 0;
   for (int s = 0; s < S; ++s) {
     const int a0 = b->seq_start[s], T = b->seq_start[s + 1] - a0, ctx = b->ctx[s];
@@ -378,12 +379,13 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
     read.tab = (int32_t)(o - h_tables);
     read.ctx = ctx;
     read.nodes = T;
+    for (int i = 0; i < 2; ++i) read.rows[i] = (int32_t)std::min<int64_t>(read_rows[i], INT32_MAX);
     reinterpret_cast<TreeReadSeq*>(H + h_reads)[s] = read;
     if (T == 0) continue;
     read.blocks[0] += (ctx + T + 15) / 16;
     read.blocks[1] += (ctx + T + 15) / 16 - ctx / 16;
-    read.rows[0] += ctx + T;
-    read.rows[1] += ctx % 16 + T;
+    read_rows[0] += ctx + T;
+    read_rows[1] += ctx % 16 + T;
     seqs.push_back({a0, T, ctx, (int32_t)(o - h_tables)});
     const int32_t* row = b->block_table + (size_t)s * b->max_blocks;
     const int nb = (ctx + T + 15) / 16;
@@ -426,8 +428,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   H[h_hdr + kHdrRowTile] = var.row_tile;
   H[h_hdr + kHdrMerges] = n_mrg;
   H[h_hdr + kHdrPages] = n_pages;
-  H[h_hdr + kHdrRows] = read.rows[0];
-  H[h_hdr + kHdrRows + 1] = read.rows[1];
+  for (int i = 0; i < 2; ++i) H[h_hdr + kHdrRows + i] = read_rows[i] > INT32_MAX ? -1 : (int32_t)read_rows[i];  // -1: no call's number
   int32_t* d = reinterpret_cast<int32_t*>(t->ws + t->lay.meta);
   TreeMeta& m = t->meta;
   m.hdr = d + h_hdr;
@@ -457,7 +458,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   t->n_pages = n_pages;
   for (int i = 0; i < 2; ++i) {
     t->read_blocks[i] = read.blocks[i];
-    t->read_rows[i] = read.rows[i];
+    t->read_rows[i] = read_rows[i];
   }
   return o;
 }
@@ -828,6 +829,8 @@ int dec_tree_read_rows(const dec_tree* t, int32_t part, int64_t* rows) {
   if (rc) return rc;
   if (!rows) return fail(DEC_EINVAL, "NULL argument");
   if (part != DEC_READ_ALL && part != DEC_READ_PAGES) return fail(DEC_EINVAL, "unknown part %d", part);
+  if (t->read_rows[part] > INT32_MAX)
+    return fail(DEC_ERANGE, "%lld rows are more than one call reads: read fewer sequences", (long long)t->read_rows[part]);
   *rows = t->read_rows[part];
   return DEC_OK;
 }

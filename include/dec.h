@@ -714,8 +714,10 @@ int dec_tree_commit(dec_tree* t, const int32_t* draft, const int32_t* target, co
  * nearest even from the cache's values; codes * 2^e above f16's range become
  * infinite), rows ld elements and layers layer_stride elements apart, either
  * may be NULL; k and v must not overlap.  Any pool.  rows: as
- * dec_tree_read_rows gives it (DEC_EINVAL otherwise); a captured call replayed
- * on a plan that has another number does nothing and sets DEC_DEV_SHAPE. */
+ * dec_tree_read_rows gives it (DEC_EINVAL otherwise; DEC_ERANGE where they are
+ * 2^31 or more, as sequences that share their cached blocks may have); a captured
+ * call replayed on a plan that has another number does nothing and sets
+ * DEC_DEV_SHAPE. */
 #define DEC_READ_ALL   0
 #define DEC_READ_PAGES 1
 int dec_tree_read_rows(const dec_tree* t, int32_t part, int64_t* rows);

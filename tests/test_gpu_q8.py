@@ -606,6 +606,37 @@ def test_read_into_given_rows_and_one_side_alone(kind):
     w.close()
 
 
+def test_rows_past_two_to_the_31_are_refused():
+    """Sequences that share a long prompt have more rows than 32 bits count; what they changed is read as ever."""
+    seqs, ctx = 53000, 40900  # 2556 shared blocks, slots 4 .. of a block of their own
+    H, Hkv, D = SHAPES["4:2x32"]
+    shape = {"vocab": 512, "d_model": 64, "n_layers": 1, "n_heads": H, "n_kv_heads": Hkv, "head_dim": D, "ff_hidden": 64}
+    shared = ctx // 16
+    pool = KvPool(shape, dec.DEC_BF16_F16KV, shared + seqs, max_positions=40960, kv_type=dec.DEC_T_I8)
+    ids = torch.tensor(pool.alloc(shared + seqs), dtype=torch.int32)
+    table = torch.empty((seqs, shared + 1), dtype=torch.int32)
+    table[:, :shared], table[:, shared] = ids[:shared], ids[shared:]
+    trees = DraftTrees(pool, seqs, seqs, shared + 1)
+    arrays = (torch.arange(seqs + 1, dtype=torch.int32), torch.full((seqs,), ctx, dtype=torch.int32), torch.full((seqs,), -1, dtype=torch.int32), table)
+    b = dec.dec_tree_batch(seqs, seqs, *(C.cast(x.data_ptr(), C.POINTER(C.c_int32)) for x in arrays), shared + 1)
+    L, st, rows = dec.lib(), C.c_void_p(torch.cuda.current_stream().cuda_stream), C.c_int64(7)
+    assert L.dec_tree_set(trees.handle, C.byref(b), st) == dec.DEC_OK
+    assert L.dec_tree_read_rows(trees.handle, dec.DEC_READ_ALL, C.byref(rows)) == dec.DEC_ERANGE and rows.value == 7
+    out = torch.full((seqs * 5, Hkv, D), 3.0, device="cuda")
+    for n in (seqs * 5, seqs * (ctx + 1), (seqs * (ctx + 1) + 2 ** 31) % 2 ** 32 - 2 ** 31):
+        assert L.dec_tree_read(trees.handle, 0, 1, dec.DEC_READ_ALL, n, dec.DEC_T_F32, out.data_ptr(), None, Hkv * D, 0, st) == dec.DEC_ERANGE
+    trees.n_tokens, trees.n_seqs = seqs, seqs
+    assert L.dec_tree_read_rows(trees.handle, dec.DEC_READ_PAGES, C.byref(rows)) == dec.DEC_OK and rows.value == seqs * 5
+    k = torch.randn((seqs, Hkv, D), device="cuda")
+    trees.append(0, None, k, k)
+    assert L.dec_tree_read(trees.handle, 0, 1, dec.DEC_READ_PAGES, seqs * 5, dec.DEC_T_F32, out.data_ptr(), None, Hkv * D, 0, st) == dec.DEC_OK
+    got = out.view(seqs, 5, Hkv, D)
+    assert not bool(got[:, :4].any()) and float((got[:, 4] - k).abs().max()) <= float(k.abs().max()) / 63 / 2
+    assert trees.status() == 0
+    trees.close()
+    pool.close()
+
+
 # ---- together, captured, on streams ------------------------------------------------------------------------------
 
 
