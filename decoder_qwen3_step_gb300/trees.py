@@ -151,7 +151,7 @@ class DraftTrees:
         self._streams = set()  # that calls were made on
         self._heads, self._kv_heads, self._dim = self.cfg.n_heads, self.cfg.n_kv_heads, self.cfg.head_dim
         self._kv_width = self._kv_heads * self._dim
-        self._read_of = ((0, 0, (0, self._kv_heads, self._dim)),) * 2  # by part: rows, elements of a layer, shape
+        self._read_of = {}  # by part, once a plan's rows are wanted: rows, elements of a layer, shape
         # a step makes these calls for every layer: the lookups are done once
         self._append, self._attend, self._commit, self._read = self.L.dec_tree_append, self.L.dec_tree_attend, self.L.dec_tree_commit, self.L.dec_tree_read
         self._qkv = dec.dec_tree_qkv()
@@ -188,15 +188,15 @@ class DraftTrees:
         if not self.pool.pool:
             raise ValueError("the pool is closed")
         b, keep = tree_batch(ctx, parents, tables)
+        self._read_of = {}
         dec.check(self.L.dec_tree_set(self.handle, C.byref(b), self._stream(stream)), "dec_tree_set")
         self.n_seqs, self.n_tokens = b.n_seqs, b.n_tokens
-        rows = (self._read_rows(part) for part in (dec.DEC_READ_ALL, dec.DEC_READ_PAGES))
-        self._read_of = tuple((n, n * self._kv_width, (n, self._kv_heads, self._dim)) for n in rows)
 
     def _read_rows(self, part):
         n = C.c_int64()
         dec.check(self.L.dec_tree_read_rows(self.handle, part, C.byref(n)), "dec_tree_read_rows")
-        return n.value
+        self._read_of[part] = n.value, n.value * self._kv_width, (n.value, self._kv_heads, self._dim)
+        return self._read_of[part]
 
     def append(self, layer: int, q, k, v, rope: RopeTable | None = None, q_norm=None, k_norm=None, q_type=torch.float32,
                out=None, stream=None):
@@ -296,8 +296,7 @@ class DraftTrees:
         `layer` on.  Rows: the sequences' slots one after the other, all of them or
         (DEC_READ_PAGES) from the block on that holds the sequence's first node.
         out: two such tensors, contiguous, or None in the place of one that is not wanted."""
-        # an unknown part is the library's to refuse
-        rows, span, shape = self._read_of[part] if part in (0, 1) else (0, 0, (0, self._kv_heads, self._dim))
+        rows, span, shape = self._read_of.get(part) or self._read_rows(part)
         n = 1
         if layers is not None:
             if layers < 1:

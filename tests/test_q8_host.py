@@ -110,3 +110,41 @@ def test_the_codes_of_the_references():
     every = torch.arange(256, dtype=torch.uint8)
     keep = (every & 0x7F) != 0x7F
     assert torch.equal(codes_of(numbers(every[keep], "e4m3"), x(0), "e4m3"), every[keep])
+
+
+def test_a_step_that_reads_nothing_back_asks_for_no_rows():
+    """set makes one call of the library; the first read of a plan asks for its rows, the next ones do not."""
+    from decoder_qwen3_step_gb300.trees import DraftTrees
+
+    calls = []
+
+    class Library:
+        def dec_tree_set(self, *_):
+            calls.append("set")
+            return 0
+
+        def dec_tree_read_rows(self, _, part, n):
+            calls.append(("rows", part))
+            n._obj.value = 5 + part
+            return 0
+
+        def dec_tree_destroy(self, _):
+            pass
+
+    class Pool:
+        pool = True
+
+    t = DraftTrees.__new__(DraftTrees)
+    t.L, t.pool, t.handle, t._read_of = Library(), Pool(), None, {}
+    t._kv_heads, t._dim, t._kv_width, t._index, t.device = 2, 32, 64, 0, "cpu"
+    t._stream = lambda stream: 0
+    t._read = lambda handle, layer, n, part, rows, *rest: calls.append(("read", rows)) and 0
+    t.set([3], [2], [[0]])
+    assert calls == ["set"]
+    for part in (0, 0, 1, 1):
+        k, v = t.read(0, part)
+        assert k.shape == v.shape == (5 + part, 2, 32)
+    assert calls[1:] == [("rows", 0), ("read", 5), ("read", 5), ("rows", 1), ("read", 6), ("read", 6)]
+    t.set([3], [2], [[0]])
+    t.read(0)
+    assert calls[7:] == ["set", ("rows", 0), ("read", 5)]
