@@ -758,7 +758,8 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
           }
           mx = kQ8 ? __fadd_rn(__fmul_rn(mx, f), e) : mx * f;
           if (__any_sync(0xffffffffu, mx - m > (kQ8 ? kAbove8 : 8.f))) {  // (a sum with m could round up to the next score)
-            const float mn = fmaxf(m, kQ8 ? mx - kBelow8 : mx), g = mn == m ? 1.f : ex2(m - mn);
+            const float below = mx - (kQ8 ? kBelow8 : 0.f);  // from 2^27 on it may round to 16 below, where weights would be infinite
+            const float mn = fmaxf(m, mx - below > kAbove8 ? mx : below), g = mn == m ? 1.f : ex2(m - mn);
             m = mn;
             l *= g;
             if (!first) {  // this group's products so far have run: its S was issued behind them
