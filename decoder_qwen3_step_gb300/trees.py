@@ -17,6 +17,9 @@ power-of-two scale per page and head: append quantises, attend and commit work o
 the codes, and ``trees.read(layer)`` gives the values back (from any pool)::
 
     pool = KvPool(shape, dec.DEC_BF16_F16KV, n_blocks, kv_type=dec.DEC_T_I8)
+
+(A page's scale is that of the largest value it was ever given: a rejected draft
+rounds the accepted tokens of its page more coarsely, for good.)
 """
 
 from __future__ import annotations

@@ -218,6 +218,11 @@ int dec_pool_refcount(const dec_pool* p, int32_t id, int32_t* refs);
  * codes that are rounded again lose less than one step of the new scale in all.
  * (amax / Q itself as the scale would give i8 half a bit more on average, but
  * each of up to 15 rises within a page would cost half a step.)
+ * What a page was given includes drafts that were rejected: over an f16 cache
+ * they leave no trace, here a rejected node's large value rounds the accepted
+ * tokens of its page to its own steps, for good, and a page that commit fills
+ * starts with the e of the nodes that were written there.  A scale falls again
+ * only when dec_tree_append writes the page's first slot.
  *
  * Layout: codes as in a pool of any type, one byte an element; then, from the
  * next multiple of 256 bytes on, fp32 scales [layers][blocks][KV heads][2] (K,
@@ -669,8 +674,8 @@ typedef struct dec_tree_qkv {
  * `layer` (f16 caches: round to nearest even).  Computed in fp32.
  * A cache held in 8 bits: a page's e becomes the smallest that the rows written
  * to it by this call need (padding nodes do not count) and, where it holds
- * cached tokens, at least what it was; if it rises, the cached tokens' codes are
- * rounded again.  Codes round to nearest even.  Infinities become the page's
+ * cached tokens, at least what it was (rejected drafts of earlier calls among
+ * it); if it rises, the cached tokens' codes are rounded again.  Codes round to nearest even.  Infinities become the page's
  * largest code and NaN 0, neither counts for e, and DEC_DEV_NONFINITE is
  * raised.  Magnitudes above Q 2^40 are cut to that. */
 int dec_tree_append(dec_tree* t, int32_t layer, const dec_tree_qkv* x, void* stream);

@@ -686,6 +686,46 @@ def test_steps_of_drafting_give_the_plain_sequence(shape, kind):
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
+def test_a_rejected_draft_rounds_the_accepted_tokens_of_its_page(kind):
+    """What the documents say of it: its scale stays, and the page's tokens keep the bits of that scale only; pages in front
+    of it, the same step without that node, and a page that begins anew do not have it."""
+    at = {}
+    for large in (False, True):
+        w = Setup8("16:8x128", kind, [20], [[-1, 0, 0]], seed=3, extra_blocks=1)
+        blocks = w.tables[0] + [b for b in range(w.blocks) if b not in w.tables[0]][:1]
+        w.tables = [blocks]
+        w.trees.close()
+        w.trees = DraftTrees(w.pool, 1, 16, 4)
+        w.trees.set([20], [[-1, 0, 0]], w.tables)
+        x = torch.randn((2, 3, w.Hkv, w.D), generator=w.g).cuda()
+        first, e = w.values()[0, blocks[1]].clone(), log2(w.scales[0, blocks[1]]).T
+        before = w.codes[0, blocks[0]].clone()
+        if large:
+            x[:, 1] *= 2.0 ** 12  # node 1 is rejected
+        w.trees.append(0, None, x[0], x[1])
+        draft, target = (torch.tensor(t, dtype=torch.int32, device="cuda") for t in ([5, 6, 7], [7, 0, 0]))
+        accepted, path, _ = w.trees.commit(draft, target)
+        assert accepted.tolist() == [2] and path.tolist() == [0, 2, -1]
+        # the next step: one token in the same page, which needs less
+        w.trees.set([22], [[-1]], w.tables)
+        w.trees.append(0, None, x[0, :1], x[1, :1])
+        e_now = log2(w.scales[0, blocks[1]]).T
+        want_e = torch.maximum(e, need(x.double().abs().amax((1, 3)), kind))
+        assert torch.equal(e_now, want_e) and torch.equal(w.codes[0, blocks[0]], before)
+        # cached tokens 16 .. 19: their codes at the scale that the page had, rounded again to what it has now
+        now = w.values()[0, blocks[1]]
+        assert torch.equal(now[:, :, :4], numbers(codes_of(first[:, :, :4], e_now[..., None, None], kind), kind) * two(e_now)[..., None, None])
+        at[large] = float((now[:, :, :4] - first[:, :, :4]).norm() / first[:, :, :4].norm())
+        # sixteen chained tokens later the next page has only its own rows' scale
+        w.trees.set([23], [10], w.tables)
+        y = torch.randn((2, 10, w.Hkv, w.D), generator=w.g).cuda()
+        w.trees.append(0, None, y[0], y[1])
+        assert torch.equal(log2(w.scales[0, blocks[2]]).T, need(y[:, 9:].double().abs().amax((1, 3)), kind))
+        w.close()
+    assert at[True] > 16 * at[False]  # seven of i8's eight bits gone, e4m3's small values among its subnormal codes
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("seqs, nodes", [(3, 6), (30, 7), (10, 60), (4, 200)])
 def test_captured_calls_follow_the_plan(seqs, nodes, kind):
     total = seqs * nodes
