@@ -14,7 +14,7 @@ torch = pytest.importorskip("torch")
 
 from decoder_qwen3_step_gb300 import dec  # noqa: E402
 from decoder_qwen3_step_gb300.trees import DraftTrees, KvPool, RopeTable  # noqa: E402
-from tests.q8_reference import E_MIN, KINDS, codes_of, log2, need, numbers, two  # noqa: E402
+from tests.q8_reference import E_MIN, KINDS, codes_of, log2, need, numbers, rounded, two  # noqa: E402
 from tests.test_gpu_trees import BATCHES, HALF_STEP, PAD, SHAPES, formed, frequencies, random_tree, walk  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -351,6 +351,55 @@ def test_append_is_the_formula(shape, rot, layout, in_type, kind):
     assert int((w.codes[0] != codes).sum()) <= 4 + 8 * eps * 2.0 ** 7 * codes.numel()
     assert torch.equal(w.codes[0, :, 1], codes[:, 1])  # values are not rotated
     assert torch.equal(w.codes[1], before[1])
+    w.close()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("in_type", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape, rot, layout", [("4:2x32", 32, dec.DEC_ROPE_INTERLEAVED), ("4:2x32", 8, dec.DEC_ROPE_HALF), ("16:8x128", 128, dec.DEC_ROPE_HALF), ("16:8x128", 72, dec.DEC_ROPE_INTERLEAVED),
+                                                ("8:4x64", 48, dec.DEC_ROPE_HALF), ("8:2x128", 128, dec.DEC_ROPE_HALF)])
+def test_every_appended_code_lies_between_the_roundings(shape, rot, layout, in_type, kind):
+    """A key's code is one that a value within fp32's reach of the formula rounds to, nothing else is written."""
+    w = Setup8(shape, kind, [37, 0, 250, 15], [random_tree(40, 1), 3, [-1, PAD, 0, 0, PAD], 1], seed=rot, spread=0)
+    Hkv, D = w.Hkv, w.D
+    k, v = (torch.randn((w.N, Hkv, D), generator=w.g).cuda().to(in_type) for _ in range(2))
+    g = 1 + 0.1 * w.rand(D)
+    rope = RopeTable(rot, 400, layout=layout, scaling=dec.DEC_ROPE_LINEAR, factor=4.0)
+    freq = frequencies(rot, 1e6, dec.DEC_ROPE_LINEAR, 4.0, 0, 0, 0)
+    pos = torch.tensor([p or 0 for *_, p in w.nodes()], device="cuda")
+    fk = formed(k, g, pos, rot, layout, freq, 1.0)
+    # as in test_append_is_the_formula: the table's rounding, two products and their sum, the norm
+    eps = (4 + D / 2 + 6) * 2.0 ** -24
+    off = eps * (fk.abs() + 2 * formed(k, g, pos, 0, 0, freq, 1.0).abs().amax(-1, keepdim=True))
+    off = torch.stack([off, torch.zeros_like(off)], 1)  # values are rounded to codes only
+    kv = torch.stack([fk, v.double()], 1)
+    codes, was = w.codes[0].clone(), log2(w.scales[0]).transpose(1, 2).clone()  # [blocks, 2, KV heads]
+    w.trees.append(0, None, k, v, rope=rope, k_norm=g)
+    got, e = numbers(w.codes[0], kind), log2(w.scales[0]).transpose(1, 2)
+    untouched = torch.ones_like(codes, dtype=torch.bool)
+    pages = {}
+    for n, s, i, slot, p in w.nodes():
+        pages.setdefault((s, slot // 16), []).append((n, slot % 16, p))
+    for (s, p), rows in pages.items():
+        b, live = w.tables[s][p], [(n, r) for n, r, at in rows if at is not None]
+        cached = max(0, min(16, w.ctx[s] - p * 16))
+        least = was[b] if cached else torch.full_like(was[b], E_MIN)
+        at = torch.tensor([n for n, _ in live], dtype=torch.long, device="cuda")
+        for bound, side in ((kv[at].abs() - off[at], 1), (kv[at].abs() + off[at], -1)):
+            edge = torch.maximum(least, need(bound.clamp(min=0).amax((0, -1)), kind)) if live else least
+            assert bool((side * (e[b] - edge) >= 0).all())
+        if cached:
+            again = codes_of(numbers(codes[b, :, :, :cached], kind) * two(was[b])[..., None, None], e[b][..., None, None], kind)
+            rose = (e[b] > was[b])[..., None, None]
+            assert torch.equal(w.codes[0][b, :, :, :cached], torch.where(rose, again, codes[b, :, :, :cached]))
+            untouched[b, :, :, :cached] = False
+        for n, r in live:
+            scale = two(e[b])[..., None]
+            low, high = (rounded((kv[n] + side * off[n]) / scale, kind) for side in (-1, 1))
+            mine = got[b, :, :, r]
+            assert bool(((low <= mine) & (mine <= high)).all()), (n, r)
+            untouched[b, :, :, r] = False
+    assert torch.equal(w.codes[0][untouched], codes[untouched])
     w.close()
 
 
