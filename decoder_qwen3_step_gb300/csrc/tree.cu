@@ -365,8 +365,11 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   const int W = std::max((max_nodes + 31) / 32, 1);
   const TreeVariant var = variant_for(t->kv_type, c.head_dim, max_nodes * G);
   const int grid = std::max(t->sms * var.ctas_per_sm - var.spare, t->sms);
-  const size_t h_hdr = take(kHdrInts), h_flags = take((size_t)t->sms * kTreeMaxCtasPerSm), h_start = take(S + 1), h_seqs = take((size_t)S * 4), h_pos = take(N), h_dst = take(N),
-               h_par = take(N), h_anc = take((size_t)N * W), h_cut = take((size_t)grid * 12), h_mrg = take((size_t)grid * 8),
+  // Where a piece lies depends on S, N and W alone, which a captured call is replayed with: the cuts and merges have room for
+  // any variant's grid, as append, commit and reading back follow plans whose attention takes another one.
+  const size_t P = (size_t)t->sms * kTreeMaxCtasPerSm;
+  const size_t h_hdr = take(kHdrInts), h_flags = take(P), h_start = take(S + 1), h_seqs = take((size_t)S * 4), h_pos = take(N), h_dst = take(N),
+               h_par = take(N), h_anc = take((size_t)N * W), h_cut = take(P * 12), h_mrg = take(P * 8),
                h_reads = take((size_t)(S + 1) * 8), h_pages = take(t->q8 ? (size_t)N * 4 : 0), h_tables = o;
   std::vector<TreeSeq> seqs;
   TreePage* pages = reinterpret_cast<TreePage*>(H + h_pages);
@@ -419,7 +422,7 @@ size_t build_plan(dec_tree* t, const dec_tree_batch* b, int32_t* H) {
   static_assert(sizeof(TreeSeq) == 16 && sizeof(TreeCut) == 48 && sizeof(TreeMerge) == 32 && sizeof(TreePage) == 16 && sizeof(TreeReadSeq) == 32, "as the pieces are measured above");
   const int n_mrg = distribute(c, seqs, var, grid, var.kernel == kTreeTcWide ? kWideGang : 1, reinterpret_cast<TreeCut*>(H + h_cut),
                                reinterpret_cast<TreeMerge*>(H + h_mrg), &t->max_parts);
-  std::fill(H + h_flags, H + h_flags + t->sms * kTreeMaxCtasPerSm, 0);
+  std::fill(H + h_flags, H + h_flags + P, 0);
   std::copy(seqs.begin(), seqs.end(), reinterpret_cast<TreeSeq*>(H + h_seqs));
   std::fill(H + h_hdr, H + h_hdr + kHdrInts, 0);
   H[h_hdr + kHdrSeqs] = S;

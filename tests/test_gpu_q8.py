@@ -831,6 +831,58 @@ def test_captured_calls_follow_the_plan(seqs, nodes, kind):
     w.close()
 
 
+@pytest.mark.parametrize("kind", ["f16", *KINDS])
+@pytest.mark.parametrize("captured, replayed", [(4, 8), (4, 20), (8, 4), (8, 30), (20, 4), (20, 8)])
+def test_captured_append_commit_and_read_follow_plans_of_other_attention_kernels(captured, replayed, kind):
+    """16 sequences, 64 nodes, one word of mask: the longest sequence decides the attention's kernel and grid, and the other
+    calls' replays do not mind."""
+    def sizes(longest, seed):
+        rng, n = random.Random(seed), [longest] + [1] * 15
+        while sum(n) < 64:
+            i = rng.randrange(1, 16)
+            n[i] += n[i] < longest
+        return n
+
+    from tests.test_gpu_trees import Setup
+
+    def trees_of(longest, seed):
+        return [random_tree(n, seed * 50 + i) for i, n in enumerate(sizes(longest, seed))]
+
+    ctx = [21 + 9 * s for s in range(16)]
+    parents = trees_of(captured, 1)
+    w = Setup("16:8x128", "f16", ctx, parents, seed=2, extra_blocks=64) if kind == "f16" else Setup8("16:8x128", kind, ctx, parents, seed=2, extra_blocks=64)
+    buf = w.slab if kind == "f16" else w.buf
+    q, k, v = w.rand(64, w.H, w.D), w.rand(64, w.Hkv, w.D), w.rand(64, w.Hkv, w.D)
+    rope = RopeTable(128, 2000)
+    draft, target = (torch.randint(2, (64,), generator=w.g, dtype=torch.int32).cuda() for _ in range(2))
+
+    def step():
+        return (w.trees.append(0, q, k, v, rope=rope), *w.trees.commit(draft, target), *w.trees.read(0, layers=2))
+
+    step()
+    torch.cuda.synchronize()
+    start = buf.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for turn in range(3):
+        parents = trees_of(replayed, turn + 2)
+        ctx = list(reversed(ctx))  # as many rows in all
+        ids = list(range(w.blocks))
+        random.Random(turn).shuffle(ids)
+        tables = [[ids.pop() for _ in range((c + len(p) + 15) // 16)] for c, p in zip(ctx, parents)]
+        w.trees.set(ctx, parents, tables)
+        buf.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed_to = [x.clone() for x in held] + [buf.clone()]
+        buf.copy_(start)
+        for x, y in zip(replayed_to, [*step(), buf]):
+            assert torch.equal(x, y)
+    assert w.trees.status() == 0
+    w.close()
+
+
 @pytest.mark.parametrize("kind", list(KINDS))
 def test_a_captured_read_of_another_number_of_rows_does_nothing(kind):
     w = Setup8("8:4x64", kind, [40, 40], [3, 3], seed=1, extra_blocks=4)
