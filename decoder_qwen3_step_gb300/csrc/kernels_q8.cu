@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kCommitThreads, 4) k_commit_q8(const __grid_co
   const bool ok = tree_shape_ok(a.m);  // the plan is older than the kernels before this one
   const int b = __ldg(a.m.seq_start + s), T = min(__ldg(a.m.seq_start + s + 1) - b, kTreeMaxNodes);
   const int ctx = __ldg(&a.m.reads[s].ctx), tab = __ldg(&a.m.reads[s].tab);
-  for (int i = threadIdx.x; i < T; i += kCommitThreads) dst[i] = __ldg(a.m.dst + b + i);
+  for (int i = threadIdx.x; ok && i < T; i += kCommitThreads) dst[i] = __ldg(a.m.dst + b + i);  // (of another plan b may be anything)
   const int n = tree_walk<kCommitThreads>(a, s, b, T, ok, part == 0, child, path, &n_path);
   const int lane = threadIdx.x & 31, sub = lane / kLanes, el = (lane % kLanes) * 16;
   int i0 = 0;

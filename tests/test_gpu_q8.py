@@ -908,6 +908,47 @@ def test_a_captured_read_of_another_number_of_rows_does_nothing(kind):
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("captured, replayed", [([5] * 20, [100]), ([5] * 20, [4] * 25), ([100], [5] * 20), ([60, 40], [100]), ([100], [120]), ([6] * 4, [6] * 5), ([9], [8])])
+def test_captured_calls_on_a_plan_of_another_shape_do_nothing(captured, replayed, kind):
+    """Sequences, nodes or mask words differ (the attention's rows in the last pair, too)."""
+    w = Setup8("16:8x128", kind, [40 + 7 * s for s in range(len(captured))], captured, seed=1, extra_blocks=300, max_tokens=128)
+    n, seqs = w.N, len(captured)
+    w.trees.close()
+    w.trees = DraftTrees(w.pool, 32, 128, 16)
+    w.trees.set(w.ctx, w.parents, w.tables)
+    q, k, v = w.rand(n, w.H, w.D), w.rand(n, w.Hkv, w.D), w.rand(n, w.Hkv, w.D)
+    draft, target = (torch.randint(2, (n,), generator=w.g, dtype=torch.int32).cuda() for _ in range(2))
+
+    def calls():
+        return ((w.trees.append(0, q, k, v),), (w.trees.attend(0, q),), w.trees.commit(draft, target), w.trees.read(0))
+
+    calls()
+    torch.cuda.synchronize()
+    graphs, held = [], []
+    for i in range(4):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append((lambda: (w.trees.append(0, q, k, v),), lambda: (w.trees.attend(0, q),), lambda: w.trees.commit(draft, target), lambda: w.trees.read(0))[i]())
+    ids = list(range(w.blocks))
+    random.Random(1).shuffle(ids)
+    ctx = [33 + 5 * s for s in range(len(replayed))]
+    tables = [[ids.pop() for _ in range((c + m + 15) // 16)] for c, m in zip(ctx, replayed)]
+    w.trees.set(ctx, replayed, tables)
+    for graph, out in zip(graphs, held):
+        for x in out:
+            x.fill_(3)
+        start = w.buf.clone()
+        graph.replay()
+        assert w.trees.status() == dec.DEC_DEV_SHAPE
+        assert torch.equal(w.buf, start) and all(bool((x == 3).all()) for x in out)
+    w.trees.set(w.ctx, w.parents, w.tables)  # and follow the plan of their capture again
+    for graph in graphs:
+        graph.replay()
+    assert w.trees.status() == 0
+    w.close()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("nodes", [4, 50, 150])
 def test_two_plans_on_two_streams(nodes, kind):
     ws = [Setup8("16:8x128", kind, [300, 77], [nodes, nodes], seed=s) for s in range(2)]
