@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(128, 5) k_append_q8(const __grid_constant__ Tr
     int block = 0, node = warp / per_node, slot0 = 0, n = min(per, a.d.H - h);
     if (!is_q) {
       const int4 p = __ldg(reinterpret_cast<const int4*>(a.m.pages) + t / (2 * a.d.Hkv));
-      block = p.x;
+      block = tree_block(a.m, a.d.n_blocks, p.x);
       node = p.y;
       slot0 = p.z;
       n = p.w;
@@ -278,7 +278,10 @@ __global__ void __launch_bounds__(kCommitThreads, 4) k_commit_q8(const __grid_co
   const bool ok = tree_shape_ok(a.m);  // the plan is older than the kernels before this one
   const int b = __ldg(a.m.seq_start + s), T = min(__ldg(a.m.seq_start + s + 1) - b, kTreeMaxNodes);
   const int ctx = __ldg(&a.m.reads[s].ctx), tab = __ldg(&a.m.reads[s].tab);
-  for (int i = threadIdx.x; ok && i < T; i += kCommitThreads) dst[i] = __ldg(a.m.dst + b + i);  // (of another plan b may be anything)
+  for (int i = threadIdx.x; ok && i < T; i += kCommitThreads) {  // (of another plan b may be anything)
+    const int d = __ldg(a.m.dst + b + i);
+    dst[i] = tree_block(a.m, a.d.n_blocks, d >> 4) * 16 + (d & 15);
+  }
   const int n = tree_walk<kCommitThreads>(a, s, b, T, ok, part == 0, child, path, &n_path);
   const int lane = threadIdx.x & 31, sub = lane / kLanes, el = (lane % kLanes) * 16;
   int i0 = 0;
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(kCommitThreads, 4) k_commit_q8(const __grid_co
   };
   auto scale_of = [&](int block) { return a.scales + q8_scale_at(a.d, layer, block, h, is_v); };
   for (int p = (ctx + i0) >> 4; p <= (ctx + n - 1) >> 4; ++p) {
-    const int block = __ldg(a.m.tables + tab + p);
+    const int block = tree_block(a.m, a.d.n_blocks, __ldg(a.m.tables + tab + p));
     uint8_t* page = page_of(block);
     uint4 w[kSteps];
     float f[kSteps];  // the sources' scales
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(256) k_tree_read(const __grid_constant__ TreeR
     from = a.part ? ctx >> 4 : 0;
     p = from + b - __ldg(&q.blocks[a.part]);
     rows = min(16, ctx + __ldg(&q.nodes) - p * 16);
-    block = __ldg(a.m.tables + __ldg(&q.tab) + p);
+    block = tree_block(a.m, a.d.n_blocks, __ldg(a.m.tables + __ldg(&q.tab) + p));
     row0 = __ldg(&q.rows[a.part]) + (p - from) * 16;
   };
   if (ok && fits && blockIdx.x < nb) place(blockIdx.x);

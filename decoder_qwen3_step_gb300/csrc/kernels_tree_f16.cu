@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kF16Threads, 2) k_tree_attend_f16(const __grid
             if (!tree_sees(a.m, node, n)) continue;
             const int p = u.ctx + n;
             const float z = __half2float(reinterpret_cast<const __half*>(
-                a.kv)[kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D) + i % D]);
+                a.kv)[kv_offset(a.layer, tree_block(a.m, a.d.n_blocks, __ldg(table + (p >> 4))), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D) + i % D]);
             if (isfinite(z)) continue;
             if (whole) tree_store(a.out, a.out_type, out_at(r) + i % D, tree_load(a.out, a.out_type, out_at(r) + i % D) + z);
             else part[i] += z;

@@ -980,7 +980,7 @@ __global__ void __launch_bounds__(kKind == kTreeF16 ? kTcTreeThreads : kTcTreeTh
             if (!tree_sees(a.m, node, x)) continue;
             const int p = u.ctx + x;
             const __half* at = reinterpret_cast<const __half*>(a.kv) +
-                               kv_offset(a.layer, __ldg(table + (p >> 4)), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D);
+                               kv_offset(a.layer, tree_block(a.m, a.d.n_blocks, __ldg(table + (p >> 4))), 1, u.head, p & 15, a.d.n_blocks, a.d.Hkv, 16, D);
 #pragma unroll 1
             for (int i = ch0; i < ch1; ++i) {
               const float z = __half2float(at[i]);

@@ -49,6 +49,20 @@ __device__ __forceinline__ void tree_unit_next(const TreeMeta& m, int gs, int R,
   tree_unit_seq(m, __ldg(reinterpret_cast<const int4*>(m.seqs + u.q)), u);
 }
 
+// Pool block blk, as the plan names it.  DEC_DEBUG builds: block 0 in place of one outside the pool, and kErrBounds.
+__device__ __forceinline__ int tree_block(const TreeMeta& m, int n_blocks, int blk) {
+#ifdef DEC_DEBUG
+  if ((unsigned)blk >= (unsigned)n_blocks) {
+    atomicOr(m.err, kErrBounds);
+    return 0;
+  }
+#else
+  (void)m;
+  (void)n_blocks;
+#endif
+  return blk;
+}
+
 // Whether node `node` (numbered over the batch) sees node j of its sequence.
 __device__ __forceinline__ bool tree_sees(const TreeMeta& m, int node, int j) {
   return (__ldg(m.anc + (size_t)node * m.words + (j >> 5)) >> (j & 31)) & 1u;
