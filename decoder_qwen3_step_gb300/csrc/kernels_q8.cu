@@ -18,10 +18,11 @@ namespace {
 // shared memory (8 KB a warp at D = 128) between the maximum and the codes, one
 // pass over the data.  Query rows go through the same code, `per` heads of a node
 // a warp.
-// HBM bounds the large calls, instructions not far behind (32 x 256 nodes: 82 us
-// with the rows in registers, every loop unrolled to 16 rows and 147 instructions
-// a row), so a task's rows are copied to shared memory all at once (with four
-// steps of them in flight 56 us; now 50: 195 MB at 3.9 TB/s), and the loops go four steps at a time: their
+// Large calls are bound by latency: 20 warps an SM, one task each, copy, wait for
+// all of it and work (32 x 256 nodes: 195 MB in 50 us, 3.9 TB/s, 44% of the issue
+// slots, 26% of the warps).  A task's rows are copied to shared memory all at once
+// (with four steps of them in flight 56 us; with the rows in registers, every loop
+// unrolled to 16 rows and 147 instructions a row, 82), and the loops go four steps at a time: their
 // sums of squares are reduced together (6 shuffles for 4 rows of 128 channels; the
 // lanes end up with one row's each, so one root and quotient serve four rows), and
 // what is rare is looked for once a page (padding, values that are not finite, e
@@ -55,7 +56,7 @@ __device__ __forceinline__ uint32_t q8_pack_fit(float4 y, float inv) {
 template <int D, int kKind, typename T>
 __global__ void __launch_bounds__(128, 5) k_append_q8(const __grid_constant__ TreeAppendArgs a, int q_tasks, int per, int kv_warps) {
   constexpr int kLanes = D / 4, kRows = 32 / kLanes, kSide = kAppendSide;
-  extern __shared__ __align__(16) float4 formed[];  // [8 warps][16 rows][kLanes]
+  extern __shared__ __align__(16) float4 formed[];  // [4 warps][16 rows][kLanes]
   const bool ok = tree_shape_ok(a.m);  // the plan is older than the kernels before this one
   const int n_pages = __ldg(a.m.hdr + kHdrPages);
   pdl_wait_prev();

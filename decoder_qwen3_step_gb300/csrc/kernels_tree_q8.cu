@@ -52,7 +52,7 @@ template <int D, int R>
 struct Q8Smem {
   static constexpr int kSlab = 16 * D;                         // K (or V) of one block
   static constexpr int kStage = 4 * 2 * kSlab;
-  static constexpr int kCtas = D == 128 && R == 16 ? 2 : 3;    // per SM: with 16 rows of 128 channels a lane needs 160 registers
+  static constexpr int kCtas = D == 128 && R == 16 ? 2 : 3;    // per SM: with 16 rows of 128 channels a lane takes 168 registers, and spills 16 to 22 words at that
   static constexpr int kStages = D == 128 ? 4 : D == 64 ? 8 : 16;  // (two CTAs of 16 rows with six: 32 x 8 over 1500 36.0 us, with four 32.3)
   static constexpr int kQPitch = D * 2 + 16;                   // bytes; rows fall into different banks
   static constexpr int kQ = kStages * kStage;                  // the queries, at a unit's end the warps' outputs

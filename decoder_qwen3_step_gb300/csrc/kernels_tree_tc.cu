@@ -50,10 +50,11 @@
 // and its V codes all times the power of two that other tiles give to their largest
 // page, so that B and b mean the same.
 // Registers are moved from the other warps to the softmax (512 threads have 128
-// each).  32 x 64 nodes over 1024-2048 keys: 52.4 us, 119 MB at 2.3 TB/s; 8 x 256
-// over 8000: 136 us, 934 TFLOP/s.  Neither the codes' bytes nor the products bound
+// each).  32 x 64 nodes over 1024-2048 keys: 52.7 us, 119 MB at 2.3 TB/s; 8 x 256
+// over 8000: 137 us, 927 TFLOP/s.  Neither the codes' bytes nor the products bound
 // it but the steps of a tile, one after the other, with a conversion more than over
-// f16: there the same calls take up to a sixth less time.
+// f16: there the same calls take up to a sixth less time.  The wide form spills: 20
+// bytes at head_dim 128, 140 (e4m3: 44) at 64.
 #include "attn_fold.cuh"
 #include "q8.cuh"
 #include "tc_common.cuh"

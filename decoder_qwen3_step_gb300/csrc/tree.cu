@@ -51,13 +51,15 @@ struct TreeLayout {
 // sequences over 8000 keys with 512 rows, narrow units 211 us, wide ones 114.
 TreeVariant variant_for(int kv_type, int D, int max_rows) {
   if (kv_type == kTreeF32) return {kTreeFfma, max_rows <= 16 ? 16 : 32, 64, D == 128 ? 2 : 3, 2, 0};
-  // a unit's start and end in tiles of 8-bit keys: 2 (before pages far apart had
-  // their own path: 8 x 256 over 8000 132 us, with 4 135, with 6 137.5; 32 x 64 over 1024-2048 50.6, 52.7, 55.5)
+  // a unit's start and end in tiles of 8-bit keys: 2 (8 x 256 over 8000, e4m3: 130.8 us, with 1 131.7, with 4 133.3, with 6
+  // 139.3; 32 x 64, i8, over 1024-2048 52.6, with 4 53.3, over 3000 79.3, 82.5; over one length of 1500 54.5, 52.5)
   const int unit = kv_type == kTreeF16 ? 4 : 2;
   if (D >= 64 && max_rows > 128) return {kTreeTcWide, 256, 128, 1, unit, 50};
   if (D >= 64 && max_rows > 16) return {kTreeTc, 128, 128, 1, unit, 25};
-  // Three CTAs per SM fill the GPU while the kernel before still drains: with 456 the last one or two found no place until
-  // others had ended, 12 us later (32 x 1 over 1024-2048: 27.0 us, with 448 23.1; over 6000: 83, 66.6)
+  // Three CTAs per SM fill the GPU while the kernel before still drains: of 456 the last ones found no place until others had
+  // ended, 12 us later.  With 0, 2, 4, 8, 16 places left free 32 x 1 over 1500 takes 27.5, 23.9, 23.2, 23.1, 23.4 us, over
+  // 6000 81.2, 69.6, 66.4, 66.3, 66.2, 64 x 1 over 1500 46.1, 40.7, 38.7, 37.8, 39.0.  Two CTAs per SM leave registers for a
+  // third and wait for nothing: 32 x 8 over 1500 31.3 us with every place, 31.8 with 4 fewer, 31.7 with 8
   if (kv_type != kTreeF16) return max_rows > 8 && D == 128 ? TreeVariant{kTreeMmaQ8, 16, 64, 2, 2, 0, 0} : TreeVariant{kTreeMmaQ8, max_rows > 8 ? 16 : 8, 64, 3, 2, 0, 8};
   return {kTreeMma, max_rows <= 16 ? 16 : 32, 64, 2, 2, 0};
 }

@@ -552,7 +552,7 @@ int dec_debug_df_exp(const double* x, double* y, int64_t n, void* stream);
  * The trees of a step are one plan, made once with dec_tree_set and used by
  * every layer's calls.  A plan's calls share its workspace: order them on one
  * stream (or by events); two plans are independent.  dec_tree_append,
- * dec_tree_attend and dec_tree_commit can be captured into a CUDA graph; a
+ * dec_tree_attend, dec_tree_commit and dec_tree_read can be captured into a CUDA graph; a
  * replay follows the plan that is set then (by dec_tree_set outside the graph,
  * ordered before the replay) if its shape is the capture's: the same n_seqs,
  * n_tokens and ceil(longest / 32), longest the most nodes of a sequence, and
@@ -714,7 +714,8 @@ int dec_tree_commit(dec_tree* t, const int32_t* draft, const int32_t* target, co
  * order of the sequences and of their slots, of whole sequences (cached tokens,
  * then nodes) or of the slots from the first one of the block on that holds the
  * sequence's first node (what dec_tree_append and dec_tree_commit change).
- * Sequences without nodes have no rows.  k, v: DEVICE
+ * Sequences without nodes have no rows; a padding node's row is what its slot
+ * holds.  k, v: DEVICE
  * [n_layers, rows, n_kv_heads, head_dim] of any DEC_T_F32, F16, BF16 (rounded to
  * nearest even from the cache's values; codes * 2^e above f16's range become
  * infinite), rows ld elements and layers layer_stride elements apart, either
