@@ -55,7 +55,7 @@ def test_many_small_weights_beside_a_page_of_larger_values(shape, seqs, nodes, g
     w.close()
 
 
-@pytest.mark.parametrize("gap", [20, 22, 23, 26, 29, 30, 31, 32, 33, 44])
+@pytest.mark.parametrize("gap", [20, 22, 23, 29, 30, 32, 44])
 @pytest.mark.parametrize("shape, nodes", [("8:4x64", 60), ("16:8x128", 40), ("16:8x128", 200), ("8:4x64", 256), ("16:8x128", 5), ("4:2x32", 60)])
 @pytest.mark.parametrize("kind, fine", [("i8", False), ("e4m3", False), ("e4m3", True)])
 def test_keys_beside_a_page_of_far_larger_ones(kind, fine, shape, nodes, gap):
@@ -76,8 +76,8 @@ def test_keys_beside_a_page_of_far_larger_ones(kind, fine, shape, nodes, gap):
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
-@pytest.mark.parametrize("values", [-38, -20, 0, 20, 34])
-@pytest.mark.parametrize("size", [3e7, 1e8, 1e9, 1e15])
+@pytest.mark.parametrize("values", [-38, 0, 34])
+@pytest.mark.parametrize("size", [1e8, 1e9, 1e15])
 @pytest.mark.parametrize("shape, nodes", [("8:4x64", 5), ("16:8x128", 3), ("16:8x128", 8), ("16:8x128", 40), ("8:4x64", 200)])
 def test_scores_past_the_last_place_of_a_values_exponent(shape, nodes, size, values, kind):
     """Queries so large that one key takes all the weight and its score has no bits left for the exponent of a value's scale:
